@@ -102,11 +102,16 @@ typedef enum {
   DSA_OP_SPARSE_MLA = 1,
   DSA_OP_GATE = 2,
   DSA_OP_CACHE_APPEND = 3,
-  DSA_OP_SPARSE_MLA_BWD = 4
+  DSA_OP_SPARSE_MLA_BWD = 4,
+  DSA_OP_LINEAR_FP8 = 5
 } dsa_op_t;
 
+/* Element type of an output that a call offers in two. */
+typedef enum { DSA_BF16 = 0, DSA_FP32 = 1 } dsa_dtype_t;
+
 /* Bytes of workspace an op needs for the given sizes (heads = H_I for the
- * indexer, H for sparse MLA, ignored for the gate).  Always >= 256. */
+ * indexer, H for sparse MLA, ignored for the gate; for the FP8 projection
+ * B = M, Tq = 1, max_kv_len = K, heads = N).  Always >= 256. */
 size_t dsa_workspace_bytes(dsa_op_t op, int B, int Tq, int max_kv_len, int heads, int topk);
 
 /* Zero the status header of a workspace (asynchronous on `stream`). */
@@ -320,6 +325,78 @@ dsa_status_t dsa_indexer_topk_fp8(const uint8_t* q_codes, const float* q_scale, 
                                   const int32_t* q_start, const int32_t* kv_len, int B, int Tq,
                                   int H_I, int D_I, int max_kv_len, int topk, int32_t* out_idx,
                                   void* workspace, size_t ws_bytes, dsa_stream_t stream);
+
+/*
+ * The FP8 projections around the step.  The indexer queries, the raw indexer
+ * keys, the latent rows and the gate input are projections of the layer's
+ * normed input, and the gated output goes through one more projection; the
+ * three calls below are that path in E4M3 with one FP32 scale per 128 values of
+ * an activation row and one per 128 x 128 block of a weight (nn.Linear layout,
+ * one row per output feature).  Codes and scales are those of dsa_quant_fp8: a
+ * group of values v stands for scale * decode(code) with
+ *   scale = max(max |v|, 2^-100) / 448,  code = E4M3(v * (1 / scale)),
+ * each operation one FP32 operation rounded to nearest, the last rounded to
+ * nearest even and saturating at +-448.  A group that holds a NaN gets a NaN
+ * scale; one that holds an infinity an infinite scale, so that it decodes to
+ * NaN.  Groups at the end of a row (or the last rows) may be shorter than 128.
+ * dsa_quant_fp8 with D = 128 gives the same activation format for a BF16 row
+ * whose width is a multiple of 128 (the gated output, viewed as rows of 128).
+ */
+
+/*
+ * Residual addition, RMS norm and quantisation of a layer's input
+ * (KimiK3TextConfig: hidden_size 7168, rms_norm_eps 1e-5).  Per row:
+ *   h = x + residual                                  (FP32; h = x without one)
+ *   y = h / sqrt(mean(h^2) + eps) * gain              (FP32)
+ *   residual_out = BF16(h),  y_out = BF16(y)          (round to nearest even)
+ *   codes, scale = the E4M3 groups of y along the row (from the FP32 y)
+ *   x, residual  [n_rows, hid] BF16     residual may be NULL
+ *   gain         [hid]         BF16
+ *   residual_out [n_rows, hid] BF16     may be NULL; needs a residual
+ *   y_out        [n_rows, hid] BF16     may be NULL (mla_gate_apply's x)
+ *   codes        [n_rows, hid] uint8
+ *   scale        [n_rows, ceil(hid / 128)] FP32
+ * The norm takes the unrounded sum h.  A row is read whole before any of it is
+ * written: residual_out and y_out may each be x or residual itself (the same
+ * pointer); apart from that no output may overlap an input or another output.
+ * Supported: hid a multiple of 16, 16 <= hid <= 65536; n_rows >= 0 (0: nothing
+ * to do, no pointer is looked at); eps >= 0 and finite.  BF16 arrays and codes
+ * 16-byte aligned, scale 4.  Nothing can fail on the device: no workspace.
+ */
+dsa_status_t dsa_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const uint16_t* gain,
+                             int64_t n_rows, int hid, float eps, uint16_t* residual_out,
+                             uint16_t* y_out, uint8_t* codes, float* scale, dsa_stream_t stream);
+
+/*
+ * A projection's weight into E4M3 codes with one scale per 128 x 128 block.
+ *   w     [N, K] BF16
+ *   codes [N, K] uint8
+ *   scale [ceil(N / 128), ceil(K / 128)] FP32
+ * Supported: N >= 1, K a multiple of 16.  w and codes 16-byte aligned, scale 4.
+ * Nothing can fail on the device: no workspace.
+ */
+dsa_status_t dsa_quant_fp8_weight(const uint16_t* w, int N, int K, uint8_t* codes, float* scale,
+                                  dsa_stream_t stream);
+
+/*
+ * The projection itself:
+ *   out[m,n] = sum_b a_scale[m,b] * w_scale[n/128,b] * sum_{k in block b} a[m,k] w[n,k]
+ * over the blocks b of 128 values of k, with FP32 accumulation (the products of
+ * two E4M3 codes are exact) and one rounding of the sum to out's type.
+ *   a_codes [M, K] uint8    a_scale [M, ceil(K / 128)] FP32
+ *   w_codes [N, K] uint8    w_scale [ceil(N / 128), ceil(K / 128)] FP32
+ *   out     [M, N]          BF16 (out_type DSA_BF16) or FP32 (DSA_FP32: raw
+ *                           indexer keys for dsa_cache_append)
+ * The sum's order depends on the sizes alone: equal calls give equal bits.
+ * Supported: M >= 0 (0: nothing to do, no pointer is looked at), N >= 1, K a
+ * multiple of 16, M, N, K < 2^30.  Codes and out 16-byte aligned, scales 4.
+ * out may overlap no input.  Workspace: dsa_workspace_bytes(DSA_OP_LINEAR_FP8,
+ * M, 1, K, N, 0).
+ */
+dsa_status_t dsa_linear_fp8(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,
+                            const float* w_scale, int M, int N, int K, void* out,
+                            dsa_dtype_t out_type, void* workspace, size_t ws_bytes,
+                            dsa_stream_t stream);
 
 /*
  * sparse_mla_fwd_noalloc -- sparse_mla_fwd for callers that cannot allocate

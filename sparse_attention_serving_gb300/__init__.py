@@ -14,6 +14,9 @@ Entry points (same names as the C ABI):
   dsa_quant_fp8, dsa_cache_append_fp8, dsa_indexer_topk_fp8
                     the FP8 (E4M3, one FP32 scale per row) indexer variant
   sparse_mla_bwd    gradients of sparse MLA for q_lat and the latent rows
+  dsa_rmsnorm_fp8, dsa_quant_fp8_weight, dsa_linear_fp8
+                    the FP8 projections around the step: residual addition + RMS
+                    norm to E4M3 codes, a weight's quantisation, the product
 """
 
 from __future__ import annotations
@@ -36,7 +39,10 @@ DSA_ERR_BAD_INDEX = 5
 DSA_ERR_WORKSPACE_TOO_SMALL = 6
 
 OP_INDEXER_TOPK, OP_SPARSE_MLA, OP_GATE, OP_CACHE_APPEND, OP_SPARSE_MLA_BWD = 0, 1, 2, 3, 4
+OP_LINEAR_FP8 = 5
 INDEXER_KEY_EPS = 1e-5   # KimiK3TextConfig rms_norm_eps
+RMS_NORM_EPS = 1e-5      # KimiK3TextConfig rms_norm_eps
+FP8_BLOCK = 128          # values per scale: along a row, and a weight's rows too
 RLAT, VLAT, PAGE = 576, 512, 64
 MLA_SCALE = 1.0 / math.sqrt(128 + 64)   # qk_nope_head_dim + qk_rope_head_dim
 
@@ -56,7 +62,8 @@ class _Rows(ctypes.Structure):
 EXPORTS = ("dsa_abi_version", "dsa_status_string", "dsa_workspace_bytes", "dsa_workspace_init",
            "dsa_read_device_status", "dsa_indexer_topk", "sparse_mla_fwd", "mla_gate_apply",
            "dsa_cache_append", "sparse_mla_fwd_sink", "dsa_selftest_wait_timeout",
-           "dsa_quant_fp8", "dsa_cache_append_fp8", "dsa_indexer_topk_fp8", "sparse_mla_bwd")
+           "dsa_quant_fp8", "dsa_cache_append_fp8", "dsa_indexer_topk_fp8", "sparse_mla_bwd",
+           "dsa_rmsnorm_fp8", "dsa_quant_fp8_weight", "dsa_linear_fp8")
 
 
 def _load(path: str = LIB_PATH):
@@ -88,7 +95,11 @@ def _load(path: str = LIB_PATH):
                                          P, P, Z, P]
     lib.sparse_mla_bwd.argtypes = [P, ctypes.POINTER(_Rows), P, P, P, I, I, I, I, I,
                                    ctypes.c_float, P, P, P, P, P, P, Z, P]
-    for f in ("sparse_mla_bwd", "dsa_workspace_init", "dsa_read_device_status", "dsa_indexer_topk",
+    lib.dsa_rmsnorm_fp8.argtypes = [P, P, P, ctypes.c_int64, I, ctypes.c_float, P, P, P, P, P]
+    lib.dsa_quant_fp8_weight.argtypes = [P, I, I, P, P, P]
+    lib.dsa_linear_fp8.argtypes = [P, P, P, P, I, I, I, P, I, P, Z, P]
+    for f in ("dsa_rmsnorm_fp8", "dsa_quant_fp8_weight", "dsa_linear_fp8",
+              "sparse_mla_bwd", "dsa_workspace_init", "dsa_read_device_status", "dsa_indexer_topk",
               "sparse_mla_fwd", "mla_gate_apply", "dsa_cache_append", "sparse_mla_fwd_sink",
               "dsa_selftest_wait_timeout", "dsa_quant_fp8", "dsa_cache_append_fp8",
               "dsa_indexer_topk_fp8"):
@@ -382,3 +393,149 @@ def sparse_mla_bwd(q_lat, kv: Rows, idx, q_start, kv_len, max_kv_len: int, o_lat
                               _ptr(o_lat), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dkv), _ptr(ws),
                               ws.numel(), _stream(stream)), "sparse_mla_bwd")
     return dq
+
+
+# ---------------------------------------------------------------------------
+# FP8 projections around the step
+# ---------------------------------------------------------------------------
+
+def _on(t, dtype, shape, dev: int, name: str) -> int:
+    """Check an operand (type, shape, layout, device) and return its address."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"{name} must be on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _device(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"{name} must be on a CUDA device")
+    return t.get_device()
+
+
+class _Launch:
+    """Device and stream of one call: its tensors' device is made the current one
+    for the launch, and outputs it allocates belong to the launch stream."""
+
+    def __init__(self, dev: int, stream):
+        if stream is not None and stream.device.index != dev:
+            raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"stream must be on cuda:{dev}")
+        self.dev, self.given = dev, stream
+        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
+
+    def empty(self, shape, dtype):
+        if self.given is None:
+            return torch.empty(shape, dtype=dtype, device=self.stream.device)
+        with torch.cuda.stream(self.given):
+            return torch.empty(shape, dtype=dtype, device=self.stream.device)
+
+    def __call__(self, fn, *args):
+        if torch.cuda.current_device() == self.dev:
+            code = fn(*args, self.stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.dev):
+                code = fn(*args, self.stream.cuda_stream)
+        if code != DSA_OK:
+            raise DsaError(code, fn.__name__)
+
+
+def dsa_rmsnorm_fp8(x, gain, residual=None, eps: float = RMS_NORM_EPS, codes=None, scale=None,
+                    residual_out=None, y=None, want_y: bool = False, stream=None):
+    """x [..., hid] bf16, gain [hid] bf16, residual like x or None ->
+    (codes [..., hid] uint8, scale [..., ceil(hid/128)] float32, residual_out, y):
+    h = x + residual, v = h / sqrt(mean(h^2) + eps) * gain, codes and scales the
+    E4M3 groups of 128 of v, residual_out = bf16(h) (None without a residual) and
+    y = bf16(v) (None unless y is given or want_y).  residual_out and y may be x
+    or residual themselves."""
+    dev = _device(x, "x")
+    run = _Launch(dev, stream)
+    shape = x.shape
+    if not shape:
+        raise ValueError("x must be [..., hid]")
+    hid = shape[-1]
+    n = x.numel() // hid if hid else 0
+    groups = (*shape[:-1], -(-hid // FP8_BLOCK))
+    if codes is None:
+        codes = run.empty(shape, torch.uint8)
+    if scale is None:
+        scale = run.empty(groups, torch.float32)
+    if residual is not None and residual_out is None:
+        residual_out = run.empty(shape, torch.bfloat16)
+    if y is None and want_y:
+        y = run.empty(shape, torch.bfloat16)
+    bf = torch.bfloat16
+    run(lib.dsa_rmsnorm_fp8, _on(x, bf, shape, dev, "x"),
+        None if residual is None else _on(residual, bf, shape, dev, "residual"),
+        _on(gain, bf, (hid,), dev, "gain"), n, hid, eps,
+        None if residual_out is None else _on(residual_out, bf, shape, dev, "residual_out"),
+        None if y is None else _on(y, bf, shape, dev, "y"),
+        _on(codes, torch.uint8, shape, dev, "codes"),
+        _on(scale, torch.float32, groups, dev, "scale"))
+    return codes, scale, residual_out, y
+
+
+def dsa_quant_fp8_weight(w, codes=None, scale=None, stream=None):
+    """w [N,K] bf16 (one row per output feature) -> (codes [N,K] uint8,
+    scale [ceil(N/128), ceil(K/128)] float32), one scale per 128 x 128 block."""
+    dev = _device(w, "w")
+    run = _Launch(dev, stream)
+    if w.dim() != 2:
+        raise ValueError("w must be [N, K]")
+    N, K = w.shape
+    groups = (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK))
+    if codes is None:
+        codes = run.empty((N, K), torch.uint8)
+    if scale is None:
+        scale = run.empty(groups, torch.float32)
+    run(lib.dsa_quant_fp8_weight, _on(w, torch.bfloat16, w.shape, dev, "w"), N, K,
+        _on(codes, torch.uint8, w.shape, dev, "codes"),
+        _on(scale, torch.float32, groups, dev, "scale"))
+    return codes, scale
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}   # dsa_dtype_t
+
+
+def dsa_linear_fp8(codes, scale, w_codes, w_scale, out=None, out_dtype=torch.bfloat16,
+                   workspace=None, stream=None):
+    """codes [..., K] uint8 with scale [..., ceil(K/128)] float32 (dsa_rmsnorm_fp8, or
+    dsa_quant_fp8 of rows of 128), w_codes [N,K] uint8 with w_scale
+    [ceil(N/128), ceil(K/128)] float32 (dsa_quant_fp8_weight) -> out [..., N] of
+    out_dtype (bfloat16 or float32; out's own when it is given)."""
+    dev = _device(codes, "codes")
+    run = _Launch(dev, stream)
+    shape = codes.shape
+    if not shape or w_codes.dim() != 2:
+        raise ValueError("codes must be [..., K] and w_codes [N, K]")
+    N, K = w_codes.shape
+    M = codes.numel() // K if K else 0
+    if shape[-1] != K:
+        raise ValueError(f"codes must be [..., {K}], got {list(shape)}")
+    kb = -(-K // FP8_BLOCK)
+    if out is None:
+        if out_dtype not in _DTYPES:
+            raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+        out = run.empty((*shape[:-1], N), out_dtype)
+    elif out.dtype not in _DTYPES:
+        raise TypeError(f"out must be bfloat16 or float32, got {out.dtype}")
+    if workspace is None:
+        need = workspace_bytes(OP_LINEAR_FP8, M, 1, K, N, 0)
+        workspace = run.empty((need,), torch.uint8)
+        run(lib.dsa_workspace_init, workspace.data_ptr(), need)
+    f32 = torch.float32
+    run(lib.dsa_linear_fp8, _on(codes, torch.uint8, shape, dev, "codes"),
+        _on(scale, f32, (*shape[:-1], kb), dev, "scale"),
+        _on(w_codes, torch.uint8, w_codes.shape, dev, "w_codes"),
+        _on(w_scale, f32, (-(-N // FP8_BLOCK), kb), dev, "w_scale"), M, N, K,
+        _on(out, out.dtype, (*shape[:-1], N), dev, "out"), _DTYPES[out.dtype],
+        _on(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel())
+    return out

@@ -260,6 +260,54 @@ dsa_status_t dsa_quant_fp8(const uint16_t* x, int64_t n_rows, int D, uint8_t* co
   return quant_fp8_launch(x, n_rows, D, codes, scale, reinterpret_cast<cudaStream_t>(stream));
 }
 
+dsa_status_t dsa_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const uint16_t* gain,
+                             int64_t n_rows, int hid, float eps, uint16_t* residual_out,
+                             uint16_t* y_out, uint8_t* codes, float* scale, dsa_stream_t stream) {
+  if (n_rows < 0 || hid <= 0 || !(eps >= 0.f) || !(eps < 3.0e38f)) return DSA_ERR_INVALID_ARGUMENT;
+  if (hid % 16 != 0 || hid > 65536 || n_rows >= (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
+  if (n_rows == 0) return DSA_OK;
+  if (!x || !gain || !codes || !scale) return DSA_ERR_INVALID_ARGUMENT;
+  if (residual_out != nullptr && residual == nullptr) return DSA_ERR_INVALID_ARGUMENT;
+  if (residual_out != nullptr && residual_out == y_out) return DSA_ERR_INVALID_ARGUMENT;
+  // a null pointer counts as aligned
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gain, 16) ||
+      !aligned(residual_out, 16) || !aligned(y_out, 16) || !aligned(codes, 16) ||
+      !aligned(scale, 4))
+    return DSA_ERR_INVALID_ARGUMENT;
+  const RmsNormArgs a{x, residual, gain, n_rows, hid, eps, residual_out, y_out, codes, scale};
+  return rmsnorm_fp8_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t dsa_quant_fp8_weight(const uint16_t* w, int N, int K, uint8_t* codes, float* scale,
+                                  dsa_stream_t stream) {
+  if (!w || !codes || !scale || N <= 0 || K <= 0) return DSA_ERR_INVALID_ARGUMENT;
+  if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scale, 4)) return DSA_ERR_INVALID_ARGUMENT;
+  if (K % 16 != 0 || N >= (1 << 30) || K >= (1 << 30)) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>((N + 127) / 128) * ((K + 127) / 128) >= (int64_t(1) << 31))
+    return DSA_ERR_UNSUPPORTED;
+  return quant_fp8_weight_launch(w, N, K, codes, scale, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t dsa_linear_fp8(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,
+                            const float* w_scale, int M, int N, int K, void* out,
+                            dsa_dtype_t out_type, void* workspace, size_t ws_bytes,
+                            dsa_stream_t stream) {
+  if (M < 0 || N <= 0 || K <= 0) return DSA_ERR_INVALID_ARGUMENT;
+  if (out_type != DSA_BF16 && out_type != DSA_FP32) return DSA_ERR_INVALID_ARGUMENT;
+  if (K % 16 != 0 || M >= (1 << 30) || N >= (1 << 30) || K >= (1 << 30)) return DSA_ERR_UNSUPPORTED;
+  if (M == 0) return DSA_OK;
+  if (!a_codes || !a_scale || !w_codes || !w_scale || !out) return DSA_ERR_INVALID_ARGUMENT;
+  if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(out, 16) ||
+      !aligned(a_scale, 4) || !aligned(w_scale, 4))
+    return DSA_ERR_INVALID_ARGUMENT;
+  dsa_status_t st =
+      check_ws(workspace, ws_bytes, dsa_workspace_bytes(DSA_OP_LINEAR_FP8, M, 1, K, N, 0));
+  if (st != DSA_OK) return st;
+  const LinearArgs a{a_codes, a_scale, w_codes, w_scale, M, N, K, out, out_type == DSA_FP32,
+                     static_cast<uint32_t*>(workspace)};
+  return linear_fp8_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 static dsa_status_t mla_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const int32_t* idx,
                             const int32_t* q_start, const int32_t* kv_len, int B, int Tq, int H,
                             int topk, int max_kv_len, float scale, const float* sink,

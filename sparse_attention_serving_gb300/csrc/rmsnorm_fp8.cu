@@ -1,0 +1,137 @@
+// rmsnorm_fp8.cu -- the head of a layer on sm_103a: residual addition, RMS norm
+// and E4M3 quantisation in one pass over the row (KimiK3TextConfig: hidden_size
+// 7168, rms_norm_eps 1e-5).
+//
+//   h = x + r,  y = h / sqrt(mean(h^2) + eps) * g
+//   residual_out = BF16(h),  y_out = BF16(y)
+//   scale_b = max(max_b |y|, 2^-100) / 448,  code = E4M3(y * (1 / scale_b)),  b = 128 values
+//
+// A row is held in registers as FP32 between the two halves (sum of squares,
+// then scaling), so each input is read once and each output written once.
+// Thread t of a row's T threads holds the 16-byte vectors t, t + T, ...; T is a
+// multiple of 32, so the 16 lanes of a half-warp hold one scale block each time
+// and its maximum is four shuffles away.
+#include <cuda_bf16.h>
+
+#include "dsa_status.cuh"
+#include "internal.h"
+#include "sm103.cuh"
+
+namespace dsa {
+namespace rms {
+
+struct Params {
+  const uint16_t* x;
+  const uint16_t* residual;
+  const uint16_t* gain;
+  int64_t n_rows;
+  int nvec;      // hid / 8
+  int nblk;      // ceil(hid / 128)
+  float inv_hid, eps;
+  uint16_t* residual_out;
+  uint16_t* y;
+  uint8_t* codes;
+  float* scale;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+// One row per CTA, VPT vectors per thread.
+template <int VPT>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const Params p) {
+  __shared__ float s_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x;
+  const int64_t row = blockIdx.x;
+  const int64_t base = row * p.nvec;
+  // x, residual and the outputs may be the same memory: no read-only loads
+  const uint4* x = reinterpret_cast<const uint4*>(p.x) + base;
+  float h[VPT][8];
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = tid + i * T;
+    if (v < p.nvec) {
+      unpack8(x[v], h[i]);
+      if (p.residual != nullptr) {
+        float r[8];
+        unpack8(reinterpret_cast<const uint4*>(p.residual)[base + v], r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] += r[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i][e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q = fmaf(h[i][e], h[i][e], q);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+  if (lane == 0) s_sum[warp] = q;
+  __syncthreads();
+  q = lane < (T >> 5) ? s_sum[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+  const float inv = 1.f / sqrtf(fmaf(q, p.inv_hid, p.eps));
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = tid + i * T;
+    const bool in = v < p.nvec;
+    if (in && p.residual_out != nullptr)
+      reinterpret_cast<uint4*>(p.residual_out)[base + v] = pack8(h[i]);
+    float y[8];
+    uint32_t top = 0;
+    if (in) {
+      unpack8(__ldg(reinterpret_cast<const uint4*>(p.gain) + v), y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] *= h[i][e] * inv;
+        // magnitudes order like their bit patterns, a NaN above everything
+        top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+      }
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (in) {
+      const float scale = __fdiv_rn(__uint_as_float(max(top, __float_as_uint(0x1p-100f))), 448.f);
+      const float k = __frcp_rn(scale);
+      if (p.y != nullptr) reinterpret_cast<uint4*>(p.y)[base + v] = pack8(y);
+      uint2 c;
+      c.x = e4m3x2(__fmul_rn(y[1], k), __fmul_rn(y[0], k)) |
+            (e4m3x2(__fmul_rn(y[3], k), __fmul_rn(y[2], k)) << 16);
+      c.y = e4m3x2(__fmul_rn(y[5], k), __fmul_rn(y[4], k)) |
+            (e4m3x2(__fmul_rn(y[7], k), __fmul_rn(y[6], k)) << 16);
+      reinterpret_cast<uint2*>(p.codes)[base + v] = c;
+      if ((v & 15) == 0) p.scale[row * p.nblk + (v >> 4)] = scale;
+    }
+  }
+}
+
+}  // namespace rms
+
+dsa_status_t rmsnorm_fp8_launch(const RmsNormArgs& a, cudaStream_t stream) {
+  using namespace rms;
+  const Params p{a.x, a.residual, a.gain, a.n_rows, a.hid / 8, (a.hid + 127) / 128,
+                 1.f / static_cast<float>(a.hid), a.eps, a.residual_out, a.y, a.codes, a.scale};
+  auto threads = [&](int vpt) { return ((p.nvec + vpt - 1) / vpt + 31) / 32 * 32; };
+  const unsigned grid = static_cast<unsigned>(a.n_rows);
+  if (p.nvec <= 1024)
+    rmsnorm_kernel<1><<<grid, threads(1), 0, stream>>>(p);
+  else
+    rmsnorm_kernel<8><<<grid, threads(8), 0, stream>>>(p);
+  return launch_status("rmsnorm_kernel");
+}
+
+}  // namespace dsa
