@@ -389,7 +389,7 @@ dsa_status_t dsa_quant_fp8_weight(const uint16_t* w, int N, int K, uint8_t* code
  *                           indexer keys for dsa_cache_append)
  * The sum's order depends on the sizes alone: equal calls give equal bits.
  * Supported: M >= 0 (0: nothing to do, no pointer is looked at), N >= 1, K a
- * multiple of 16, M, N, K < 2^30.  Codes and out 16-byte aligned, scales 4.
+ * multiple of 16, M, N, K < 2^30, M * N < 2^40.  Codes and out 16-byte aligned, scales 4.
  * out may overlap no input.  Workspace: dsa_workspace_bytes(DSA_OP_LINEAR_FP8,
  * M, 1, K, N, 0).
  */

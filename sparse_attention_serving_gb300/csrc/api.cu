@@ -294,7 +294,9 @@ dsa_status_t dsa_linear_fp8(const uint8_t* a_codes, const float* a_scale, const 
                             dsa_stream_t stream) {
   if (M < 0 || N <= 0 || K <= 0) return DSA_ERR_INVALID_ARGUMENT;
   if (out_type != DSA_BF16 && out_type != DSA_FP32) return DSA_ERR_INVALID_ARGUMENT;
-  if (K % 16 != 0 || M >= (1 << 30) || N >= (1 << 30) || K >= (1 << 30)) return DSA_ERR_UNSUPPORTED;
+  if (K % 16 != 0 || M >= (1 << 30) || N >= (1 << 30) || K >= (1 << 30) ||
+      static_cast<int64_t>(M) * N >= (int64_t(1) << 40))
+    return DSA_ERR_UNSUPPORTED;
   if (M == 0) return DSA_OK;
   if (!a_codes || !a_scale || !w_codes || !w_scale || !out) return DSA_ERR_INVALID_ARGUMENT;
   if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(out, 16) ||
