@@ -78,6 +78,24 @@ __device__ __forceinline__ void store_out(const Params& p, int m, int n, float v
     static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
 }
 
+// Features n .. n+3 of token m (n a multiple of 4), those that exist.
+__device__ __forceinline__ void store_out4(const Params& p, int m, int n, const float4& v) {
+  const int64_t o = static_cast<int64_t>(m) * p.N + n;
+  if ((p.N & 3) == 0) {
+    if (n >= p.N) return;
+    if (p.fp32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = v;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  } else {
+    const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (n + k < p.N) store_out(p, m, n + k, e[k]);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Split kernel: Dt[128 features x NT tokens] = W . A^T over a slice of K per CTA,
 // the slices of a tile on one cluster and joined through its shared memory.
@@ -104,7 +122,9 @@ struct Split {
   static constexpr int TCOLS = NT * NB;
   static constexpr int OFF_MISC = NST * STAGE;           // barriers, then two sets of factors
   static constexpr int OFF_FACT = OFF_MISC + 256;
-  static constexpr int SMEM = 1024 + OFF_FACT + 2 * NT * 4;
+  static constexpr int CH = 8;                           // blocks of K per set of factors
+  static constexpr int FROW = NT + 4;
+  static constexpr int SMEM = 1024 + OFF_FACT + 2 * CH * FROW * 4;
   static_assert(TCOLS >= 32 && TCOLS * CTAS <= 512, "TMEM columns");
   static_assert(NT * 128 * 4 <= NST * STAGE, "the partial tile reuses the stages");
   static_assert((SMEM + 1024) * CTAS <= 228 * 1024, "shared memory");
@@ -134,11 +154,22 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kb) * rank / S);
   const int nkb = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / S) - kb0;
 
+  auto load = [&](int i) {
+    const int st = i % C::NST;
+    uint8_t* w = sm + st * C::STAGE;
+    mbar_expect_tx(&full[st], C::STAGE);
+    tma_load_2d(w, &tm_w, &full[st], 64 * (kb0 + i), n0);
+    tma_load_2d(w + 128 * 128, &tm_a, &full[st], 64 * (kb0 + i), m0);
+  };
   if (tid == 0) {
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_a);
     for (int k = 0; k < 2 * C::NST + C::NB; ++k) mbar_init(&full[k], 1);
     for (int k = 0; k < C::NB; ++k) mbar_init(&acc_free[k], C::EW);
     s_abort[0] = 0;
     fence_mbar_init();
+    // the copying thread fills the ring before the other warps are set up
+    for (int i = 0; i < min(C::NST, nkb); ++i) load(i);
   }
   if (warp == 1) {
     tmem_alloc(tslot, C::TCOLS);
@@ -155,17 +186,12 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
 
   if (warp == 0) {
     if (lane == 0) {
-      tma_prefetch_desc(&tm_w);
-      tma_prefetch_desc(&tm_a);
-      int i = 0;
+      int i = min(C::NST, nkb);
       for (; i < nkb; ++i) {
-        const int st = i % C::NST, use = i / C::NST;
-        if (use > 0 && !mbar_wait(&empty[st], (use - 1) & 1, p.status, kWaitLimitNs, SITE_S_E)) break;
+        if (!mbar_wait(&empty[i % C::NST], (i / C::NST - 1) & 1, p.status, kWaitLimitNs, SITE_S_E))
+          break;
         if (s_abort[0]) break;
-        uint8_t* w = sm + st * C::STAGE;
-        mbar_expect_tx(&full[st], C::STAGE);
-        tma_load_2d(w, &tm_w, &full[st], 64 * (kb0 + i), n0);
-        tma_load_2d(w + 128 * 128, &tm_a, &full[st], 64 * (kb0 + i), m0);
+        load(i);
       }
       if (i < nkb) s_abort[0] = 1;
       // the copies in flight have landed before anything else touches the stages
@@ -202,26 +228,43 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
     const int sub = warp & 3;                              // TMEM lane quarter of this warp
     const int c0 = (et >> 7) * C::COLS;                    // its first token
     const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + c0;
-    // factors w_scale * a_scale of token m0 + et, two blocks ahead of their use
-    const bool has = et < NT && m0 + et < p.M;
-    const float* as = p.a_scale + static_cast<int64_t>(has ? m0 + et : 0) * p.kb + kb0;
+    // Factors a_scale * w_scale, CH blocks of K at a time: loaded into registers
+    // one chunk ahead, multiplied and put into shared memory at the chunk's start.
+    // A thread always holds the same block of a chunk.
+    constexpr int T = C::EW * 32, PER = C::CH * NT / T;
+    const int fk = et % C::CH;
     const float* ws = p.w_scale + static_cast<int64_t>(nb) * p.kb + kb0;
-    auto factor = [&](int i) { return has && i < nkb ? __ldg(as + i) * __ldg(ws + i) : 0.f; };
-    float f0 = factor(0), f1 = factor(1);
+    float fa[PER], fw = 0.f;
+    auto fetch = [&](int i0) {
+      const bool in = i0 + fk < nkb;
+      fw = in ? __ldg(ws + i0 + fk) : 0.f;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int m = m0 + (et + k * T) / C::CH;
+        fa[k] = in && m < p.M ? __ldg(p.a_scale + static_cast<int64_t>(m) * p.kb + kb0 + i0 + fk) : 0.f;
+      }
+    };
+    fetch(0);
     bool ok = true;
     for (int i = 0; i < nkb; ++i) {
       const int bu = i % C::NB;
-      float* fb = fact + (i & 1) * NT;
-      if (et < NT) fb[et] = f0;
-      f0 = f1;
-      f1 = factor(i + 2);
-      // all epilogue warps leave together if one of them gave up
-      if (named_bar_or(1, C::EW * 32, !ok)) {
-        ok = false;
-        break;
+      const float* fb = fact + ((i / C::CH) & 1) * (C::CH * C::FROW);
+      if (i % C::CH == 0) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+          fact[((i / C::CH) & 1) * (C::CH * C::FROW) + fk * C::FROW + (et + k * T) / C::CH] = fa[k] * fw;
+        fetch(i + C::CH);
+        // all epilogue warps leave together if one of them gave up
+        if (named_bar_or(1, T, !ok)) {
+          ok = false;
+          break;
+        }
       }
-      ok = mbar_wait(&acc_full[bu], (i / C::NB) & 1, p.status, kWaitLimitNs, SITE_S_ACC);
-      __syncwarp();
+      fb += (i % C::CH) * C::FROW + c0;
+      if (!ok) continue;
+      ok = !__any_sync(0xffffffffu, !mbar_wait(&acc_full[bu], (i / C::NB) & 1, p.status, kWaitLimitNs,
+                                               SITE_S_ACC));
+      if (!ok) continue;
       tc_fence_after();
       constexpr int STEP = C::COLS < 32 ? 16 : 32;
 #pragma unroll
@@ -234,7 +277,7 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < STEP; e += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(fb + c0 + c + e);
+          const float4 f = *reinterpret_cast<const float4*>(fb + c + e);
           fma2_rn(acc[c + e], acc[c + e + 1], __uint_as_float(d[e]), __uint_as_float(d[e + 1]), f.x, f.y);
           fma2_rn(acc[c + e + 2], acc[c + e + 3], __uint_as_float(d[e + 2]),
                   __uint_as_float(d[e + 3]), f.z, f.w);
@@ -264,14 +307,26 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
       for (int c = 0; c < C::COLS; ++c) part[(grp * C::COLS + c) * 128 + row] = acc[c];
     }
     cluster_sync();
-    if (warp >= 2 && n0 + row < p.N) {
-      // this CTA's share of the tokens, the slices of K added in their order
+    if (warp >= 2) {
+      // this CTA's share of the tokens, a warp per token and four features per
+      // lane, the slices of K added in their order
       const int live = min(NT, p.M - m0);
-      for (int c = rank + grp * S; c < live; c += S * (C::EW / 4)) {
-        float v = 0.f;
-        const uint32_t at = smem_u32(part + c * 128 + row);
-        for (int r = 0; r < S; ++r) v += ld_cluster_f32(at, r);
-        store_out(p, m0 + c, n0 + row, v);
+#pragma unroll 2
+      for (int c = rank + (warp - 2) * S; c < live; c += S * C::EW) {
+        const uint32_t at = smem_u32(part + c * 128 + lane * 4);
+        float4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < S) v[r] = ld_cluster_f32x4(at, r);
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (r < S) {
+            v[0].x += v[r].x;
+            v[0].y += v[r].y;
+            v[0].z += v[r].z;
+            v[0].w += v[r].w;
+          }
+        store_out4(p, m0 + c, n0 + lane * 4, v[0]);
       }
     }
     cluster_sync();   // no CTA leaves while another still reads its shared memory
@@ -310,6 +365,293 @@ dsa_status_t launch_split(const LinearArgs& a, int S, cudaStream_t stream) {
   return launch_status("split_kernel");
 }
 
+// ---------------------------------------------------------------------------
+// Wide kernel: 256 tokens x 256 features per pair of CTAs (cta_group::2).
+//
+// One SM alone would move 48 KB into and out of its shared memory for every
+// 128 x 256 x 128 block, about 750 cycles of its port against 512 of the tensor
+// core.  The pair splits the weight tile: each SM stages its own 128 tokens and
+// half of the 256 features (32 KB) and multiplies against both halves, so the
+// port needs no longer than the MMA.  Tokens are the M side: a lane is a token,
+// whose factor a_scale * w_scale is one scalar per block of K.  Persistent: a
+// pair walks the tiles, and the epilogue's store of one tile overlaps the first
+// blocks of the next.
+// ---------------------------------------------------------------------------
+enum : uint32_t { SITE_P_E = 0x710, SITE_P_F = 0x711, SITE_P_ACC = 0x712, SITE_P_FREE = 0x713,
+                  SITE_P_DRAIN = 0x714, SITE_P_FACT = 0x715 };
+
+struct Wide {
+  static constexpr int NST = 6;
+  static constexpr int STAGE = 2 * 128 * 128;            // 128 tokens, 128 features
+  static constexpr int EW = 8;                           // epilogue warps 0..7, two warpgroups
+  static constexpr int NTHREADS = EW * 32 + 128;         // and one warpgroup for copies and MMA
+  static constexpr int OFF_MISC = NST * STAGE;
+  static constexpr int CH = 8;                           // blocks of K per set of factors
+  static constexpr int FROW = 132;                       // 128 tokens, 2 weight blocks, padding
+  static constexpr int FSET = CH * FROW;
+  static constexpr int OFF_FACT = OFF_MISC + 256;
+  static constexpr int NF = 3;                           // sets of factors
+  static constexpr int SMEM = 1024 + OFF_FACT + NF * FSET * 4;
+  static constexpr int GROUP = 8;                        // token tiles that share a weight sweep
+};
+
+// Tiles in groups of GROUP token tiles, token tiles fastest: the pairs at work
+// at one time share few weight and token tiles, which stay in L2.
+__device__ __forceinline__ void wide_tile(int tile, int ntm, int ntn, int& mt, int& nt) {
+  const int per = Wide::GROUP * ntn, g = tile / per, rem = tile - g * per;
+  const int gm = min(Wide::GROUP, ntm - g * Wide::GROUP);
+  nt = rem / gm;
+  mt = g * Wide::GROUP + rem - nt * gm;
+}
+
+// 32 consecutive features n .. n+31 (n a multiple of 32) of token m.
+__device__ __forceinline__ void store_out32(const Params& p, int m, int n, const float* v) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 8) {
+    if (!p.fp32 && (p.N & 7) == 0) {
+      if (n + k < p.N)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(m) * p.N + n + k) =
+            make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
+                       pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
+    } else {
+      store_out4(p, m, n + k, make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]));
+      store_out4(p, m, n + k + 4, make_float4(v[k + 4], v[k + 5], v[k + 6], v[k + 7]));
+    }
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::NTHREADS, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                const Params p) {
+  using C = Wide;
+  constexpr uint32_t IDESC = idesc_e4m3(256, 256);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);   // used in the even CTA
+  uint64_t* done = full + C::NST;      // a stage's MMAs are complete: it is empty and its block summed
+  uint64_t* acc_free = done + C::NST;                                // used in the even CTA
+  uint64_t* f_full = acc_free + 2;
+  uint64_t* f_free = f_full + C::NF;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(f_free + C::NF);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
+  float* fact = reinterpret_cast<float*>(sm + C::OFF_FACT);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x & 1;
+  const int ntm = (p.M + 255) / 256, ntn = (p.N + 255) / 256;
+  const int ntiles = ntm * ntn, step = gridDim.x >> 1;
+
+  if (tid == 0) {
+    for (int k = 0; k < 2 * C::NST; ++k) mbar_init(&full[k], 1);
+    for (int k = 0; k < 2; ++k) mbar_init(&acc_free[k], 2 * C::EW);
+    for (int k = 0; k < C::NF; ++k) {
+      mbar_init(&f_full[k], 2);                                      // the two factor warps
+      mbar_init(&f_free[k], C::EW);
+    }
+    s_abort[0] = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::EW + 1) {
+    tmem_alloc_pair(tslot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+
+  if (warp >= C::EW) {
+    regs_dec<56>();
+    if (warp == C::EW && lane == 0) {
+      tma_prefetch_desc(&tm_a);
+      tma_prefetch_desc(&tm_w);
+      int st = 0, i = 0;
+      uint32_t ph = 0;       // parity of the stage's current use
+      bool ok = true;
+      for (int tile = blockIdx.x >> 1; ok && tile < ntiles; tile += step) {
+        int mt, nt;
+        wide_tile(tile, ntm, ntn, mt, nt);
+        for (int b = 0; b < p.kb; ++b, ++i) {
+          ok = (i < C::NST || mbar_wait(&done[st], ph ^ 1, p.status, kWaitLimitNs, SITE_P_E)) &&
+               !s_abort[0];
+          if (!ok) break;
+          uint8_t* a = sm + st * C::STAGE;
+          if (rank == 0) mbar_expect_tx(&full[st], 2 * C::STAGE);   // both CTAs' bytes
+          const uint32_t bar = mapa_u32(smem_u32(&full[st]), 0);
+          tma_load_2d_pair(a, &tm_a, bar, 64 * b, mt * 256 + rank * 128);
+          tma_load_2d_pair(a + 128 * 128, &tm_w, bar, 64 * b, nt * 256 + rank * 128);
+          if (++st == C::NST) st = 0, ph ^= 1;
+        }
+      }
+      if (!ok) s_abort[0] = 1;
+      // the pair's copies in flight have landed before either CTA leaves
+      if (rank == 0)
+        for (int k = max(0, i - C::NST); k < i; ++k)
+          mbar_wait(&full[k % C::NST], (k / C::NST) & 1, p.status, kWaitLimitNs, SITE_P_F);
+    } else if (warp == C::EW + 1 && rank == 0 && lane == 0) {
+      const uint64_t desc0 = smem_desc(smem_u32(sm), 16, 1024);
+      int st = 0, i = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x >> 1; ok && tile < ntiles; tile += step) {
+        for (int b = 0; b < p.kb; ++b, ++i) {
+          const int bu = i & 1;
+          ok = (i < 2 || mbar_wait(&acc_free[bu], ((i >> 1) - 1) & 1, p.status, kWaitLimitNs,
+                                   SITE_P_FREE)) &&
+               mbar_wait(&full[st], ph, p.status, kWaitLimitNs, SITE_P_F);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t ad = desc_add(desc0, st * C::STAGE), wd = desc_add(ad, 128 * 128);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_e4m3_pair(tmem + bu * 256, desc_add(ad, kk * 32), desc_add(wd, kk * 32), IDESC,
+                           kk ? 1u : 0u);
+          umma_commit_pair(&done[st]);
+          if (++st == C::NST) st = 0, ph ^= 1;
+        }
+      }
+      if (!ok) s_abort[0] = 1;
+      for (int k = max(0, i - C::NST); k < i; ++k)
+        mbar_wait(&done[k % C::NST], (k / C::NST) & 1, p.status, kWaitLimitNs, SITE_P_DRAIN);
+    } else if (warp >= C::EW + 2) {
+      // Factors: sets of CH blocks of K, in a ring of NF.  Eight lanes read eight
+      // neighbouring scales of a token; 64 threads hold 8 tokens a pass.
+      const int et = tid - (C::EW + 2) * 32, fk = et % C::CH, fr = et / C::CH;
+      int ch = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x >> 1; ok && tile < ntiles; tile += step) {
+        int mt, nt;
+        wide_tile(tile, ntm, ntn, mt, nt);
+        const int m0 = mt * 256 + rank * 128 + fr, nb = nt * 2 + fr;
+        const float* as = p.a_scale + static_cast<int64_t>(m0) * p.kb + fk;
+        for (int b = 0; b < p.kb; b += C::CH, ++ch) {
+          const int fs = ch % C::NF;
+          ok = ch < C::NF ||
+               mbar_wait(&f_free[fs], (ch / C::NF - 1) & 1, p.status, kWaitLimitNs, SITE_P_FACT);
+          ok = __all_sync(0xffffffffu, ok) && !s_abort[0];
+          if (!ok) break;
+          float* to = fact + fs * C::FSET + fk * C::FROW + fr;
+          const bool in = b + fk < p.kb;
+#pragma unroll 1
+          for (int k0 = 0; k0 < 16; k0 += 4) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = 8 * (k0 + k);
+              v[k] = in && m0 + r < p.M ? __ldg(as + static_cast<int64_t>(r) * p.kb + b) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) to[8 * (k0 + k)] = v[k];
+          }
+          if (fr < 2)
+            to[128] = in && nb * 128 < p.N ? __ldg(p.w_scale + static_cast<int64_t>(nb) * p.kb + b + fk)
+                                           : 0.f;
+          mbar_arrive_warp(&f_full[fs]);
+        }
+      }
+      if (!ok) s_abort[0] = 1;
+    }
+    __syncwarp();
+  } else {
+    regs_inc<224>();
+    const int sub = warp & 3, half = warp >> 2, row = sub * 32 + lane;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + half * 128;
+    const uint32_t free0 = mapa_u32(smem_u32(&acc_free[0]), 0);
+    // A warp's state runs one block ahead of its sums: the next block's factor and
+    // first 32 columns are on their way while the last columns of this one are
+    // added.  A lane that gave up keeps its warp together until the vote at the
+    // next set of factors.
+    int st = 0, fs = 0, bu = 0, b = 0;
+    uint32_t ph = 0, fph = 0;
+    bool ok = true, live = true;   // live: the same in all lanes
+    float f = 0.f;
+    uint32_t d[2][32];
+    auto next_block = [&]() {
+      if (b % C::CH == 0) {
+        ok = ok && mbar_wait(&f_full[fs], fph, p.status, kWaitLimitNs, SITE_P_FACT);
+        live = ok = __all_sync(0xffffffffu, ok);
+      }
+      const float* fb = fact + fs * C::FSET + (b % C::CH) * C::FROW;
+      f = fb[row] * fb[128 + half];
+      ok = ok && mbar_wait(&done[st], ph, p.status, kWaitLimitNs, SITE_P_ACC);
+      __syncwarp();
+      tc_fence_after();
+      tmem_ld32(taddr + bu * 256, d[0]);
+    };
+    if ((blockIdx.x >> 1) < ntiles) next_block();
+    for (int tile = blockIdx.x >> 1; live && tile < ntiles; tile += step) {
+      float acc[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) acc[c] = 0.f;
+      bool last;
+      do {
+        const float fc = f;
+        last = b == p.kb - 1;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait_regs(d[c & 1]);
+          if (c < 3) {
+            tmem_ld32(taddr + bu * 256 + 32 * (c + 1), d[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(free0 + bu * 8);
+            if (b % C::CH == C::CH - 1 || last) {
+              if (lane == 0) mbar_arrive(&f_free[fs]);
+              if (++fs == C::NF) fs = 0, fph ^= 1;
+            }
+            bu ^= 1;
+            if (++st == C::NST) st = 0, ph ^= 1;
+            b = last ? 0 : b + 1;
+            if (!last || tile + step < ntiles) next_block();
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            fma2_rn(acc[32 * c + e], acc[32 * c + e + 1], __uint_as_float(d[c & 1][e]),
+                    __uint_as_float(d[c & 1][e + 1]), fc, fc);
+        }
+      } while (!last && live);
+      int mt, nt;
+      wide_tile(tile, ntm, ntn, mt, nt);
+      const int m = mt * 256 + rank * 128 + row, n = nt * 256 + half * 128;
+      if (last && ok && m < p.M) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) store_out32(p, m, n + c, acc + c);
+      }
+    }
+    // (a first load in flight when the warp gave up)
+    tmem_ld_wait();
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) s_abort[0] = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the pair's MMAs, copies and TMEM reads are done
+  if (warp == C::EW + 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+dsa_status_t launch_wide(const LinearArgs& a, cudaStream_t stream) {
+  using C = Wide;
+  CUtensorMap ta, tw;
+  const uint64_t K = static_cast<uint64_t>(a.K);
+  if (!encode_tmap_2d(&ta, a.a, a.M, K / 2, K, 64, 128, true) ||
+      !encode_tmap_2d(&tw, a.w, a.N, K / 2, K, 64, 128, true))
+    return DSA_ERR_CUDA;
+  const Params p{a.a_scale, a.w_scale, a.M, a.N, (a.K + 127) / 128, a.out, a.fp32, a.status};
+  if (cudaFuncSetAttribute(wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+      cudaSuccess)
+    return launch_status("cudaFuncSetAttribute");
+  const int64_t tiles = static_cast<int64_t>((a.M + 255) / 256) * ((a.N + 255) / 256);
+  const int64_t pairs = num_sms() / 2;
+  wide_kernel<<<static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), C::NTHREADS, C::SMEM,
+                stream>>>(ta, tw, p);
+  return launch_status("wide_kernel");
+}
+
 }  // namespace lin
 
 dsa_status_t quant_fp8_weight_launch(const uint16_t* w, int N, int K, uint8_t* codes, float* scale,
@@ -321,6 +663,8 @@ dsa_status_t quant_fp8_weight_launch(const uint16_t* w, int N, int K, uint8_t* c
 
 dsa_status_t linear_fp8_launch(const LinearArgs& a, cudaStream_t stream) {
   const int kb = (a.K + 127) / 128;
+  if (static_cast<int64_t>((a.M + 255) / 256) * ((a.N + 255) / 256) >= 60)
+    return lin::launch_wide(a, stream);
   const int nt = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : a.M <= 128 ? 128 : 256;
   const int per_sm = nt <= 16 ? 3 : nt <= 64 ? 2 : 1;
   const int64_t tiles = static_cast<int64_t>((a.N + 127) / 128) * ((a.M + nt - 1) / nt);
