@@ -385,6 +385,7 @@ struct Wide {
   static constexpr int STAGE = 2 * 128 * 128;            // 128 tokens, 128 features
   static constexpr int EW = 8;                           // epilogue warps 0..7, two warpgroups
   static constexpr int NTHREADS = EW * 32 + 128;         // and one warpgroup for copies and MMA
+  static_assert(NST % 2 == 0, "each issuing thread owns every other stage");
   static constexpr int OFF_MISC = NST * STAGE;
   static constexpr int CH = 8;                           // blocks of K per set of factors
   static constexpr int FROW = 132;                       // 128 tokens, 2 weight blocks, padding
@@ -445,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::NTHREADS, 1)
     for (int k = 0; k < 2 * C::NST; ++k) mbar_init(&full[k], 1);
     for (int k = 0; k < 2; ++k) mbar_init(&acc_free[k], 2 * C::EW);
     for (int k = 0; k < C::NF; ++k) {
-      mbar_init(&f_full[k], 2);                                      // the two factor warps
+      mbar_init(&f_full[k], 1);
       mbar_init(&f_free[k], C::EW);
     }
     s_abort[0] = 0;
@@ -489,35 +490,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::NTHREADS, 1)
       if (rank == 0)
         for (int k = max(0, i - C::NST); k < i; ++k)
           mbar_wait(&full[k % C::NST], (k / C::NST) & 1, p.status, kWaitLimitNs, SITE_P_F);
-    } else if (warp == C::EW + 1 && rank == 0 && lane == 0) {
+    } else if ((warp == C::EW + 1 || warp == C::EW + 2) && rank == 0 && lane == 0) {
+      // Two issuing threads, one per TMEM buffer (even and odd blocks): while one
+      // waits for its operands and its buffer, the other's MMAs keep the tensor
+      // core busy.  One thread alone left it idle for about 110 cycles a block.
       const uint64_t desc0 = smem_desc(smem_u32(sm), 16, 1024);
-      int st = 0, i = 0;
-      uint32_t ph = 0;
+      const int bu = warp - (C::EW + 1);
+      const int64_t blocks = static_cast<int64_t>((ntiles - (blockIdx.x >> 1) + step - 1) / step) * p.kb;
+      int st = bu;
+      uint32_t ph = 0, fph = 1;
+      int64_t i = bu;
       bool ok = true;
-      for (int tile = blockIdx.x >> 1; ok && tile < ntiles; tile += step) {
-        for (int b = 0; b < p.kb; ++b, ++i) {
-          const int bu = i & 1;
-          ok = (i < 2 || mbar_wait(&acc_free[bu], ((i >> 1) - 1) & 1, p.status, kWaitLimitNs,
-                                   SITE_P_FREE)) &&
-               mbar_wait(&full[st], ph, p.status, kWaitLimitNs, SITE_P_F);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t ad = desc_add(desc0, st * C::STAGE), wd = desc_add(ad, 128 * 128);
+      for (; i < blocks; i += 2) {
+        const uint64_t ad = desc_add(desc0, st * C::STAGE), wd = desc_add(ad, 128 * 128);
+        ok = mbar_wait(&full[st], ph, p.status, kWaitLimitNs, SITE_P_F) &&
+             (i < 2 || mbar_wait(&acc_free[bu], fph, p.status, kWaitLimitNs, SITE_P_FREE));
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_e4m3_pair(tmem + bu * 256, desc_add(ad, kk * 32), desc_add(wd, kk * 32), IDESC,
-                           kk ? 1u : 0u);
-          umma_commit_pair(&done[st]);
-          if (++st == C::NST) st = 0, ph ^= 1;
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          umma_e4m3_pair(tmem + bu * 256, desc_add(ad, kk * 32), desc_add(wd, kk * 32), IDESC,
+                         kk ? 1u : 0u);
+        umma_commit_pair(&done[st]);
+        fph ^= 1;
+        if ((st += 2) >= C::NST) st -= C::NST, ph ^= 1;
       }
       if (!ok) s_abort[0] = 1;
-      for (int k = max(0, i - C::NST); k < i; ++k)
-        mbar_wait(&done[k % C::NST], (k / C::NST) & 1, p.status, kWaitLimitNs, SITE_P_DRAIN);
-    } else if (warp >= C::EW + 2) {
+      // every MMA issued here has finished before the stages or the TMEM are given up
+      if (i > bu) {
+        i -= 2;
+        mbar_wait(&done[i % C::NST], (i / C::NST) & 1, p.status, kWaitLimitNs, SITE_P_DRAIN);
+      }
+    } else if (warp == C::EW + 3) {
       // Factors: sets of CH blocks of K, in a ring of NF.  Eight lanes read eight
-      // neighbouring scales of a token; 64 threads hold 8 tokens a pass.
-      const int et = tid - (C::EW + 2) * 32, fk = et % C::CH, fr = et / C::CH;
+      // neighbouring scales of a token, the warp 4 tokens a pass.
+      const int fk = lane % C::CH, fr = lane / C::CH;
       int ch = 0;
       bool ok = true;
       for (int tile = blockIdx.x >> 1; ok && tile < ntiles; tile += step) {
@@ -534,15 +541,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::NTHREADS, 1)
           float* to = fact + fs * C::FSET + fk * C::FROW + fr;
           const bool in = b + fk < p.kb;
 #pragma unroll 1
-          for (int k0 = 0; k0 < 16; k0 += 4) {
-            float v[4];
+          for (int r0 = 0; r0 < 128; r0 += 32) {
+            float v[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = 8 * (k0 + k);
+            for (int k = 0; k < 8; ++k) {
+              const int r = r0 + 4 * k;
               v[k] = in && m0 + r < p.M ? __ldg(as + static_cast<int64_t>(r) * p.kb + b) : 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) to[8 * (k0 + k)] = v[k];
+            for (int k = 0; k < 8; ++k) to[r0 + 4 * k] = v[k];
           }
           if (fr < 2)
             to[128] = in && nb * 128 < p.N ? __ldg(p.w_scale + static_cast<int64_t>(nb) * p.kb + b + fk)
@@ -558,70 +565,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::NTHREADS, 1)
     const int sub = warp & 3, half = warp >> 2, row = sub * 32 + lane;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + half * 128;
     const uint32_t free0 = mapa_u32(smem_u32(&acc_free[0]), 0);
-    // A warp's state runs one block ahead of its sums: the next block's factor and
-    // first 32 columns are on their way while the last columns of this one are
-    // added.  A lane that gave up keeps its warp together until the vote at the
-    // next set of factors.
-    int st = 0, fs = 0, bu = 0, b = 0;
+    // The block's columns leave TMEM in two halves; only the first half's sums
+    // stand between the block's completion and the buffer's return, the second
+    // half's overlap the wait for the next block.  A lane that gave up keeps its
+    // warp together until the vote at the next set of factors.
+    int st = 0, fs = 0, bu = 0;
     uint32_t ph = 0, fph = 0;
     bool ok = true, live = true;   // live: the same in all lanes
-    float f = 0.f;
-    uint32_t d[2][32];
-    auto next_block = [&]() {
-      if (b % C::CH == 0) {
-        ok = ok && mbar_wait(&f_full[fs], fph, p.status, kWaitLimitNs, SITE_P_FACT);
-        live = ok = __all_sync(0xffffffffu, ok);
-      }
-      const float* fb = fact + fs * C::FSET + (b % C::CH) * C::FROW;
-      f = fb[row] * fb[128 + half];
-      ok = ok && mbar_wait(&done[st], ph, p.status, kWaitLimitNs, SITE_P_ACC);
-      __syncwarp();
-      tc_fence_after();
-      tmem_ld32(taddr + bu * 256, d[0]);
-    };
-    if ((blockIdx.x >> 1) < ntiles) next_block();
     for (int tile = blockIdx.x >> 1; live && tile < ntiles; tile += step) {
       float acc[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.f;
-      bool last;
-      do {
-        const float fc = f;
-        last = b == p.kb - 1;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait_regs(d[c & 1]);
-          if (c < 3) {
-            tmem_ld32(taddr + bu * 256 + 32 * (c + 1), d[(c + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(free0 + bu * 8);
-            if (b % C::CH == C::CH - 1 || last) {
-              if (lane == 0) mbar_arrive(&f_free[fs]);
-              if (++fs == C::NF) fs = 0, fph ^= 1;
-            }
-            bu ^= 1;
-            if (++st == C::NST) st = 0, ph ^= 1;
-            b = last ? 0 : b + 1;
-            if (!last || tile + step < ntiles) next_block();
-          }
+      for (int b = 0; b < p.kb; ++b) {
+        if (b % C::CH == 0) {
+          ok = ok && mbar_wait(&f_full[fs], fph, p.status, kWaitLimitNs, SITE_P_FACT);
+          live = ok = __all_sync(0xffffffffu, ok);
+          if (!live) break;
+        }
+        const float* fb = fact + fs * C::FSET + (b % C::CH) * C::FROW;
+        const float f = fb[row] * fb[128 + half];
+        ok = ok && mbar_wait(&done[st], ph, p.status, kWaitLimitNs, SITE_P_ACC);
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t ta = taddr + bu * 256;
+        uint32_t d[2][32];
+        auto add = [&](int c, const uint32_t (&x)[32]) {
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
-            fma2_rn(acc[32 * c + e], acc[32 * c + e + 1], __uint_as_float(d[c & 1][e]),
-                    __uint_as_float(d[c & 1][e + 1]), fc, fc);
+            fma2_rn(acc[c + e], acc[c + e + 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f, f);
+        };
+        tmem_ld32(ta, d[0]);
+        tmem_ld32(ta + 32, d[1]);
+        tmem_ld_wait_regs(d[0]);
+        tmem_ld_wait_regs(d[1]);
+        add(0, d[0]);
+        tmem_ld32(ta + 64, d[0]);
+        add(32, d[1]);
+        tmem_ld32(ta + 96, d[1]);
+        tmem_ld_wait_regs(d[0]);
+        tmem_ld_wait_regs(d[1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0)
+            mbar_arrive(&acc_free[bu]);
+          else
+            mbar_arrive_cluster_relaxed(free0 + bu * 8);
         }
-      } while (!last && live);
+        add(64, d[0]);
+        add(96, d[1]);
+        bu ^= 1;
+        if (++st == C::NST) st = 0, ph ^= 1;
+        if (b % C::CH == C::CH - 1 || b == p.kb - 1) {
+          if (lane == 0) mbar_arrive(&f_free[fs]);   // (every lane's f was read before its sums)
+          if (++fs == C::NF) fs = 0, fph ^= 1;
+        }
+      }
       int mt, nt;
       wide_tile(tile, ntm, ntn, mt, nt);
       const int m = mt * 256 + rank * 128 + row, n = nt * 256 + half * 128;
-      if (last && ok && m < p.M) {
+      if (live && ok && m < p.M) {
 #pragma unroll
         for (int c = 0; c < 128; c += 32) store_out32(p, m, n + c, acc + c);
       }
     }
-    // (a first load in flight when the warp gave up)
-    tmem_ld_wait();
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) s_abort[0] = 1;
   }
