@@ -33,9 +33,9 @@ static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return g_encode;
 }
 
-bool encode_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
-                    uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
-                    bool swizzle128) {
+static bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t rows,
+                      uint64_t cols, uint64_t row_stride_bytes, uint32_t box_cols,
+                      uint32_t box_rows, bool swizzle128) {
   auto enc = encoder();
   if (enc == nullptr || rows == 0 || cols == 0) return false;
   cuuint64_t dims[2] = {cols, rows};
@@ -43,11 +43,25 @@ bool encode_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t es[2] = {1, 1};
   const CUresult r =
-      enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+      enc(map, type, 2, const_cast<void*>(base), dims, strides, box, es,
           CU_TENSOR_MAP_INTERLEAVE_NONE,
           swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool encode_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                    uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
+                    bool swizzle128) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, cols, row_stride_bytes,
+                   box_cols, box_rows, swizzle128);
+}
+
+bool encode_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                        uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
+                        bool swizzle128) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, rows, cols, row_stride_bytes,
+                   box_cols, box_rows, swizzle128);
 }
 
 int num_sms() {

@@ -31,6 +31,11 @@ bool encode_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
                     uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
                     bool swizzle128);
 
+// The same for FP32 elements.
+bool encode_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                        uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
+                        bool swizzle128);
+
 // --- sparse MLA ---------------------------------------------------------------
 struct SparseMlaArgs {
   const uint16_t* q_lat;
