@@ -96,6 +96,13 @@ __device__ __forceinline__ void store_out4(const Params& p, int m, int n, const 
   }
 }
 
+// A value that is the same in every lane, known to be so by the compiler.  Warps
+// that issue copies and MMAs run their loops whole, on such values, and elect a
+// lane for the instructions themselves: with one lane running the loop, every
+// MMA and every commit cost about 45 cycles more (a block of 128 x 16 x 128 276
+// cycles instead of 160).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // ---------------------------------------------------------------------------
 // Split kernel: Dt[128 features x NT tokens] = W . A^T over a slice of K per CTA,
 // the slices of a tile on one cluster and joined through its shared memory.
@@ -146,7 +153,7 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
   float* fact = reinterpret_cast<float*>(sm + C::OFF_FACT);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int tile = blockIdx.x / S, rank = blockIdx.x - tile * S;   // the cluster is S CTAs along x
   const int ntn = (p.N + 127) / 128;
   const int nb = tile % ntn;
@@ -178,51 +185,49 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = uniform(*tslot);
 
   float acc[C::COLS];
 #pragma unroll
   for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int i = min(C::NST, nkb);
-      for (; i < nkb; ++i) {
-        if (!mbar_wait(&empty[i % C::NST], (i / C::NST - 1) & 1, p.status, kWaitLimitNs, SITE_S_E))
-          break;
-        if (s_abort[0]) break;
-        load(i);
-      }
-      if (i < nkb) s_abort[0] = 1;
-      // the copies in flight have landed before anything else touches the stages
-      for (int k = max(0, i - C::NST); k < i; ++k)
-        mbar_wait(&full[k % C::NST], (k / C::NST) & 1, p.status, kWaitLimitNs, SITE_S_F);
+    int i = min(C::NST, nkb);
+    for (; i < nkb; ++i) {
+      const bool ok = mbar_wait(&empty[i % C::NST], (i / C::NST - 1) & 1, p.status, kWaitLimitNs,
+                                SITE_S_E) && !s_abort[0];
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (elect_one_lane()) load(i);
+      __syncwarp();
     }
-    __syncwarp();
+    if (i < nkb) s_abort[0] = 1;
+    // the copies in flight have landed before anything else touches the stages
+    for (int k = max(0, i - C::NST); k < i; ++k)
+      mbar_wait(&full[k % C::NST], (k / C::NST) & 1, p.status, kWaitLimitNs, SITE_S_F);
   } else if (warp == 1) {
-    if (lane == 0) {
-      int i = 0;
-      for (; i < nkb; ++i) {
-        const int st = i % C::NST, bu = i % C::NB, use = i / C::NB;
-        if (!mbar_wait(&full[st], (i / C::NST) & 1, p.status, kWaitLimitNs, SITE_S_F)) break;
-        if (use > 0 &&
-            !mbar_wait(&acc_free[bu], (use - 1) & 1, p.status, kWaitLimitNs, SITE_S_FREE))
-          break;
-        tc_fence_after();
-        const uint64_t wd = smem_desc(smem_u32(sm + st * C::STAGE), 16, 1024);
-        const uint64_t ad = desc_add(wd, 128 * 128);
+    const uint64_t desc0 = smem_desc(smem_u32(sm), 16, 1024);
+    int i = 0;
+    bool ok = true;
+    for (; i < nkb; ++i) {
+      const int st = i % C::NST, bu = i % C::NB, use = i / C::NB;
+      ok = mbar_wait(&full[st], (i / C::NST) & 1, p.status, kWaitLimitNs, SITE_S_F) &&
+           (use == 0 || mbar_wait(&acc_free[bu], (use - 1) & 1, p.status, kWaitLimitNs, SITE_S_FREE));
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint64_t wd = desc_add(desc0, st * C::STAGE), ad = desc_add(wd, 128 * 128);
+      if (elect_one_lane()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_e4m3(tmem + bu * NT, desc_add(wd, kk * 32), desc_add(ad, kk * 32), IDESC, kk ? 1u : 0u);
         umma_commit(&empty[st]);
         umma_commit(&acc_full[bu]);
       }
-      if (i < nkb) s_abort[0] = 1;
-      // every MMA issued has finished before the stages or the TMEM are given up
-      for (int k = max(0, i - C::NST); k < i; ++k)
-        mbar_wait(&empty[k % C::NST], (k / C::NST) & 1, p.status, kWaitLimitNs, SITE_S_DRAIN);
+      __syncwarp();
     }
-    __syncwarp();
+    if (i < nkb) s_abort[0] = 1;
+    // every MMA issued has finished before the stages or the TMEM are given up
+    for (int k = max(0, i - C::NST); k < i; ++k)
+      mbar_wait(&empty[k % C::NST], (k / C::NST) & 1, p.status, kWaitLimitNs, SITE_S_DRAIN);
   } else {
     const int et = tid - 64;                               // epilogue thread
     const int sub = warp & 3;                              // TMEM lane quarter of this warp
@@ -385,7 +390,6 @@ struct Wide {
   static constexpr int STAGE = 2 * 128 * 128;            // 128 tokens, 128 features
   static constexpr int EW = 8;                           // epilogue warps 0..7, two warpgroups
   static constexpr int NTHREADS = EW * 32 + 128;         // and one warpgroup for copies and MMA
-  static_assert(NST % 2 == 0, "each issuing thread owns every other stage");
   static constexpr int BOX = 32 * 128;                   // 32 tokens x 128 bytes of out
   static constexpr int OFF_OUT = NST * STAGE;            // two boxes per epilogue warp
   static constexpr int OFF_MISC = OFF_OUT + EW * 2 * BOX;
@@ -454,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::NTHREADS, 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
   float* fact = reinterpret_cast<float*>(sm + C::OFF_FACT);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int rank = blockIdx.x & 1;
   const int ntm = (p.M + 255) / 256, ntn = (p.N + 255) / 256;
   const int ntiles = ntm * ntn, step = gridDim.x >> 1;
@@ -477,68 +481,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::NTHREADS, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = uniform(*tslot);
 
   if (warp >= C::EW) {
     regs_dec<56>();
-    if (warp == C::EW && lane == 0) {
-      tma_prefetch_desc(&tm_a);
-      tma_prefetch_desc(&tm_w);
+    if (warp == C::EW) {
+      if (elect_one_lane()) {
+        tma_prefetch_desc(&tm_a);
+        tma_prefetch_desc(&tm_w);
+        tma_prefetch_desc(&tm_out);
+      }
+      __syncwarp();
       int st = 0, i = 0;
       uint32_t ph = 0;       // parity of the stage's current use
       bool ok = true;
       for (int tile = blockIdx.x >> 1; ok && tile < ntiles; tile += step) {
         int mt, nt;
         wide_tile(tile, ntm, ntn, mt, nt);
-        for (int b = 0; b < p.kb; ++b, ++i) {
+        for (int b = 0; b < p.kb; ++b) {
           ok = (i < C::NST || mbar_wait(&done[st], ph ^ 1, p.status, kWaitLimitNs, SITE_P_E)) &&
                !s_abort[0];
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           uint8_t* a = sm + st * C::STAGE;
-          if (rank == 0) mbar_expect_tx(&full[st], 2 * C::STAGE);   // both CTAs' bytes
-          const uint32_t bar = mapa_u32(smem_u32(&full[st]), 0);
-          tma_load_2d_pair(a, &tm_a, bar, 64 * b, mt * 256 + rank * 128);
-          tma_load_2d_pair(a + 128 * 128, &tm_w, bar, 64 * b, nt * 256 + rank * 128);
+          if (elect_one_lane()) {
+            if (rank == 0) mbar_expect_tx(&full[st], 2 * C::STAGE);   // both CTAs' bytes
+            const uint32_t bar = mapa_u32(smem_u32(&full[st]), 0);
+            tma_load_2d_pair(a, &tm_a, bar, 64 * b, mt * 256 + rank * 128);
+            tma_load_2d_pair(a + 128 * 128, &tm_w, bar, 64 * b, nt * 256 + rank * 128);
+          }
+          __syncwarp();
+          if (i < C::NST) ++i;
           if (++st == C::NST) st = 0, ph ^= 1;
         }
       }
       if (!ok) s_abort[0] = 1;
-      // the pair's copies in flight have landed before either CTA leaves
+      // the pair's copies in flight (the last i uses of the ring) have landed
+      // before either CTA leaves
       if (rank == 0)
-        for (int k = max(0, i - C::NST); k < i; ++k)
-          mbar_wait(&full[k % C::NST], (k / C::NST) & 1, p.status, kWaitLimitNs, SITE_P_F);
-    } else if ((warp == C::EW + 1 || warp == C::EW + 2) && rank == 0 && lane == 0) {
-      // Two issuing threads, one per TMEM buffer (even and odd blocks): while one
-      // waits for its operands and its buffer, the other's MMAs keep the tensor
-      // core busy.  One thread alone left it idle for about 110 cycles a block.
+        for (; i > 0; --i) {
+          if (--st < 0) st = C::NST - 1, ph ^= 1;
+          mbar_wait(&full[st], ph, p.status, kWaitLimitNs, SITE_P_F);
+        }
+    } else if (warp == C::EW + 1 && rank == 0) {
       const uint64_t desc0 = smem_desc(smem_u32(sm), 16, 1024);
-      const int bu = warp - (C::EW + 1);
-      const int64_t blocks = static_cast<int64_t>((ntiles - (blockIdx.x >> 1) + step - 1) / step) * p.kb;
-      int st = bu;
-      uint32_t ph = 0, fph = 1;
-      int64_t i = bu;
+      int st = 0, i = 0;
+      uint32_t ph = 0, fph = 1, bu = 0;
       bool ok = true;
-      for (; i < blocks; i += 2) {
-        const uint64_t ad = desc_add(desc0, st * C::STAGE), wd = desc_add(ad, 128 * 128);
-        ok = mbar_wait(&full[st], ph, p.status, kWaitLimitNs, SITE_P_F) &&
-             (i < 2 || mbar_wait(&acc_free[bu], fph, p.status, kWaitLimitNs, SITE_P_FREE));
-        if (!ok) break;
-        tc_fence_after();
+      for (int tile = blockIdx.x >> 1; ok && tile < ntiles; tile += step) {
+        for (int b = 0; b < p.kb; ++b) {
+          ok = mbar_wait(&full[st], ph, p.status, kWaitLimitNs, SITE_P_F) &&
+               (i < 2 || mbar_wait(&acc_free[bu], fph, p.status, kWaitLimitNs, SITE_P_FREE));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t ad = desc_add(desc0, st * C::STAGE), wd = desc_add(ad, 128 * 128);
+          if (elect_one_lane()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_e4m3_pair(tmem + bu * 256, desc_add(ad, kk * 32), desc_add(wd, kk * 32), IDESC,
-                         kk ? 1u : 0u);
-        umma_commit_pair(&done[st]);
-        fph ^= 1;
-        if ((st += 2) >= C::NST) st -= C::NST, ph ^= 1;
+            for (int kk = 0; kk < 4; ++kk)
+              umma_e4m3_pair(tmem + bu * 256, desc_add(ad, kk * 32), desc_add(wd, kk * 32), IDESC,
+                             kk ? 1u : 0u);
+            umma_commit_pair(&done[st]);
+          }
+          __syncwarp();
+          if (i < C::NST) ++i;
+          if (bu) fph ^= 1;
+          bu ^= 1;
+          if (++st == C::NST) st = 0, ph ^= 1;
+        }
       }
       if (!ok) s_abort[0] = 1;
-      // every MMA issued here has finished before the stages or the TMEM are given up
-      if (i > bu) {
-        i -= 2;
-        mbar_wait(&done[i % C::NST], (i / C::NST) & 1, p.status, kWaitLimitNs, SITE_P_DRAIN);
+      // every MMA issued has finished before the stages or the TMEM are given up
+      for (; i > 0; --i) {
+        if (--st < 0) st = C::NST - 1, ph ^= 1;
+        mbar_wait(&done[st], ph, p.status, kWaitLimitNs, SITE_P_DRAIN);
       }
-    } else if (warp == C::EW + 3) {
+    } else if (warp == C::EW + 2) {
       // Factors: sets of CH blocks of K, in a ring of NF.  Eight lanes read eight
       // neighbouring scales of a token, the warp 4 tokens a pass.
       const int fk = lane % C::CH, fr = lane / C::CH;
