@@ -401,17 +401,19 @@ def sparse_mla_bwd(q_lat, kv: Rows, idx, q_start, kv_len, max_kv_len: int, o_lat
 
 def _on(t, dtype, shape, dev: int, name: str) -> int:
     """Check an operand (type, shape, layout, device) and return its address."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.get_device() == dev):
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"{name} must be contiguous")
-    if t.get_device() != dev:
-        raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"{name} must be on cuda:{dev}")
-    return t.data_ptr()
+    raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"{name} must be on cuda:{dev}")
 
 
 def _device(t, name: str) -> int:
@@ -422,30 +424,36 @@ def _device(t, name: str) -> int:
     return t.get_device()
 
 
-class _Launch:
-    """Device and stream of one call: its tensors' device is made the current one
-    for the launch, and outputs it allocates belong to the launch stream."""
+# The current stream's handle without building a Stream object, where torch has it.
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream",
+                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-    def __init__(self, dev: int, stream):
-        if stream is not None and stream.device.index != dev:
-            raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"stream must be on cuda:{dev}")
-        self.dev, self.given = dev, stream
-        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
 
-    def empty(self, shape, dtype):
-        if self.given is None:
-            return torch.empty(shape, dtype=dtype, device=self.stream.device)
-        with torch.cuda.stream(self.given):
-            return torch.empty(shape, dtype=dtype, device=self.stream.device)
+def _stream_on(dev: int, stream) -> int:
+    if stream is None:
+        return _current_raw(dev)
+    if stream.device_index != dev:
+        raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"stream must be on cuda:{dev}")
+    return stream.cuda_stream
 
-    def __call__(self, fn, *args):
-        if torch.cuda.current_device() == self.dev:
-            code = fn(*args, self.stream.cuda_stream)
-        else:
-            with torch.cuda.device(self.dev):
-                code = fn(*args, self.stream.cuda_stream)
-        if code != DSA_OK:
-            raise DsaError(code, fn.__name__)
+
+def _empty(shape, dtype, dev: int, stream):
+    """An output that belongs to the launch stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _launch(fn, dev: int, *args):
+    """Call with the tensors' device as the current one."""
+    if torch.cuda.current_device() == dev:
+        code = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args)
+    if code != DSA_OK:
+        raise DsaError(code, fn.__name__)
 
 
 def dsa_rmsnorm_fp8(x, gain, residual=None, eps: float = RMS_NORM_EPS, codes=None, scale=None,
@@ -457,29 +465,28 @@ def dsa_rmsnorm_fp8(x, gain, residual=None, eps: float = RMS_NORM_EPS, codes=Non
     y = bf16(v) (None unless y is given or want_y).  residual_out and y may be x
     or residual themselves."""
     dev = _device(x, "x")
-    run = _Launch(dev, stream)
+    raw = _stream_on(dev, stream)
     shape = x.shape
     if not shape:
         raise ValueError("x must be [..., hid]")
     hid = shape[-1]
-    n = x.numel() // hid if hid else 0
     groups = (*shape[:-1], -(-hid // FP8_BLOCK))
-    if codes is None:
-        codes = run.empty(shape, torch.uint8)
-    if scale is None:
-        scale = run.empty(groups, torch.float32)
-    if residual is not None and residual_out is None:
-        residual_out = run.empty(shape, torch.bfloat16)
-    if y is None and want_y:
-        y = run.empty(shape, torch.bfloat16)
     bf = torch.bfloat16
-    run(lib.dsa_rmsnorm_fp8, _on(x, bf, shape, dev, "x"),
-        None if residual is None else _on(residual, bf, shape, dev, "residual"),
-        _on(gain, bf, (hid,), dev, "gain"), n, hid, eps,
-        None if residual_out is None else _on(residual_out, bf, shape, dev, "residual_out"),
-        None if y is None else _on(y, bf, shape, dev, "y"),
-        _on(codes, torch.uint8, shape, dev, "codes"),
-        _on(scale, torch.float32, groups, dev, "scale"))
+    if codes is None:
+        codes = _empty(shape, torch.uint8, dev, stream)
+    if scale is None:
+        scale = _empty(groups, torch.float32, dev, stream)
+    if residual is not None and residual_out is None:
+        residual_out = _empty(shape, bf, dev, stream)
+    if y is None and want_y:
+        y = _empty(shape, bf, dev, stream)
+    _launch(lib.dsa_rmsnorm_fp8, dev, _on(x, bf, shape, dev, "x"),
+            None if residual is None else _on(residual, bf, shape, dev, "residual"),
+            _on(gain, bf, (hid,), dev, "gain"), x.numel() // hid if hid else 0, hid, eps,
+            None if residual_out is None else _on(residual_out, bf, shape, dev, "residual_out"),
+            None if y is None else _on(y, bf, shape, dev, "y"),
+            _on(codes, torch.uint8, shape, dev, "codes"),
+            _on(scale, torch.float32, groups, dev, "scale"), raw)
     return codes, scale, residual_out, y
 
 
@@ -487,18 +494,19 @@ def dsa_quant_fp8_weight(w, codes=None, scale=None, stream=None):
     """w [N,K] bf16 (one row per output feature) -> (codes [N,K] uint8,
     scale [ceil(N/128), ceil(K/128)] float32), one scale per 128 x 128 block."""
     dev = _device(w, "w")
-    run = _Launch(dev, stream)
-    if w.dim() != 2:
+    raw = _stream_on(dev, stream)
+    shape = w.shape
+    if len(shape) != 2:
         raise ValueError("w must be [N, K]")
-    N, K = w.shape
+    N, K = shape
     groups = (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK))
     if codes is None:
-        codes = run.empty((N, K), torch.uint8)
+        codes = _empty(shape, torch.uint8, dev, stream)
     if scale is None:
-        scale = run.empty(groups, torch.float32)
-    run(lib.dsa_quant_fp8_weight, _on(w, torch.bfloat16, w.shape, dev, "w"), N, K,
-        _on(codes, torch.uint8, w.shape, dev, "codes"),
-        _on(scale, torch.float32, groups, dev, "scale"))
+        scale = _empty(groups, torch.float32, dev, stream)
+    _launch(lib.dsa_quant_fp8_weight, dev, _on(w, torch.bfloat16, shape, dev, "w"), N, K,
+            _on(codes, torch.uint8, shape, dev, "codes"),
+            _on(scale, torch.float32, groups, dev, "scale"), raw)
     return codes, scale
 
 
@@ -512,30 +520,28 @@ def dsa_linear_fp8(codes, scale, w_codes, w_scale, out=None, out_dtype=torch.bfl
     [ceil(N/128), ceil(K/128)] float32 (dsa_quant_fp8_weight) -> out [..., N] of
     out_dtype (bfloat16 or float32; out's own when it is given)."""
     dev = _device(codes, "codes")
-    run = _Launch(dev, stream)
-    shape = codes.shape
-    if not shape or w_codes.dim() != 2:
+    raw = _stream_on(dev, stream)
+    u8, f32 = torch.uint8, torch.float32
+    shape, w_shape = codes.shape, getattr(w_codes, "shape", ())
+    if len(w_shape) != 2 or not shape or shape[-1] != w_shape[1]:
         raise ValueError("codes must be [..., K] and w_codes [N, K]")
-    N, K = w_codes.shape
+    N, K = w_shape
     M = codes.numel() // K if K else 0
-    if shape[-1] != K:
-        raise ValueError(f"codes must be [..., {K}], got {list(shape)}")
     kb = -(-K // FP8_BLOCK)
+    lead = shape[:-1]
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _DTYPES:
+        raise TypeError(f"out must be bfloat16 or float32, got {out_dtype}")
     if out is None:
-        if out_dtype not in _DTYPES:
-            raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
-        out = run.empty((*shape[:-1], N), out_dtype)
-    elif out.dtype not in _DTYPES:
-        raise TypeError(f"out must be bfloat16 or float32, got {out.dtype}")
+        out = _empty((*lead, N), out_dtype, dev, stream)
     if workspace is None:
         need = workspace_bytes(OP_LINEAR_FP8, M, 1, K, N, 0)
-        workspace = run.empty((need,), torch.uint8)
-        run(lib.dsa_workspace_init, workspace.data_ptr(), need)
-    f32 = torch.float32
-    run(lib.dsa_linear_fp8, _on(codes, torch.uint8, shape, dev, "codes"),
-        _on(scale, f32, (*shape[:-1], kb), dev, "scale"),
-        _on(w_codes, torch.uint8, w_codes.shape, dev, "w_codes"),
-        _on(w_scale, f32, (-(-N // FP8_BLOCK), kb), dev, "w_scale"), M, N, K,
-        _on(out, out.dtype, (*shape[:-1], N), dev, "out"), _DTYPES[out.dtype],
-        _on(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel())
+        workspace = _empty((need,), u8, dev, stream)
+        _launch(lib.dsa_workspace_init, dev, workspace.data_ptr(), need, raw)
+    _launch(lib.dsa_linear_fp8, dev, _on(codes, u8, shape, dev, "codes"),
+            _on(scale, f32, (*lead, kb), dev, "scale"), _on(w_codes, u8, w_shape, dev, "w_codes"),
+            _on(w_scale, f32, (-(-N // FP8_BLOCK), kb), dev, "w_scale"), M, N, K,
+            _on(out, out_dtype, (*lead, N), dev, "out"), _DTYPES[out_dtype],
+            _on(workspace, u8, workspace.shape, dev, "workspace"), workspace.numel(), raw)
     return out

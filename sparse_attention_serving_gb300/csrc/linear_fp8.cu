@@ -125,7 +125,7 @@ struct Split {
   // three CTAs per SM up to 16 tokens, two up to 64, one above
   static constexpr int CTAS = NT <= 16 ? 3 : NT <= 64 ? 2 : 1;
   static constexpr int NST = NT == 32 ? 5 : NT == 128 ? 6 : 4;
-  static constexpr int NB = NT <= 128 ? 4 : 2;           // TMEM buffers
+  static constexpr int NB = 4;                           // TMEM buffers
   static constexpr int TCOLS = NT * NB;
   static constexpr int OFF_MISC = NST * STAGE;           // barriers, then two sets of factors
   static constexpr int OFF_FACT = OFF_MISC + 256;
@@ -292,54 +292,59 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
       mbar_arrive_warp(&acc_free[bu]);
     }
     if (!ok) s_abort[0] = 1;
-    const int n = n0 + sub * 32 + lane;
     if (S == 1) {
-      if (n < p.N) {
+      const int n = n0 + sub * 32 + lane;
+      if (ok && n < p.N) {
 #pragma unroll
         for (int c = 0; c < C::COLS; ++c)
           if (m0 + c0 + c < p.M) store_out(p, m0 + c0 + c, n, acc[c]);
       }
+    } else if (ok) {
+      // the last block is summed, so every copy and MMA of this CTA is done: its
+      // stages hold the partial tile [NT][128] now
+      float* part = reinterpret_cast<float*>(sm) + c0 * 128 + sub * 32 + lane;
+#pragma unroll
+      for (int c = 0; c < C::COLS; ++c) part[c * 128] = acc[c];
     }
   }
   tc_fence_before();
-  __syncthreads();
-  if (S > 1) {
-    // every copy and MMA of this CTA is done: its stages hold the partial tile now
-    float* part = reinterpret_cast<float*>(sm);            // [NT][128]
-    const int et = tid - 64, row = ((warp & 3) << 5) + lane, grp = et >> 7;
-    if (warp >= 2) {
-#pragma unroll
-      for (int c = 0; c < C::COLS; ++c) part[(grp * C::COLS + c) * 128 + row] = acc[c];
-    }
+  if (S == 1) {
+    __syncthreads();
+  } else {
     cluster_sync();
     if (warp >= 2) {
       // this CTA's share of the tokens, a warp per token and four features per
-      // lane, the slices of K added in their order
+      // lane, the slices of K added in their order, eight loads in flight
       const int live = min(NT, p.M - m0);
-#pragma unroll 2
       for (int c = rank + (warp - 2) * S; c < live; c += S * C::EW) {
-        const uint32_t at = smem_u32(part + c * 128 + lane * 4);
-        float4 v[8];
+        const uint32_t at = smem_u32(sm) + (c * 128 + lane * 4) * 4;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r0 = 0; r0 < S; r0 += 8) {
+          float4 v[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < S) v[r] = ld_cluster_f32x4(at, r);
+          for (int r = 0; r < 8; ++r)
+            if (r0 + r < S) v[r] = ld_cluster_f32x4(at, r0 + r);
 #pragma unroll
-        for (int r = 1; r < 8; ++r)
-          if (r < S) {
-            v[0].x += v[r].x;
-            v[0].y += v[r].y;
-            v[0].z += v[r].z;
-            v[0].w += v[r].w;
-          }
-        store_out4(p, m0 + c, n0 + lane * 4, v[0]);
+          for (int r = 0; r < 8; ++r)
+            if (r0 + r < S) {
+              sum.x += v[r].x;
+              sum.y += v[r].y;
+              sum.z += v[r].z;
+              sum.w += v[r].w;
+            }
+        }
+        store_out4(p, m0 + c, n0 + lane * 4, sum);
       }
     }
-    cluster_sync();   // no CTA leaves while another still reads its shared memory
+    // no CTA leaves while another may still read its shared memory; the reads
+    // are over (their values are in the stores), so nothing has to be ordered
+    cluster_arrive_relaxed();
   }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TCOLS);
   }
+  if (S > 1) cluster_wait();
 }
 
 template <int NT>
@@ -354,6 +359,9 @@ dsa_status_t launch_split(const LinearArgs& a, int S, cudaStream_t stream) {
   const Params p{a.a_scale, a.w_scale, a.M, a.N, (a.K + 127) / 128, a.out, a.fp32, a.status};
   if (cudaFuncSetAttribute(split_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
       cudaSuccess)
+    return launch_status("cudaFuncSetAttribute");
+  if (S > 8 && cudaFuncSetAttribute(split_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                    1) != cudaSuccess)
     return launch_status("cudaFuncSetAttribute");
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(((a.N + 127) / 128) * ((a.M + NT - 1) / NT) * S));
@@ -737,23 +745,64 @@ dsa_status_t quant_fp8_weight_launch(const uint16_t* w, int N, int K, uint8_t* c
   return launch_status("quant_weight_kernel");
 }
 
+namespace lin {
+
+// Which kernel, tile and number of K slices: the cheapest by an estimate of the
+// time in microseconds.  Its terms are what was measured on the GPU; over 160
+// sizes (1 to 4,096 tokens, 64 to 8,192 features, K 256 to 12,288) the choice
+// was on average 1.2 % slower than the fastest of all combinations, and at most
+// 19 %.  A CTA's block of K takes the longer of its own latency and its bytes
+// at an SM's share of L2 bandwidth (59 bytes a cycle); joining slices costs a
+// cluster barrier and the partial tiles' way through distributed shared memory
+// (17 bytes a cycle and SM); large clusters do not fill every GPC.  Examples
+// (us; tokens x features x K): 1 x 8,192 x 7,168: 16 tokens and 4 slices 12.5,
+// unsliced 17.8; 64 x 128 x 7,168: 16 tokens and 16 slices 4.6, 64 tokens and 8
+// slices 6.4; 777 x 1,001 x 1,040: 64 tokens unsliced 6.2, 64 tokens and 2
+// slices 9.7; 512 x 7,168 x 12,288: pairs 47, 128 tokens 66.
+struct Pick {
+  int nt, S;   // nt = 0: the pair kernel
+};
+Pick pick(int M, int N, int kb, int sms) {
+  const int64_t pairs = sms / 2;
+  const int64_t wt = static_cast<int64_t>((M + 255) / 256) * ((N + 255) / 256);
+  double best = 1.0 + static_cast<double>((wt + pairs - 1) / pairs) * (kb * 0.51 + 1.2);
+  Pick at{0, 1};
+  constexpr struct { int nt, ctas; double latency; } kTile[] = {
+      {16, 3, 0.22}, {32, 2, 0.23}, {64, 2, 0.28}, {128, 1, 0.34}};
+  constexpr struct { int S; double fill; } kSlices[] = {   // the part of the SMs clusters of S reach
+      {1, 1.0}, {2, 1.0}, {3, 0.9}, {4, 0.9}, {5, 0.9}, {6, 0.9}, {8, 0.78}, {12, 0.78}, {16, 0.7}};
+  for (const auto& t : kTile) {
+    const int64_t tiles = static_cast<int64_t>((N + 127) / 128) * ((M + t.nt - 1) / t.nt);
+    for (const auto& s : kSlices) {
+      if (s.S > kb) break;
+      const int64_t n = tiles * s.S;
+      const int64_t reach = static_cast<int64_t>(sms * s.fill), slots = static_cast<int64_t>(sms * t.ctas * s.fill);
+      const double rounds = static_cast<double>((n + slots - 1) / slots);
+      const int64_t per = (n + reach - 1) / reach;
+      const double on = static_cast<double>(per < t.ctas ? per : t.ctas);   // CTAs on one SM
+      const double load = on * (128 + t.nt) * 128 / 96.5e3;
+      const double block = load > t.latency ? load : t.latency;
+      const double join = s.S > 1 ? 0.41 + on * t.nt * 512 / 29.4e3 : on * t.nt * 0.0026;
+      const double us = rounds * (0.97 + (kb + s.S - 1) / s.S * block + join);
+      if (us < best) {
+        best = us;
+        at = Pick{t.nt, s.S};
+      }
+    }
+  }
+  return at;
+}
+
+}  // namespace lin
+
 dsa_status_t linear_fp8_launch(const LinearArgs& a, cudaStream_t stream) {
-  const int kb = (a.K + 127) / 128;
-  if (static_cast<int64_t>((a.M + 255) / 256) * ((a.N + 255) / 256) >= 60)
-    return lin::launch_wide(a, stream);
-  const int nt = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : a.M <= 128 ? 128 : 256;
-  const int per_sm = nt <= 16 ? 3 : nt <= 64 ? 2 : 1;
-  const int64_t tiles = static_cast<int64_t>((a.N + 127) / 128) * ((a.M + nt - 1) / nt);
-  // as many slices of K as fill the GPU, up to the portable cluster size
-  int64_t S = num_sms() * per_sm / tiles;
-  S = S < 1 ? 1 : S > 8 ? 8 : S;
-  if (S > kb) S = kb;
-  switch (nt) {
-    case 16: return lin::launch_split<16>(a, static_cast<int>(S), stream);
-    case 32: return lin::launch_split<32>(a, static_cast<int>(S), stream);
-    case 64: return lin::launch_split<64>(a, static_cast<int>(S), stream);
-    case 128: return lin::launch_split<128>(a, static_cast<int>(S), stream);
-    default: return lin::launch_split<256>(a, static_cast<int>(S), stream);
+  const lin::Pick at = lin::pick(a.M, a.N, (a.K + 127) / 128, num_sms());
+  switch (at.nt) {
+    case 16: return lin::launch_split<16>(a, at.S, stream);
+    case 32: return lin::launch_split<32>(a, at.S, stream);
+    case 64: return lin::launch_split<64>(a, at.S, stream);
+    case 128: return lin::launch_split<128>(a, at.S, stream);
+    default: return lin::launch_wide(a, stream);
   }
 }
 

@@ -241,7 +241,8 @@ SIZES = [(1, 1, 16), (1, 8, 128), (1, 128, 7168), (2, 129, 144), (1, 8192, 1024)
          (127, 1024, 1024), (128, 1024, 1024), (129, 130, 272), (200, 512, 4096), (256, 576, 7168),
          (257, 255, 400), (300, 257, 1024), (512, 1001, 640), (777, 1001, 1040), (1000, 640, 7168),
          (1025, 1300, 144), (2048, 576, 896), (2500, 2305, 528), (4097, 520, 1024),
-         (4100, 1304, 272), (5000, 1000, 2064), (2049, 2564, 144)]
+         (4100, 1304, 272), (5000, 1000, 2064), (2049, 2564, 144),
+         (64, 128, 7168), (400, 256, 7168), (2048, 130, 7168), (96, 1024, 2048), (300, 8192, 512)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
