@@ -23,6 +23,8 @@ __global__ void __launch_bounds__(256)
   const int row0 = static_cast<int>(blockIdx.x / kb) * 128 + (tid >> 4);
   uint4 u[8];
   uint32_t top = 0;
+  pdl_wait();
+  pdl_start_next();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = row0 + 16 * i;
@@ -122,17 +124,17 @@ struct Split {
   static constexpr int COLS = NT / (EW / 4);             // tokens per epilogue thread
   static constexpr int NTHREADS = 64 + EW * 32;
   static constexpr int STAGE = (128 + NT) * 128;
-  // three CTAs per SM up to 16 tokens, two up to 64, one above
-  static constexpr int CTAS = NT <= 16 ? 3 : NT <= 64 ? 2 : 1;
-  static constexpr int NST = NT == 32 ? 5 : NT == 128 ? 6 : 4;
+  static constexpr int CTAS = NT <= 16 ? 3 : NT <= 64 ? 2 : 1;  // per SM
+  static constexpr int NST = NT == 32 ? 5 : NT > 64 ? 6 : 4;
   static constexpr int NB = 4;                           // TMEM buffers
-  static constexpr int TCOLS = NT * NB;
+  static constexpr int STEP = COLS % 32 == 0 ? 32 : 16;  // columns per TMEM load
+  static constexpr int TCOLS = NT == 96 ? 512 : NT * NB; // a power of two
   static constexpr int OFF_MISC = NST * STAGE;           // barriers, then two sets of factors
   static constexpr int OFF_FACT = OFF_MISC + 256;
   static constexpr int CH = 8;                           // blocks of K per set of factors
   static constexpr int FROW = NT + 4;
   static constexpr int SMEM = 1024 + OFF_FACT + 2 * CH * FROW * 4;
-  static_assert(TCOLS >= 32 && TCOLS * CTAS <= 512, "TMEM columns");
+  static_assert(NT <= EW * 32 && TCOLS >= 32 && TCOLS * CTAS <= 512, "TMEM columns");
   static_assert(NT * 128 * 4 <= NST * STAGE, "the partial tile reuses the stages");
   static_assert((SMEM + 1024) * CTAS <= 228 * 1024, "shared memory");
 };
@@ -175,6 +177,7 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
     for (int k = 0; k < C::NB; ++k) mbar_init(&acc_free[k], C::EW);
     s_abort[0] = 0;
     fence_mbar_init();
+    pdl_wait();
     // the copying thread fills the ring before the other warps are set up
     for (int i = 0; i < min(C::NST, nkb); ++i) load(i);
   }
@@ -186,6 +189,8 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(*tslot);
+  pdl_wait();
+  pdl_start_next();
 
   float acc[C::COLS];
 #pragma unroll
@@ -271,25 +276,29 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
                                                SITE_S_ACC));
       if (!ok) continue;
       tc_fence_after();
-      constexpr int STEP = C::COLS < 32 ? 16 : 32;
 #pragma unroll
-      for (int c = 0; c < C::COLS; c += STEP) {
-        uint32_t d[STEP];
-        if constexpr (STEP == 16)
+      for (int c = 0; c < C::COLS; c += C::STEP) {
+        uint32_t d[C::STEP];
+        if constexpr (C::STEP == 16)
           tmem_ld16(taddr + bu * NT + c, d);
         else
           tmem_ld32(taddr + bu * NT + c, d);
-        tmem_ld_wait();
+        float4 f[C::STEP / 4];                             // on their way beside the load
 #pragma unroll
-        for (int e = 0; e < STEP; e += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(fb + c + e);
-          fma2_rn(acc[c + e], acc[c + e + 1], __uint_as_float(d[e]), __uint_as_float(d[e + 1]), f.x, f.y);
+        for (int e = 0; e < C::STEP / 4; ++e) f[e] = reinterpret_cast<const float4*>(fb + c)[e];
+        tmem_ld_wait();
+        if (c + C::STEP == C::COLS) {
+          tc_fence_before();
+          mbar_arrive_warp(&acc_free[bu]);
+        }
+#pragma unroll
+        for (int e = 0; e < C::STEP; e += 4) {
+          const float4 g = f[e / 4];
+          fma2_rn(acc[c + e], acc[c + e + 1], __uint_as_float(d[e]), __uint_as_float(d[e + 1]), g.x, g.y);
           fma2_rn(acc[c + e + 2], acc[c + e + 3], __uint_as_float(d[e + 2]),
-                  __uint_as_float(d[e + 3]), f.z, f.w);
+                  __uint_as_float(d[e + 3]), g.z, g.w);
         }
       }
-      tc_fence_before();
-      mbar_arrive_warp(&acc_free[bu]);
     }
     if (!ok) s_abort[0] = 1;
     if (S == 1) {
@@ -363,18 +372,9 @@ dsa_status_t launch_split(const LinearArgs& a, int S, cudaStream_t stream) {
   if (S > 8 && cudaFuncSetAttribute(split_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed,
                                     1) != cudaSuccess)
     return launch_status("cudaFuncSetAttribute");
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(((a.N + 127) / 128) * ((a.M + NT - 1) / NT) * S));
-  cfg.blockDim = dim3(C::NTHREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = static_cast<unsigned>(S);
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, split_kernel<NT>, ta, tw, p, S);
+  launch_overlapped(split_kernel<NT>,
+                    static_cast<unsigned>(((a.N + 127) / 128) * ((a.M + NT - 1) / NT) * S),
+                    C::NTHREADS, C::SMEM, static_cast<unsigned>(S), stream, ta, tw, p, S);
   return launch_status("split_kernel");
 }
 
@@ -450,7 +450,7 @@ __device__ __forceinline__ void put_box_bf16(uint8_t* box, int lane, const float
                    pack_bf16x2(v[8 * u + 4], v[8 * u + 5]), pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::NTHREADS, 1)
+__global__ void __launch_bounds__(Wide::NTHREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                 const __grid_constant__ CUtensorMap tm_out, const bool by_tma, const Params p) {
   using C = Wide;
@@ -490,6 +490,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::NTHREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = uniform(*tslot);
+  pdl_wait();
+  pdl_start_next();
 
   if (warp >= C::EW) {
     regs_dec<56>();
@@ -731,8 +733,8 @@ dsa_status_t launch_wide(const LinearArgs& a, cudaStream_t stream) {
     return launch_status("cudaFuncSetAttribute");
   const int64_t tiles = static_cast<int64_t>((a.M + 255) / 256) * ((a.N + 255) / 256);
   const int64_t pairs = num_sms() / 2;
-  wide_kernel<<<static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), C::NTHREADS, C::SMEM,
-                stream>>>(ta, tw, to, by_tma, p);
+  launch_overlapped(wide_kernel, static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)),
+                    C::NTHREADS, C::SMEM, 2, stream, ta, tw, to, by_tma, p);
   return launch_status("wide_kernel");
 }
 
@@ -741,49 +743,55 @@ dsa_status_t launch_wide(const LinearArgs& a, cudaStream_t stream) {
 dsa_status_t quant_fp8_weight_launch(const uint16_t* w, int N, int K, uint8_t* codes, float* scale,
                                      cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>((K + 127) / 128) * static_cast<unsigned>((N + 127) / 128);
-  lin::quant_weight_kernel<<<grid, 256, 0, stream>>>(w, N, K, codes, scale);
+  launch_overlapped(lin::quant_weight_kernel, grid, 256, 0, 0, stream, w, N, K, codes, scale);
   return launch_status("quant_weight_kernel");
 }
 
 namespace lin {
 
 // Which kernel, tile and number of K slices: the cheapest by an estimate of the
-// time in microseconds.  Its terms are what was measured on the GPU; over 160
-// sizes (1 to 4,096 tokens, 64 to 8,192 features, K 256 to 12,288) the choice
-// was on average 1.2 % slower than the fastest of all combinations, and at most
-// 19 %.  A CTA's block of K takes the longer of its own latency and its bytes
-// at an SM's share of L2 bandwidth (59 bytes a cycle); joining slices costs a
-// cluster barrier and the partial tiles' way through distributed shared memory
-// (17 bytes a cycle and SM); large clusters do not fill every GPC.  Examples
-// (us; tokens x features x K): 1 x 8,192 x 7,168: 16 tokens and 4 slices 12.5,
-// unsliced 17.8; 64 x 128 x 7,168: 16 tokens and 16 slices 4.6, 64 tokens and 8
-// slices 6.4; 777 x 1,001 x 1,040: 64 tokens unsliced 6.2, 64 tokens and 2
-// slices 9.7; 512 x 7,168 x 12,288: pairs 47, 128 tokens 66.
+// time in microseconds, whose terms were fitted to the measured time of every
+// combination at 180 sizes (1 to 4,096 tokens, 64 to 8,192 features, K 256 to
+// 12,288): the choice is on average 0.5 % slower than the fastest combination,
+// at most 9 %.  The terms: a CTA's time per block of K, by how many CTAs share
+// its SM (its bytes at an SM's share of L2 bandwidth, 59 a cycle, or the
+// epilogue's latency); a start; the join of K slices, a cluster barrier and the
+// partial tiles' way through distributed shared memory (about 13 bytes a cycle);
+// the part of the SMs that clusters of a size can fill.  Examples (us; tokens x
+// features x K): 1 x 8,192 x 7,168: 16 tokens and 4 slices 11.7, unsliced 17;
+// 64 x 128 x 7,168: 16 tokens and 16 slices 3.7, 64 tokens and 8 slices 5.5;
+// 777 x 1,001 x 1,040: 64 tokens unsliced 5.3, with 2 slices 9; 2,048 x 576 x
+// 7,168: 96 tokens 17, 128 tokens 20, pairs 28; 512 x 7,168 x 12,288: pairs 46,
+// 128 tokens 65.
 struct Pick {
   int nt, S;   // nt = 0: the pair kernel
 };
 Pick pick(int M, int N, int kb, int sms) {
   const int64_t pairs = sms / 2;
   const int64_t wt = static_cast<int64_t>((M + 255) / 256) * ((N + 255) / 256);
-  double best = 1.0 + static_cast<double>((wt + pairs - 1) / pairs) * (kb * 0.51 + 1.2);
+  double best = 2.23 + static_cast<double>((wt + pairs - 1) / pairs) * (kb * 0.47 + 2.3);
   Pick at{0, 1};
-  constexpr struct { int nt, ctas; double latency; } kTile[] = {
-      {16, 3, 0.22}, {32, 2, 0.23}, {64, 2, 0.28}, {128, 1, 0.34}};
-  constexpr struct { int S; double fill; } kSlices[] = {   // the part of the SMs clusters of S reach
-      {1, 1.0}, {2, 1.0}, {3, 0.9}, {4, 0.9}, {5, 0.9}, {6, 0.9}, {8, 0.78}, {12, 0.78}, {16, 0.7}};
+  constexpr struct {
+    int nt, ctas;      // the tile's tokens, its CTAs per SM
+    double block[3];   // time per block of K with 1, 2, 3 CTAs on the SM
+  } kTile[] = {{16, 3, {0.15, 0.26, 0.34}}, {32, 2, {0.18, 0.30}}, {64, 2, {0.25, 0.37}},
+               {96, 1, {0.26}}, {128, 1, {0.31}}};
+  constexpr struct {
+    int S;
+    double reach;      // the part of the SMs that clusters of S fill
+  } kSlices[] = {{1, 1.0}, {2, 1.0}, {3, 0.91}, {4, 0.95}, {5, 0.92}, {6, 0.91}, {8, 0.79},
+                 {12, 0.7}, {16, 0.7}};
   for (const auto& t : kTile) {
     const int64_t tiles = static_cast<int64_t>((N + 127) / 128) * ((M + t.nt - 1) / t.nt);
     for (const auto& s : kSlices) {
       if (s.S > kb) break;
-      const int64_t n = tiles * s.S;
-      const int64_t reach = static_cast<int64_t>(sms * s.fill), slots = static_cast<int64_t>(sms * t.ctas * s.fill);
+      const int64_t n = tiles * s.S, reach = static_cast<int64_t>(sms * s.reach),
+                    slots = static_cast<int64_t>(sms * t.ctas * s.reach);
       const double rounds = static_cast<double>((n + slots - 1) / slots);
       const int64_t per = (n + reach - 1) / reach;
-      const double on = static_cast<double>(per < t.ctas ? per : t.ctas);   // CTAs on one SM
-      const double load = on * (128 + t.nt) * 128 / 96.5e3;
-      const double block = load > t.latency ? load : t.latency;
-      const double join = s.S > 1 ? 0.41 + on * t.nt * 512 / 29.4e3 : on * t.nt * 0.0026;
-      const double us = rounds * (0.97 + (kb + s.S - 1) / s.S * block + join);
+      const int on = static_cast<int>(per < t.ctas ? per : t.ctas);
+      const double join = s.S > 1 ? 0.585 + on * t.nt * 512 / 25.1e3 : on * t.nt * 0.0019;
+      const double us = rounds * (2.84 + (kb + s.S - 1) / s.S * t.block[on - 1] + join);
       if (us < best) {
         best = us;
         at = Pick{t.nt, s.S};
@@ -801,6 +809,7 @@ dsa_status_t linear_fp8_launch(const LinearArgs& a, cudaStream_t stream) {
     case 16: return lin::launch_split<16>(a, at.S, stream);
     case 32: return lin::launch_split<32>(a, at.S, stream);
     case 64: return lin::launch_split<64>(a, at.S, stream);
+    case 96: return lin::launch_split<96>(a, at.S, stream);
     case 128: return lin::launch_split<128>(a, at.S, stream);
     default: return lin::launch_wide(a, stream);
   }
