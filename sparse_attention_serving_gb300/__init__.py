@@ -399,14 +399,10 @@ def sparse_mla_bwd(q_lat, kv: Rows, idx, q_start, kv_len, max_kv_len: int, o_lat
 # FP8 projections around the step
 # ---------------------------------------------------------------------------
 
-def _on(t, dtype, shape, dev: int, name: str) -> int:
-    """Check an operand (type, shape, layout, device) and return its address."""
-    try:
-        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
-                and t.get_device() == dev):
-            return t.data_ptr()
-    except AttributeError:
-        raise TypeError(f"{name} must be a torch.Tensor") from None
+def _refuse(t, dtype, shape, dev: int, name: str):
+    """What is wrong with an operand, as an exception."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -416,17 +412,28 @@ def _on(t, dtype, shape, dev: int, name: str) -> int:
     raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"{name} must be on cuda:{dev}")
 
 
+def _on(t, dtype, shape, dev: int, name: str) -> int:
+    """Check an operand (type, shape, layout, device) and return its address."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, dtype, shape, dev, name)
+
+
 def _device(t, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"{name} must be on a CUDA device")
-    return t.get_device()
+    return dev
 
 
-# The current stream's handle without building a Stream object, where torch has it.
+# The current stream's handle and the current device without building objects,
+# where torch has them: a call's host time is most of a small call's time.
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream",
                        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_on(dev: int, stream) -> int:
@@ -445,15 +452,7 @@ def _empty(shape, dtype, dev: int, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _launch(fn, dev: int, *args):
-    """Call with the tensors' device as the current one."""
-    if torch.cuda.current_device() == dev:
-        code = fn(*args)
-    else:
-        with torch.cuda.device(dev):
-            code = fn(*args)
-    if code != DSA_OK:
-        raise DsaError(code, fn.__name__)
+_BF16, _U8, _F32 = torch.bfloat16, torch.uint8, torch.float32
 
 
 def dsa_rmsnorm_fp8(x, gain, residual=None, eps: float = RMS_NORM_EPS, codes=None, scale=None,
@@ -465,28 +464,33 @@ def dsa_rmsnorm_fp8(x, gain, residual=None, eps: float = RMS_NORM_EPS, codes=Non
     y = bf16(v) (None unless y is given or want_y).  residual_out and y may be x
     or residual themselves."""
     dev = _device(x, "x")
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return dsa_rmsnorm_fp8(x, gain, residual, eps, codes, scale, residual_out, y, want_y,
+                                   stream)
     raw = _stream_on(dev, stream)
     shape = x.shape
     if not shape:
         raise ValueError("x must be [..., hid]")
     hid = shape[-1]
     groups = (*shape[:-1], -(-hid // FP8_BLOCK))
-    bf = torch.bfloat16
     if codes is None:
-        codes = _empty(shape, torch.uint8, dev, stream)
+        codes = _empty(shape, _U8, dev, stream)
     if scale is None:
-        scale = _empty(groups, torch.float32, dev, stream)
+        scale = _empty(groups, _F32, dev, stream)
     if residual is not None and residual_out is None:
-        residual_out = _empty(shape, bf, dev, stream)
+        residual_out = _empty(shape, _BF16, dev, stream)
     if y is None and want_y:
-        y = _empty(shape, bf, dev, stream)
-    _launch(lib.dsa_rmsnorm_fp8, dev, _on(x, bf, shape, dev, "x"),
-            None if residual is None else _on(residual, bf, shape, dev, "residual"),
-            _on(gain, bf, (hid,), dev, "gain"), x.numel() // hid if hid else 0, hid, eps,
-            None if residual_out is None else _on(residual_out, bf, shape, dev, "residual_out"),
-            None if y is None else _on(y, bf, shape, dev, "y"),
-            _on(codes, torch.uint8, shape, dev, "codes"),
-            _on(scale, torch.float32, groups, dev, "scale"), raw)
+        y = _empty(shape, _BF16, dev, stream)
+    code = lib.dsa_rmsnorm_fp8(
+        _on(x, _BF16, shape, dev, "x"),
+        None if residual is None else _on(residual, _BF16, shape, dev, "residual"),
+        _on(gain, _BF16, (hid,), dev, "gain"), x.numel() // hid if hid else 0, hid, eps,
+        None if residual_out is None else _on(residual_out, _BF16, shape, dev, "residual_out"),
+        None if y is None else _on(y, _BF16, shape, dev, "y"),
+        _on(codes, _U8, shape, dev, "codes"), _on(scale, _F32, groups, dev, "scale"), raw)
+    if code:
+        raise DsaError(code, "dsa_rmsnorm_fp8")
     return codes, scale, residual_out, y
 
 
@@ -494,6 +498,9 @@ def dsa_quant_fp8_weight(w, codes=None, scale=None, stream=None):
     """w [N,K] bf16 (one row per output feature) -> (codes [N,K] uint8,
     scale [ceil(N/128), ceil(K/128)] float32), one scale per 128 x 128 block."""
     dev = _device(w, "w")
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return dsa_quant_fp8_weight(w, codes, scale, stream)
     raw = _stream_on(dev, stream)
     shape = w.shape
     if len(shape) != 2:
@@ -501,12 +508,14 @@ def dsa_quant_fp8_weight(w, codes=None, scale=None, stream=None):
     N, K = shape
     groups = (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK))
     if codes is None:
-        codes = _empty(shape, torch.uint8, dev, stream)
+        codes = _empty(shape, _U8, dev, stream)
     if scale is None:
-        scale = _empty(groups, torch.float32, dev, stream)
-    _launch(lib.dsa_quant_fp8_weight, dev, _on(w, torch.bfloat16, shape, dev, "w"), N, K,
-            _on(codes, torch.uint8, shape, dev, "codes"),
-            _on(scale, torch.float32, groups, dev, "scale"), raw)
+        scale = _empty(groups, _F32, dev, stream)
+    code = lib.dsa_quant_fp8_weight(_on(w, _BF16, shape, dev, "w"), N, K,
+                                    _on(codes, _U8, shape, dev, "codes"),
+                                    _on(scale, _F32, groups, dev, "scale"), raw)
+    if code:
+        raise DsaError(code, "dsa_quant_fp8_weight")
     return codes, scale
 
 
@@ -520,8 +529,10 @@ def dsa_linear_fp8(codes, scale, w_codes, w_scale, out=None, out_dtype=torch.bfl
     [ceil(N/128), ceil(K/128)] float32 (dsa_quant_fp8_weight) -> out [..., N] of
     out_dtype (bfloat16 or float32; out's own when it is given)."""
     dev = _device(codes, "codes")
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return dsa_linear_fp8(codes, scale, w_codes, w_scale, out, out_dtype, workspace, stream)
     raw = _stream_on(dev, stream)
-    u8, f32 = torch.uint8, torch.float32
     shape, w_shape = codes.shape, getattr(w_codes, "shape", ())
     if len(w_shape) != 2 or not shape or shape[-1] != w_shape[1]:
         raise ValueError("codes must be [..., K] and w_codes [N, K]")
@@ -529,19 +540,24 @@ def dsa_linear_fp8(codes, scale, w_codes, w_scale, out=None, out_dtype=torch.bfl
     M = codes.numel() // K if K else 0
     kb = -(-K // FP8_BLOCK)
     lead = shape[:-1]
+    out_shape = (*lead, N)
     if out is not None:
         out_dtype = out.dtype
-    if out_dtype not in _DTYPES:
+    out_type = _DTYPES.get(out_dtype)
+    if out_type is None:
         raise TypeError(f"out must be bfloat16 or float32, got {out_dtype}")
     if out is None:
-        out = _empty((*lead, N), out_dtype, dev, stream)
+        out = _empty(out_shape, out_dtype, dev, stream)
     if workspace is None:
         need = workspace_bytes(OP_LINEAR_FP8, M, 1, K, N, 0)
-        workspace = _empty((need,), u8, dev, stream)
-        _launch(lib.dsa_workspace_init, dev, workspace.data_ptr(), need, raw)
-    _launch(lib.dsa_linear_fp8, dev, _on(codes, u8, shape, dev, "codes"),
-            _on(scale, f32, (*lead, kb), dev, "scale"), _on(w_codes, u8, w_shape, dev, "w_codes"),
-            _on(w_scale, f32, (-(-N // FP8_BLOCK), kb), dev, "w_scale"), M, N, K,
-            _on(out, out_dtype, (*lead, N), dev, "out"), _DTYPES[out_dtype],
-            _on(workspace, u8, workspace.shape, dev, "workspace"), workspace.numel(), raw)
+        workspace = _empty((need,), _U8, dev, stream)
+        _check(lib.dsa_workspace_init(workspace.data_ptr(), need, raw), "dsa_workspace_init")
+    code = lib.dsa_linear_fp8(
+        _on(codes, _U8, shape, dev, "codes"), _on(scale, _F32, (*lead, kb), dev, "scale"),
+        _on(w_codes, _U8, w_shape, dev, "w_codes"),
+        _on(w_scale, _F32, (-(-N // FP8_BLOCK), kb), dev, "w_scale"), M, N, K,
+        _on(out, out_dtype, out_shape, dev, "out"), out_type,
+        _on(workspace, _U8, workspace.shape, dev, "workspace"), workspace.numel(), raw)
+    if code:
+        raise DsaError(code, "dsa_linear_fp8")
     return out

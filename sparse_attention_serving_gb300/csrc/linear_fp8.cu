@@ -787,9 +787,8 @@ Pick pick(int M, int N, int kb, int sms) {
       if (s.S > kb) break;
       const int64_t n = tiles * s.S, reach = static_cast<int64_t>(sms * s.reach),
                     slots = static_cast<int64_t>(sms * t.ctas * s.reach);
-      const double rounds = static_cast<double>((n + slots - 1) / slots);
-      const int64_t per = (n + reach - 1) / reach;
-      const int on = static_cast<int>(per < t.ctas ? per : t.ctas);
+      const double rounds = n <= slots ? 1.0 : static_cast<double>((n + slots - 1) / slots);
+      const int on = n <= reach ? 1 : n <= 2 * reach ? (t.ctas < 2 ? 1 : 2) : t.ctas;
       const double join = s.S > 1 ? 0.585 + on * t.nt * 512 / 25.1e3 : on * t.nt * 0.0019;
       const double us = rounds * (2.84 + (kb + s.S - 1) / s.S * t.block[on - 1] + join);
       if (us < best) {
