@@ -401,11 +401,11 @@ struct Wide {
   static constexpr int BOX = 32 * 128;                   // 32 tokens x 128 bytes of out
   static constexpr int OFF_OUT = NST * STAGE;            // two boxes per epilogue warp
   static constexpr int OFF_MISC = OFF_OUT + EW * 2 * BOX;
-  static constexpr int CH = 8;                           // blocks of K per set of factors
+  static constexpr int CH = 16;                          // blocks of K per set of factors
   static constexpr int FROW = 132;                       // 128 tokens, 2 weight blocks, padding
   static constexpr int FSET = CH * FROW;
   static constexpr int OFF_FACT = OFF_MISC + 256;
-  static constexpr int NF = 3;                           // sets of factors
+  static constexpr int NF = 2;                           // sets of factors
   static constexpr int SMEM = 1024 + OFF_FACT + NF * FSET * 4;
   static constexpr int GROUP = 8;                        // token tiles that share a weight sweep
 };
@@ -567,8 +567,10 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
         mbar_wait(&done[st], ph, p.status, kWaitLimitNs, SITE_P_DRAIN);
       }
     } else if (warp == C::EW + 2) {
-      // Factors: sets of CH blocks of K, in a ring of NF.  Eight lanes read eight
-      // neighbouring scales of a token, the warp 4 tokens a pass.
+      // Factors: sets of CH blocks of K, in a ring of NF.  CH lanes read CH
+      // neighbouring scales of a token, the warp RP tokens a pass.
+      constexpr int RP = 32 / C::CH;
+      static_assert(RP >= 2, "a lane for each of the two weight blocks");
       const int fk = lane % C::CH, fr = lane / C::CH;
       int ch = 0;
       bool ok = true;
@@ -586,15 +588,15 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
           float* to = fact + fs * C::FSET + fk * C::FROW + fr;
           const bool in = b + fk < p.kb;
 #pragma unroll 1
-          for (int r0 = 0; r0 < 128; r0 += 32) {
+          for (int r0 = 0; r0 < 128; r0 += 8 * RP) {
             float v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const int r = r0 + 4 * k;
+              const int r = r0 + RP * k;
               v[k] = in && m0 + r < p.M ? __ldg(as + static_cast<int64_t>(r) * p.kb + b) : 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) to[r0 + 4 * k] = v[k];
+            for (int k = 0; k < 8; ++k) to[r0 + RP * k] = v[k];
           }
           if (fr < 2)
             to[128] = in && nb * 128 < p.N ? __ldg(p.w_scale + static_cast<int64_t>(nb) * p.kb + b + fk)
@@ -621,6 +623,7 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
       float acc[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.f;
+#pragma unroll 1
       for (int b = 0; b < p.kb; ++b) {
         if (b % C::CH == 0) {
           ok = ok && mbar_wait(&f_full[fs], fph, p.status, kWaitLimitNs, SITE_P_FACT);
@@ -628,10 +631,11 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
           if (!live) break;
         }
         const float* fb = fact + fs * C::FSET + (b % C::CH) * C::FROW;
-        const float f = fb[row] * fb[128 + half];
+        const float fa = fb[row], fw = fb[128 + half];
         ok = ok && mbar_wait(&done[st], ph, p.status, kWaitLimitNs, SITE_P_ACC);
         __syncwarp();
         tc_fence_after();
+        const float f = fa * fw;
         const uint32_t ta = taddr + bu * 256;
         uint32_t d[2][32];
         auto add = [&](int c, const uint32_t (&x)[32]) {
