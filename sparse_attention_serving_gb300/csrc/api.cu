@@ -11,6 +11,7 @@
 
 #include "dsa_status.cuh"
 #include "internal.h"
+#include "projection.h"
 
 namespace dsa {
 

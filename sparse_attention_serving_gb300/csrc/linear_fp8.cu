@@ -4,9 +4,9 @@
 //   out[m,n] = sum_b a_scale[m,b] * w_scale[n/128,b] * sum_{k in b} a[m,k] * w[n,k]
 #include <cuda_bf16.h>
 
+#include "cluster.cuh"
 #include "dsa_status.cuh"
-#include "internal.h"
-#include "sm103.cuh"
+#include "projection.h"
 
 namespace dsa {
 namespace lin {

@@ -13,9 +13,9 @@
 // and its maximum is four shuffles away.
 #include <cuda_bf16.h>
 
+#include "cluster.cuh"
 #include "dsa_status.cuh"
-#include "internal.h"
-#include "sm103.cuh"
+#include "projection.h"
 
 namespace dsa {
 namespace rms {
