@@ -356,7 +356,8 @@ dsa_status_t dsa_indexer_topk_fp8(const uint8_t* q_codes, const float* q_scale, 
  *   y_out        [n_rows, hid] BF16     may be NULL (mla_gate_apply's x)
  *   codes        [n_rows, hid] uint8
  *   scale        [n_rows, ceil(hid / 128)] FP32
- * The norm takes the unrounded sum h.  A row is read whole before any of it is
+ * The norm takes the unrounded sum h.  Its sum of squares is FP32: a row whose
+ * sum overflows (values beyond about 1e19) gives y = 0.  A row is read whole before any of it is
  * written: residual_out and y_out may each be x or residual itself (the same
  * pointer); apart from that no output may overlap an input or another output.
  * Supported: hid a multiple of 16, 16 <= hid <= 65536; n_rows >= 0 (0: nothing
@@ -390,7 +391,8 @@ dsa_status_t dsa_quant_fp8_weight(const uint16_t* w, int N, int K, uint8_t* code
  * The sum's order depends on the sizes alone: equal calls give equal bits.
  * Supported: M >= 0 (0: nothing to do, no pointer is looked at), N >= 1, K a
  * multiple of 16, M, N, K < 2^30, M * N < 2^40.  Codes and out 16-byte aligned, scales 4.
- * out may overlap no input.  Workspace: dsa_workspace_bytes(DSA_OP_LINEAR_FP8,
+ * out may overlap no input; after DSA_ERR_DEVICE_TIMEOUT it is unspecified.
+ * Workspace: dsa_workspace_bytes(DSA_OP_LINEAR_FP8,
  * M, 1, K, N, 0).
  */
 dsa_status_t dsa_linear_fp8(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,

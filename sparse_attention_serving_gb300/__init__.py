@@ -532,8 +532,11 @@ def dsa_linear_fp8(codes, scale, w_codes, w_scale, out=None, out_dtype=torch.bfl
     if _current_device() != dev:
         with torch.cuda.device(dev):
             return dsa_linear_fp8(codes, scale, w_codes, w_scale, out, out_dtype, workspace, stream)
+    for t, name in ((w_codes, "w_codes"), (out, "out"), (workspace, "workspace")):
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
     raw = _stream_on(dev, stream)
-    shape, w_shape = codes.shape, getattr(w_codes, "shape", ())
+    shape, w_shape = codes.shape, w_codes.shape
     if len(w_shape) != 2 or not shape or shape[-1] != w_shape[1]:
         raise ValueError("codes must be [..., K] and w_codes [N, K]")
     N, K = w_shape

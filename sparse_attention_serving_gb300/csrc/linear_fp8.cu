@@ -788,7 +788,8 @@ Pick pick(int M, int N, int kb, int sms) {
   for (const auto& t : kTile) {
     const int64_t tiles = static_cast<int64_t>((N + 127) / 128) * ((M + t.nt - 1) / t.nt);
     for (const auto& s : kSlices) {
-      if (s.S > kb) break;
+      // (above 8 only where a GPC holds such a cluster without needing 16 free SMs)
+      if (s.S > kb || (s.S > 8 && t.ctas == 1)) break;
       const int64_t n = tiles * s.S, reach = static_cast<int64_t>(sms * s.reach),
                     slots = static_cast<int64_t>(sms * t.ctas * s.reach);
       const double rounds = n <= slots ? 1.0 : static_cast<double>((n + slots - 1) / slots);

@@ -308,6 +308,56 @@ def test_linear_on_another_stream_and_without_a_workspace(dsa):
         assert torch.equal(a, b)
 
 
+def test_calls_in_a_row_see_each_other(dsa):
+    """Kernels on one stream may start while the one before finishes: what a call
+    reads is the call's before, and what it overwrites has been read."""
+    M, hid, N = 96, 1040, 1040
+    gain = (1 + 0.1 * torch.randn(hid, generator=_gen(5), device="cuda")).to(torch.bfloat16)
+    weights = [dsa.dsa_quant_fp8_weight(_rows(40 + k, N, hid, 0.03)) for k in range(2)]
+    w_bf = [_rows(40 + k, N, hid, 0.03) for k in range(2)]
+    ws = dsa.new_workspace(256)
+
+    def run(sync):
+        x, h = _rows(50, M, hid), _rows(51, M, hid)
+        codes = torch.empty((M, hid), dtype=torch.uint8, device="cuda")
+        scale = torch.empty((M, 9), device="cuda")
+        wc, wsc = torch.empty_like(weights[0][0]), torch.empty_like(weights[0][1])
+        seen = []
+        for k in range(40):
+            wait = torch.cuda.synchronize if sync else (lambda: None)
+            dsa.dsa_rmsnorm_fp8(x, gain, residual=h, codes=codes, scale=scale, residual_out=h, y=x)
+            wait()
+            dsa.dsa_quant_fp8_weight(w_bf[k % 2], codes=wc, scale=wsc)
+            wait()
+            dsa.dsa_linear_fp8(codes, scale, wc, wsc, out=x, workspace=ws)
+            wait()
+            if k % 8 == 7:
+                seen.append((x.clone(), h.clone(), codes.clone(), scale.clone()))
+        torch.cuda.synchronize()
+        return seen
+
+    for a, b in zip(run(True), run(False)):
+        for s, t in zip(a, b):
+            assert torch.equal(s, t)
+
+
+def test_two_streams_at_once(dsa):
+    cases = [_operands(dsa, 60, 2500, 2304, 1040), _operands(dsa, 61, 24, 1024, 7168),
+             _operands(dsa, 62, 700, 576, 2064)]
+    want = [dsa.dsa_linear_fp8(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [dsa.new_workspace(256) for _ in cases]
+    outs = [[torch.empty_like(w) for _ in range(10)] for w in want]
+    torch.cuda.synchronize()
+    for k in range(10):
+        for c, s, ws, o in zip(cases, streams, spaces, outs):
+            dsa.dsa_linear_fp8(*c, out=o[k], workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for w, o, ws in zip(want, outs, spaces):
+        assert all(torch.equal(w, t) for t in o)
+        assert dsa.read_device_status(ws)[0] == dsa.DSA_OK
+
+
 def test_binding_refusals_on_device(dsa):
     codes, scale, w_codes, w_scale = _operands(dsa, 8, 6, 200, 256)
     lin = dsa.dsa_linear_fp8
@@ -330,6 +380,12 @@ def test_binding_refusals_on_device(dsa):
             w_codes, w_scale)
     with pytest.raises(dsa.DsaError):
         lin(codes, scale, w_codes.cpu(), w_scale)
+    with pytest.raises(TypeError):
+        lin(codes, scale, [1], w_scale)
+    with pytest.raises(TypeError):
+        lin(codes, scale, w_codes, w_scale, workspace=256)
+    with pytest.raises(dsa.DsaError):                          # a workspace without its header
+        lin(codes, scale, w_codes, w_scale, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     x = torch.zeros((4, 256), dtype=torch.bfloat16, device="cuda")
     gain = torch.ones(256, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):
