@@ -482,13 +482,30 @@ def dsa_rmsnorm_fp8(x, gain, residual=None, eps: float = RMS_NORM_EPS, codes=Non
         residual_out = _empty(shape, _BF16, dev, stream)
     if y is None and want_y:
         y = _empty(shape, _BF16, dev, stream)
+    try:
+        good = (x.dtype is _BF16 and gain.dtype is _BF16 and codes.dtype is _U8
+                and scale.dtype is _F32 and gain.shape == (hid,) and codes.shape == shape
+                and scale.shape == groups and x.is_contiguous() and gain.is_contiguous()
+                and codes.is_contiguous() and scale.is_contiguous()
+                and dev == gain.get_device() == codes.get_device() == scale.get_device())
+        for t in (residual, residual_out, y):
+            if t is not None:
+                good = (good and t.dtype is _BF16 and t.shape == shape and t.is_contiguous()
+                        and t.get_device() == dev)
+    except AttributeError:
+        good = False
+    if not good:
+        for t, dtype, sh, name in ((x, _BF16, shape, "x"), (gain, _BF16, (hid,), "gain"),
+                                   (residual, _BF16, shape, "residual"), (y, _BF16, shape, "y"),
+                                   (residual_out, _BF16, shape, "residual_out"),
+                                   (codes, _U8, shape, "codes"), (scale, _F32, groups, "scale")):
+            if t is not None:
+                _on(t, dtype, sh, dev, name)
     code = lib.dsa_rmsnorm_fp8(
-        _on(x, _BF16, shape, dev, "x"),
-        None if residual is None else _on(residual, _BF16, shape, dev, "residual"),
-        _on(gain, _BF16, (hid,), dev, "gain"), x.numel() // hid if hid else 0, hid, eps,
-        None if residual_out is None else _on(residual_out, _BF16, shape, dev, "residual_out"),
-        None if y is None else _on(y, _BF16, shape, dev, "y"),
-        _on(codes, _U8, shape, dev, "codes"), _on(scale, _F32, groups, dev, "scale"), raw)
+        x.data_ptr(), None if residual is None else residual.data_ptr(), gain.data_ptr(),
+        x.numel() // hid if hid else 0, hid, eps,
+        None if residual_out is None else residual_out.data_ptr(),
+        None if y is None else y.data_ptr(), codes.data_ptr(), scale.data_ptr(), raw)
     if code:
         raise DsaError(code, "dsa_rmsnorm_fp8")
     return codes, scale, residual_out, y
@@ -532,10 +549,9 @@ def dsa_linear_fp8(codes, scale, w_codes, w_scale, out=None, out_dtype=torch.bfl
     if _current_device() != dev:
         with torch.cuda.device(dev):
             return dsa_linear_fp8(codes, scale, w_codes, w_scale, out, out_dtype, workspace, stream)
-    for t, name in ((w_codes, "w_codes"), (out, "out"), (workspace, "workspace")):
-        if t is not None and not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
     raw = _stream_on(dev, stream)
+    if not isinstance(w_codes, torch.Tensor):
+        raise TypeError("w_codes must be a torch.Tensor")
     shape, w_shape = codes.shape, w_codes.shape
     if len(w_shape) != 2 or not shape or shape[-1] != w_shape[1]:
         raise ValueError("codes must be [..., K] and w_codes [N, K]")
@@ -544,23 +560,37 @@ def dsa_linear_fp8(codes, scale, w_codes, w_scale, out=None, out_dtype=torch.bfl
     kb = -(-K // FP8_BLOCK)
     lead = shape[:-1]
     out_shape = (*lead, N)
-    if out is not None:
-        out_dtype = out.dtype
-    out_type = _DTYPES.get(out_dtype)
-    if out_type is None:
-        raise TypeError(f"out must be bfloat16 or float32, got {out_dtype}")
+    w_groups = (-(-N // FP8_BLOCK), kb)
     if out is None:
+        if out_dtype not in _DTYPES:
+            raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
         out = _empty(out_shape, out_dtype, dev, stream)
     if workspace is None:
         need = workspace_bytes(OP_LINEAR_FP8, M, 1, K, N, 0)
         workspace = _empty((need,), _U8, dev, stream)
         _check(lib.dsa_workspace_init(workspace.data_ptr(), need, raw), "dsa_workspace_init")
-    code = lib.dsa_linear_fp8(
-        _on(codes, _U8, shape, dev, "codes"), _on(scale, _F32, (*lead, kb), dev, "scale"),
-        _on(w_codes, _U8, w_shape, dev, "w_codes"),
-        _on(w_scale, _F32, (-(-N // FP8_BLOCK), kb), dev, "w_scale"), M, N, K,
-        _on(out, out_dtype, out_shape, dev, "out"), out_type,
-        _on(workspace, _U8, workspace.shape, dev, "workspace"), workspace.numel(), raw)
+    try:
+        good = (codes.dtype is _U8 and w_codes.dtype is _U8 and scale.dtype is _F32
+                and w_scale.dtype is _F32 and out.dtype in _DTYPES and workspace.dtype is _U8
+                and scale.shape == (*lead, kb) and w_scale.shape == w_groups
+                and out.shape == out_shape and codes.is_contiguous() and w_codes.is_contiguous()
+                and scale.is_contiguous() and w_scale.is_contiguous() and out.is_contiguous()
+                and workspace.is_contiguous()
+                and dev == w_codes.get_device() == scale.get_device() == w_scale.get_device()
+                == out.get_device() == workspace.get_device())
+    except AttributeError:
+        good = False
+    if not good:
+        for t, dtype, sh, name in ((codes, _U8, shape, "codes"), (scale, _F32, (*lead, kb), "scale"),
+                                   (w_codes, _U8, w_shape, "w_codes"),
+                                   (w_scale, _F32, w_groups, "w_scale"),
+                                   (out, getattr(out, "dtype", None), out_shape, "out"),
+                                   (workspace, _U8, getattr(workspace, "shape", None), "workspace")):
+            _on(t, dtype, sh, dev, name)
+        raise TypeError(f"out must be bfloat16 or float32, got {out.dtype}")
+    code = lib.dsa_linear_fp8(codes.data_ptr(), scale.data_ptr(), w_codes.data_ptr(),
+                              w_scale.data_ptr(), M, N, K, out.data_ptr(), _DTYPES[out.dtype],
+                              workspace.data_ptr(), workspace.numel(), raw)
     if code:
         raise DsaError(code, "dsa_linear_fp8")
     return out
