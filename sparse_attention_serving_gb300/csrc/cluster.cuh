@@ -22,12 +22,18 @@ template <int N>
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
+// Until all of them have been written.
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
 
 // ---------------------------------------------------------------------------
 // programmatic dependent launch: a kernel launched with launch_overlapped() may
 // start while the kernel before it on the stream is finishing.  Nothing that it
 // reads or writes in global memory may be touched before pdl_wait(), which
-// returns once that kernel is complete and its writes are visible.
+// returns once that kernel is complete and its writes are visible.  Its loads are
+// plain ones: read-only loads want memory that nothing writes while the kernel
+// lives, and it may live while the kernel before it still writes.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The kernel after this one may be started once every CTA has come here.

