@@ -638,51 +638,52 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.f;
 #pragma unroll 1
-      for (int b = 0; b < p.kb; ++b) {
-        if (b % C::CH == 0) {
-          ok = ok && mbar_wait(&f_full[fs], fph, p.status, kWaitLimitNs, SITE_P_FACT);
-          live = ok = __all_sync(0xffffffffu, ok);
-          if (!live) break;
-        }
-        const float* fb = fact + fs * C::FSET + (b % C::CH) * C::FROW;
-        const float fa = fb[row], fw = fb[128 + half];
-        ok = ok && mbar_wait(&done[st], ph, p.status, kWaitLimitNs, SITE_P_ACC);
-        __syncwarp();
-        tc_fence_after();
-        const float f = fa * fw;
-        const uint32_t ta = taddr + bu * 256;
-        uint32_t d[2][32];
-        auto add = [&](int c, const uint32_t (&x)[32]) {
+      for (int b = 0; b < p.kb; b += C::CH) {
+        ok = ok && mbar_wait(&f_full[fs], fph, p.status, kWaitLimitNs, SITE_P_FACT);
+        live = ok = __all_sync(0xffffffffu, ok);
+        if (!live) break;
+        const float* fb = fact + fs * C::FSET;
+        const float* const fe = fb + min(C::CH, p.kb - b) * C::FROW;
+#pragma unroll 1
+        do {
+          const float fa = fb[row], fw = fb[128 + half];
+          ok = ok && mbar_wait(&done[st], ph, p.status, kWaitLimitNs, SITE_P_ACC);
+          __syncwarp();
+          tc_fence_after();
+          const float f = fa * fw;
+          const uint32_t ta = taddr + bu * 256;
+          uint32_t d[2][32];
+          auto add = [&](int c, const uint32_t (&x)[32]) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            fma2_rn(acc[c + e], acc[c + e + 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f, f);
-        };
-        tmem_ld32(ta, d[0]);
-        tmem_ld32(ta + 32, d[1]);
-        tmem_ld_wait_regs(d[0]);
-        tmem_ld_wait_regs(d[1]);
-        add(0, d[0]);
-        tmem_ld32(ta + 64, d[0]);
-        add(32, d[1]);
-        tmem_ld32(ta + 96, d[1]);
-        tmem_ld_wait_regs(d[0]);
-        tmem_ld_wait_regs(d[1]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (rank == 0)
-            mbar_arrive(&acc_free[bu]);
-          else
-            mbar_arrive_cluster_relaxed(free0 + bu * 8);
-        }
-        add(64, d[0]);
-        add(96, d[1]);
-        bu ^= 1;
-        if (++st == C::NST) st = 0, ph ^= 1;
-        if (b % C::CH == C::CH - 1 || b == p.kb - 1) {
-          if (lane == 0) mbar_arrive(&f_free[fs]);   // (every lane's f was read before its sums)
-          if (++fs == C::NF) fs = 0, fph ^= 1;
-        }
+            for (int e = 0; e < 32; e += 2)
+              fma2_rn(acc[c + e], acc[c + e + 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f, f);
+          };
+          tmem_ld32(ta, d[0]);
+          tmem_ld32(ta + 32, d[1]);
+          tmem_ld_wait_regs(d[0]);
+          tmem_ld_wait_regs(d[1]);
+          add(0, d[0]);
+          tmem_ld32(ta + 64, d[0]);
+          add(32, d[1]);
+          tmem_ld32(ta + 96, d[1]);
+          tmem_ld_wait_regs(d[0]);
+          tmem_ld_wait_regs(d[1]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (rank == 0)
+              mbar_arrive(&acc_free[bu]);
+            else
+              mbar_arrive_cluster_relaxed(free0 + bu * 8);
+          }
+          add(64, d[0]);
+          add(96, d[1]);
+          bu ^= 1;
+          if (++st == C::NST) st = 0, ph ^= 1;
+          fb += C::FROW;
+        } while (fb != fe);
+        mbar_arrive_warp(&f_free[fs]);
+        if (++fs == C::NF) fs = 0, fph ^= 1;
       }
       int mt, nt;
       wide_tile(tile, ntm, ntn, mt, nt);
