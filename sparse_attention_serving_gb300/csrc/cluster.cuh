@@ -28,6 +28,19 @@ __device__ __forceinline__ void bulk_wait_all() {
 }
 
 // ---------------------------------------------------------------------------
+// TMEM loads: tmem_ld_wait_regs for 16 columns
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_ld_wait_regs(uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+        "+r"(r[14]), "+r"(r[15])
+      :
+      : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // programmatic dependent launch: a kernel launched with launch_overlapped() may
 // start while the kernel before it on the stream is finishing.  Nothing that it
 // reads or writes in global memory may be touched before pdl_wait(), which

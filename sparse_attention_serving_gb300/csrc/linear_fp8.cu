@@ -263,49 +263,51 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
       }
     };
     fetch(0);
+    int bu = 0;
+    uint32_t ph = 0;
     bool ok = true;
-    for (int i = 0; i < nkb; ++i) {
-      const int bu = i % C::NB;
-      const float* fb = fact + ((i / C::CH) & 1) * (C::CH * C::FROW);
-      if (i % C::CH == 0) {
+#pragma unroll 1
+    for (int i = 0; i < nkb; i += C::CH) {
+      float* set = fact + ((i / C::CH) & 1) * (C::CH * C::FROW);
 #pragma unroll
-        for (int k = 0; k < PER; ++k)
-          fact[((i / C::CH) & 1) * (C::CH * C::FROW) + fk * C::FROW + (et + k * T) / C::CH] = fa[k] * fw;
-        fetch(i + C::CH);
-        // all epilogue warps leave together if one of them gave up
-        if (named_bar_or(1, T, !ok)) {
-          ok = false;
-          break;
-        }
+      for (int k = 0; k < PER; ++k) set[fk * C::FROW + (et + k * T) / C::CH] = fa[k] * fw;
+      fetch(i + C::CH);
+      // all epilogue warps leave together if one of them gave up
+      if (named_bar_or(1, T, !ok)) {
+        ok = false;
+        break;
       }
-      fb += (i % C::CH) * C::FROW + c0;
-      if (!ok) continue;
-      ok = !__any_sync(0xffffffffu, !mbar_wait(&acc_full[bu], (i / C::NB) & 1, p.status, kWaitLimitNs,
-                                               SITE_S_ACC));
-      if (!ok) continue;
-      tc_fence_after();
+      const float* fb = set + c0;
+      const float* const fe = fb + min(C::CH, nkb - i) * C::FROW;
+#pragma unroll 1
+      for (; ok && fb != fe; fb += C::FROW) {
+        ok = !__any_sync(0xffffffffu, !mbar_wait(&acc_full[bu], ph, p.status, kWaitLimitNs, SITE_S_ACC));
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < C::COLS; c += C::STEP) {
-        uint32_t d[C::STEP];
-        if constexpr (C::STEP == 16)
-          tmem_ld16(taddr + bu * NT + c, d);
-        else
-          tmem_ld32(taddr + bu * NT + c, d);
-        float4 f[C::STEP / 4];                             // on their way beside the load
+        for (int c = 0; c < C::COLS; c += C::STEP) {
+          uint32_t d[C::STEP];
+          if constexpr (C::STEP == 16)
+            tmem_ld16(taddr + bu * NT + c, d);
+          else
+            tmem_ld32(taddr + bu * NT + c, d);
+          float4 f[C::STEP / 4];                           // on their way beside the load
 #pragma unroll
-        for (int e = 0; e < C::STEP / 4; ++e) f[e] = reinterpret_cast<const float4*>(fb + c)[e];
-        tmem_ld_wait();
-        if (c + C::STEP == C::COLS) {
-          tc_fence_before();
-          mbar_arrive_warp(&acc_free[bu]);
+          for (int e = 0; e < C::STEP / 4; ++e) f[e] = reinterpret_cast<const float4*>(fb + c)[e];
+          tmem_ld_wait_regs(d);
+          if (c + C::STEP == C::COLS) {
+            tc_fence_before();
+            mbar_arrive_warp(&acc_free[bu]);
+          }
+#pragma unroll
+          for (int e = 0; e < C::STEP; e += 4) {
+            const float4 g = f[e / 4];
+            fma2_rn(acc[c + e], acc[c + e + 1], __uint_as_float(d[e]), __uint_as_float(d[e + 1]), g.x, g.y);
+            fma2_rn(acc[c + e + 2], acc[c + e + 3], __uint_as_float(d[e + 2]),
+                    __uint_as_float(d[e + 3]), g.z, g.w);
+          }
         }
-#pragma unroll
-        for (int e = 0; e < C::STEP; e += 4) {
-          const float4 g = f[e / 4];
-          fma2_rn(acc[c + e], acc[c + e + 1], __uint_as_float(d[e]), __uint_as_float(d[e + 1]), g.x, g.y);
-          fma2_rn(acc[c + e + 2], acc[c + e + 3], __uint_as_float(d[e + 2]),
-                  __uint_as_float(d[e + 3]), g.z, g.w);
-        }
+        if (++bu == C::NB) bu = 0, ph ^= 1;
       }
     }
     if (!ok) s_abort[0] = 1;
