@@ -128,7 +128,7 @@ enum : uint32_t { SITE_S_E = 0x700, SITE_S_F = 0x701, SITE_S_ACC = 0x702, SITE_S
 
 template <int NT>
 struct Split {
-  static constexpr int EW = NT > 64 ? 8 : 4;             // epilogue warps
+  static constexpr int EW = NT == 96 ? 12 : NT > 64 ? 8 : 4;    // epilogue warps
   static constexpr int COLS = NT / (EW / 4);             // tokens per epilogue thread
   static constexpr int NTHREADS = 64 + EW * 32;
   static constexpr int STAGE = (128 + NT) * 128;
@@ -436,22 +436,6 @@ __device__ __forceinline__ void wide_tile(int tile, int ntm, int ntn, int& mt, i
   mt = g * Wide::GROUP + rem - nt * gm;
 }
 
-// 32 consecutive features n .. n+31 (n a multiple of 32) of token m.
-__device__ __forceinline__ void store_out32(const Params& p, int m, int n, const float* v) {
-#pragma unroll
-  for (int k = 0; k < 32; k += 8) {
-    if (!p.fp32 && (p.N & 7) == 0) {
-      if (n + k < p.N)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(m) * p.N + n + k) =
-            make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
-                       pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
-    } else {
-      store_out4(p, m, n + k, make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]));
-      store_out4(p, m, n + k + 4, make_float4(v[k + 4], v[k + 5], v[k + 6], v[k + 7]));
-    }
-  }
-}
-
 // A lane's row of a 128-byte-swizzled box.
 __device__ __forceinline__ void put_box_f32(uint8_t* box, int lane, const float* v) {
 #pragma unroll
@@ -467,9 +451,35 @@ __device__ __forceinline__ void put_box_bf16(uint8_t* box, int lane, const float
                    pack_bf16x2(v[8 * u + 4], v[8 * u + 5]), pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
 }
 
+// The box's 32 rows to tokens m0 .. of out, features n .. (128 bytes of them), one
+// row at a time: 4 bytes a lane, or 2 where rows start on 2-byte boundaries.
+__device__ __forceinline__ void store_rows(const Params& p, const uint8_t* box, int m0, int n, int lane) {
+  const int rows = min(32, p.M - m0);
+  const int size = p.fp32 ? 4 : 2, width = min(128, (p.N - n) * size);   // bytes of a row that exist
+  uint8_t* out = static_cast<uint8_t*>(p.out) + (static_cast<int64_t>(m0) * p.N + n) * size;
+  const int64_t pitch = static_cast<int64_t>(p.N) * size;
+  if (pitch % 4 == 0) {
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r)
+      if (lane * 4 < width)
+        *reinterpret_cast<uint32_t*>(out + r * pitch + lane * 4) =
+            *reinterpret_cast<const uint32_t*>(box + sw128_unit(r, lane >> 2) + (lane & 3) * 4);
+  } else {
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r)
+#pragma unroll
+      for (int c = lane * 2; c < 128; c += 64)
+        if (c < width)
+          *reinterpret_cast<uint16_t*>(out + r * pitch + c) =
+              *reinterpret_cast<const uint16_t*>(box + sw128_unit(r, c >> 4) + (c & 15));
+  }
+}
+
+// TMA: rows of out start on 16-byte boundaries, so that TMA can store it.
+template <bool TMA>
 __global__ void __launch_bounds__(Wide::NTHREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
-                const __grid_constant__ CUtensorMap tm_out, const bool by_tma, const Params p) {
+                const __grid_constant__ CUtensorMap tm_out, const Params p) {
   using C = Wide;
   constexpr uint32_t IDESC = idesc_e4m3(256, 256);
   extern __shared__ uint8_t smem_raw[];
@@ -492,7 +502,7 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
     for (int k = 0; k < 2 * C::NST; ++k) mbar_init(&full[k], 1);
     for (int k = 0; k < 2; ++k) mbar_init(&acc_free[k], 2 * C::EW);
     for (int k = 0; k < C::NF; ++k) {
-      mbar_init(&f_full[k], 1);
+      mbar_init(&f_full[k], 2);                                      // the two staging warps
       mbar_init(&f_free[k], C::EW);
     }
     s_abort[0] = 0;
@@ -516,7 +526,7 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
       if (elect_one_lane()) {
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_w);
-        tma_prefetch_desc(&tm_out);
+        if (TMA) tma_prefetch_desc(&tm_out);
       }
       __syncwarp();
       int st = 0, i = 0;
@@ -583,12 +593,14 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
         if (--st < 0) st = C::NST - 1, ph ^= 1;
         mbar_wait(&done[st], ph, p.status, kWaitLimitNs, SITE_P_DRAIN);
       }
-    } else if (warp == C::EW + 2) {
-      // Factors: sets of CH blocks of K, in a ring of NF.  CH lanes read CH
-      // neighbouring scales of a token, the warp RP tokens a pass.
+    } else if (warp >= C::EW + 2) {
+      // Factors: sets of CH blocks of K, in a ring of NF; each of two warps stages
+      // 64 tokens.  CH lanes read CH neighbouring scales of a token, the warp RP
+      // tokens a load, 16 loads in flight (a set's latency is what a tile of few
+      // blocks waits for).
       constexpr int RP = 32 / C::CH;
       static_assert(RP >= 2, "a lane for each of the two weight blocks");
-      const int fk = lane % C::CH, fr = lane / C::CH;
+      const int fk = lane % C::CH, fr = lane / C::CH, first = (warp - (C::EW + 2)) * 64;
       int ch = 0;
       bool ok = true;
       for (int tile = blockIdx.x >> 1; ok && tile < ntiles; tile += step) {
@@ -605,17 +617,17 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
           float* to = fact + fs * C::FSET + fk * C::FROW + fr;
           const bool in = b + fk < p.kb;
 #pragma unroll 1
-          for (int r0 = 0; r0 < 128; r0 += 8 * RP) {
-            float v[8];
+          for (int r0 = first; r0 < first + 64; r0 += 16 * RP) {
+            float v[16];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 16; ++k) {
               const int r = r0 + RP * k;
               v[k] = in && m0 + r < p.M ? as[static_cast<int64_t>(r) * p.kb + b] : 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) to[r0 + RP * k] = v[k];
+            for (int k = 0; k < 16; ++k) to[r0 + RP * k] = v[k];
           }
-          if (fr < 2)
+          if (first == 0 && fr < 2)
             to[128] = in && nb * 128 < p.N ? p.w_scale[static_cast<int64_t>(nb) * p.kb + b + fk] : 0.f;
           mbar_arrive_warp(&f_full[fs]);
         }
@@ -690,14 +702,16 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
       int mt, nt;
       wide_tile(tile, ntm, ntn, mt, nt);
       const int m = mt * 256 + rank * 128 + row, n = nt * 256 + half * 128;
-      if (live && by_tma) {
+      if (live) {
         // A box of 128 bytes of 32 tokens at a time through this warp's shared
-        // memory.  Stored straight from the registers, 16 bytes of 32 different
-        // rows at a time, a tile's output took about 7,000 cycles.
+        // memory and out by TMA, or, where rows of out do not start on 16-byte
+        // boundaries, row by row.  Stored straight from the registers, 16 bytes
+        // of 32 different rows at a time, a tile's output took 7,000 cycles.
         const int m0 = m - lane, per = p.fp32 ? 32 : 64;     // features per box
         for (int q = 0; q < 128 / per; ++q) {
           uint8_t* box = sm + C::OFF_OUT + (warp * 2 + (q & 1)) * C::BOX;
-          if (lane == 0) bulk_wait_read<1>();                // the box's last store has read it
+          const int nq = n + q * per;
+          if (TMA && lane == 0) bulk_wait_read<1>();         // the box's last store has read it
           __syncwarp();
           if (p.fp32) {
 #pragma unroll
@@ -708,19 +722,21 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
             for (int s = 0; s < 2; ++s)
               if (q == s) put_box_bf16(box, lane, acc + 64 * s);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (m0 < p.M && n + q * per < p.N) tma_store_2d(&tm_out, box, n + q * per, m0);
-            bulk_commit();
+          if constexpr (TMA) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (m0 < p.M && nq < p.N) tma_store_2d(&tm_out, box, nq, m0);
+              bulk_commit();
+            }
+          } else {
+            __syncwarp();
+            store_rows(p, box, m0, nq, lane);
           }
         }
-      } else if (live && ok && m < p.M) {
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) store_out32(p, m, n + c, acc + c);
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (TMA && lane == 0) bulk_wait_all();
     __syncwarp();
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) s_abort[0] = 1;
@@ -749,13 +765,13 @@ dsa_status_t launch_wide(const LinearArgs& a, cudaStream_t stream) {
                     : encode_tmap_2d(&to, a.out, a.M, N, 2 * N, 64, 32, true)))
     return DSA_ERR_CUDA;
   const Params p{a.a_scale, a.w_scale, a.M, a.N, (a.K + 127) / 128, a.out, a.fp32, a.status};
-  if (cudaFuncSetAttribute(wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
-      cudaSuccess)
+  const auto kernel = by_tma ? wide_kernel<true> : wide_kernel<false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return launch_status("cudaFuncSetAttribute");
   const int64_t tiles = static_cast<int64_t>((a.M + 255) / 256) * ((a.N + 255) / 256);
   const int64_t pairs = num_sms() / 2;
-  launch_overlapped(wide_kernel, static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)),
-                    C::NTHREADS, C::SMEM, 2, stream, ta, tw, to, by_tma, p);
+  launch_overlapped(kernel, static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), C::NTHREADS,
+                    C::SMEM, 2, stream, ta, tw, to, p);
   return launch_status("wide_kernel");
 }
 
