@@ -120,7 +120,7 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 // A few tokens are bound by the weight's bytes (1 x 7,168 x 12,288 in 15.8 us,
 // 5.6 TB/s; 64 tokens in 18.7), small products by their latencies (64 x 128 x
 // 7,168 in 3.7 us), more tokens by the way from L2 into an SM's shared memory,
-// about 59 bytes a cycle (2,048 x 576 x 7,168 in 17.4 us: (128 + 96) * 128 bytes
+// about 59 bytes a cycle (2,048 x 576 x 7,168 in 16.9 us: (128 + 96) * 128 bytes
 // a block and CTA).
 // ---------------------------------------------------------------------------
 enum : uint32_t { SITE_S_E = 0x700, SITE_S_F = 0x701, SITE_S_ACC = 0x702, SITE_S_FREE = 0x703,
@@ -400,9 +400,9 @@ dsa_status_t launch_split(const LinearArgs& a, int S, cudaStream_t stream) {
 // pair walks the tiles, and the epilogue's store of one tile overlaps the first
 // blocks of the next.
 //
-// 16,384 x 7,168 x 12,288 in 0.98 ms, 2.9 PFLOP/s; a library product of the same
+// 16,384 x 7,168 x 12,288 in 0.92 to 0.96 ms by the box, 3.0 to 3.15 PFLOP/s; a library product of the same
 // codes with one scale for the whole matrix takes 0.77 to 0.83 ms.  A block takes
-// about 830 cycles of a pair, its MMAs 512: the rest is the chain through the two
+// about 780 cycles of a pair, its MMAs 512: the rest is the chain through the two
 // TMEM buffers (all 512 columns): commit, the epilogue's 128 columns a thread, the
 // buffer's return to the issuing CTA.  A third buffer would need a narrower tile,
 // and the MMAs of one take as long per feature (128 features: 418 cycles).
@@ -788,31 +788,32 @@ namespace lin {
 
 // Which kernel, tile and number of K slices: the cheapest by an estimate of the
 // time in microseconds, whose terms were fitted to the measured time of every
-// combination at 180 sizes (1 to 4,096 tokens, 64 to 8,192 features, K 256 to
-// 12,288): the choice is on average 0.5 % slower than the fastest combination,
-// at most 9 %.  The terms: a CTA's time per block of K, by how many CTAs share
-// its SM (its bytes at an SM's share of L2 bandwidth, 59 a cycle, or the
-// epilogue's latency); a start; the join of K slices, a cluster barrier and the
-// partial tiles' way through distributed shared memory (about 13 bytes a cycle);
-// the part of the SMs that clusters of a size can fill.  Examples (us; tokens x
-// features x K): 1 x 8,192 x 7,168: 16 tokens and 4 slices 11.7, unsliced 17;
-// 64 x 128 x 7,168: 16 tokens and 16 slices 3.7, 64 tokens and 8 slices 5.5;
-// 777 x 1,001 x 1,040: 64 tokens unsliced 5.3, with 2 slices 9; 2,048 x 576 x
-// 7,168: 96 tokens 17, 128 tokens 20, pairs 28; 512 x 7,168 x 12,288: pairs 46,
-// 128 tokens 65.
+// combination at 210 sizes (1 to 4,096 tokens, 64 to 8,192 features, K 256 to
+// 12,288): the choice is on average 0.7 % slower than the fastest combination,
+// at most 17 % (0.4 us at 4 x 64 x 512).  The terms: a CTA's time per block of K,
+// by how many CTAs share its SM (its bytes at an SM's share of L2 bandwidth, 59 a
+// cycle, or the epilogue's latency); a start; the join of K slices, a cluster
+// barrier and the partial tiles' way through distributed shared memory (about 12
+// bytes a cycle); the part of the SMs that clusters of a size can fill; the wide
+// kernel's way of storing rows that TMA cannot.  Examples (us; tokens x features
+// x K): 1 x 8,192 x 7,168: 16 tokens and 4 slices 11.6, unsliced 17; 64 x 128 x
+// 7,168: 16 tokens and 16 slices 3.7, 64 tokens and 8 slices 5.5; 777 x 1,001 x
+// 1,040: 64 tokens unsliced 5.4, with 2 slices 9; 2,048 x 576 x 7,168: 96 tokens
+// 16.9, 128 tokens 20, wide 27; 512 x 7,168 x 12,288: wide 45, 128 tokens 65.
 struct Pick {
   int nt, S;   // nt = 0: the pair kernel
 };
-Pick pick(int M, int N, int kb, int sms) {
+Pick pick(int M, int N, int kb, int sms, int64_t row_bytes) {
   const int64_t pairs = sms / 2;
   const int64_t wt = static_cast<int64_t>((M + 255) / 256) * ((N + 255) / 256);
-  double best = 2.23 + static_cast<double>((wt + pairs - 1) / pairs) * (kb * 0.47 + 2.3);
+  const double rows = row_bytes % 4 != 0 ? 8.3 : row_bytes % 16 != 0 ? 1.3 : 0.0;
+  double best = 1.98 + static_cast<double>((wt + pairs - 1) / pairs) * (kb * 0.40 + 1.79 + rows);
   Pick at{0, 1};
   constexpr struct {
     int nt, ctas;      // the tile's tokens, its CTAs per SM
     double block[3];   // time per block of K with 1, 2, 3 CTAs on the SM
-  } kTile[] = {{16, 3, {0.15, 0.26, 0.34}}, {32, 2, {0.18, 0.30}}, {64, 2, {0.25, 0.37}},
-               {96, 1, {0.26}}, {128, 1, {0.31}}};
+  } kTile[] = {{16, 3, {0.152, 0.275, 0.364}}, {32, 2, {0.19, 0.293}}, {64, 2, {0.273, 0.366}},
+               {96, 1, {0.284}}, {128, 1, {0.33}}};
   constexpr struct {
     int S;
     double reach;      // the part of the SMs that clusters of S fill
@@ -827,8 +828,8 @@ Pick pick(int M, int N, int kb, int sms) {
                     slots = static_cast<int64_t>(sms * t.ctas * s.reach);
       const double rounds = n <= slots ? 1.0 : static_cast<double>((n + slots - 1) / slots);
       const int on = n <= reach ? 1 : n <= 2 * reach ? (t.ctas < 2 ? 1 : 2) : t.ctas;
-      const double join = s.S > 1 ? 0.585 + on * t.nt * 512 / 25.1e3 : on * t.nt * 0.0019;
-      const double us = rounds * (2.84 + (kb + s.S - 1) / s.S * t.block[on - 1] + join);
+      const double join = s.S > 1 ? 0.49 + on * t.nt * 512 / 21.9e3 : on * t.nt * 0.0021;
+      const double us = rounds * (3.17 + (kb + s.S - 1) / s.S * t.block[on - 1] + join);
       if (us < best) {
         best = us;
         at = Pick{t.nt, s.S};
@@ -841,7 +842,8 @@ Pick pick(int M, int N, int kb, int sms) {
 }  // namespace lin
 
 dsa_status_t linear_fp8_launch(const LinearArgs& a, cudaStream_t stream) {
-  const lin::Pick at = lin::pick(a.M, a.N, (a.K + 127) / 128, num_sms());
+  const lin::Pick at = lin::pick(a.M, a.N, (a.K + 127) / 128, num_sms(),
+                                 static_cast<int64_t>(a.N) * (a.fp32 ? 4 : 2));
   switch (at.nt) {
     case 16: return lin::launch_split<16>(a, at.S, stream);
     case 32: return lin::launch_split<32>(a, at.S, stream);
