@@ -400,8 +400,9 @@ dsa_status_t launch_split(const LinearArgs& a, int S, cudaStream_t stream) {
 // pair walks the tiles, and the epilogue's store of one tile overlaps the first
 // blocks of the next.
 //
-// 16,384 x 7,168 x 12,288 in 0.92 to 0.96 ms by the box, 3.0 to 3.15 PFLOP/s; a library product of the same
-// codes with one scale for the whole matrix takes 0.77 to 0.83 ms.  A block takes
+// 16,384 x 7,168 x 12,288 in 0.92 to 0.96 ms by the box, 3.0 to 3.15 PFLOP/s (1.04 ms
+// in a row of 600 calls, at the power cap's 1.7 GHz); a library product of the same
+// codes with one scale for the whole matrix takes 0.75 to 0.83 ms.  A block takes
 // about 780 cycles of a pair, its MMAs 512: the rest is the chain through the two
 // TMEM buffers (all 512 columns): commit, the epilogue's 128 columns a thread, the
 // buffer's return to the issuing CTA.  A third buffer would need a narrower tile,
@@ -788,7 +789,7 @@ namespace lin {
 
 // Which kernel, tile and number of K slices: the cheapest by an estimate of the
 // time in microseconds, whose terms were fitted to the measured time of every
-// combination at 210 sizes (1 to 4,096 tokens, 64 to 8,192 features, K 256 to
+// combination at 220 sizes (1 to 4,096 tokens, 64 to 8,192 features, K 256 to
 // 12,288): the choice is on average 0.7 % slower than the fastest combination,
 // at most 17 % (0.4 us at 4 x 64 x 512).  The terms: a CTA's time per block of K,
 // by how many CTAs share its SM (its bytes at an SM's share of L2 bandwidth, 59 a
