@@ -453,6 +453,12 @@ def _empty(shape, dtype, dev: int, stream):
 
 
 _BF16, _U8, _F32 = torch.bfloat16, torch.uint8, torch.float32
+_SIZES = 1 << 30   # sizes at and beyond it are refused here: the C ABI's are 32-bit
+
+
+def _too_large(call: str, **sizes):
+    got = ", ".join(f"{n} = {v}" for n, v in sizes.items())
+    raise DsaError(DSA_ERR_UNSUPPORTED, f"{call}: {got}, all below 2^30")
 
 
 def dsa_rmsnorm_fp8(x, gain, residual=None, eps: float = RMS_NORM_EPS, codes=None, scale=None,
@@ -473,6 +479,8 @@ def dsa_rmsnorm_fp8(x, gain, residual=None, eps: float = RMS_NORM_EPS, codes=Non
     if not shape:
         raise ValueError("x must be [..., hid]")
     hid = shape[-1]
+    if hid >= _SIZES:
+        _too_large("dsa_rmsnorm_fp8", hid=hid)
     groups = (*shape[:-1], -(-hid // FP8_BLOCK))
     if codes is None:
         codes = _empty(shape, _U8, dev, stream)
@@ -523,6 +531,8 @@ def dsa_quant_fp8_weight(w, codes=None, scale=None, stream=None):
     if len(shape) != 2:
         raise ValueError("w must be [N, K]")
     N, K = shape
+    if N >= _SIZES or K >= _SIZES:
+        _too_large("dsa_quant_fp8_weight", N=N, K=K)
     groups = (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK))
     if codes is None:
         codes = _empty(shape, _U8, dev, stream)
@@ -557,6 +567,8 @@ def dsa_linear_fp8(codes, scale, w_codes, w_scale, out=None, out_dtype=torch.bfl
         raise ValueError("codes must be [..., K] and w_codes [N, K]")
     N, K = w_shape
     M = codes.numel() // K if K else 0
+    if M >= _SIZES or N >= _SIZES or K >= _SIZES:
+        _too_large("dsa_linear_fp8", M=M, N=N, K=K)
     kb = -(-K // FP8_BLOCK)
     lead = shape[:-1]
     out_shape = (*lead, N)

@@ -401,6 +401,25 @@ def test_binding_refusals_on_device(dsa):
         dsa.dsa_rmsnorm_fp8(x, gain, residual_out=torch.empty_like(x))
 
 
+def test_sizes_beyond_32_bits_are_refused(dsa):
+    """A size whose low 32 bits are a supported one (2^32 + 16 as 16).  The sizes are
+    looked at first, so views of a few bytes stand for the large arrays."""
+    big = (1 << 32) + 16
+    few = lambda shape, dtype=torch.uint8: torch.zeros(  # noqa: E731
+        (1,) * len(shape), dtype=dtype, device="cuda").expand(shape)
+    calls = [lambda: dsa.dsa_rmsnorm_fp8(few((1, big), torch.bfloat16), few((big,), torch.bfloat16)),
+             lambda: dsa.dsa_quant_fp8_weight(few((1, big), torch.bfloat16)),
+             lambda: dsa.dsa_quant_fp8_weight(few((big, 16), torch.bfloat16))]
+    for m, n, k in ((1, 1, big), (big, 1, 16), (1, big, 16)):
+        calls.append(lambda m=m, n=n, k=k: dsa.dsa_linear_fp8(
+            few((m, k)), few((m, -(-k // 128)), torch.float32), few((n, k)),
+            few((-(-n // 128), -(-k // 128)), torch.float32)))
+    for call in calls:
+        with pytest.raises(dsa.DsaError) as e:
+            call()
+        assert e.value.code == dsa.DSA_ERR_UNSUPPORTED
+
+
 # ---------------------------------------------------------------------------
 # the path as a layer uses it
 # ---------------------------------------------------------------------------
