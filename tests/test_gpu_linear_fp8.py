@@ -274,6 +274,54 @@ def test_linear_no_rows_and_leading_dims(dsa):
     assert none.shape == (0, 130)
 
 
+def _repeats(t, period):
+    """Row i + period equals row i, to the last row."""
+    assert torch.equal(t[period:].view(torch.uint8), t[:-period].view(torch.uint8))
+
+
+def test_norm_and_weight_offsets_beyond_31_bits(dsa):
+    n, hid, period = 300_032, 7168, 1024                       # 2.15e9 values
+    few = _rows(5, period, hid)
+    x = few.repeat(n // period, 1)
+    gain = torch.ones(hid, dtype=torch.bfloat16, device="cuda")
+    codes, scale, h, y = dsa.dsa_rmsnorm_fp8(x, gain, residual=x, want_y=True)
+    first = dsa.dsa_rmsnorm_fp8(few, gain, residual=few, want_y=True)
+    for got, want in zip((codes, scale, h, y), first):
+        assert torch.equal(got[:period], want)
+        _repeats(got, period)
+    del h, y, codes, scale
+    codes, scale = dsa.dsa_quant_fp8_weight(x)
+    want_codes, want_scale = dsa.dsa_quant_fp8_weight(few)
+    assert torch.equal(codes[:period], want_codes) and torch.equal(scale[:period // 128], want_scale)
+    _repeats(codes, period)
+    _repeats(scale, period // 128)
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [
+    (270_001, 8192, 144, torch.bfloat16),                      # out: TMA and, with odd rows, plain
+    (270_001, 8193, 144, torch.bfloat16), (270_001, 8194, 144, torch.float32),
+    (300_001, 128, 7168, torch.float32),                       # codes
+    (3, 300_032, 7168, torch.bfloat16), (300, 300_032, 7168, torch.bfloat16)])   # weight
+def test_linear_offsets_beyond_31_bits(dsa, M, N, K, dtype):
+    period = 1024
+    m, n = min(M, period), N if N < 10_000 else period
+    codes, scale, w_codes, w_scale = _operands(dsa, 6, m, n, K)
+    ref, mag = _linear_ref(codes, scale, w_codes, w_scale)
+    if M > m:
+        i = torch.arange(M, device="cuda") % period
+        codes, scale = codes[i], scale[i]
+    if N > n:
+        w_codes, w_scale = w_codes.repeat(N // n, 1), w_scale.repeat(N // n, 1)
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_LINEAR_FP8, M, 1, K, N, 0))
+    out = dsa.dsa_linear_fp8(codes, scale, w_codes, w_scale, out_dtype=dtype, workspace=ws)
+    assert dsa.read_device_status(ws)[0] == dsa.DSA_OK
+    _check_linear(out[:m, :n], ref, mag, K, f"{M}x{N}x{K}")
+    if M > m:
+        _repeats(out, period)
+    if N > n:
+        _repeats(out.t().contiguous(), n)
+
+
 @pytest.mark.parametrize("M", [2, 40, 500])
 def test_linear_non_finite_values_stay_in_their_row_and_block(dsa, M):
     codes, scale, w_codes, w_scale = _operands(dsa, M, M, 400, 1040)
