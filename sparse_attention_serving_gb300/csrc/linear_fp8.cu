@@ -6,6 +6,7 @@
 
 #include "cluster.cuh"
 #include "dsa_status.cuh"
+#include "linear_plan.h"
 #include "projection.h"
 
 namespace dsa {
@@ -456,7 +457,7 @@ __device__ __forceinline__ void put_box_bf16(uint8_t* box, int lane, const float
 // row at a time: 4 bytes a lane, or 2 where rows start on 2-byte boundaries.
 __device__ __forceinline__ void store_rows(const Params& p, const uint8_t* box, int m0, int n, int lane) {
   const int rows = min(32, p.M - m0);
-  const int size = p.fp32 ? 4 : 2, width = min(128, (p.N - n) * size);   // bytes of a row that exist
+  const int size = p.fp32 ? 4 : 2, width = row_bytes_left(p.N, n, size, 128);
   uint8_t* out = static_cast<uint8_t*>(p.out) + (static_cast<int64_t>(m0) * p.N + n) * size;
   const int64_t pitch = static_cast<int64_t>(p.N) * size;
   if (pitch % 4 == 0) {
