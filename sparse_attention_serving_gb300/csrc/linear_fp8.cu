@@ -327,6 +327,9 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
       for (int c = 0; c < C::COLS; ++c) part[c * 128] = acc[c];
     }
   }
+  // lanes leave a wait one by one; the cluster barriers and the release of the TMEM
+  // are for whole warps
+  __syncwarp();
   tc_fence_before();
   if (S == 1) {
     __syncthreads();
@@ -358,6 +361,7 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
     }
     // no CTA leaves while another may still read its shared memory; the reads
     // are over (their values are in the stores), so nothing has to be ordered
+    __syncwarp();
     cluster_arrive_relaxed();
   }
   if (warp == 1) {

@@ -547,3 +547,20 @@ def test_layer_around_the_step(dsa):
             assert torch.equal(c[n], want[n]), n
         assert torch.isfinite(c["out"].float()).all()
     assert dsa.read_device_status(ws)[0] == dsa.DSA_OK
+
+
+# K slices of one block, of fewer blocks than the ring has stages, of as many, of many
+# more: the copying and the issuing warp then end in different waits, one lane at a
+# time, before the cluster's barriers.
+@pytest.mark.parametrize("M,N,K", [(16, 128, 2048), (5, 300, 528), (64, 128, 7168), (40, 1000, 4624),
+                                   (3, 129, 12288), (200, 512, 4096), (512, 500, 7168)])
+def test_joined_slices_many_times(dsa, M, N, K):
+    codes, scale, w_codes, w_scale = _operands(dsa, M + N + K, M, N, K)
+    ws = dsa.new_workspace(256)
+    out = [torch.empty((M, N), device="cuda") for _ in range(60)]
+    for o in out:
+        dsa.dsa_linear_fp8(codes, scale, w_codes, w_scale, out=o, workspace=ws)
+    assert dsa.read_device_status(ws)[0] == dsa.DSA_OK
+    ref, mag = _linear_ref(codes, scale, w_codes, w_scale)
+    _check_linear(out[0], ref, mag, K, f"{M}x{N}x{K}")
+    assert all(torch.equal(o, out[0]) for o in out)
