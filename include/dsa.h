@@ -454,6 +454,18 @@ dsa_status_t dsa_read_device_status(void* workspace, dsa_stream_t stream, uint32
 dsa_status_t dsa_selftest_wait_timeout(void* workspace, size_t ws_bytes, uint64_t limit_ns,
                                        dsa_stream_t stream);
 
+/*
+ * Self-test of the FP8 projection's kernels: dsa_linear_fp8 by the kernel named,
+ * whatever the sizes would have taken.  tokens 16, 32, 64, 96 or 128: 128
+ * features x that many tokens per CTA, K in `slices` (1, 2, 3, 4, 5, 6, 8, and up
+ * to 64 tokens 12 or 16; at most one slice per 128 of K); tokens 0, slices 1:
+ * 256 features x 256 tokens per pair of SMs.  Others: DSA_ERR_UNSUPPORTED.
+ */
+dsa_status_t dsa_selftest_linear_fp8(const uint8_t* a_codes, const float* a_scale,
+                                     const uint8_t* w_codes, const float* w_scale, int M, int N,
+                                     int K, void* out, dsa_dtype_t out_type, int tokens, int slices,
+                                     void* workspace, size_t ws_bytes, dsa_stream_t stream);
+
 /* Static string for a status code. */
 const char* dsa_status_string(dsa_status_t status);
 

@@ -63,7 +63,8 @@ EXPORTS = ("dsa_abi_version", "dsa_status_string", "dsa_workspace_bytes", "dsa_w
            "dsa_read_device_status", "dsa_indexer_topk", "sparse_mla_fwd", "mla_gate_apply",
            "dsa_cache_append", "sparse_mla_fwd_sink", "dsa_selftest_wait_timeout",
            "dsa_quant_fp8", "dsa_cache_append_fp8", "dsa_indexer_topk_fp8", "sparse_mla_bwd",
-           "dsa_rmsnorm_fp8", "dsa_quant_fp8_weight", "dsa_linear_fp8")
+           "dsa_rmsnorm_fp8", "dsa_quant_fp8_weight", "dsa_linear_fp8",
+           "dsa_selftest_linear_fp8")
 
 
 def _load(path: str = LIB_PATH):
@@ -98,7 +99,8 @@ def _load(path: str = LIB_PATH):
     lib.dsa_rmsnorm_fp8.argtypes = [P, P, P, ctypes.c_int64, I, ctypes.c_float, P, P, P, P, P]
     lib.dsa_quant_fp8_weight.argtypes = [P, I, I, P, P, P]
     lib.dsa_linear_fp8.argtypes = [P, P, P, P, I, I, I, P, I, P, Z, P]
-    for f in ("dsa_rmsnorm_fp8", "dsa_quant_fp8_weight", "dsa_linear_fp8",
+    lib.dsa_selftest_linear_fp8.argtypes = [P, P, P, P, I, I, I, P, I, I, I, P, Z, P]
+    for f in ("dsa_selftest_linear_fp8", "dsa_rmsnorm_fp8", "dsa_quant_fp8_weight", "dsa_linear_fp8",
               "sparse_mla_bwd", "dsa_workspace_init", "dsa_read_device_status", "dsa_indexer_topk",
               "sparse_mla_fwd", "mla_gate_apply", "dsa_cache_append", "sparse_mla_fwd_sink",
               "dsa_selftest_wait_timeout", "dsa_quant_fp8", "dsa_cache_append_fp8",

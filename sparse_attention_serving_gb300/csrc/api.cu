@@ -303,15 +303,16 @@ dsa_status_t dsa_quant_fp8_weight(const uint16_t* w, int N, int K, uint8_t* code
   return quant_fp8_weight_launch(w, N, K, codes, scale, reinterpret_cast<cudaStream_t>(stream));
 }
 
-dsa_status_t dsa_linear_fp8(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,
-                            const float* w_scale, int M, int N, int K, void* out,
-                            dsa_dtype_t out_type, void* workspace, size_t ws_bytes,
-                            dsa_stream_t stream) {
+static dsa_status_t linear_fp8(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,
+                               const float* w_scale, int M, int N, int K, void* out,
+                               dsa_dtype_t out_type, const lin::Pick* forced, void* workspace,
+                               size_t ws_bytes, dsa_stream_t stream) {
   if (M < 0 || N <= 0 || K <= 0) return DSA_ERR_INVALID_ARGUMENT;
   if (out_type != DSA_BF16 && out_type != DSA_FP32) return DSA_ERR_INVALID_ARGUMENT;
   if (K % 16 != 0 || M >= (1 << 30) || N >= (1 << 30) || K >= (1 << 30) ||
       static_cast<int64_t>(M) * N >= (int64_t(1) << 40))
     return DSA_ERR_UNSUPPORTED;
+  if (forced != nullptr && !lin::offered(*forced, M, N, (K + 127) / 128)) return DSA_ERR_UNSUPPORTED;
   if (M == 0) return DSA_OK;
   if (!a_codes || !a_scale || !w_codes || !w_scale || !out) return DSA_ERR_INVALID_ARGUMENT;
   if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(out, 16) ||
@@ -322,7 +323,24 @@ dsa_status_t dsa_linear_fp8(const uint8_t* a_codes, const float* a_scale, const 
   if (st != DSA_OK) return st;
   const LinearArgs a{a_codes, a_scale, w_codes, w_scale, M, N, K, out, out_type == DSA_FP32,
                      static_cast<uint32_t*>(workspace)};
-  return linear_fp8_launch(a, reinterpret_cast<cudaStream_t>(stream));
+  return linear_fp8_launch(a, forced, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t dsa_linear_fp8(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,
+                            const float* w_scale, int M, int N, int K, void* out,
+                            dsa_dtype_t out_type, void* workspace, size_t ws_bytes,
+                            dsa_stream_t stream) {
+  return linear_fp8(a_codes, a_scale, w_codes, w_scale, M, N, K, out, out_type, nullptr, workspace,
+                    ws_bytes, stream);
+}
+
+dsa_status_t dsa_selftest_linear_fp8(const uint8_t* a_codes, const float* a_scale,
+                                     const uint8_t* w_codes, const float* w_scale, int M, int N,
+                                     int K, void* out, dsa_dtype_t out_type, int tokens, int slices,
+                                     void* workspace, size_t ws_bytes, dsa_stream_t stream) {
+  const lin::Pick at{tokens, slices};
+  return linear_fp8(a_codes, a_scale, w_codes, w_scale, M, N, K, out, out_type, &at, workspace,
+                    ws_bytes, stream);
 }
 
 static dsa_status_t mla_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const int32_t* idx,

@@ -6,7 +6,6 @@
 
 #include "cluster.cuh"
 #include "dsa_status.cuh"
-#include "linear_plan.h"
 #include "projection.h"
 
 namespace dsa {
@@ -388,7 +387,7 @@ dsa_status_t launch_split(const LinearArgs& a, int S, cudaStream_t stream) {
                                     1) != cudaSuccess)
     return launch_status("cudaFuncSetAttribute");
   launch_overlapped(split_kernel<NT>,
-                    static_cast<unsigned>(((a.N + 127) / 128) * ((a.M + NT - 1) / NT) * S),
+                    static_cast<unsigned>(split_tiles(a.M, a.N, NT) * S),
                     C::NTHREADS, C::SMEM, static_cast<unsigned>(S), stream, ta, tw, p, S);
   return launch_status("split_kernel");
 }
@@ -790,66 +789,11 @@ dsa_status_t quant_fp8_weight_launch(const uint16_t* w, int N, int K, uint8_t* c
   return launch_status("quant_weight_kernel");
 }
 
-namespace lin {
-
-// Which kernel, tile and number of K slices: the cheapest by an estimate of the
-// time in microseconds, whose terms were fitted to the measured time of every
-// combination at 220 sizes (1 to 4,096 tokens, 64 to 8,192 features, K 256 to
-// 12,288): the choice is on average 0.7 % slower than the fastest combination,
-// at most 17 % (0.4 us at 4 x 64 x 512).  The terms: a CTA's time per block of K,
-// by how many CTAs share its SM (its bytes at an SM's share of L2 bandwidth, 59 a
-// cycle, or the epilogue's latency); a start; the join of K slices, a cluster
-// barrier and the partial tiles' way through distributed shared memory (about 12
-// bytes a cycle); the part of the SMs that clusters of a size can fill; the wide
-// kernel's way of storing rows that TMA cannot.  Examples (us; tokens x features
-// x K): 1 x 8,192 x 7,168: 16 tokens and 4 slices 11.6, unsliced 17; 64 x 128 x
-// 7,168: 16 tokens and 16 slices 3.7, 64 tokens and 8 slices 5.5; 777 x 1,001 x
-// 1,040: 64 tokens unsliced 5.4, with 2 slices 9; 2,048 x 576 x 7,168: 96 tokens
-// 16.9, 128 tokens 20, wide 27; 512 x 7,168 x 12,288: wide 45, 128 tokens 65.
-struct Pick {
-  int nt, S;   // nt = 0: the pair kernel
-};
-Pick pick(int M, int N, int kb, int sms, int64_t row_bytes) {
-  const int64_t pairs = sms / 2;
-  const int64_t wt = static_cast<int64_t>((M + 255) / 256) * ((N + 255) / 256);
-  const double rows = row_bytes % 4 != 0 ? 8.3 : row_bytes % 16 != 0 ? 1.3 : 0.0;
-  double best = 1.98 + static_cast<double>((wt + pairs - 1) / pairs) * (kb * 0.40 + 1.79 + rows);
-  Pick at{0, 1};
-  constexpr struct {
-    int nt, ctas;      // the tile's tokens, its CTAs per SM
-    double block[3];   // time per block of K with 1, 2, 3 CTAs on the SM
-  } kTile[] = {{16, 3, {0.152, 0.275, 0.364}}, {32, 2, {0.19, 0.293}}, {64, 2, {0.273, 0.366}},
-               {96, 1, {0.284}}, {128, 1, {0.33}}};
-  constexpr struct {
-    int S;
-    double reach;      // the part of the SMs that clusters of S fill
-  } kSlices[] = {{1, 1.0}, {2, 1.0}, {3, 0.91}, {4, 0.95}, {5, 0.92}, {6, 0.91}, {8, 0.79},
-                 {12, 0.7}, {16, 0.7}};
-  for (const auto& t : kTile) {
-    const int64_t tiles = static_cast<int64_t>((N + 127) / 128) * ((M + t.nt - 1) / t.nt);
-    for (const auto& s : kSlices) {
-      // (above 8 only where a GPC holds such a cluster without needing 16 free SMs)
-      if (s.S > kb || (s.S > 8 && t.ctas == 1)) break;
-      const int64_t n = tiles * s.S, reach = static_cast<int64_t>(sms * s.reach),
-                    slots = static_cast<int64_t>(sms * t.ctas * s.reach);
-      const double rounds = n <= slots ? 1.0 : static_cast<double>((n + slots - 1) / slots);
-      const int on = n <= reach ? 1 : n <= 2 * reach ? (t.ctas < 2 ? 1 : 2) : t.ctas;
-      const double join = s.S > 1 ? 0.49 + on * t.nt * 512 / 21.9e3 : on * t.nt * 0.0021;
-      const double us = rounds * (3.17 + (kb + s.S - 1) / s.S * t.block[on - 1] + join);
-      if (us < best) {
-        best = us;
-        at = Pick{t.nt, s.S};
-      }
-    }
-  }
-  return at;
-}
-
-}  // namespace lin
-
-dsa_status_t linear_fp8_launch(const LinearArgs& a, cudaStream_t stream) {
-  const lin::Pick at = lin::pick(a.M, a.N, (a.K + 127) / 128, num_sms(),
-                                 static_cast<int64_t>(a.N) * (a.fp32 ? 4 : 2));
+dsa_status_t linear_fp8_launch(const LinearArgs& a, const lin::Pick* forced, cudaStream_t stream) {
+  const lin::Pick at = forced != nullptr
+                           ? *forced
+                           : lin::pick(a.M, a.N, (a.K + 127) / 128, num_sms(),
+                                       static_cast<int64_t>(a.N) * (a.fp32 ? 4 : 2));
   switch (at.nt) {
     case 16: return lin::launch_split<16>(a, at.S, stream);
     case 32: return lin::launch_split<32>(a, at.S, stream);

@@ -3,6 +3,7 @@
 // and its kernel files.
 #pragma once
 #include "internal.h"
+#include "linear_plan.h"
 
 namespace dsa {
 
@@ -36,6 +37,7 @@ struct LinearArgs {
   bool fp32;
   uint32_t* status;
 };
-dsa_status_t linear_fp8_launch(const LinearArgs& a, cudaStream_t stream);
+// By the kernel that `forced` names, or (null) the one that lin::pick takes.
+dsa_status_t linear_fp8_launch(const LinearArgs& a, const lin::Pick* forced, cudaStream_t stream);
 
 }  // namespace dsa

@@ -78,3 +78,16 @@ def test_binding_refuses_host_tensors_and_wrong_types(dsa):
         dsa.dsa_linear_fp8(x.view(torch.uint8), torch.zeros(4, 2), x.view(torch.uint8), torch.zeros(1, 2))
     with pytest.raises(TypeError):
         dsa.dsa_rmsnorm_fp8([1.0], g)
+
+
+def test_selftest_refusals(dsa):
+    def call(tokens, slices, K=7168, M=64, a=FAKE):
+        return dsa.lib.dsa_selftest_linear_fp8(a, FAKE, FAKE, FAKE, M, 8192, K, FAKE, 0, tokens, slices,
+                                               WS, 256, None)
+
+    for at in ((0, 2), (1, 1), (16, 0), (16, 7), (16, 17), (96, 12), (128, 16), (256, 1), (-16, 1)):
+        assert call(*at) == dsa.DSA_ERR_UNSUPPORTED, at
+    assert call(64, 4, K=384) == dsa.DSA_ERR_UNSUPPORTED          # three blocks of K
+    assert call(64, 4, K=7160) == dsa.DSA_ERR_UNSUPPORTED
+    assert call(64, 4, a=None) == dsa.DSA_ERR_INVALID_ARGUMENT
+    assert call(64, 4, M=0) == dsa.DSA_OK
