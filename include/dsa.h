@@ -388,6 +388,9 @@ dsa_status_t dsa_quant_fp8_weight(const uint16_t* w, int N, int K, uint8_t* code
  *   w_codes [N, K] uint8    w_scale [ceil(N / 128), ceil(K / 128)] FP32
  *   out     [M, N]          BF16 (out_type DSA_BF16) or FP32 (DSA_FP32: raw
  *                           indexer keys for dsa_cache_append)
+ * The scales may be any FP32 numbers: where the product of two leaves FP32's range
+ * they are applied one after the other, so that a normal term stays exact to its
+ * roundings (slower, by the blocks that need it).
  * The sum's order depends on the sizes alone: equal calls give equal bits.
  * Supported: M >= 0 (0: nothing to do, no pointer is looked at), N >= 1, K a
  * multiple of 16, M, N, K < 2^30, M * N < 2^40.  Codes and out 16-byte aligned, scales 4.

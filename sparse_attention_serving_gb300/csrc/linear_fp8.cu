@@ -4,6 +4,8 @@
 //   out[m,n] = sum_b a_scale[m,b] * w_scale[n/128,b] * sum_{k in b} a[m,k] * w[n,k]
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "cluster.cuh"
 #include "dsa_status.cuh"
 #include "projection.h"
@@ -99,6 +101,55 @@ __device__ __forceinline__ void store_out4(const Params& p, int m, int n, const 
   }
 }
 
+// The factor a_scale * w_scale of a block's sum d (0 or 2^-18 to 2^25 in magnitude).
+// The scales are FP32 of any size, so their product may leave FP32's normal range
+// though d times it does not.  Then it is applied as pre * mul with mul a power of
+// two, (d * pre) * mul: below the range pre = product * 2^32 (where that is not normal
+// its error, 2^-150, comes to less than 2^-156 of out); above it pre = product * 2^-127,
+// cut to the largest number where it overflows (d * product is then infinite or 0
+// either way).  In the range pre = 1 and mul is the product.  A set of factors that
+// has one out of range takes the loop with pre: with no other sets 64 x 7,168 x 12,288
+// takes 22.5 us instead of 15.6 (the weight in L2), 16,384 x 7,168 x 12,288 1.29 ms
+// instead of 0.93; products all in range take no longer than without it.
+struct Factor {
+  float pre, mul;
+};
+constexpr float kLeastNormal = 0x1p-126f, kMost = 0x1.fffffep127f;
+__device__ __forceinline__ Factor factor(float a, float w) {
+  const float f = a * w;
+  if (fabsf(f) < kLeastNormal)
+    return fabsf(a) < fabsf(w) ? Factor{(a * 0x1p32f) * w, 0x1p-32f} : Factor{(w * 0x1p32f) * a, 0x1p-32f};
+  if (fabsf(f) > kMost && fmaxf(fabsf(a), fabsf(w)) <= kMost) {   // two numbers, so both above 1
+    const float pre = (a * 0x1p-64f) * (w * 0x1p-63f);
+    return {fmaxf(-kMost, fminf(kMost, pre)), 0x1p127f};
+  }
+  return {1.f, f};
+}
+// The least and the largest magnitude of some numbers (a NaN does not count: no
+// Factor changes what it gives).
+struct Span {
+  float least = kMost, most = 0.f;
+  template <int N>
+  __device__ __forceinline__ void add(const float (&v)[N]) {
+    float lo[N], hi[N];                    // a tree: a chain of 16 is what a set waits for
+#pragma unroll
+    for (int k = 0; k < N; ++k) lo[k] = hi[k] = fabsf(v[k]);
+#pragma unroll
+    for (int d = 1; d < N; d *= 2)
+#pragma unroll
+      for (int k = 0; k + d < N; k += 2 * d) {
+        lo[k] = fminf(lo[k], lo[k + d]);
+        hi[k] = fmaxf(hi[k], hi[k + d]);
+      }
+    least = fminf(least, lo[0]);
+    most = fmaxf(most, hi[0]);
+  }
+  // Whether all of them times w are normal numbers.
+  __device__ __forceinline__ bool normal_times(float w) const {
+    return fabsf(least * w) >= kLeastNormal && fabsf(most * w) <= kMost;
+  }
+};
+
 // A value that is the same in every lane, known to be so by the compiler.  Warps
 // that issue copies and MMAs run their loops whole, on such values, and elect a
 // lane for the instructions themselves: with one lane running the loop, every
@@ -120,7 +171,7 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 // A few tokens are bound by the weight's bytes (1 x 7,168 x 12,288 in 15.8 us,
 // 5.6 TB/s; 64 tokens in 18.7), small products by their latencies (64 x 128 x
 // 7,168 in 3.7 us), more tokens by the way from L2 into an SM's shared memory,
-// about 59 bytes a cycle (2,048 x 576 x 7,168 in 16.9 us: (128 + 96) * 128 bytes
+// about 59 bytes a cycle (2,048 x 576 x 7,168 in 16.1 us: (128 + 96) * 128 bytes
 // a block and CTA).
 // ---------------------------------------------------------------------------
 enum : uint32_t { SITE_S_E = 0x700, SITE_S_F = 0x701, SITE_S_ACC = 0x702, SITE_S_FREE = 0x703,
@@ -141,7 +192,8 @@ struct Split {
   static constexpr int OFF_FACT = OFF_MISC + 256;
   static constexpr int CH = 8;                           // blocks of K per set of factors
   static constexpr int FROW = NT + 4;
-  static constexpr int SMEM = 1024 + OFF_FACT + 2 * CH * FROW * 4;
+  static constexpr int OFF_PRE = OFF_FACT + 2 * CH * FROW * 4;   // one set's Factor::pre
+  static constexpr int SMEM = 1024 + OFF_PRE + CH * NT * 4;
   static_assert(NT <= EW * 32 && TCOLS >= 32 && TCOLS * CTAS <= 512, "TMEM columns");
   static_assert(NT * 128 * 4 <= NST * STAGE, "the partial tile reuses the stages");
   static_assert((SMEM + 1024) * CTAS <= 228 * 1024, "shared memory");
@@ -162,6 +214,7 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(acc_free + C::NB);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
   float* fact = reinterpret_cast<float*>(sm + C::OFF_FACT);
+  float* pre = reinterpret_cast<float*>(sm + C::OFF_PRE);
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int tile = blockIdx.x / S, rank = blockIdx.x - tile * S;   // the cluster is S CTAs along x
@@ -252,35 +305,26 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
     constexpr int T = C::EW * 32, PER = C::CH * NT / T;
     const int fk = et % C::CH;
     const float* ws = p.w_scale + static_cast<int64_t>(nb) * p.kb + kb0;
-    float fa[PER], fw = 0.f;
+    // Tokens and blocks that do not exist have the factor 1 (and codes of 0).
+    float fa[PER], fw = 1.f;
+    auto token_scale = [&](int m, int i) {
+      return m < p.M ? p.a_scale[static_cast<int64_t>(m) * p.kb + kb0 + i] : 1.f;
+    };
     auto fetch = [&](int i0) {
       const bool in = i0 + fk < nkb;
-      fw = in ? ws[i0 + fk] : 0.f;
+      fw = in ? ws[i0 + fk] : 1.f;
 #pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const int m = m0 + (et + k * T) / C::CH;
-        fa[k] = in && m < p.M ? p.a_scale[static_cast<int64_t>(m) * p.kb + kb0 + i0 + fk] : 0.f;
-      }
+      for (int k = 0; k < PER; ++k)
+        fa[k] = in ? token_scale(m0 + (et + k * T) / C::CH, i0 + fk) : 1.f;
     };
     fetch(0);
     int bu = 0;
     uint32_t ph = 0;
     bool ok = true;
+    // Blocks i .. end - 1 with their factors from fb on; RARE: and Factor::pre from pr on.
+    auto add_blocks = [&](auto RARE, int i, int end, const float* fb, const float* pr) {
 #pragma unroll 1
-    for (int i = 0; i < nkb; i += C::CH) {
-      float* set = fact + ((i / C::CH) & 1) * (C::CH * C::FROW);
-#pragma unroll
-      for (int k = 0; k < PER; ++k) set[fk * C::FROW + (et + k * T) / C::CH] = fa[k] * fw;
-      fetch(i + C::CH);
-      // all epilogue warps leave together if one of them gave up
-      if (named_bar_or(1, T, !ok)) {
-        ok = false;
-        break;
-      }
-      const float* fb = set + c0;
-      const float* const fe = fb + min(C::CH, nkb - i) * C::FROW;
-#pragma unroll 1
-      for (; ok && fb != fe; fb += C::FROW) {
+      for (; ok && i != end; ++i, fb += C::FROW, pr += NT) {
         ok = !__any_sync(0xffffffffu, !mbar_wait(&acc_full[bu], ph, p.status, kWaitLimitNs, SITE_S_ACC));
         if (!ok) break;
         tc_fence_after();
@@ -299,6 +343,11 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
             tc_fence_before();
             mbar_arrive_warp(&acc_free[bu]);
           }
+          if constexpr (RARE.value) {
+            const volatile float* pb = pr + c;
+#pragma unroll
+            for (int e = 0; e < C::STEP; ++e) d[e] = __float_as_uint(__uint_as_float(d[e]) * pb[e]);
+          }
 #pragma unroll
           for (int e = 0; e < C::STEP; e += 4) {
             const float4 g = f[e / 4];
@@ -309,6 +358,39 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
         }
         if (++bu == C::NB) bu = 0, ph ^= 1;
       }
+    };
+#pragma unroll 1
+    for (int i = 0; i < nkb; i += C::CH) {
+      float* set = fact + ((i / C::CH) & 1) * (C::CH * C::FROW);
+      Span span;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) set[fk * C::FROW + (et + k * T) / C::CH] = fa[k] * fw;
+      span.add(fa);
+      const bool far = !span.normal_times(fw);
+      // One vote for what is rare: a factor out of range, or a warp that gave up, when
+      // all epilogue warps leave together.  (A warp's vote makes the result known to be
+      // the same in all lanes, as the loops' counts are: 2,048 x 576 x 7,168 takes 16.1
+      // us, 17.4 with the barrier's result itself.)
+      const bool rare = __any_sync(0xffffffffu, named_bar_or(1, T, far || !ok));
+      if (rare) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int c = (et + k * T) / C::CH;
+          const Factor g = factor(fa[k], fw);
+          set[fk * C::FROW + c] = g.mul;
+          pre[fk * NT + c] = g.pre;
+        }
+        if (__any_sync(0xffffffffu, named_bar_or(1, T, !ok))) {
+          ok = false;
+          break;
+        }
+      }
+      fetch(i + C::CH);
+      const int end = min(nkb, i + C::CH);
+      if (rare)
+        add_blocks(std::true_type{}, i, end, set + c0, pre + c0);
+      else
+        add_blocks(std::false_type{}, i, end, set + c0, pre + c0);
     }
     if (!ok) s_abort[0] = 1;
     if (S == 1) {
@@ -496,6 +578,7 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
   uint64_t* f_free = f_full + C::NF;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(f_free + C::NF);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
+  int* s_far = reinterpret_cast<int*>(tslot + 2);   // per set and staging warp: far factors
   float* fact = reinterpret_cast<float*>(sm + C::OFF_FACT);
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -611,7 +694,7 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
       for (int tile = blockIdx.x >> 1; ok && tile < ntiles; tile += step) {
         int mt, nt;
         wide_tile(tile, ntm, ntn, mt, nt);
-        const int m0 = mt * 256 + rank * 128 + fr, nb = nt * 2 + fr;
+        const int m0 = mt * 256 + rank * 128 + fr;
         const float* as = p.a_scale + static_cast<int64_t>(m0) * p.kb + fk;
         for (int b = 0; b < p.kb; b += C::CH, ++ch) {
           const int fs = ch % C::NF;
@@ -621,19 +704,24 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
           if (!ok) break;
           float* to = fact + fs * C::FSET + fk * C::FROW + fr;
           const bool in = b + fk < p.kb;
+          const float* wsc = p.w_scale + static_cast<int64_t>(nt * 2) * p.kb + b + fk;
+          const float w0 = in ? wsc[0] : 1.f, w1 = in && nt * 256 + 128 < p.N ? wsc[p.kb] : 1.f;
+          Span span;
 #pragma unroll 1
           for (int r0 = first; r0 < first + 64; r0 += 16 * RP) {
             float v[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const int r = r0 + RP * k;
-              v[k] = in && m0 + r < p.M ? as[static_cast<int64_t>(r) * p.kb + b] : 0.f;
+              v[k] = in && m0 + r < p.M ? as[static_cast<int64_t>(r) * p.kb + b] : 1.f;
             }
 #pragma unroll
             for (int k = 0; k < 16; ++k) to[r0 + RP * k] = v[k];
+            span.add(v);
           }
-          if (first == 0 && fr < 2)
-            to[128] = in && nb * 128 < p.N ? p.w_scale[static_cast<int64_t>(nb) * p.kb + b + fk] : 0.f;
+          if (first == 0 && fr < 2) to[128] = fr == 0 ? w0 : w1;
+          const bool any_far = __any_sync(0xffffffffu, !span.normal_times(w0) || !span.normal_times(w1));
+          if (lane == 0) s_far[fs * 2 + (first != 0)] = any_far;
           mbar_arrive_warp(&f_full[fs]);
         }
       }
@@ -663,19 +751,24 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
         if (!live) break;
         const float* fb = fact + fs * C::FSET;
         const float* const fe = fb + min(C::CH, p.kb - b) * C::FROW;
-#pragma unroll 1
-        do {
+        auto add_block = [&](auto FAR) {
           const float fa = fb[row], fw = fb[128 + half];
           ok = ok && mbar_wait(&done[st], ph, p.status, kWaitLimitNs, SITE_P_ACC);
           __syncwarp();
           tc_fence_after();
-          const float f = fa * fw;
+          Factor f{1.f, fa * fw};
+          if constexpr (FAR.value) f = factor(fa, fw);
           const uint32_t ta = taddr + bu * 256;
           uint32_t d[2][32];
-          auto add = [&](int c, const uint32_t (&x)[32]) {
+          auto add = [&](int c, uint32_t (&x)[32]) {
+            if constexpr (FAR.value) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f.pre);
+            }
 #pragma unroll
             for (int e = 0; e < 32; e += 2)
-              fma2_rn(acc[c + e], acc[c + e + 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]), f, f);
+              fma2_rn(acc[c + e], acc[c + e + 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]),
+                      f.mul, f.mul);
           };
           tmem_ld32(ta, d[0]);
           tmem_ld32(ta + 32, d[1]);
@@ -700,7 +793,17 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
           bu ^= 1;
           if (++st == C::NST) st = 0, ph ^= 1;
           fb += C::FROW;
-        } while (fb != fe);
+        };
+        const int2 far = reinterpret_cast<const int2*>(s_far)[fs];
+        if ((far.x | far.y) == 0) {
+#pragma unroll 1
+          do add_block(std::false_type{});
+          while (fb != fe);
+        } else {
+#pragma unroll 1
+          do add_block(std::true_type{});
+          while (fb != fe);
+        }
         mbar_arrive_warp(&f_free[fs]);
         if (++fs == C::NF) fs = 0, fph ^= 1;
       }
