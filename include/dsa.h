@@ -357,7 +357,9 @@ dsa_status_t dsa_indexer_topk_fp8(const uint8_t* q_codes, const float* q_scale, 
  *   codes        [n_rows, hid] uint8
  *   scale        [n_rows, ceil(hid / 128)] FP32
  * The norm takes the unrounded sum h.  Its sum of squares is FP32: a row whose
- * sum overflows (values beyond about 1e19) gives y = 0.  A row is read whole before any of it is
+ * sum overflows (values beyond about 1e19) gives y = 0; with an eps below 2^-100,
+ * beside which an underflow counts, a row whose sum is below 2^-100 is summed
+ * again, scaled.  A row is read whole before any of it is
  * written: residual_out and y_out may each be x or residual itself (the same
  * pointer); apart from that no output may overlap an input or another output.
  * Supported: hid a multiple of 16, 16 <= hid <= 65536; n_rows >= 0 (0: nothing
