@@ -393,7 +393,8 @@ dsa_status_t dsa_quant_fp8_weight(const uint16_t* w, int N, int K, uint8_t* code
  * The scales may be any FP32 numbers: where the product of two leaves FP32's range
  * they are applied one after the other, so that a normal term stays exact to its
  * roundings (slower, by the blocks that need it).
- * The sum's order depends on the sizes alone: equal calls give equal bits.
+ * The sum's order depends on the sizes and the SMs that the context has: equal
+ * calls give equal bits.
  * Supported: M >= 0 (0: nothing to do, no pointer is looked at), N >= 1, K a
  * multiple of 16, M, N, K < 2^30, M * N < 2^40.  Codes and out 16-byte aligned, scales 4.
  * out may overlap no input; after DSA_ERR_DEVICE_TIMEOUT it is unspecified.

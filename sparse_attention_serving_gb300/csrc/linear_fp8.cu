@@ -452,6 +452,28 @@ __global__ void __launch_bounds__(Split<NT>::NTHREADS, Split<NT>::CTAS)
   if (S > 1) cluster_wait();
 }
 
+// Whether one cluster of S CTAs fits on the SMs that this context has (0.25 us).
+template <int NT>
+bool split_fits(int S, cudaStream_t stream) {
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(S);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(S));
+  cfg.blockDim = dim3(Split<NT>::NTHREADS);
+  cfg.dynamicSmemBytes = Split<NT>::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, split_kernel<NT>, &cfg) == cudaSuccess)
+    return clusters > 0;
+  cudaGetLastError();   // an answer, not a failure of the call
+  return false;
+}
+
+// DSA_ERR_UNSUPPORTED: a cluster of S CTAs, more than kPortable, does not fit.
 template <int NT>
 dsa_status_t launch_split(const LinearArgs& a, int S, cudaStream_t stream) {
   using C = Split<NT>;
@@ -465,9 +487,12 @@ dsa_status_t launch_split(const LinearArgs& a, int S, cudaStream_t stream) {
   if (cudaFuncSetAttribute(split_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
       cudaSuccess)
     return launch_status("cudaFuncSetAttribute");
-  if (S > 8 && cudaFuncSetAttribute(split_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                                    1) != cudaSuccess)
-    return launch_status("cudaFuncSetAttribute");
+  if (S > kPortable) {
+    if (cudaFuncSetAttribute(split_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+        cudaSuccess)
+      return launch_status("cudaFuncSetAttribute");
+    if (!split_fits<NT>(S, stream)) return DSA_ERR_UNSUPPORTED;
+  }
   launch_overlapped(split_kernel<NT>,
                     static_cast<unsigned>(split_tiles(a.M, a.N, NT) * S),
                     C::NTHREADS, C::SMEM, static_cast<unsigned>(S), stream, ta, tw, p, S);
@@ -893,18 +918,24 @@ dsa_status_t quant_fp8_weight_launch(const uint16_t* w, int N, int K, uint8_t* c
 }
 
 dsa_status_t linear_fp8_launch(const LinearArgs& a, const lin::Pick* forced, cudaStream_t stream) {
-  const lin::Pick at = forced != nullptr
-                           ? *forced
-                           : lin::pick(a.M, a.N, (a.K + 127) / 128, num_sms(),
-                                       static_cast<int64_t>(a.N) * (a.fp32 ? 4 : 2));
-  switch (at.nt) {
-    case 16: return lin::launch_split<16>(a, at.S, stream);
-    case 32: return lin::launch_split<32>(a, at.S, stream);
-    case 64: return lin::launch_split<64>(a, at.S, stream);
-    case 96: return lin::launch_split<96>(a, at.S, stream);
-    case 128: return lin::launch_split<128>(a, at.S, stream);
-    default: return lin::launch_wide(a, stream);
-  }
+  auto launch = [&](const lin::Pick& at) {
+    switch (at.nt) {
+      case 16: return lin::launch_split<16>(a, at.S, stream);
+      case 32: return lin::launch_split<32>(a, at.S, stream);
+      case 64: return lin::launch_split<64>(a, at.S, stream);
+      case 96: return lin::launch_split<96>(a, at.S, stream);
+      case 128: return lin::launch_split<128>(a, at.S, stream);
+      default: return lin::launch_wide(a, stream);
+    }
+  };
+  if (forced != nullptr) return launch(*forced);
+  dsa_status_t st = DSA_OK;
+  lin::take_one_that_fits(a.M, a.N, (a.K + 127) / 128, num_sms(),
+                          static_cast<int64_t>(a.N) * (a.fp32 ? 4 : 2), [&](const lin::Pick& at) {
+                            st = launch(at);
+                            return st != DSA_ERR_UNSUPPORTED;
+                          });
+  return st;
 }
 
 }  // namespace dsa

@@ -26,8 +26,9 @@ constexpr struct {
   double reach;      // the part of the SMs that clusters of S fill
 } kSlices[] = {{1, 1.0}, {2, 1.0}, {3, 0.91}, {4, 0.95}, {5, 0.92}, {6, 0.91}, {8, 0.79},
                {12, 0.7}, {16, 0.7}};
-inline int most_slices(int ctas, int kb) {
-  const int most = ctas == 1 ? 8 : 16;
+constexpr int kPortable = 8, kLargest = 16;   // CTAs of a cluster: on any GPU, on this one
+inline int most_slices(int ctas, int kb, int cluster = kLargest) {
+  const int most = ctas == 1 ? kPortable : cluster;
   return most < kb ? most : kb;
 }
 inline int64_t split_tiles(int M, int N, int nt) {
@@ -51,7 +52,8 @@ inline int64_t split_tiles(int M, int N, int nt) {
 struct Pick {
   int nt, S;   // nt = 0: the pair kernel
 };
-inline Pick pick(int M, int N, int kb, int sms, int64_t row_bytes) {
+// cluster: the most CTAs that a cluster may have.
+inline Pick pick(int M, int N, int kb, int sms, int64_t row_bytes, int cluster = kLargest) {
   const int64_t pairs = sms / 2;
   const int64_t wt = static_cast<int64_t>((M + 255) / 256) * ((N + 255) / 256);
   const double rows = row_bytes % 4 != 0 ? 8.3 : row_bytes % 16 != 0 ? 1.3 : 0.0;
@@ -60,7 +62,7 @@ inline Pick pick(int M, int N, int kb, int sms, int64_t row_bytes) {
   for (const auto& t : kTile) {
     const int64_t tiles = split_tiles(M, N, t.nt);
     for (const auto& s : kSlices) {
-      if (s.S > most_slices(t.ctas, kb)) break;
+      if (s.S > most_slices(t.ctas, kb, cluster)) break;
       const int64_t n = tiles * s.S, reach = static_cast<int64_t>(sms * s.reach),
                     slots = static_cast<int64_t>(sms * t.ctas * s.reach);
       const double rounds = n <= slots ? 1.0 : static_cast<double>((n + slots - 1) / slots);
@@ -74,6 +76,15 @@ inline Pick pick(int M, int N, int kb, int sms, int64_t row_bytes) {
     }
   }
   return at;
+}
+
+// Takes the choice, where clusters of more than kPortable CTAs may not fit: a process
+// that has a part of the SMs only (a partition's, a shared server's) may have no GPC with
+// so many.  take(at) is false where the cluster does not fit.
+template <typename Take>
+void take_one_that_fits(int M, int N, int kb, int sms, int64_t row_bytes, Take take) {
+  const Pick at = pick(M, N, kb, sms, row_bytes);
+  if (!take(at) && at.S > kPortable) take(pick(M, N, kb, sms, row_bytes, kPortable));
 }
 
 // Whether a kernel can be asked for by its tile and slices at these sizes (a grid

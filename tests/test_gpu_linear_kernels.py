@@ -98,3 +98,22 @@ def test_norm_vectors_per_thread(dsa, n, hid, full):
     codes, scale, ro, y = dsa.dsa_rmsnorm_fp8(x, gain, residual=r, eps=EPS, want_y=full)
     d = lambda t: None if t is None else t.double().cpu().numpy()  # noqa: E731
     _check_norm(d(x), d(r), d(gain), EPS, codes, scale, ro, y, f"{n}x{hid}")
+
+
+def test_large_clusters_in_a_graph(dsa):
+    """A product whose K is cut into more than eight slices asks whether their cluster fits;
+    captured, with a workspace of the graph's own and with the caller's."""
+    codes, scale, w_codes, w_scale = _operands(dsa, 9, 64, 128, 7168)
+    ws = dsa.new_workspace(256)
+    out = torch.empty((64, 128), device="cuda")
+    want = dsa.dsa_linear_fp8(codes, scale, w_codes, w_scale, out=out, workspace=ws).clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        own = dsa.dsa_linear_fp8(codes, scale, w_codes, w_scale, out_dtype=torch.float32)
+        dsa.dsa_linear_fp8(codes, scale, w_codes, w_scale, out=out, workspace=ws)
+    out.zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(own, want)
+    assert dsa.read_device_status(ws)[0] == dsa.DSA_OK

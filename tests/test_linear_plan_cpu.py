@@ -23,6 +23,17 @@ extern "C" long long pick(int M, int N, int K, int sms, int size, int* tokens, i
   *slices = at.S;
   return at.nt == 0 ? 0 : dsa::lin::split_tiles(M, N, at.nt) * at.S;
 }
+extern "C" int take(int M, int N, int K, int sms, int size, int fits, int* tokens, int* slices) {
+  int times = 0;    // the last one taken, and how many were tried
+  dsa::lin::take_one_that_fits(M, N, (K + 127) / 128, sms, (long long)N * size,
+                               [&](const dsa::lin::Pick& at) {
+                                 ++times;
+                                 *tokens = at.nt;
+                                 *slices = at.S;
+                                 return at.S <= 8 || fits != 0;
+                               });
+  return times;
+}
 extern "C" int offered(int tokens, int slices, int M, int N, int K) {
   return dsa::lin::offered(dsa::lin::Pick{tokens, slices}, M, N, (K + 127) / 128);
 }
@@ -100,3 +111,25 @@ def test_grids_of_the_largest_sizes(plan):
                     for sms in (8, 152):
                         at, ctas = _pick(plan, M, N, K, sms, 4)
                         assert at in KERNELS and ctas < 1 << 31, (M, N, K, at, ctas)
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 128, 7168), (1, 128, 7168), (16, 64, 12288), (1, 576, 7168),
+                                   (64, 7168, 12288), (777, 1001, 1040)])
+def test_clusters_above_eight_ctas_are_taken_only_where_they_fit(plan, M, N, K):
+    t, s = ctypes.c_int(), ctypes.c_int()
+
+    def take(fits):
+        times = plan.take(M, N, K, 152, 4, fits, ctypes.byref(t), ctypes.byref(s))
+        return times, (t.value, s.value)
+
+    free, _ = _pick(plan, M, N, K, 152, 4)
+    assert take(1) == (1, free)
+    times, at = take(0)
+    if free[1] <= 8:
+        assert times == 1 and at == free
+    else:
+        assert times == 2 and at in KERNELS and at[1] <= 8 and plan.offered(*at, M, N, K)
+
+
+def test_a_choice_with_large_clusters_is_among_those(plan):
+    assert _pick(plan, 64, 128, 7168, 152, 4)[0][1] > 8
