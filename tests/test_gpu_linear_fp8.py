@@ -564,3 +564,31 @@ def test_joined_slices_many_times(dsa, M, N, K):
     ref, mag = _linear_ref(codes, scale, w_codes, w_scale)
     _check_linear(out[0], ref, mag, K, f"{M}x{N}x{K}")
     assert all(torch.equal(o, out[0]) for o in out)
+
+
+def test_each_operand_is_refused_by_its_name(dsa):
+    """Wrong type, wrong shape, a strided view, another device: for every operand of the
+    three calls, the message names it (or says what the shapes have to be together)."""
+    codes, scale, w_codes, w_scale = _operands(dsa, 8, 6, 200, 256)
+    x, gain = _rows(1, 6, 256), torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    calls = [
+        (dsa.dsa_rmsnorm_fp8, dict(x=x, gain=gain, residual=x.clone(), codes=torch.empty_like(codes),
+                                   scale=torch.empty_like(scale), residual_out=torch.empty_like(x),
+                                   y=torch.empty_like(x))),
+        (dsa.dsa_quant_fp8_weight, dict(w=x, codes=torch.empty_like(codes),
+                                        scale=torch.empty((1, 2), device="cuda"))),
+        (dsa.dsa_linear_fp8, dict(codes=codes, scale=scale, w_codes=w_codes, w_scale=w_scale,
+                                  out=torch.empty((6, 200), device="cuda"),
+                                  workspace=dsa.new_workspace(256)))]
+    for call, args in calls:
+        call(**args)
+        for name, t in args.items():
+            strided = torch.zeros((*t.shape, 2), dtype=t.dtype, device="cuda")[..., 0]
+            for wrong in (t.to(torch.int16), strided, t.cpu(), [1.0], t.new_zeros((*t.shape, 1))):
+                if name == "workspace" and isinstance(wrong, torch.Tensor) and wrong.dim() == 2:
+                    continue                                       # any shape will do there
+                with pytest.raises((TypeError, ValueError, dsa.DsaError)) as e:
+                    call(**dict(args, **{name: wrong}))
+                said = str(e.value)
+                assert name in said or "must be [" in said, (call.__name__, name, said)
+        call(**args)

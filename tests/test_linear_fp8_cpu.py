@@ -91,3 +91,24 @@ def test_selftest_refusals(dsa):
     assert call(64, 4, K=7160) == dsa.DSA_ERR_UNSUPPORTED
     assert call(64, 4, a=None) == dsa.DSA_ERR_INVALID_ARGUMENT
     assert call(64, 4, M=0) == dsa.DSA_OK
+
+
+def test_refuse_names_the_operand_and_never_returns(dsa):
+    bf, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
+    t = lambda dtype, *shape: torch.zeros(shape, dtype=dtype)  # noqa: E731
+    good = [(t(bf, 4, 256), (bf,), (4, 256), "x"), (t(u8, 4, 256), (u8,), None, "codes"),
+            (t(f32, 4, 2), (bf, f32), (4, 2), "out")]
+    with pytest.raises(dsa.DsaError, match="call: operands"):      # nothing to find
+        dsa._refuse("call", -1, *good)
+    for i, (x, dtypes, shape, name) in enumerate(good):
+        wrong = [(x.double(), TypeError), ([1.0], TypeError), (None, TypeError),
+                 (torch.zeros(256, 4, dtype=x.dtype).t()[:x.shape[0], :x.shape[1]], dsa.DsaError)]
+        if shape is not None:
+            wrong.append((x[:2], ValueError))
+        for y, error in wrong:
+            rules = list(good)
+            rules[i] = (y, dtypes, shape, name)
+            with pytest.raises(error, match=name):
+                dsa._refuse("call", -1, *rules)
+    with pytest.raises(dsa.DsaError, match="x must be on cuda:0"):
+        dsa._refuse("call", 0, *good)
