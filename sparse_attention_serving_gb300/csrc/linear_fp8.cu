@@ -171,8 +171,8 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 // A few tokens are bound by the weight's bytes (1 x 7,168 x 12,288 in 15.8 us,
 // 5.6 TB/s; 64 tokens in 18.7), small products by their latencies (64 x 128 x
 // 7,168 in 3.7 us), more tokens by the way from L2 into an SM's shared memory,
-// about 59 bytes a cycle (2,048 x 576 x 7,168 in 16.1 us: (128 + 96) * 128 bytes
-// a block and CTA).
+// about 61 bytes a cycle, and by the epilogue's loop (2,048 x 576 x 7,168 in 16.0 us:
+// (128 + 96) * 128 bytes a block and CTA).
 // ---------------------------------------------------------------------------
 enum : uint32_t { SITE_S_E = 0x700, SITE_S_F = 0x701, SITE_S_ACC = 0x702, SITE_S_FREE = 0x703,
                   SITE_S_DRAIN = 0x704 };
@@ -493,8 +493,7 @@ dsa_status_t launch_split(const LinearArgs& a, int S, cudaStream_t stream) {
       return launch_status("cudaFuncSetAttribute");
     if (!split_fits<NT>(S, stream)) return DSA_ERR_UNSUPPORTED;
   }
-  launch_overlapped(split_kernel<NT>,
-                    static_cast<unsigned>(split_tiles(a.M, a.N, NT) * S),
+  launch_overlapped(split_kernel<NT>, static_cast<unsigned>(split_tiles(a.M, a.N, NT) * S),
                     C::NTHREADS, C::SMEM, static_cast<unsigned>(S), stream, ta, tw, p, S);
   return launch_status("split_kernel");
 }
@@ -511,9 +510,9 @@ dsa_status_t launch_split(const LinearArgs& a, int S, cudaStream_t stream) {
 // pair walks the tiles, and the epilogue's store of one tile overlaps the first
 // blocks of the next.
 //
-// 16,384 x 7,168 x 12,288 in 0.92 to 0.96 ms by the box, 3.0 to 3.15 PFLOP/s (1.04 ms
+// 16,384 x 7,168 x 12,288 in 0.93 to 0.95 ms by the box, 3.0 to 3.1 PFLOP/s (1.04 ms
 // in a row of 600 calls, at the power cap's 1.7 GHz); a library product of the same
-// codes with one scale for the whole matrix takes 0.75 to 0.83 ms.  A block takes
+// codes with one scale for the whole matrix takes 0.77 to 0.83 ms.  A block takes
 // about 780 cycles of a pair, its MMAs 512: the rest is the chain through the two
 // TMEM buffers (all 512 columns): commit, the epilogue's 128 columns a thread, the
 // buffer's return to the issuing CTA.  A third buffer would need a narrower tile,

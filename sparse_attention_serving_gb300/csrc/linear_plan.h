@@ -39,16 +39,20 @@ inline int64_t split_tiles(int M, int N, int nt) {
 // time in microseconds, whose terms were fitted to the measured time of every
 // combination at 220 sizes (1 to 4,096 tokens, 64 to 8,192 features, K 256 to
 // 12,288): the choice is on average 0.7 % slower than the fastest combination,
-// at most 17 % (0.4 us at 4 x 64 x 512).  The terms: a CTA's time per block of K,
+// at most 17 % (0.4 us at 4 x 64 x 512); at 70 other sizes (up to 16,384 tokens) 2 %
+// and 19 % (1.7 us at 7 x 6,432 x 7,792).  There is no term for the memory's rate:
+// 64 x 55,296 x 7,168 is put at 48 us and takes 67, by the best kernel all the same.
+// The terms: a CTA's time per block of K,
 // by how many CTAs share its SM (its bytes at an SM's share of L2 bandwidth, 59 a
 // cycle, or the epilogue's latency); a start; the join of K slices, a cluster
 // barrier and the partial tiles' way through distributed shared memory (about 12
-// bytes a cycle); the part of the SMs that clusters of a size can fill; the wide
+// bytes a cycle at 1.9 GHz); the part of the SMs that clusters of a size can fill; the wide
 // kernel's way of storing rows that TMA cannot.  Examples (us; tokens x features
-// x K): 1 x 8,192 x 7,168: 16 tokens and 4 slices 11.6, unsliced 17; 64 x 128 x
-// 7,168: 16 tokens and 16 slices 3.7, 64 tokens and 8 slices 5.5; 777 x 1,001 x
-// 1,040: 64 tokens unsliced 5.4, with 2 slices 9; 2,048 x 576 x 7,168: 96 tokens
-// 16.9, 128 tokens 20, wide 27; 512 x 7,168 x 12,288: wide 45, 128 tokens 65.
+// x K): 1 x 8,192 x 7,168: 16 tokens and 4 slices 11.6, unsliced 17; and with the
+// operands in L2, 64 x 128 x 7,168: 16 tokens and 16 slices 3.7, 64 tokens and 8
+// slices 5.3; 777 x 1,001 x 1,040: 64 tokens unsliced 5.1, with 2 slices 8; 2,048 x
+// 576 x 7,168: 96 tokens 15.4, 128 tokens 18, wide 25; 512 x 7,168 x 12,288: wide 42,
+// 128 tokens 60.
 struct Pick {
   int nt, S;   // nt = 0: the pair kernel
 };

@@ -161,7 +161,8 @@ dsa_status_t rmsnorm_fp8_launch(const RmsNormArgs& a, cudaStream_t stream) {
   // threads crowd an SM, when two let twice as many rows be in flight
   // (16,384 x 7,168 with everything on: 180 us with one, 156 with two, 172 with
   // four; 16,384 x 1,024: 23.8 against 24.7; one row of 7,168: 2.5 against 3.1),
-  // or the row needs more.  Short rows share a CTA.
+  // or the row needs more (with eight the values do not all fit the registers: 4,096 x
+  // 65,536 with everything on 530 us, 4.6 TB/s).  Short rows share a CTA.
   const int vpt = p.nvec > 4096 ? 8 : p.nvec > 2048 ? 4
                   : p.nvec > 1024 || (p.nvec > 512 && a.n_rows > 2 * num_sms()) ? 2 : 1;
   const int T = ((p.nvec + vpt - 1) / vpt + 31) / 32 * 32;
