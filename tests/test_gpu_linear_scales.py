@@ -97,3 +97,40 @@ def test_products_of_the_quantisers_smallest_scales(dsa, kernel, M, N):
     kb = -(-K // 128)
     tol = (128 + kb + 3) * 2.0 ** -23 * mag + (kb + 2) * 2.0 ** -150
     assert ((out - ref).abs() <= tol).all() and (out[::2, 128:] > 2.0 ** -120).all()
+
+
+@pytest.mark.parametrize("kernel,M,N", SHAPES)
+def test_non_finite_scales_and_codes_stay_where_they_are(dsa, kernel, M, N):
+    """A NaN or an infinite scale, alone, against a scale of 0 and against a subnormal one, and
+    NaN codes, beside factors out of range: by the formula, and the others keep their bits."""
+    codes, scale, w_codes, w_scale = _operands(dsa, M + N, M, N, K)
+    clean = _run(dsa, kernel, codes, scale, w_codes, w_scale, torch.float32)
+    codes, scale, w_codes, w_scale = (t.clone() for t in (codes, scale, w_codes, w_scale))
+    scale[1, 2] = float("nan")
+    scale[2, 9] = float("inf")
+    codes[4, 700] = 0x7F                              # a NaN code
+    scale[6, 5] = 0.0
+    scale[7, 19] = 2.0 ** -149
+    w_codes[300, K - 1] = 0xFF
+    w_scale[1, 8] = float("nan")
+    out = _run(dsa, kernel, codes, scale, w_codes, w_scale, torch.float32)
+    nan = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+    nan[1] = nan[4] = True
+    nan[:, 300] = True
+    nan[:, 128:256] = True
+    assert torch.isnan(out[nan]).all()
+    assert not torch.isfinite(out[2]).any()           # infinite, or infinite times 0
+    rest = ~nan
+    rest[[2, 6, 7]] = False
+    assert torch.equal(out[rest], clean[rest])
+    ref, mag = _linear_ref(codes, scale, w_codes, w_scale)
+    ok = ~nan
+    ok[2] = False
+    tol = (128 + -(-K // 128) + 3) * 2.0 ** -23 * mag + 2.0 ** -24 * ref.abs() + 2.0 ** -140
+    assert ((out.double() - ref).abs() <= tol)[ok].all()
+    # an infinite scale on a scale of 0 is NaN
+    scale[2, 9] = 0.0
+    w_scale[1, 8] = 1.0
+    w_scale[0, 9] = float("inf")
+    out = _run(dsa, kernel, codes, scale, w_codes, w_scale, torch.float32)
+    assert torch.isnan(out[2, :128]).all() and torch.isfinite(out[2, 128:256]).all()
