@@ -103,15 +103,23 @@ typedef enum {
   DSA_OP_GATE = 2,
   DSA_OP_CACHE_APPEND = 3,
   DSA_OP_SPARSE_MLA_BWD = 4,
-  DSA_OP_LINEAR_FP8 = 5
+  DSA_OP_LINEAR_FP8 = 5,
+  DSA_OP_MLA_TREE = 6,
+  DSA_OP_MLA_WINDOW = 7,
+  DSA_OP_MLA_WINDOW_BWD = 8
 } dsa_op_t;
 
 /* Element type of an output that a call offers in two. */
 typedef enum { DSA_BF16 = 0, DSA_FP32 = 1 } dsa_dtype_t;
 
+/* Which of 64 position dims are rotated together: none, (i, i + 32) or (2i, 2i + 1). */
+typedef enum { DSA_ROPE_NONE = 0, DSA_ROPE_HALVES = 1, DSA_ROPE_PAIRS = 2 } dsa_rope_t;
+
 /* Bytes of workspace an op needs for the given sizes (heads = H_I for the
  * indexer, H for sparse MLA, ignored for the gate; for the FP8 projection
- * B = M, Tq = 1, max_kv_len = K, heads = N).  Always >= 256. */
+ * B = M, Tq = 1, max_kv_len = K, heads = N; for the tree Tq = T and topk is
+ * ignored; for the window and its backward pass topk = window + n_first).
+ * Always >= 256. */
 size_t dsa_workspace_bytes(dsa_op_t op, int B, int Tq, int max_kv_len, int heads, int topk);
 
 /* Zero the status header of a workspace (asynchronous on `stream`). */
@@ -405,6 +413,118 @@ dsa_status_t dsa_linear_fp8(const uint8_t* a_codes, const float* a_scale, const 
                             const float* w_scale, int M, int N, int K, void* out,
                             dsa_dtype_t out_type, void* workspace, size_t ws_bytes,
                             dsa_stream_t stream);
+
+/*
+ * dsa_cache_append for layers whose keys carry their position as a rotation, with
+ * the queries that go with them.  Of the latent row the 64 k_pe dims are rotated,
+ * of the indexer key (after its LayerNorm) dims 0..63:
+ *   (a, b) -> (a cos - b sin, b cos + a sin)   for the dim pairs that the style names,
+ * in FP32, rounded once to BF16 (the key after LayerNorm and rotation).
+ *   k_pre, kv_new, k_cache, kv_cache, q_start, eps   as for dsa_cache_append
+ *   rope     [n_pos, 64] FP32   per position 32 cosines, then 32 sines
+ *   pos      [B, Tq] int32      position of each new token in the table, or NULL:
+ *            q_start[b] + i (the row that it is written to).  A drafted token's is
+ *            its depth in the tree behind the prefix, whatever its row.
+ *   n_new    [B] int32          new tokens of each sequence (a ragged batch), or
+ *            NULL: Tq.  Nothing is written for the tokens behind them.
+ *   q_pe     [B, Tq, H, 64] BF16    position dims of the absorbed queries, or NULL;
+ *            rotated (kv_style) into dims 512..575 of
+ *   q_lat    [B, Tq, H, 576] BF16   whose dims 0..511 are left alone
+ *   q_idx    [B, Tq, H_I, D_I] BF16 indexer queries, or NULL; dims 0..63 rotated
+ *            (key_style), the rest copied, into
+ *   q_idx_out                       the same shape; may be q_idx itself
+ *   kv_style, key_style             DSA_ROPE_NONE copies
+ * A row that does not exist is not written, as for dsa_cache_append; a position
+ * outside the table leaves out all of its token; n_new outside [0, Tq] is taken as
+ * the nearer bound.  Each is recorded as DSA_ERR_BAD_INDEX.  No output may overlap
+ * an input (q_idx_out = q_idx apart) or another output.
+ * Supported: D_I in {64, 128}; B, Tq >= 1; 1 <= H, H_I <= 1024 where given; n_pos >= 1.
+ * All arrays but the int32 ones (4) 16-byte aligned.  Workspace: the 256-byte
+ * status header.
+ */
+dsa_status_t dsa_cache_append_rope(const float* k_pre, const uint16_t* kv_new,
+                                   const dsa_rows_t* k_cache, const dsa_rows_t* kv_cache,
+                                   const int32_t* q_start, const float* rope, int n_pos,
+                                   const int32_t* pos, const int32_t* n_new, const uint16_t* q_pe,
+                                   uint16_t* q_lat, int H, const uint16_t* q_idx,
+                                   uint16_t* q_idx_out, int H_I, int B, int Tq, int D_I,
+                                   dsa_rope_t kv_style, dsa_rope_t key_style, float eps,
+                                   void* workspace, size_t ws_bytes, dsa_stream_t stream);
+
+/*
+ * Dense attention of a tree of drafted tokens over a latent cache, in latent space
+ * as sparse_mla_fwd: the verification step of speculative decoding where every key
+ * is kept (caches of up to topk tokens, layers without an indexer).  T = 1 with
+ * tree = {1} is a decode step's dense attention.
+ *   q_lat   [B, T, H, 576] BF16   absorbed queries of the drafted tokens
+ *   kv      rows of width 576     the prefix's rows 0 .. kv_len[b]-1, then drafted
+ *           token j's row at kv_len[b] + j
+ *   tree    [B, T] uint64         bit j of tree[b,i]: token i sees token j (itself
+ *           too only where its bit says so); bits of tokens that are not there are
+ *           ignored.  Every token sees the whole prefix.
+ *   kv_len  [B] int32             rows of the prefix (0 is allowed)
+ *   n_draft [B] int32             drafted tokens of each sequence, or NULL: T.  The
+ *           outputs of the tokens behind them are left as they were.
+ *   scale, o_lat [B, T, H, 512] BF16, lse [B, T, H] FP32 or NULL   as sparse_mla_fwd
+ * A token that sees nothing gets o_lat = 0 and lse = -inf.  Rows that no token of
+ * the sequence sees may hold anything, and what a row holds (an infinity or a NaN
+ * too) reaches only the tokens that see it.
+ * kv_len[b] < 0, kv_len[b] + n_draft[b] > max_kv_len (the sequence's tokens then see
+ * nothing), n_draft outside [0, T] (taken as the nearer bound) and pages outside the
+ * pool (not seen) are recorded as DSA_ERR_BAD_INDEX.
+ * Supported: 1 <= H <= 128, 1 <= T <= 64.  Equal calls give equal bits.
+ * Workspace: dsa_workspace_bytes(DSA_OP_MLA_TREE, B, T, max_kv_len, H, 0).
+ */
+dsa_status_t mla_tree_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const uint64_t* tree,
+                          const int32_t* kv_len, const int32_t* n_draft, int B, int T, int H,
+                          int max_kv_len, float scale, uint16_t* o_lat, float* lse,
+                          void* workspace, size_t ws_bytes, dsa_stream_t stream);
+
+/*
+ * Dense attention in latent space with a sliding window and first tokens that stay
+ * visible: query i of sequence b, at position t = q_start[b] + i, sees the rows
+ *   s <= t  with  s > t - window  or  s < n_first.
+ * Prefill, chunks and decode steps as sparse_mla_fwd (q_start, kv_len, max_kv_len);
+ * the fixed pattern takes the place of its index list.
+ *   q_lat, kv, scale, o_lat, lse   as sparse_mla_fwd
+ *   window >= 0, n_first >= 0      both 0: every query gets o_lat = 0, lse = -inf
+ * Only rows that some query sees are needed (a cache may have dropped the rest:
+ * pages in between are not looked up).  What a row holds reaches only the queries
+ * that see it.  A query at or beyond kv_len[b], kv_len[b] > max_kv_len, q_start < 0
+ * (nothing seen) and pages outside the pool (not seen): DSA_ERR_BAD_INDEX.
+ * Supported: 1 <= H <= 128.  Equal calls give equal bits.
+ * Workspace: dsa_workspace_bytes(DSA_OP_MLA_WINDOW, B, Tq, max_kv_len, H, window + n_first).
+ */
+dsa_status_t mla_window_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const int32_t* q_start,
+                            const int32_t* kv_len, int B, int Tq, int H, int window, int n_first,
+                            int max_kv_len, float scale, uint16_t* o_lat, float* lse,
+                            void* workspace, size_t ws_bytes, dsa_stream_t stream);
+
+/*
+ * Its backward pass: the gradient of sum(d_o * o_lat) given the forward's outputs,
+ *   p_s = exp(scale * q . kv[s] - lse),  dz_s = scale * p_s (d_o . kv[s, 0:512] - d_o . o_lat)
+ *   dq = sum_s dz_s kv[s],   dkv[s] = sum over queries and heads that see s of dz_s q,
+ *                            and of p_s d_o in dims 0..511
+ *   q_lat, kv, q_start, kv_len, window, n_first, scale   as for mla_window_fwd;
+ *                       kv contiguous, its sequences in separate rows
+ *   o_lat, lse          the forward's outputs
+ *   d_o   [B,Tq,H,512]  BF16   upstream gradient of o_lat
+ *   dq    [B,Tq,H,576]  BF16   written; 0 for a query that sees nothing
+ *   dkv                 BF16   rows numbered like kv's ([B, seq_stride, 576]):
+ *                       rows 0 .. kv_len[b]-1 are written (0 where no query of the
+ *                       call sees them), the rows behind them left as they were
+ * Sums are FP32 and rounded once; p and dz are rounded to BF16 for the products.
+ * They are added in a fixed order: equal calls give equal bits.
+ * A sequence with kv_len[b] > max_kv_len or q_start[b] < 0 gets dq = 0 and no dkv;
+ * errors as for mla_window_fwd.  A paged kv: DSA_ERR_UNSUPPORTED.
+ * Supported: 1 <= H <= 128.
+ * Workspace: dsa_workspace_bytes(DSA_OP_MLA_WINDOW_BWD, B, Tq, max_kv_len, H, window + n_first).
+ */
+dsa_status_t mla_window_bwd(const uint16_t* q_lat, const dsa_rows_t* kv, const int32_t* q_start,
+                            const int32_t* kv_len, int B, int Tq, int H, int window, int n_first,
+                            int max_kv_len, float scale, const uint16_t* o_lat, const float* lse,
+                            const uint16_t* d_o, uint16_t* dq, uint16_t* dkv, void* workspace,
+                            size_t ws_bytes, dsa_stream_t stream);
 
 /*
  * sparse_mla_fwd_noalloc -- sparse_mla_fwd for callers that cannot allocate

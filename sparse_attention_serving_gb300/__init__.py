@@ -17,6 +17,13 @@ Entry points (same names as the C ABI):
   dsa_rmsnorm_fp8, dsa_quant_fp8_weight, dsa_linear_fp8
                     the FP8 projections around the step: residual addition + RMS
                     norm to E4M3 codes, a weight's quantisation, the product
+  dsa_cache_append_rope
+                    dsa_cache_append with positions rotated on the way, in the keys,
+                    the latent rows and the queries that go with them
+  mla_tree_fwd      dense attention of a tree of drafted tokens over a latent cache
+  mla_window_fwd, mla_window_bwd
+                    dense attention with a sliding window and first tokens that stay
+                    visible, and its gradients
 """
 
 from __future__ import annotations
@@ -40,6 +47,9 @@ DSA_ERR_WORKSPACE_TOO_SMALL = 6
 
 OP_INDEXER_TOPK, OP_SPARSE_MLA, OP_GATE, OP_CACHE_APPEND, OP_SPARSE_MLA_BWD = 0, 1, 2, 3, 4
 OP_LINEAR_FP8 = 5
+OP_MLA_TREE, OP_MLA_WINDOW, OP_MLA_WINDOW_BWD = 6, 7, 8
+ROPE_NONE, ROPE_HALVES, ROPE_PAIRS = 0, 1, 2   # dims rotated together: (i, i+32) or (2i, 2i+1)
+ROPE_DIMS = 64
 INDEXER_KEY_EPS = 1e-5   # KimiK3TextConfig rms_norm_eps
 RMS_NORM_EPS = 1e-5      # KimiK3TextConfig rms_norm_eps
 FP8_BLOCK = 128          # values per scale: along a row, and a weight's rows too
@@ -64,7 +74,8 @@ EXPORTS = ("dsa_abi_version", "dsa_status_string", "dsa_workspace_bytes", "dsa_w
            "dsa_cache_append", "sparse_mla_fwd_sink", "dsa_selftest_wait_timeout",
            "dsa_quant_fp8", "dsa_cache_append_fp8", "dsa_indexer_topk_fp8", "sparse_mla_bwd",
            "dsa_rmsnorm_fp8", "dsa_quant_fp8_weight", "dsa_linear_fp8",
-           "dsa_selftest_linear_fp8")
+           "dsa_selftest_linear_fp8", "dsa_cache_append_rope", "mla_tree_fwd", "mla_window_fwd",
+           "mla_window_bwd")
 
 
 def _load(path: str = LIB_PATH):
@@ -100,7 +111,15 @@ def _load(path: str = LIB_PATH):
     lib.dsa_quant_fp8_weight.argtypes = [P, I, I, P, P, P]
     lib.dsa_linear_fp8.argtypes = [P, P, P, P, I, I, I, P, I, P, Z, P]
     lib.dsa_selftest_linear_fp8.argtypes = [P, P, P, P, I, I, I, P, I, I, I, P, Z, P]
-    for f in ("dsa_selftest_linear_fp8", "dsa_rmsnorm_fp8", "dsa_quant_fp8_weight", "dsa_linear_fp8",
+    rows = ctypes.POINTER(_Rows)
+    lib.dsa_cache_append_rope.argtypes = [P, P, rows, rows, P, P, I, P, P, P, P, I, P, P, I, I, I, I,
+                                          I, I, ctypes.c_float, P, Z, P]
+    lib.mla_tree_fwd.argtypes = [P, rows, P, P, P, I, I, I, I, ctypes.c_float, P, P, P, Z, P]
+    lib.mla_window_fwd.argtypes = [P, rows, P, P, I, I, I, I, I, I, ctypes.c_float, P, P, P, Z, P]
+    lib.mla_window_bwd.argtypes = [P, rows, P, P, I, I, I, I, I, I, ctypes.c_float, P, P, P, P, P,
+                                   P, Z, P]
+    for f in ("dsa_cache_append_rope", "mla_tree_fwd", "mla_window_fwd", "mla_window_bwd",
+              "dsa_selftest_linear_fp8", "dsa_rmsnorm_fp8", "dsa_quant_fp8_weight", "dsa_linear_fp8",
               "sparse_mla_bwd", "dsa_workspace_init", "dsa_read_device_status", "dsa_indexer_topk",
               "sparse_mla_fwd", "mla_gate_apply", "dsa_cache_append", "sparse_mla_fwd_sink",
               "dsa_selftest_wait_timeout", "dsa_quant_fp8", "dsa_cache_append_fp8",
@@ -609,3 +628,261 @@ def dsa_linear_fp8(codes, scale, w_codes, w_scale, out=None, out_dtype=torch.bfl
     if code:
         raise DsaError(code, "dsa_linear_fp8")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Rotated positions, and dense attention over latent rows
+# ---------------------------------------------------------------------------
+
+_I32, _I64 = torch.int32, torch.int64
+
+
+def _rows_on(rows, B: int, width: int, need_rows: int, dev: int, name: str):
+    """Refuse a row store that does not hold BF16 rows of `width`, at least `need_rows` of
+    each of B sequences, on the device."""
+    if not isinstance(rows, Rows):
+        raise TypeError(f"{name} must be Rows")
+    base, table = rows.base, rows.block_table
+    if base.dtype is not _BF16:
+        raise TypeError(f"{name} must hold bfloat16 rows, got {base.dtype}")
+    if base.shape[2] != width:
+        raise ValueError(f"{name} must hold rows of {width}, got {base.shape[2]}")
+    if base.get_device() != dev or (table is not None and table.get_device() != dev):
+        raise DsaError(DSA_ERR_INVALID_ARGUMENT, f"{name} must be on cuda:{dev}")
+    if table is not None:
+        if table.dim() != 2 or table.shape[0] < B:
+            raise ValueError(f"{name}'s block_table must be [B, max_pages]")
+    elif (B - 1) * rows.seq_stride + need_rows > base.shape[0] * base.shape[1]:
+        raise ValueError(f"{name} has fewer rows than {B} sequences of {need_rows} every "
+                         f"{rows.seq_stride}")
+
+
+def _operands(call: str, dev: int, operands):
+    """Refuse a call unless every operand (tensor, types, shape, name) has one of its types,
+    its shape, is contiguous and on the device."""
+    try:
+        for t, dtypes, shape, _ in operands:
+            if (t.dtype not in dtypes or t.shape != shape or not t.is_contiguous()
+                    or t.get_device() != dev):
+                _refuse(call, dev, *operands)
+    except AttributeError:
+        _refuse(call, dev, *operands)
+
+
+def _shape4(t, name: str, last: int):
+    if t.dim() != 4 or t.shape[3] != last:
+        raise ValueError(f"{name} must be [B, T, H, {last}], got {list(t.shape)}")
+    if max(t.shape) >= _SIZES:
+        _too_large(name, B=t.shape[0], T=t.shape[1], H=t.shape[2])
+    return t.shape[:3]
+
+
+def _int32(call: str, **sizes):
+    for name, v in sizes.items():
+        if not isinstance(v, int):
+            raise TypeError(f"{name} must be an int")
+        if v >= 1 << 31 or v < -(1 << 31):
+            raise DsaError(DSA_ERR_UNSUPPORTED, f"{call}: {name} = {v}")
+
+
+def _workspace_for(workspace, dev: int, stream, raw: int, *sizes):
+    if workspace is not None:
+        return workspace
+    need = workspace_bytes(*sizes)
+    workspace = _empty((need,), _U8, dev, stream)
+    _check(lib.dsa_workspace_init(workspace.data_ptr(), need, raw), "dsa_workspace_init")
+    return workspace
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def dsa_cache_append_rope(k_pre, kv_new, k_cache: Rows, kv_cache: Rows, q_start, rope, pos=None,
+                          n_new=None, q_pe=None, q_lat=None, q_idx=None, q_idx_out=None,
+                          kv_style: int = ROPE_HALVES, key_style: int = ROPE_HALVES,
+                          eps: float = INDEXER_KEY_EPS, workspace=None, stream=None):
+    """dsa_cache_append with rotated positions.  k_pre [B,Tq,D_I] float32, kv_new [B,Tq,576]
+    bf16, caches as Rows (written in place), q_start [B] int32, rope [n_pos,64] float32 (32
+    cosines, 32 sines per position), pos [B,Tq] int32 (None: q_start[b]+i), n_new [B] int32
+    tokens that are there (None: Tq).  q_pe [B,Tq,H,64] bf16 is rotated into dims 512..575 of
+    q_lat [B,Tq,H,576] bf16; q_idx [B,Tq,H_I,D_I] bf16 into q_idx_out (None: in place).
+    Returns the workspace (its status word holds any BAD_INDEX)."""
+    dev = _device(k_pre, "k_pre")
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return dsa_cache_append_rope(k_pre, kv_new, k_cache, kv_cache, q_start, rope, pos, n_new,
+                                         q_pe, q_lat, q_idx, q_idx_out, kv_style, key_style, eps,
+                                         workspace, stream)
+    raw = _stream_on(dev, stream)
+    if k_pre.dim() != 3:
+        raise ValueError("k_pre must be [B, Tq, D_I]")
+    B, Tq, D_I = k_pre.shape
+    if max(B, Tq, D_I) >= _SIZES:
+        _too_large("dsa_cache_append_rope", B=B, Tq=Tq, D_I=D_I)
+    if not isinstance(rope, torch.Tensor):
+        raise TypeError("rope must be a torch.Tensor")
+    if rope.dim() != 2 or rope.shape[0] >= _SIZES:
+        raise ValueError("rope must be [n_pos, 64], n_pos below 2^30")
+    if (q_pe is None) != (q_lat is None):
+        raise ValueError("q_pe and q_lat go together")
+    if q_idx is None and q_idx_out is not None:
+        raise ValueError("q_idx_out needs q_idx")
+    H = H_I = 0
+    workspace = _workspace_for(workspace, dev, stream, raw, OP_CACHE_APPEND, B, Tq, 0, 0, 0)
+    operands = [(k_pre, (_F32,), k_pre.shape, "k_pre"), (kv_new, (_BF16,), (B, Tq, RLAT), "kv_new"),
+                (q_start, (_I32,), (B,), "q_start"),
+                (rope, (_F32,), (rope.shape[0], ROPE_DIMS), "rope")]
+    if pos is not None:
+        operands.append((pos, (_I32,), (B, Tq), "pos"))
+    if n_new is not None:
+        operands.append((n_new, (_I32,), (B,), "n_new"))
+    if q_pe is not None:
+        _device(q_pe, "q_pe")
+        _, _, H = _shape4(q_pe, "q_pe", ROPE_DIMS)
+        operands += [(q_pe, (_BF16,), (B, Tq, H, ROPE_DIMS), "q_pe"),
+                     (q_lat, (_BF16,), (B, Tq, H, RLAT), "q_lat")]
+    if q_idx is not None:
+        _device(q_idx, "q_idx")
+        _, _, H_I = _shape4(q_idx, "q_idx", D_I)
+        if q_idx_out is None:
+            q_idx_out = q_idx
+        operands += [(q_idx, (_BF16,), (B, Tq, H_I, D_I), "q_idx"),
+                     (q_idx_out, (_BF16,), (B, Tq, H_I, D_I), "q_idx_out")]
+    operands.append((workspace, (_U8,), getattr(workspace, "shape", None), "workspace"))
+    _operands("dsa_cache_append_rope", dev, operands)
+    _rows_on(k_cache, B, D_I, k_cache.seq_stride if isinstance(k_cache, Rows) else 0, dev, "k_cache")
+    _rows_on(kv_cache, B, RLAT, kv_cache.seq_stride if isinstance(kv_cache, Rows) else 0, dev,
+             "kv_cache")
+    kr, vr = k_cache.c(), kv_cache.c()
+    code = lib.dsa_cache_append_rope(
+        k_pre.data_ptr(), kv_new.data_ptr(), kr, vr, q_start.data_ptr(), rope.data_ptr(),
+        rope.shape[0], _at(pos), _at(n_new), _at(q_pe), _at(q_lat), H, _at(q_idx), _at(q_idx_out),
+        H_I, B, Tq, D_I, kv_style, key_style, eps, workspace.data_ptr(), workspace.numel(), raw)
+    if code:
+        raise DsaError(code, "dsa_cache_append_rope")
+    return workspace
+
+
+def mla_tree_fwd(q_lat, kv: Rows, tree, kv_len, max_kv_len: int, n_draft=None,
+                 scale: float = MLA_SCALE, o_lat=None, lse=None, want_lse: bool = True,
+                 workspace=None, stream=None):
+    """Dense attention of drafted tokens over a latent cache.  q_lat [B,T,H,576] bf16, kv Rows
+    (width 576) with the prefix's kv_len[b] rows and then the drafted tokens', tree [B,T]
+    int64 (bit j of tree[b,i]: token i sees drafted token j), kv_len [B] int32, n_draft [B]
+    int32 drafted tokens that are there (None: T) -> (o_lat [B,T,H,512] bf16, lse [B,T,H]
+    float32 or None); outputs of tokens that are not there stay as they were (a new o_lat
+    and lse: zeros)."""
+    dev = _device(q_lat, "q_lat")
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return mla_tree_fwd(q_lat, kv, tree, kv_len, max_kv_len, n_draft, scale, o_lat, lse,
+                                want_lse, workspace, stream)
+    raw = _stream_on(dev, stream)
+    B, T, H = _shape4(q_lat, "q_lat", RLAT)
+    _int32("mla_tree_fwd", max_kv_len=max_kv_len)
+    if o_lat is None:
+        o_lat = _empty((B, T, H, VLAT), _BF16, dev, stream)
+        if n_draft is not None:
+            _zero(o_lat, stream)
+    if lse is None and want_lse:
+        lse = _empty((B, T, H), _F32, dev, stream)
+        if n_draft is not None:
+            _zero(lse, stream)
+    workspace = _workspace_for(workspace, dev, stream, raw, OP_MLA_TREE, B, T, max_kv_len, H, 0)
+    operands = [(q_lat, (_BF16,), q_lat.shape, "q_lat"), (tree, (_I64,), (B, T), "tree"),
+                (kv_len, (_I32,), (B,), "kv_len"), (o_lat, (_BF16,), (B, T, H, VLAT), "o_lat"),
+                (workspace, (_U8,), getattr(workspace, "shape", None), "workspace")]
+    if n_draft is not None:
+        operands.append((n_draft, (_I32,), (B,), "n_draft"))
+    if lse is not None:
+        operands.append((lse, (_F32,), (B, T, H), "lse"))
+    _operands("mla_tree_fwd", dev, operands)
+    _rows_on(kv, B, RLAT, max_kv_len, dev, "kv")
+    code = lib.mla_tree_fwd(q_lat.data_ptr(), kv.c(), tree.data_ptr(), kv_len.data_ptr(),
+                            _at(n_draft), B, T, H, max_kv_len, scale, o_lat.data_ptr(), _at(lse),
+                            workspace.data_ptr(), workspace.numel(), raw)
+    if code:
+        raise DsaError(code, "mla_tree_fwd")
+    return o_lat, lse
+
+
+def _zero(t, stream):
+    if stream is None:
+        t.zero_()
+    else:
+        with torch.cuda.stream(stream):
+            t.zero_()
+
+
+def mla_window_fwd(q_lat, kv: Rows, q_start, kv_len, window: int, n_first: int, max_kv_len: int,
+                   scale: float = MLA_SCALE, o_lat=None, lse=None, want_lse: bool = True,
+                   workspace=None, stream=None):
+    """Dense attention with a sliding window: the query at position t = q_start[b] + i sees the
+    rows s <= t with s > t - window or s < n_first.  q_lat [B,Tq,H,576] bf16, kv Rows (width
+    576), q_start/kv_len [B] int32 -> (o_lat [B,Tq,H,512] bf16, lse [B,Tq,H] float32 or None)."""
+    dev = _device(q_lat, "q_lat")
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return mla_window_fwd(q_lat, kv, q_start, kv_len, window, n_first, max_kv_len, scale,
+                                  o_lat, lse, want_lse, workspace, stream)
+    raw = _stream_on(dev, stream)
+    B, Tq, H = _shape4(q_lat, "q_lat", RLAT)
+    _int32("mla_window_fwd", window=window, n_first=n_first, max_kv_len=max_kv_len)
+    if o_lat is None:
+        o_lat = _empty((B, Tq, H, VLAT), _BF16, dev, stream)
+    if lse is None and want_lse:
+        lse = _empty((B, Tq, H), _F32, dev, stream)
+    workspace = _workspace_for(workspace, dev, stream, raw, OP_MLA_WINDOW, B, Tq, max_kv_len, H,
+                               min(window + n_first, max_kv_len))
+    operands = [(q_lat, (_BF16,), q_lat.shape, "q_lat"), (q_start, (_I32,), (B,), "q_start"),
+                (kv_len, (_I32,), (B,), "kv_len"), (o_lat, (_BF16,), (B, Tq, H, VLAT), "o_lat"),
+                (workspace, (_U8,), getattr(workspace, "shape", None), "workspace")]
+    if lse is not None:
+        operands.append((lse, (_F32,), (B, Tq, H), "lse"))
+    _operands("mla_window_fwd", dev, operands)
+    _rows_on(kv, B, RLAT, max_kv_len, dev, "kv")
+    code = lib.mla_window_fwd(q_lat.data_ptr(), kv.c(), q_start.data_ptr(), kv_len.data_ptr(), B, Tq,
+                              H, window, n_first, max_kv_len, scale, o_lat.data_ptr(), _at(lse),
+                              workspace.data_ptr(), workspace.numel(), raw)
+    if code:
+        raise DsaError(code, "mla_window_fwd")
+    return o_lat, lse
+
+
+def mla_window_bwd(q_lat, kv: Rows, q_start, kv_len, window: int, n_first: int, max_kv_len: int,
+                   o_lat, lse, d_o, scale: float = MLA_SCALE, dq=None, dkv=None, workspace=None,
+                   stream=None):
+    """Backward of mla_window_fwd: (dq [B,Tq,H,576] bf16, dkv bf16 like kv's rows [B,S,576])
+    from the forward's o_lat and lse and the gradient d_o [B,Tq,H,512] bf16.  kv contiguous.
+    Rows 0..kv_len[b]-1 of dkv are written, the rows behind them left as they were (a new
+    dkv: zeros)."""
+    dev = _device(q_lat, "q_lat")
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return mla_window_bwd(q_lat, kv, q_start, kv_len, window, n_first, max_kv_len, o_lat, lse,
+                                  d_o, scale, dq, dkv, workspace, stream)
+    raw = _stream_on(dev, stream)
+    B, Tq, H = _shape4(q_lat, "q_lat", RLAT)
+    _int32("mla_window_bwd", window=window, n_first=n_first, max_kv_len=max_kv_len)
+    _rows_on(kv, B, RLAT, max_kv_len, dev, "kv")
+    if dq is None:
+        dq = _empty((B, Tq, H, RLAT), _BF16, dev, stream)
+    if dkv is None:
+        dkv = _empty(kv.base.shape, _BF16, dev, stream)
+        _zero(dkv, stream)
+    workspace = _workspace_for(workspace, dev, stream, raw, OP_MLA_WINDOW_BWD, B, Tq, max_kv_len, H,
+                               min(window + n_first, max_kv_len))
+    _operands("mla_window_bwd", dev, [
+        (q_lat, (_BF16,), q_lat.shape, "q_lat"), (q_start, (_I32,), (B,), "q_start"),
+        (kv_len, (_I32,), (B,), "kv_len"), (o_lat, (_BF16,), (B, Tq, H, VLAT), "o_lat"),
+        (lse, (_F32,), (B, Tq, H), "lse"), (d_o, (_BF16,), (B, Tq, H, VLAT), "d_o"),
+        (dq, (_BF16,), (B, Tq, H, RLAT), "dq"), (dkv, (_BF16,), kv.base.shape, "dkv"),
+        (workspace, (_U8,), getattr(workspace, "shape", None), "workspace")])
+    code = lib.mla_window_bwd(q_lat.data_ptr(), kv.c(), q_start.data_ptr(), kv_len.data_ptr(), B, Tq,
+                              H, window, n_first, max_kv_len, scale, o_lat.data_ptr(), lse.data_ptr(),
+                              d_o.data_ptr(), dq.data_ptr(), dkv.data_ptr(), workspace.data_ptr(),
+                              workspace.numel(), raw)
+    if code:
+        raise DsaError(code, "mla_window_bwd")
+    return dq, dkv

@@ -9,6 +9,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "dense.h"
 #include "dsa_status.cuh"
 #include "internal.h"
 #include "projection.h"
@@ -170,6 +171,13 @@ size_t dsa_workspace_bytes(dsa_op_t op, int B, int Tq, int max_kv_len, int heads
       // P and dZ of up to 512 queries at a time for the tensor-core kernels
       const int64_t nq = static_cast<int64_t>(B) * Tq;
       extra = static_cast<size_t>(nq < 512 ? nq : 512) * sparse_mla_bwd_tc_query_bytes(topk);
+    }
+    if (heads > 0) {
+      const int64_t span = topk > 0 && topk < max_kv_len ? topk : max_kv_len;
+      if (op == DSA_OP_MLA_TREE) extra = dense_scratch_bytes(B, Tq, heads, max_kv_len);
+      if (op == DSA_OP_MLA_WINDOW) extra = dense_scratch_bytes(B, Tq, heads, span);
+      if (op == DSA_OP_MLA_WINDOW_BWD)
+        extra = window_bwd_scratch_bytes(B, Tq, heads, max_kv_len, span);
     }
   }
   return kWorkspaceHeader + ((extra + 255) / 256) * 256;
@@ -509,6 +517,157 @@ dsa_status_t dsa_cache_append_fp8(const float* k_pre, const uint16_t* kv_new,
   if (k_scale == nullptr) return DSA_ERR_INVALID_ARGUMENT;
   return cache_append(k_pre, kv_new, k_codes, k_scale, kv_cache, q_start, B, Tq, D_I, eps,
                       workspace, ws_bytes, stream);
+}
+
+dsa_status_t dsa_cache_append_rope(const float* k_pre, const uint16_t* kv_new,
+                                   const dsa_rows_t* k_cache, const dsa_rows_t* kv_cache,
+                                   const int32_t* q_start, const float* rope, int n_pos,
+                                   const int32_t* pos, const int32_t* n_new, const uint16_t* q_pe,
+                                   uint16_t* q_lat, int H, const uint16_t* q_idx,
+                                   uint16_t* q_idx_out, int H_I, int B, int Tq, int D_I,
+                                   dsa_rope_t kv_style, dsa_rope_t key_style, float eps,
+                                   void* workspace, size_t ws_bytes, dsa_stream_t stream) {
+  if (!k_pre || !kv_new || !q_start || !rope) return DSA_ERR_INVALID_ARGUMENT;
+  if ((q_pe != nullptr) != (q_lat != nullptr) || (q_idx != nullptr) != (q_idx_out != nullptr))
+    return DSA_ERR_INVALID_ARGUMENT;
+  // a null pointer counts as aligned
+  if (!aligned(k_pre, 16) || !aligned(kv_new, 16) || !aligned(rope, 16) || !aligned(q_pe, 16) ||
+      !aligned(q_lat, 16) || !aligned(q_idx, 16) || !aligned(q_idx_out, 16) ||
+      !aligned(q_start, 4) || !aligned(pos, 4) || !aligned(n_new, 4))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (B <= 0 || Tq <= 0 || n_pos <= 0 || !(eps >= 0.f) || !(eps < 3.0e38f) ||
+      (q_pe != nullptr && H <= 0) || (q_idx != nullptr && H_I <= 0))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (kv_style < DSA_ROPE_NONE || kv_style > DSA_ROPE_PAIRS || key_style < DSA_ROPE_NONE ||
+      key_style > DSA_ROPE_PAIRS)
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (D_I != 64 && D_I != 128) return DSA_ERR_UNSUPPORTED;
+  if ((q_pe != nullptr && H > 1024) || (q_idx != nullptr && H_I > 1024)) return DSA_ERR_UNSUPPORTED;
+  // at most 49 CTAs a token
+  if (static_cast<int64_t>(B) * Tq >= (int64_t(1) << 25)) return DSA_ERR_UNSUPPORTED;
+  AppendRopeArgs a{};
+  dsa_status_t st = resolve_rows(k_cache, B, 0, D_I, &a.k_cache);
+  if (st != DSA_OK) return st;
+  st = resolve_rows(kv_cache, B, 0, kRlat, &a.kv_cache);
+  if (st != DSA_OK) return st;
+  st = check_ws(workspace, ws_bytes, kWorkspaceHeader);
+  if (st != DSA_OK) return st;
+  a.k_pre = k_pre;
+  a.kv_new = kv_new;
+  a.q_start = q_start;
+  a.rope = rope;
+  a.n_pos = n_pos;
+  a.pos = pos;
+  a.n_new = n_new;
+  a.q_pe = q_pe;
+  a.q_lat = q_lat;
+  a.H = H;
+  a.q_idx = q_idx;
+  a.q_idx_out = q_idx_out;
+  a.H_I = H_I;
+  a.B = B;
+  a.Tq = Tq;
+  a.D_I = D_I;
+  a.kv_style = kv_style;
+  a.key_style = key_style;
+  a.eps = eps;
+  a.status = static_cast<uint32_t*>(workspace);
+  return cache_append_rope_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// What the tree, the window and its backward pass check alike.
+static dsa_status_t dense_args(const uint16_t* q_lat, const dsa_rows_t* kv, const int32_t* pos0,
+                               const int32_t* lim, int B, int T, int H, int max_kv_len,
+                               float scale, const uint16_t* o_lat, const float* lse, dsa_op_t op,
+                               int64_t span, void* workspace, size_t ws_bytes, DenseArgs* a) {
+  if (!q_lat || !pos0 || !o_lat) return DSA_ERR_INVALID_ARGUMENT;
+  if (!aligned(q_lat, 16) || !aligned(o_lat, 16) || !aligned(lse, 4) || !aligned(pos0, 4) ||
+      !aligned(lim, 4))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (B <= 0 || T <= 0 || H <= 0 || max_kv_len <= 0) return DSA_ERR_INVALID_ARGUMENT;
+  if (!(scale > 0.f) || !(scale < 3.0e38f)) return DSA_ERR_INVALID_ARGUMENT;
+  if (H > 128) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * T * H >= (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
+  dsa_status_t st = resolve_rows(kv, B, max_kv_len, kRlat, &a->kv);
+  if (st != DSA_OK) return st;
+  st = check_ws(workspace, ws_bytes,
+                dsa_workspace_bytes(op, B, T, max_kv_len, H,
+                                    static_cast<int>(span < max_kv_len ? span : max_kv_len)));
+  if (st != DSA_OK) return st;
+  a->q_lat = q_lat;
+  a->pos0 = pos0;
+  a->lim = lim;
+  a->B = B;
+  a->T = T;
+  a->H = H;
+  a->max_kv_len = max_kv_len;
+  a->scale = scale;
+  a->o_lat = const_cast<uint16_t*>(o_lat);
+  a->lse = const_cast<float*>(lse);
+  a->status = static_cast<uint32_t*>(workspace);
+  a->scratch = static_cast<uint8_t*>(workspace) + kWorkspaceHeader;
+  a->scratch_bytes = ws_bytes - kWorkspaceHeader;
+  return DSA_OK;
+}
+
+dsa_status_t mla_tree_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const uint64_t* tree,
+                          const int32_t* kv_len, const int32_t* n_draft, int B, int T, int H,
+                          int max_kv_len, float scale, uint16_t* o_lat, float* lse,
+                          void* workspace, size_t ws_bytes, dsa_stream_t stream) {
+  if (!tree || !aligned(tree, 8)) return DSA_ERR_INVALID_ARGUMENT;
+  if (T > 64) return DSA_ERR_UNSUPPORTED;
+  DenseArgs a{};
+  dsa_status_t st = dense_args(q_lat, kv, kv_len, n_draft, B, T, H, max_kv_len, scale, o_lat, lse,
+                               DSA_OP_MLA_TREE, max_kv_len, workspace, ws_bytes, &a);
+  if (st != DSA_OK) return st;
+  a.tree = tree;
+  return dense_fwd_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static dsa_status_t window_args(int window, int n_first, const int32_t* kv_len, int64_t* span) {
+  if (!kv_len || window < 0 || n_first < 0) return DSA_ERR_INVALID_ARGUMENT;
+  *span = static_cast<int64_t>(window) + n_first;
+  if (*span == 0) *span = 1;
+  return DSA_OK;
+}
+
+dsa_status_t mla_window_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const int32_t* q_start,
+                            const int32_t* kv_len, int B, int Tq, int H, int window, int n_first,
+                            int max_kv_len, float scale, uint16_t* o_lat, float* lse,
+                            void* workspace, size_t ws_bytes, dsa_stream_t stream) {
+  int64_t span = 0;
+  dsa_status_t st = window_args(window, n_first, kv_len, &span);
+  if (st != DSA_OK) return st;
+  DenseArgs a{};
+  st = dense_args(q_lat, kv, q_start, kv_len, B, Tq, H, max_kv_len, scale, o_lat, lse,
+                  DSA_OP_MLA_WINDOW, span, workspace, ws_bytes, &a);
+  if (st != DSA_OK) return st;
+  a.window = window;
+  a.n_first = n_first;
+  return dense_fwd_launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t mla_window_bwd(const uint16_t* q_lat, const dsa_rows_t* kv, const int32_t* q_start,
+                            const int32_t* kv_len, int B, int Tq, int H, int window, int n_first,
+                            int max_kv_len, float scale, const uint16_t* o_lat, const float* lse,
+                            const uint16_t* d_o, uint16_t* dq, uint16_t* dkv, void* workspace,
+                            size_t ws_bytes, dsa_stream_t stream) {
+  int64_t span = 0;
+  dsa_status_t st = window_args(window, n_first, kv_len, &span);
+  if (st != DSA_OK) return st;
+  if (!lse || !d_o || !dq || !dkv || !aligned(d_o, 16) || !aligned(dq, 16) || !aligned(dkv, 16))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (kv != nullptr && kv->block_table != nullptr) return DSA_ERR_UNSUPPORTED;
+  WindowBwdArgs a{};
+  st = dense_args(q_lat, kv, q_start, kv_len, B, Tq, H, max_kv_len, scale, o_lat, lse,
+                  DSA_OP_MLA_WINDOW_BWD, span, workspace, ws_bytes, &a.f);
+  if (st != DSA_OK) return st;
+  a.f.window = window;
+  a.f.n_first = n_first;
+  a.d_o = d_o;
+  a.dq = dq;
+  a.dkv = dkv;
+  return window_bwd_launch(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

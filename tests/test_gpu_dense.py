@@ -1,0 +1,478 @@
+"""GPU tests of mla_tree_fwd, mla_window_fwd and mla_window_bwd against plain 64-bit forms
+(dense_ref.py: the formulas and the bounds)."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import dense_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+SENTINEL = 77.0
+
+
+@pytest.fixture(scope="module")
+def dsa():
+    import sparse_attention_serving_gb300 as m
+    return m
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _normal(gen, *shape, scale=1.0):
+    return (torch.randn(shape, generator=gen, device="cuda") * scale).to(torch.bfloat16)
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _store(dsa, base, gen, is_paged):
+    if not is_paged:
+        return dsa.Rows(base), base, None
+    pool, table = ref.paged(base, gen)
+    return dsa.Rows(pool, table), pool, table
+
+
+def _outputs(B, T, H):
+    return (torch.full((B, T, H, 512), SENTINEL, dtype=torch.bfloat16, device="cuda"),
+            torch.full((B, T, H), SENTINEL, device="cuda"))
+
+
+def _ok(dsa, ws):
+    assert dsa.read_device_status(ws)[0] == dsa.DSA_OK
+
+
+# ---------------------------------------------------------------------------
+# window
+# ---------------------------------------------------------------------------
+
+WINDOW_CASES = [
+    # B, Tq, H, q_start, window, n_first, paged
+    (1, 1, 96, [0], 1, 0, False),                  # the very first token
+    (1, 1, 96, [0], 512, 4, True),
+    (3, 1, 96, [5, 511, 700], 512, 4, True),       # decode, around the window's length
+    (2, 1, 96, [3000, 64], 1000, 70, True),
+    (5, 1, 8, [63, 64, 65, 127, 128], 64, 1, True),
+    (1, 1, 1, [257], 100, 3, False),
+    (2, 1, 128, [300, 40], 129, 0, True),
+    (2, 5, 96, [60, 0], 64, 0, False),             # a page boundary inside the queries
+    (1, 130, 8, [0], 1, 0, False),                 # every query its own row
+    (2, 77, 8, [0, 200], 33, 5, False),
+    (1, 200, 96, [0], 64, 0, False),
+    (1, 67, 96, [450], 300, 16, True),
+    (2, 33, 17, [100, 129], 128, 200, False),      # first tokens and window meet
+    (1, 50, 128, [0], 1000, 0, True),              # window longer than the sequence
+    (1, 9, 40, [500], 128, 4, True),
+    (2, 20, 96, [30, 0], 0, 3, False),             # first tokens only
+    (2, 3, 96, [70, 0], 0, 0, False),              # nothing at all
+    (1, 300, 3, [77], 64, 64, False),
+    (1, 4, 96, [4000], 2 ** 31 - 1, 2 ** 31 - 1, True),   # everything
+    (70, 3, 5, [i * 7 for i in range(70)], 90, 2, True),
+]
+
+
+def _window_case(dsa, case, seed, values=1.0):
+    B, Tq, H, start, window, first, is_paged = case
+    gen = _gen(seed)
+    S = max(start) + Tq
+    base = _normal(gen, B, S, 576, scale=values)
+    base[:, :1] *= 2
+    for b in range(B):
+        base[b, start[b] + Tq:] = math.nan           # behind the sequence: anything
+    rows, store, table = _store(dsa, base, gen, is_paged)
+    q = _normal(gen, B, Tq, H, 576)
+    return base, rows, q, _i32(start), _i32([v + Tq for v in start]), S
+
+
+@pytest.mark.parametrize("case", WINDOW_CASES, ids=str)
+def test_window_forward(dsa, case):
+    B, Tq, H, start, window, first, _ = case
+    base, rows, q, qs, kl, S = _window_case(dsa, case, 1)
+    o, lse = _outputs(B, Tq, H)
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_WINDOW, B, Tq, S, H, min(window + first, S)))
+    dsa.mla_window_fwd(q, rows, qs, kl, window, first, S, o_lat=o, lse=lse, workspace=ws)
+    _ok(dsa, ws)
+    for b in range(B):
+        n = start[b] + Tq
+        see = ref.window_sees(torch.arange(start[b], n, device="cuda")[:, None],
+                              torch.arange(n, device="cuda"), window, first)
+        r_o, r_lse, o_off, lse_off = ref.forward(q[b], base[b, :n], see)
+        ref.within(o[b], r_o, o_off, f"o_lat of sequence {b}")
+        ref.within(lse[b], r_lse, lse_off, f"lse of sequence {b}")
+
+
+def test_window_forward_makes_its_outputs(dsa):
+    case = (2, 19, 8, [4, 0], 7, 1, False)
+    base, rows, q, qs, kl, S = _window_case(dsa, case, 2)
+    o, lse = dsa.mla_window_fwd(q, rows, qs, kl, 7, 1, S)
+    o2, none = dsa.mla_window_fwd(q, rows, qs, kl, 7, 1, S, want_lse=False)
+    assert none is None and torch.equal(o, o2) and lse.shape == (2, 19, 8)
+
+
+@pytest.mark.parametrize("rise", [20.0, 600.0])
+def test_window_forward_rising_scores(dsa, rise):
+    """Scores that rise along the sequence by far more than an exponent holds: the softmax's
+    reference has to move."""
+    gen = _gen(3)
+    B, Tq, H, S = 1, 130, 8, 900
+    q = _normal(gen, B, Tq, H, 576)
+    q[..., 0] = 16.0
+    base = _normal(gen, B, S, 576)
+    # dim 0 of row s: score rise * s / S, exactly representable steps
+    base[0, :, 0] = (torch.arange(S, device="cuda") / S * rise / (16 * ref.SCALE)).to(torch.bfloat16)
+    start = S - Tq
+    o, lse = dsa.mla_window_fwd(q, dsa.Rows(base), _i32([start]), _i32([S]), 700, 4, S)
+    see = ref.window_sees(torch.arange(start, S, device="cuda")[:, None],
+                          torch.arange(S, device="cuda"), 700, 4)
+    r_o, r_lse, o_off, lse_off = ref.forward(q[0], base[0], see)
+    ref.within(o[0], r_o, o_off, "o_lat")
+    ref.within(lse[0], r_lse, lse_off, "lse")
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_window_row_reaches_only_who_sees_it(dsa, value):
+    """A row that holds an infinity or a NaN: queries whose window has left it are clean."""
+    case = (1, 40, 8, [100], 16, 2, False)
+    base, rows, q, qs, kl, S = _window_case(dsa, case, 4)
+    clean, _ = dsa.mla_window_fwd(q, rows, qs, kl, 16, 2, S)
+    at = 104
+    base[0, at, 100] = value
+    got, lse = dsa.mla_window_fwd(q, rows, qs, kl, 16, 2, S)
+    t = torch.arange(100, 140, device="cuda")
+    sees = (t >= at) & (t < at + 16)
+    assert torch.equal(got[0, ~sees], clean[0, ~sees])
+    assert not torch.isfinite(lse[0, sees] + got[0, sees].float().sum(-1)).all()
+
+
+def test_window_drops_pages_between(dsa):
+    """Pages that no query sees may be gone from the table; one that is seen and is outside
+    the pool is flagged, its rows not seen."""
+    case = (1, 1, 96, [1000], 100, 4, True)
+    base, rows, q, qs, kl, S = _window_case(dsa, case, 5)
+    want, _ = dsa.mla_window_fwd(q, rows, qs, kl, 100, 4, S)
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_WINDOW, 1, 1, S, 96, 104))
+    rows.block_table[0, 1:14] = -7                      # rows 64..895
+    got, _ = dsa.mla_window_fwd(q, rows, qs, kl, 100, 4, S, workspace=ws)
+    _ok(dsa, ws)
+    assert torch.equal(got, want)
+    rows.block_table[0, 15] = 10 ** 6                   # rows 960..1000
+    got, lse = dsa.mla_window_fwd(q, rows, qs, kl, 100, 4, S, workspace=ws)
+    assert dsa.read_device_status(ws)[0] == dsa.DSA_ERR_BAD_INDEX
+    see = ref.window_sees(torch.tensor([[1000]], device="cuda"), torch.arange(S, device="cuda"), 100, 4)
+    see[:, 960:] = False
+    r_o, r_lse, o_off, lse_off = ref.forward(q[0], base[0], see)
+    ref.within(got[0], r_o, o_off, "o_lat")
+    ref.within(lse[0], r_lse, lse_off, "lse")
+
+
+def test_window_bad_lengths_are_flagged(dsa):
+    """Queries beyond kv_len, a kv_len beyond max_kv_len, a negative start: nothing seen."""
+    gen = _gen(6)
+    q = _normal(gen, 4, 3, 8, 576)
+    base = _normal(gen, 4, 40, 576)
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_WINDOW, 4, 3, 40, 8, 9))
+    qs, kl = _i32([10, 38, -1, 30]), _i32([13, 40, 5, 41])
+    o, lse = dsa.mla_window_fwd(q, dsa.Rows(base), qs, kl, 8, 1, 40, workspace=ws)
+    assert dsa.read_device_status(ws)[0] == dsa.DSA_ERR_BAD_INDEX
+    assert torch.isfinite(lse[0]).all() and torch.isfinite(lse[1, :2]).all()
+    for bad in (lse[1, 2:], lse[2], lse[3]):
+        assert (bad == -math.inf).all()
+    for bad in (o[1, 2:], o[2], o[3]):
+        assert (bad == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# tree
+# ---------------------------------------------------------------------------
+
+def _masks(seed, B, T, kind):
+    pick = torch.Generator()
+    pick.manual_seed(seed)
+    out = []
+    for _ in range(B):
+        sees = []
+        for j in range(T):
+            if kind == "any":                          # any bits at all, later tokens' too
+                v = sum(1 << k for k in range(64) if torch.randint(0, 2, (), generator=pick))
+            else:
+                parent = int(torch.randint(-1, j, (), generator=pick)) if j else -1
+                v = (sees[parent] if parent >= 0 else 0) | 1 << j
+            sees.append(v)
+        out.append([0 if kind == "none" else v - (1 << 64) if v >> 63 else v for v in sees])
+    return torch.tensor(out, dtype=torch.int64, device="cuda")
+
+
+TREE_CASES = [
+    # B, T, H, prefix, n_draft, masks, paged
+    (1, 1, 96, [0], None, "tree", False),
+    (1, 1, 96, [1], None, "tree", True),
+    (4, 1, 96, [63, 64, 700, 2049], None, "tree", True),
+    (2, 1, 8, [5000, 31], None, "tree", True),
+    (3, 1, 128, [200, 0, 129], None, "tree", False),
+    (2, 8, 96, [1000, 60], None, "tree", True),
+    (3, 7, 8, [0, 64, 130], [7, 0, 3], "tree", False),
+    (2, 33, 8, [100, 3], [33, 20], "tree", True),
+    (2, 64, 3, [61, 500], None, "tree", True),
+    (1, 64, 96, [90], None, "any", False),
+    (2, 16, 40, [0, 10], None, "none", False),        # prefix or nothing
+    (2, 5, 96, [0, 0], [5, 2], "any", True),
+    (1, 3, 1, [300], None, "tree", False),
+]
+
+
+def _tree_case(dsa, case, seed):
+    B, T, H, prefix, n_draft, kind, is_paged = case
+    gen = _gen(seed)
+    S = max(prefix) + T
+    base = _normal(gen, B, S, 576)
+    n = n_draft or [T] * B
+    for b in range(B):
+        base[b, prefix[b] + n[b]:] = math.nan
+    rows, store, table = _store(dsa, base, gen, is_paged)
+    return base, rows, _normal(gen, B, T, H, 576), _masks(seed, B, T, kind), n, S
+
+
+def _tree_sees(masks, prefix, n, T):
+    """[n, prefix + T]"""
+    bits = torch.tensor([[v >> j & 1 for j in range(T)] for v in masks.tolist()],
+                        dtype=torch.bool, device="cuda")
+    bits[:, n:] = False
+    return torch.cat([torch.ones((T, prefix), dtype=torch.bool, device="cuda"), bits], 1)[:n]
+
+
+@pytest.mark.parametrize("case", TREE_CASES, ids=str)
+def test_tree_forward(dsa, case):
+    B, T, H, prefix, n_draft, _, _ = case
+    base, rows, q, masks, n, S = _tree_case(dsa, case, 11)
+    o, lse = _outputs(B, T, H)
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_TREE, B, T, S, H, 0))
+    dsa.mla_tree_fwd(q, rows, masks, _i32(prefix), S, n_draft=None if n_draft is None else _i32(n_draft),
+                     o_lat=o, lse=lse, workspace=ws)
+    _ok(dsa, ws)
+    for b in range(B):
+        see = _tree_sees(masks[b], prefix[b], n[b], T)[:, :prefix[b] + n[b]]
+        r_o, r_lse, o_off, lse_off = ref.forward(q[b, :n[b]], base[b, :prefix[b] + n[b]], see)
+        ref.within(o[b, :n[b]], r_o, o_off, f"o_lat of sequence {b}")
+        ref.within(lse[b, :n[b]], r_lse, lse_off, f"lse of sequence {b}")
+        assert (o[b, n[b]:] == SENTINEL).all() and (lse[b, n[b]:] == SENTINEL).all()
+
+
+def test_tree_sibling_with_nan_is_not_seen(dsa):
+    """Drafted token 1's row is a NaN: only the tokens that see it are touched."""
+    case = (1, 4, 96, [70], None, "tree", False)
+    base, rows, q, _, _, S = _tree_case(dsa, case, 12)
+    masks = torch.tensor([[1, 2 | 1, 4 | 1, 8 | 2 | 1]], dtype=torch.int64, device="cuda")
+    clean, clean_lse = dsa.mla_tree_fwd(q, rows, masks, _i32([70]), S)
+    base[0, 71] = math.nan
+    o, lse = dsa.mla_tree_fwd(q, rows, masks, _i32([70]), S)
+    assert torch.equal(o[0, [0, 2]], clean[0, [0, 2]]) and torch.equal(lse[0, [0, 2]], clean_lse[0, [0, 2]])
+    assert torch.isnan(o[0, [1, 3]]).all()
+
+
+def test_tree_bad_lengths_are_flagged(dsa):
+    gen = _gen(13)
+    q, base = _normal(gen, 4, 3, 8, 576), _normal(gen, 4, 40, 576)
+    masks = _masks(13, 4, 3, "tree")
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_TREE, 4, 3, 40, 8, 0))
+    o, lse = dsa.mla_tree_fwd(q, dsa.Rows(base), masks, _i32([37, 38, -1, 30]), 40,
+                              n_draft=_i32([3, 3, 1, 4]), workspace=ws)
+    assert dsa.read_device_status(ws)[0] == dsa.DSA_ERR_BAD_INDEX
+    assert torch.isfinite(lse[0]).all() and torch.isfinite(lse[3]).all()
+    assert (lse[1] == -math.inf).all() and (lse[2, 0] == -math.inf).all() and (o[1] == 0).all()
+
+
+def test_tree_of_one_chain_is_the_window_without_end(dsa):
+    """A chain of drafted tokens sees what causal queries see."""
+    gen = _gen(14)
+    q, base = _normal(gen, 1, 6, 96, 576), _normal(gen, 1, 206, 576)
+    chain = torch.tensor([[(1 << i + 1) - 1 for i in range(6)]], dtype=torch.int64, device="cuda")
+    o, lse = dsa.mla_tree_fwd(q, dsa.Rows(base), chain, _i32([200]), 206)
+    w, w_lse = dsa.mla_window_fwd(q, dsa.Rows(base), _i32([200]), _i32([206]), 1000, 0, 206)
+    see = ref.window_sees(torch.arange(200, 206, device="cuda")[:, None],
+                          torch.arange(206, device="cuda"), 1000, 0)
+    _, _, o_off, lse_off = ref.forward(q[0], base[0], see)
+    ref.within(o[0], w[0].double(), 2 * o_off, "o_lat")
+    ref.within(lse[0], w_lse[0].double(), 2 * lse_off, "lse")
+
+
+# ---------------------------------------------------------------------------
+# backward
+# ---------------------------------------------------------------------------
+
+BWD_CASES = [
+    # B, Tq, H, q_start, window, n_first
+    (1, 1, 96, [0], 1, 0),
+    (1, 1, 1, [200], 65, 2),
+    (2, 7, 8, [0, 130], 5, 1),
+    (1, 130, 8, [0], 64, 0),
+    (1, 70, 96, [0], 33, 3),
+    (2, 40, 96, [100, 0], 70, 16),
+    (1, 20, 128, [64], 20, 0),
+    (1, 150, 17, [3], 100, 130),
+    (1, 33, 40, [0], 1000, 0),
+    (2, 5, 96, [70, 0], 0, 3),
+    (2, 5, 3, [70, 0], 0, 0),
+    (1, 300, 2, [0], 2 ** 31 - 1, 0),
+]
+
+
+def _bwd_case(dsa, case, seed):
+    B, Tq, H, start, window, first = case
+    base, rows, q, qs, kl, S = _window_case(dsa, (*case, False), seed)
+    gen = _gen(seed + 1)
+    d_o = _normal(gen, B, Tq, H, 512)
+    o = torch.empty((B, Tq, H, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((B, Tq, H), device="cuda")
+    sees = []
+    for b in range(B):
+        n = start[b] + Tq
+        see = ref.window_sees(torch.arange(start[b], n, device="cuda")[:, None],
+                              torch.arange(n, device="cuda"), window, first)
+        r_o, r_lse, _, _ = ref.forward(q[b], base[b, :n], see)
+        o[b], lse[b] = r_o.to(torch.bfloat16), r_lse.float()
+        sees.append(see)
+    return base, rows, q, qs, kl, S, o, lse, d_o, sees
+
+
+@pytest.mark.parametrize("case", BWD_CASES, ids=str)
+def test_window_backward(dsa, case):
+    B, Tq, H, start, window, first = case
+    base, rows, q, qs, kl, S, o, lse, d_o, sees = _bwd_case(dsa, case, 21)
+    dq = torch.full((B, Tq, H, 576), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    dkv = torch.full((B, S, 576), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_WINDOW_BWD, B, Tq, S, H, min(window + first, S)))
+    dsa.mla_window_bwd(q, rows, qs, kl, window, first, S, o, lse, d_o, dq=dq, dkv=dkv, workspace=ws)
+    _ok(dsa, ws)
+    for b in range(B):
+        n = start[b] + Tq
+        r_dq, r_dkv, dq_off, dkv_off = ref.backward(q[b], base[b, :n], sees[b], o[b], lse[b], d_o[b])
+        ref.within(dq[b], r_dq, dq_off, f"dq of sequence {b}")
+        ref.within(dkv[b, :n], r_dkv, dkv_off, f"dkv of sequence {b}")
+        assert (dkv[b, n:] == SENTINEL).all()
+
+
+def test_window_backward_against_differences(dsa):
+    """Along random directions of q and of the rows: the kernel's gradients against central
+    differences of the 64-bit forward."""
+    case = (1, 40, 8, [10], 12, 2)
+    base, rows, q, qs, kl, S, o, lse, d_o, sees = _bwd_case(dsa, case, 23)
+    dq, dkv = dsa.mla_window_bwd(q, rows, qs, kl, 12, 2, S, o, lse, d_o)
+    _, _, dq_off, dkv_off = ref.backward(q[0], base[0], sees[0], o[0], lse[0], d_o[0])
+    gen = _gen(24)
+    q64, kv64, g64 = q[0].double(), base[0].double(), d_o[0].double()
+
+    def value(qq, kk):
+        return float((ref.forward(qq, kk, sees[0])[0] * g64).sum())
+
+    # what rounding o_lat to BF16 does to d_o . o_lat, and so to each dz
+    p = torch.exp(torch.einsum("thr,nr->thn", q64, kv64) * ref.SCALE - lse[0].double()[..., None])
+    p = torch.where(sees[0][:, None], p, 0.0)
+    D_off = ref.HALF * torch.einsum("thv,thv->th", g64.abs(), o[0].double().abs())
+    z_off = ref.SCALE * p * D_off[..., None]
+    dq_off = dq_off + torch.einsum("thn,nr->thr", z_off, kv64.abs())
+    dkv_off = dkv_off + torch.einsum("thn,thr->nr", z_off, q64.abs())
+    for _ in range(4):
+        u = torch.randn(q64.shape, generator=gen, device="cuda", dtype=torch.float64)
+        w = torch.randn(kv64.shape, generator=gen, device="cuda", dtype=torch.float64)
+        e = 1e-4
+        for got, off, d, f in ((dq[0], dq_off, u, lambda x: value(q64 + x * u, kv64)),
+                               (dkv[0], dkv_off, w, lambda x: value(q64, kv64 + x * w))):
+            slope = (8 * (f(e) - f(-e)) - (f(2 * e) - f(-2 * e))) / (12 * e)
+            along = float((got.double() * d).sum())
+            assert abs(slope - along) <= float((off * d.abs()).sum()) + 1e-6 * abs(slope)
+
+
+def test_window_backward_follows_its_forward(dsa):
+    """Forward and backward as a training step runs them, with an accumulated loss."""
+    gen = _gen(25)
+    B, Tq, H, S, window, first = 2, 90, 96, 90, 40, 4
+    base, q = _normal(gen, B, S, 576), _normal(gen, B, Tq, H, 576)
+    d_o = _normal(gen, B, Tq, H, 512)
+    rows, qs, kl = dsa.Rows(base), _i32([0, 0]), _i32([S, S])
+    need = max(dsa.workspace_bytes(op, B, Tq, S, H, window + first)
+               for op in (dsa.OP_MLA_WINDOW, dsa.OP_MLA_WINDOW_BWD))
+    ws = dsa.new_workspace(need)
+    o, lse = dsa.mla_window_fwd(q, rows, qs, kl, window, first, S, workspace=ws)
+    dq, dkv = dsa.mla_window_bwd(q, rows, qs, kl, window, first, S, o, lse, d_o, workspace=ws)
+    _ok(dsa, ws)
+    t = torch.arange(S, device="cuda")
+    see = ref.window_sees(t[:, None], t, window, first)
+    for b in range(B):
+        r_dq, r_dkv, dq_off, dkv_off = ref.backward(q[b], base[b], see, o[b], lse[b], d_o[b])
+        ref.within(dq[b], r_dq, dq_off, "dq")
+        ref.within(dkv[b], r_dkv, dkv_off, "dkv")
+
+
+def test_window_backward_bad_sequence(dsa):
+    """A sequence whose length is out of range: dq = 0, its dkv untouched, the others right."""
+    gen = _gen(26)
+    q, base, d_o = _normal(gen, 2, 3, 8, 576), _normal(gen, 2, 40, 576), _normal(gen, 2, 3, 8, 512)
+    qs, kl = _i32([10, 30]), _i32([13, 41])
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_WINDOW_BWD, 2, 3, 40, 8, 9))
+    o = torch.zeros((2, 3, 8, 512), dtype=torch.bfloat16, device="cuda")
+    dkv = torch.full((2, 40, 576), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    dq, _ = dsa.mla_window_bwd(q, dsa.Rows(base), qs, kl, 8, 1, 40, o, torch.zeros((2, 3, 8), device="cuda"),
+                               d_o, dkv=dkv, workspace=ws)
+    assert dsa.read_device_status(ws)[0] == dsa.DSA_ERR_BAD_INDEX
+    assert (dq[1] == 0).all() and (dkv[1] == SENTINEL).all()
+    assert (dkv[0, 13:] == SENTINEL).all() and (dkv[0, 3:13] != SENTINEL).any()
+
+
+# ---------------------------------------------------------------------------
+# both: equal bits, graphs, streams
+# ---------------------------------------------------------------------------
+
+def test_equal_calls_give_equal_bits(dsa):
+    case = (2, 100, 96, [0, 37], 50, 4, False)
+    base, rows, q, qs, kl, S = _window_case(dsa, case, 31)
+    first = dsa.mla_window_fwd(q, rows, qs, kl, 50, 4, S)
+    for _ in range(3):
+        again = dsa.mla_window_fwd(q, rows, qs, kl, 50, 4, S)
+        assert all(torch.equal(x, y) for x, y in zip(first, again))
+    d_o = _normal(_gen(32), 2, 100, 96, 512)
+    base = torch.nan_to_num(base)
+    rows = dsa.Rows(base)
+    grads = dsa.mla_window_bwd(q, rows, qs, kl, 50, 4, S, *first, d_o)
+    for _ in range(3):
+        again = dsa.mla_window_bwd(q, rows, qs, kl, 50, 4, S, *first, d_o)
+        assert all(torch.equal(x, y) for x, y in zip(grads, again))
+
+
+def test_streams_and_graphs(dsa):
+    """Two calls at once on streams of their own, and a captured call replayed on new inputs."""
+    gen = _gen(33)
+    S, H = 3000, 96
+    base = _normal(gen, 2, S, 576)
+    rows, kl = dsa.Rows(base), _i32([S - 4, 1000])
+    masks = _masks(33, 2, 4, "tree")
+    qs = [_normal(gen, 2, 4, H, 576) for _ in range(2)]
+    need = dsa.workspace_bytes(dsa.OP_MLA_TREE, 2, 4, S, H, 0)
+    work = [dsa.new_workspace(need) for _ in range(2)]
+    want = [dsa.mla_tree_fwd(q, rows, masks, kl, S) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        got[k] = dsa.mla_tree_fwd(qs[k], rows, masks, kl, S, workspace=work[k], stream=streams[k])
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        assert all(torch.equal(x, y) for x, y in zip(got[k], want[k]))
+    q = qs[0].clone()
+    o, lse = _outputs(2, 4, H)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dsa.mla_tree_fwd(q, rows, masks, kl, S, o_lat=o, lse=lse, workspace=work[0])
+    q.copy_(qs[1])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[1][0]) and torch.equal(lse, want[1][1])
+    for ws in work:
+        _ok(dsa, ws)
