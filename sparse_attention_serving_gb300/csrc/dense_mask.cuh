@@ -101,6 +101,15 @@ __device__ __forceinline__ Pages pages_of(const Mask& m, const Seq& s, int i0, i
   return p;
 }
 
+// The rows kb..kb+63 that any of the queries i0..i1 may see.
+__device__ __forceinline__ uint64_t span_mask(const Mask& m, const Seq& s, int i0, int i1, int kb) {
+  if (!s.ok) return 0;
+  if (m.tree != nullptr) return range_bits(0, s.L, kb);
+  const int t0 = s.pos0 + i0, t1 = min(s.pos0 + i1, s.L - 1);
+  return range_bits(t0 - m.window + 1, m.window > 0 ? t1 + 1 : 0, kb) |
+         range_bits(0, min(m.n_first, t1 + 1), kb);
+}
+
 struct Store {
   const uint16_t* base;
   int64_t seq_stride;

@@ -4,28 +4,80 @@
 //   z_s = scale * q_lat[t,h,:] . KV[s,:]  over the rows s that query t sees,
 //   o = sum_s softmax(z)_s KV[s, 0:512],   lse = log sum_s exp(z_s)
 //
-// One warp per (query, head): each lane holds dims 64c + 2 lane (+1) of the query,
-// the running maximum and sum of the softmax go along with the rows.
+// The (query, head) rows of a sequence are packed: a unit is 2R consecutive ones
+// (R = 96, or 48 where a sequence has no more than 96), done by a pair of CTAs.
+// Rows of the cache come 64 at a time (a page), a block is two such pages.
+//   S [R rows per CTA x 128 keys] = Q . K^T      cta_group::2, M = 256, N = 128:
+//        each CTA holds its own R queries (the MMA's other 128 - R rows alias what
+//        lies behind them and are not read) and the keys of one of the two pages
+//   O^T [512 x 2R] += V^T . P^T                  cta_group::2, M = 256, N = 2R, twice:
+//        CTA c holds dims 256c .. 256c+255 of all 128 keys and P of its own rows,
+//        and accumulates its dims of all 2R rows
+// in TMEM columns 0 .. 4R-1 (O^T) and 128 more (S).  Transposing the value product
+// is what makes room: 512 dims of 96 rows would be all of a CTA's TMEM the other
+// way round.  Sharing the keys between two CTAs halves what the score product reads
+// of them through the shared-memory port: per block 216 KB (S) + 112 KB (O^T) are
+// read, 136 KB copied in and 24 KB of P written, about 3,800 cycles at 128 bytes,
+// beside 3,840 cycles of MMAs (R = 96).
+//
+// Roles (8 warps): 0 copies Q and K, 1 copies V, 2 and 3 of the even CTA issue the
+// two products, 4..7 hold a row a thread: its 128 scores, P = 2^(z - m) to BF16 in
+// shared memory.  m is the maximum of the first block in which the row sees
+// anything, so O^T is never rescaled; a row whose later scores exceed it by 2^100
+// sends its unit to attend_row.  So does a row that one query of the unit sees and
+// another does not and that holds an infinity or a NaN (0 * NaN would reach both).
+// Rows of a page that nobody in the unit sees are zeroed in V before use.
+//
+// Few units: the blocks of a unit are split over several pairs, and combine_kernel
+// joins their normalised FP32 outputs by their log-sum-exps, in order.
 #include <cmath>
 
 #include <cuda_bf16.h>
 
+#include "cluster.cuh"
 #include "dense_mask.cuh"
-#include "sm103.cuh"
 
 namespace dsa {
 namespace dense {
 
-constexpr int WARPS = 8;
+constexpr int WARPS = 8, THREADS = WARPS * 32;
+constexpr int CHUNK = 64 * 128;           // 64 rows x 64 dims
+constexpr float FAR = 100.f;              // exponents that P may reach
+
+template <int R_>
+struct Cfg {
+  static constexpr int R = R_;
+  static constexpr int NK = R == 96 ? 5 : 8;          // K slots: a chunk of own keys
+  static constexpr int NV = R == 96 ? 3 : 5;          // V slots: 64 keys x 128 dims
+  static constexpr int QCH = R * 128;                 // 64 dims of the queries
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_P = OFF_Q + 9 * QCH;
+  static constexpr int OFF_K = OFF_P + 2 * QCH;
+  static constexpr int OFF_V = OFF_K + NK * CHUNK;
+  static constexpr int OFF_MISC = OFF_V + NV * 2 * CHUNK;
+  static constexpr int SMEM = OFF_MISC + 1536 + 1024;
+  static constexpr uint32_t S_COL = 4 * R;
+  static_assert(SMEM <= 232448, "shared memory");
+  static_assert(OFF_Q + 8 * QCH + 128 * 128 <= OFF_K, "the aliased rows stay inside Q and P");
+  static_assert(4 * R + 128 <= 512, "TMEM columns");
+};
+
+enum : uint32_t {
+  SITE_Q = 0x710, SITE_KF = 0x711, SITE_KE = 0x712, SITE_VF = 0x713, SITE_VE = 0x714,
+  SITE_SF = 0x715, SITE_SE = 0x716, SITE_P = 0x717, SITE_O = 0x718, SITE_VT = 0x719,
+  SITE_DRAIN = 0x71a
+};
 
 struct Params {
   const uint16_t* q;
   Store kv;
   Mask m;
-  int B, H;
+  int B, H, tiles, splits;
   float scale_log2;
   uint16_t* o;
   float* lse;
+  float* part_o;      // [unit, split, 2R, 512] normalised
+  float* part_lse;    // [unit, split, 2R] base 2
   uint32_t* status;
 };
 
@@ -36,44 +88,40 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
-__global__ void __launch_bounds__(WARPS * 32) rows_kernel(const Params p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(p.B) * p.m.T * p.H) return;
-  const int64_t qi = row / p.H;
-  const int b = static_cast<int>(qi / p.m.T), i = static_cast<int>(qi % p.m.T);
-  const Seq s = seq_of(p.m, b);
-  if (row % (static_cast<int64_t>(p.m.T) * p.H) == 0 && lane == 0) report_seq(p.m, s, b, p.status);
-  if (i >= s.n) return;
-  const uint64_t bits = p.m.tree != nullptr ? __ldg(p.m.tree + qi) : 0;
+// One row by a warp over pages k0..k1-1 of `pages`, in FP32 with a running maximum:
+// for what the products above cannot give.  Into o / lse, or (part) the partials.
+__device__ __noinline__ void attend_row(const Params& p, const Seq& s, const Pages& pages, int k0,
+                                        int k1, int b, int row, float* part_o, float* part_lse) {
+  const int lane = threadIdx.x & 31, i = row / p.H;
+  const int64_t at = static_cast<int64_t>(b) * p.m.T * p.H + row;
+  const uint64_t bits = p.m.tree != nullptr ? p.m.tree[static_cast<int64_t>(b) * p.m.T + i] : 0;
   float q[18], acc[16];
-  const uint32_t* qr = reinterpret_cast<const uint32_t*>(p.q + row * kRlat) + lane;
+  const uint32_t* qr = reinterpret_cast<const uint32_t*>(p.q + at * kRlat) + lane;
 #pragma unroll
   for (int c = 0; c < 9; ++c) {
-    const uint32_t v = __ldg(qr + 32 * c);
+    const uint32_t v = qr[32 * c];
     q[2 * c] = lo_f(v), q[2 * c + 1] = hi_f(v);
   }
 #pragma unroll
   for (int d = 0; d < 16; ++d) acc[d] = 0.f;
   float top = -INFINITY, sum = 0.f;
-  const Pages pages = pages_of(p.m, s, i, i);
-  for (int k = 0; k < pages.count(); ++k) {
+  for (int k = k0; k < k1; ++k) {
     const int pg = pages.page(k);
-    uint64_t see = row_mask(p.m, s, i, bits, pg * 64);
-    if (see == 0) continue;
     const int64_t r0 = page_row(p.kv, b, pg);
-    if (r0 < 0) {
-      if (lane == 0) status_raise(p.status, DSA_ERR_BAD_INDEX, SITE_PAGE, static_cast<uint32_t>(pg));
-      continue;
-    }
-    for (; see != 0; see &= see - 1) {
+    if (r0 < 0) continue;
+    for (uint64_t see = row_mask(p.m, s, i, bits, pg * 64); see != 0; see &= see - 1) {
       const int64_t r = r0 + __ffsll(static_cast<long long>(see)) - 1;
       const uint32_t* kr = reinterpret_cast<const uint32_t*>(p.kv.base + r * kRlat) + lane;
       float x[18], z = 0.f;
 #pragma unroll
       for (int c = 0; c < 9; ++c) {
-        const uint32_t v = __ldg(kr + 32 * c);
+        const uint32_t v = kr[32 * c];
         x[2 * c] = lo_f(v), x[2 * c + 1] = hi_f(v);
         z = fmaf(q[2 * c], x[2 * c], fmaf(q[2 * c + 1], x[2 * c + 1], z));
       }
@@ -91,28 +139,553 @@ __global__ void __launch_bounds__(WARPS * 32) rows_kernel(const Params p) {
       for (int d = 0; d < 16; ++d) acc[d] = fmaf(e, x[d], acc[d]);
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-  uint32_t* o = reinterpret_cast<uint32_t*>(p.o + row * kVlat) + lane;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+  if (part_o != nullptr) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c) o[32 * c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-  if (lane == 0 && p.lse != nullptr)
+    for (int c = 0; c < 8; ++c)
+      reinterpret_cast<float2*>(part_o)[32 * c + lane] = make_float2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+    if (lane == 0) *part_lse = lse2;
+  } else {
+    uint32_t* o = reinterpret_cast<uint32_t*>(p.o + at * kVlat) + lane;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[32 * c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+    if (lane == 0 && p.lse != nullptr) p.lse[at] = lse2 * 0.6931471805599453f;
+  }
+}
+
+// A bounded wait by a whole warp; false (for all lanes) once the CTA has given up.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* s_abort,
+                                     uint32_t* status, uint32_t where) {
+  auto test = [&] { return CLUSTER ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity); };
+  bool ok = test();
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+      for (int k = 0; k < 16 && !ok; ++k) ok = test();
+      if (ok || *s_abort != 0) break;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        status_raise(status, DSA_ERR_DEVICE_TIMEOUT, where);
+        *s_abort = 1;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// A ring's slot and the parity of its current use.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) slot = 0, ph ^= 1;
+  }
+};
+
+template <int R>
+__global__ void __launch_bounds__(THREADS, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                const Params p) {
+  using C = Cfg<R>;
+  constexpr uint32_t IDESC_S = idesc_bf16(256, 128, false, false);
+  constexpr uint32_t IDESC_O = idesc_bf16(256, 2 * R, true, false);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_align1024(smem_raw);
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);   // even CTA
+  uint64_t* kempty = kfull + C::NK;
+  uint64_t* vfull = kempty + C::NK;                                  // even CTA
+  uint64_t* vempty = vfull + C::NV;
+  uint64_t* qfull = vempty + C::NV;                                  // even CTA
+  uint64_t* sfull = qfull + 1;
+  uint64_t* sfree = qfull + 2;                                       // even CTA
+  uint64_t* pready = qfull + 3;                                      // even CTA
+  uint64_t* odone = qfull + 4;
+  uint64_t* vland = qfull + 5;                                       // this CTA's own copies
+  uint64_t* drain = qfull + 6;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(qfull + 7);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
+  int* s_slow = reinterpret_cast<int*>(tslot + 2);
+  float* s_inv = reinterpret_cast<float*>(tslot + 4);                // [2R]
+  static_assert((2 * C::NK + 2 * C::NV + 7) * 8 + 16 + 8 * R <= 1536, "misc");
+
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int rank = blockIdx.x & 1;
+  int u = blockIdx.x >> 1;
+  const int sp = u % p.splits;
+  u /= p.splits;
+  const int tile = u % p.tiles, b = u / p.tiles;
+
+  if (tid == 0) {
+    for (int k = 0; k < C::NK; ++k) mbar_init(&kfull[k], 1), mbar_init(&kempty[k], 1);
+    for (int k = 0; k < C::NV; ++k) mbar_init(&vfull[k], 2), mbar_init(&vempty[k], 1);
+    mbar_init(qfull, 1);
+    mbar_init(sfull, 1);
+    mbar_init(sfree, 8);
+    mbar_init(pready, 8);
+    mbar_init(odone, 1);
+    mbar_init(vland, 1);
+    mbar_init(drain, 2);
+    s_abort[0] = 0;
+    s_slow[0] = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_kv);
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(tslot, 512);
+    tmem_relinquish_pair();
+  }
+  const Seq s = seq_of(p.m, b);
+  const int g0 = tile * 2 * R, rows = s.n * p.H;        // rows of the sequence: T * H < 2^31
+  const int i0 = g0 / p.H, i1 = (min(g0 + 2 * R, rows) - 1) / p.H;
+  Pages pages{0, 0, 0};
+  if (g0 < rows) pages = pages_of(p.m, s, i0, i1);
+  const int np = pages.count();
+  const int bps = ((np + 1) / 2 + p.splits - 1) / p.splits;
+  const int k0 = min(2 * sp * bps, np), k1 = min(k0 + 2 * bps, np);   // this unit's pages
+  const int nb = (k1 - k0 + 1) / 2;
+  if (rank == 0 && tid == 0 && tile == 0 && sp == 0) report_seq(p.m, s, b, p.status);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+
+  float l_sum = 0.f, m_ref = -INFINITY;                  // softmax threads
+  if (nb > 0) {
+    if (warp == 0) {
+      // ---- Q, then the own page's K, chunk by chunk ----
+      const uint32_t qbar = mapa_u32(smem_u32(qfull), 0);
+      if (elect_one_lane()) {
+        if (rank == 0) mbar_expect_tx(qfull, 2u * 9u * C::QCH);
+        const int row = static_cast<int>(static_cast<int64_t>(b) * p.m.T * p.H) + g0 + rank * R;
+#pragma unroll 1
+        for (int c = 0; c < 9; ++c)
+          tma_load_2d_pair(sm + C::OFF_Q + c * C::QCH, &tm_q, qbar, 64 * c, row);
+      }
+      __syncwarp();
+      Ring<C::NK> r;
+      int used = 0;
+      bool ok = true;
+      for (int j = 0; j < nb && ok; ++j) {
+        const int k = k0 + 2 * j + rank;
+        int64_t row = -1;
+        if (k < k1) {
+          row = page_row(p.kv, b, pages.page(k));
+          if (row < 0 && lane == 0)
+            status_raise(p.status, DSA_ERR_BAD_INDEX, SITE_PAGE, static_cast<uint32_t>(pages.page(k)));
+        }
+        if (row < 0) row = 0;                            // nobody sees it
+        for (int c = 0; c < 9; ++c) {
+          ok = used < C::NK || wait(&kempty[r.slot], r.ph ^ 1, s_abort, p.status, SITE_KE);
+          if (!ok) break;
+          if (elect_one_lane()) {
+            if (rank == 0) mbar_expect_tx(&kfull[r.slot], 2 * CHUNK);
+            tma_load_2d_pair(sm + C::OFF_K + r.slot * CHUNK, &tm_kv, mapa_u32(smem_u32(&kfull[r.slot]), 0),
+                             64 * c, static_cast<int>(row));
+          }
+          __syncwarp();
+          if (used < C::NK) ++used;
+          r.next();
+        }
+      }
+      // the pair's copies have landed and the last arrivals of the MMAs have come
+      // before either CTA leaves
+      if (rank == 0) wait(qfull, 0, s_abort, p.status, SITE_Q);
+      for (; used > 0; --used) {
+        if (--r.slot < 0) r.slot = C::NK - 1, r.ph ^= 1;
+        if (rank == 0) wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
+        if (ok) wait(&kempty[r.slot], r.ph, s_abort, p.status, SITE_KE);
+      }
+    } else if (warp == 1) {
+      // ---- V: the own 256 dims of both pages, 128 at a time ----
+      Ring<C::NV> r;
+      int used = 0;
+      uint32_t vph = 0;
+      bool ok = true;
+      for (int j = 0; j < nb && ok; ++j) {
+#pragma unroll 1
+        for (int half = 0; half < 2 && ok; ++half) {
+          const int k = k0 + 2 * j + half;
+          int64_t row = -1;
+          uint64_t any = 0;
+          if (k < k1) {
+            row = page_row(p.kv, b, pages.page(k));
+            if (row >= 0) any = span_mask(p.m, s, i0, i1, pages.page(k) * 64);
+          }
+#pragma unroll 1
+          for (int m = 0; m < 2; ++m) {
+            ok = used < C::NV || wait(&vempty[r.slot], r.ph ^ 1, s_abort, p.status, SITE_VE);
+            if (!ok) break;
+            uint8_t* dst = sm + C::OFF_V + r.slot * 2 * CHUNK;
+            const uint32_t bar = mapa_u32(smem_u32(&vfull[r.slot]), 0);
+            const int col = 256 * rank + 128 * m;
+            if (any == ~0ull) {
+              if (elect_one_lane()) {
+                mbar_expect_tx_cluster(bar, 2 * CHUNK);
+                tma_load_2d_pair(dst, &tm_kv, bar, col, static_cast<int>(row));
+                tma_load_2d_pair(dst + CHUNK, &tm_kv, bar, col + 64, static_cast<int>(row));
+              }
+              __syncwarp();
+            } else {
+              // rows that nobody sees become zeros: whatever they hold must not
+              // meet the zeros of P
+              if (any != 0) {
+                if (elect_one_lane()) {
+                  mbar_expect_tx(vland, 2 * CHUNK);
+                  tma_load_2d(dst, &tm_kv, vland, col, static_cast<int>(row));
+                  tma_load_2d(dst + CHUNK, &tm_kv, vland, col + 64, static_cast<int>(row));
+                }
+                __syncwarp();
+                ok = wait(vland, vph, s_abort, p.status, SITE_VT);
+                vph ^= 1;
+                if (!ok) break;
+              }
+#pragma unroll 4
+              for (int e = lane; e < 1024; e += 32)     // 16 bytes of row (e >> 3) & 63
+                if (!(any >> ((e >> 3) & 63) & 1))
+                  reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(bar);
+            }
+            if (used < C::NV) ++used;
+            r.next();
+          }
+        }
+      }
+      for (; used > 0; --used) {
+        if (--r.slot < 0) r.slot = C::NV - 1, r.ph ^= 1;
+        if (rank == 0) wait(&vfull[r.slot], r.ph, s_abort, p.status, SITE_VF);
+        if (ok) wait(&vempty[r.slot], r.ph, s_abort, p.status, SITE_VE);
+      }
+    } else if (warp == 2) {
+      if (rank == 0) {
+        // ---- scores ----
+        const uint64_t qd = smem_desc(smem_u32(sm + C::OFF_Q), 16, 1024);
+        const uint64_t kd = smem_desc(smem_u32(sm + C::OFF_K), 16, 1024);
+        Ring<C::NK> r;
+        bool ok = wait(qfull, 0, s_abort, p.status, SITE_Q);
+        for (int j = 0; j < nb && ok; ++j) {
+          if (j > 0) ok = wait<true>(sfree, (j - 1) & 1, s_abort, p.status, SITE_SE);
+          tc_fence_after();
+          for (int c = 0; c < 9 && ok; ++c) {
+            ok = wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one_lane()) {
+              const uint64_t a = desc_add(qd, c * C::QCH), w = desc_add(kd, r.slot * CHUNK);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16_pair(tmem + C::S_COL, desc_add(a, kk * 32), desc_add(w, kk * 32), IDESC_S,
+                               c > 0 || kk > 0);
+              umma_commit_pair(&kempty[r.slot]);
+              if (c == 8) umma_commit_pair(sfull);
+            }
+            __syncwarp();
+            r.next();
+          }
+        }
+        if (elect_one_lane()) umma_commit_pair(drain);
+        __syncwarp();
+      }
+    } else if (warp == 3) {
+      if (rank == 0) {
+        // ---- values ----
+        const uint64_t pd = smem_desc(smem_u32(sm + C::OFF_P), 16, 1024);
+        const uint64_t vd = smem_desc(smem_u32(sm + C::OFF_V), CHUNK, 1024);
+        Ring<C::NV> r;
+        bool ok = true;
+        for (int j = 0; j < nb && ok; ++j) {
+          ok = wait<true>(pready, j & 1, s_abort, p.status, SITE_P);
+          for (int t = 0; t < 4 && ok; ++t) {            // page t >> 1, dims 128 (t & 1)
+            ok = wait<true>(&vfull[r.slot], r.ph, s_abort, p.status, SITE_VF);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one_lane()) {
+              const uint64_t a = desc_add(vd, r.slot * 2 * CHUNK), w = desc_add(pd, (t >> 1) * C::QCH);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16_pair(tmem + (t & 1) * 2 * R, desc_add(a, kk * 2048), desc_add(w, kk * 32),
+                               IDESC_O, j > 0 || t > 1 || kk > 0);
+              umma_commit_pair(&vempty[r.slot]);
+              if (t == 3) umma_commit_pair(odone);
+            }
+            __syncwarp();
+            r.next();
+          }
+        }
+        if (elect_one_lane()) umma_commit_pair(drain);
+        __syncwarp();
+        // every MMA of the pair is complete before anything is given up
+        wait(drain, 0, s_abort, p.status, SITE_DRAIN);
+      }
+    } else {
+      // ---- softmax: a row a thread ----
+      const int sub = warp & 3, r = sub * 32 + lane, g = g0 + rank * R + r;
+      const bool live = r < R && g < rows;
+      const int i = live ? g / p.H : 0;
+      const uint64_t bits =
+          live && p.m.tree != nullptr ? __ldg(p.m.tree + static_cast<int64_t>(b) * p.m.T + i) : 0;
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + C::S_COL;
+      const uint32_t free_bar = mapa_u32(smem_u32(sfree), 0), p_bar = mapa_u32(smem_u32(pready), 0);
+      uint8_t* prow = sm + C::OFF_P + (r >> 3) * 1024 + (r & 7) * 128;
+      bool slow = false, ok = true;
+      for (int j = 0; j < nb && ok; ++j) {
+        // who sees what of the block's two pages (a row that is not there: all)
+        uint64_t see[2], any[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = k0 + 2 * j + h;
+          see[h] = any[h] = 0;
+          if (k < k1 && page_row(p.kv, b, pages.page(k)) >= 0) {
+            any[h] = span_mask(p.m, s, i0, i1, pages.page(k) * 64);
+            see[h] = live ? row_mask(p.m, s, i, bits, pages.page(k) * 64) : any[h];
+          }
+        }
+        ok = wait(sfull, j & 1, s_abort, p.status, SITE_SF);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t z[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(taddr + 32 * c, z[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait_regs(z[c]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(sfree);
+          else mbar_arrive_cluster_relaxed(free_bar);
+        }
+        const bool full = __all_sync(0xffffffffu, (see[0] & see[1]) == ~0ull);
+        if (!full) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t sees = static_cast<uint32_t>(see[c >> 1] >> (32 * (c & 1)));
+            const uint32_t others = static_cast<uint32_t>(any[c >> 1] >> (32 * (c & 1))) & ~sees;
+            float hidden = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (others >> e & 1) hidden = fmaf(__uint_as_float(z[c][e]), 0.f, hidden);
+              if (!(sees >> e & 1)) z[c][e] = 0xff800000u;
+            }
+            if (hidden != 0.f) slow = true;              // a NaN: somebody else's row holds one
+          }
+        }
+        if (__any_sync(0xffffffffu, m_ref == -INFINITY && (see[0] | see[1]) != 0)) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(z[c][e]));
+          if (m_ref == -INFINITY) m_ref = top * p.scale_log2;
+        }
+        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+        float sums[4] = {0.f, 0.f, 0.f, 0.f}, most = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float a0 = fmaf(__uint_as_float(z[c][e]), p.scale_log2, neg);
+            const float a1 = fmaf(__uint_as_float(z[c][e + 1]), p.scale_log2, neg);
+            most = fmaxf(most, fmaxf(a0, a1));
+            const float p0 = ex2(a0), p1 = ex2(a1);
+            sums[(e >> 1) & 3] += p0 + p1;
+            z[c][e >> 1] = pack_bf16x2(p0, p1);
+          }
+        if (most > FAR) slow = true;
+        l_sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        // P is free once the block before has been multiplied
+        if (j > 0) ok = wait(odone, (j - 1) & 1, s_abort, p.status, SITE_O);
+        if (!ok) break;
+        if (r < R) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(prow + (c >> 1) * C::QCH + (((4 * (c & 1) + q) ^ (r & 7)) << 4)) =
+                  make_uint4(z[c][4 * q], z[c][4 * q + 1], z[c][4 * q + 2], z[c][4 * q + 3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(pready);
+          else mbar_arrive_cluster(p_bar);
+        }
+      }
+      if (ok) ok = wait(odone, (nb - 1) & 1, s_abort, p.status, SITE_O);
+      tc_fence_after();
+      // what the epilogues of both CTAs need of this row
+      if (r < R) {
+        const float inv = ok && l_sum != 0.f ? 1.f / l_sum : 0.f;
+        s_inv[rank * R + r] = inv;
+        st_cluster_u32(smem_u32(&s_inv[rank * R + r]), rank ^ 1, __float_as_uint(inv));
+      }
+      if (__any_sync(0xffffffffu, slow && live) && lane == 0) {
+        s_slow[0] = 1;
+        st_cluster_u32(smem_u32(s_slow), rank ^ 1, 1);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+
+  // ---- epilogue: warp w has dims 256 rank + 128 (w / 4) + 32 (w % 4) + lane ----
+  const int64_t first = static_cast<int64_t>(b) * p.m.T * p.H + g0;
+  const int64_t part = static_cast<int64_t>(blockIdx.x >> 1) * 2 * R;
+  const bool parts = p.splits > 1;
+  const int here = min(2 * R, rows - g0);                // rows of the unit that are there
+  if (s_slow[0]) {
+    for (int r = rank * R + warp; r < min(here, rank * R + R); r += WARPS)
+      attend_row(p, s, pages, k0, k1, b, g0 + r, parts ? p.part_o + (part + r) * kVlat : nullptr,
+                 parts ? p.part_lse + part + r : nullptr);
+  } else {
+    const int sub = warp & 3, m = warp >> 2, dim = 256 * rank + 128 * m + 32 * sub + lane;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + m * 2 * R;
+#pragma unroll 1
+    for (int c0 = 0; c0 < here; c0 += 32) {
+      uint32_t x[32];
+      if (nb > 0) {
+        tmem_ld32(taddr + c0, x);
+        tmem_ld_wait_regs(x);
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        if (c0 + e >= here) break;
+        const float v = nb > 0 ? __uint_as_float(x[e]) * s_inv[c0 + e] : 0.f;
+        if (parts)
+          p.part_o[(part + c0 + e) * kVlat + dim] = v;
+        else
+          p.o[(first + c0 + e) * kVlat + dim] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+      }
+    }
+    const int r = sub * 32 + lane, at = rank * R + r;
+    if (m == 1 && r < R && at < here) {
+      const float lse2 = l_sum == 0.f ? -INFINITY : m_ref + log2f(l_sum);
+      if (parts)
+        p.part_lse[part + at] = lse2;
+      else if (p.lse != nullptr)
+        p.lse[first + at] = lse2 * 0.6931471805599453f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// Joins the splits of a row: lse = log2 sum 2^lse_k, o = sum 2^(lse_k - lse) o_k, in
+// FP32 and in order.  A CTA per row, four dims a thread.
+__global__ void __launch_bounds__(128) combine_kernel(const Params p, int R2) {
+  const int64_t row = blockIdx.x;                        // of all sequences
+  const int per = p.m.T * p.H, b = static_cast<int>(row / per), g = static_cast<int>(row % per);
+  if (g >= seq_of(p.m, b).n * p.H) return;
+  const int64_t unit = static_cast<int64_t>(b) * p.tiles + g / R2;
+  const int64_t at = unit * p.splits * R2 + g % R2;
+  float top = -INFINITY;
+  for (int k = 0; k < p.splits; ++k) top = fmaxf(top, p.part_lse[at + static_cast<int64_t>(k) * R2]);
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < p.splits; ++k) {
+    const int64_t a = at + static_cast<int64_t>(k) * R2;
+    const float l = p.part_lse[a];
+    const float4 v = reinterpret_cast<const float4*>(p.part_o + a * kVlat)[threadIdx.x];
+    if (l == -INFINITY) continue;
+    const float w = exp2f(l - top);
+    sum += w;
+    acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  reinterpret_cast<uint2*>(p.o + row * kVlat)[threadIdx.x] =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (threadIdx.x == 0 && p.lse != nullptr)
     p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Rows per CTA, units and splits.  A unit's blocks are split where the units leave
+// pairs of SMs idle, into parts of at least two blocks.
+struct Plan {
+  int R, tiles, splits;
+};
+Plan plan(int B, int T, int H, int64_t span) {
+  Plan q{};
+  const int64_t rows = static_cast<int64_t>(T) * H;
+  q.R = rows <= 96 ? 48 : 96;
+  q.tiles = static_cast<int>((rows + 2 * q.R - 1) / (2 * q.R));
+  const int64_t units = static_cast<int64_t>(B) * q.tiles, pairs = num_sms() / 2;
+  const int64_t blocks = (span + 2 * q.R / H + 2 + 128) / 128 + 1;
+  int64_t n = pairs / units;
+  if (n > blocks / 2) n = blocks / 2;
+  q.splits = n < 1 ? 1 : static_cast<int>(n);
+  return q;
+}
+
+template <int R>
+dsa_status_t launch(const DenseArgs& a, const Plan& q, const Params& p, cudaStream_t stream) {
+  using C = Cfg<R>;
+  CUtensorMap tq, tk;
+  // contiguous rows: none behind the last sequence's max_kv_len is read
+  const int64_t kv_rows = a.kv.block_table != nullptr
+                              ? a.kv.total_rows
+                              : (a.B - 1) * a.kv.seq_stride + a.max_kv_len;
+  if (!encode_tmap_2d(&tq, a.q_lat, static_cast<uint64_t>(a.B) * a.T * a.H, kRlat, kRlat * 2, 64, R, true) ||
+      !encode_tmap_2d(&tk, a.kv.base, static_cast<uint64_t>(kv_rows), kRlat, kRlat * 2, 64, 64, true))
+    return DSA_ERR_CUDA;
+  if (cudaFuncSetAttribute(pair_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+      cudaSuccess)
+    return launch_status("cudaFuncSetAttribute");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(2ll * a.B * q.tiles * q.splits));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, pair_kernel<R>, tq, tk, p);
+  return launch_status("pair_kernel");
 }
 
 }  // namespace dense
 
 size_t dense_scratch_bytes(int B, int T, int H, int64_t span) {
-  (void)B, (void)T, (void)H, (void)span;
-  return 0;
+  const dense::Plan q = dense::plan(B, T, H, span);
+  if (q.splits == 1) return 0;
+  return static_cast<size_t>(B) * q.tiles * q.splits * 2 * q.R * (kVlat + 1) * sizeof(float);
 }
 
 dsa_status_t dense_fwd_launch(const DenseArgs& a, cudaStream_t stream) {
   using namespace dense;
-  const Params p{a.q_lat, store_of(a), mask_of(a), a.B, a.H, a.scale * 1.4426950408889634f,
-                 a.o_lat, a.lse, a.status};
-  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.H;
-  rows_kernel<<<static_cast<unsigned>((rows + WARPS - 1) / WARPS), WARPS * 32, 0, stream>>>(p);
-  return launch_status("rows_kernel");
+  int64_t span = a.max_kv_len;
+  if (a.tree == nullptr && static_cast<int64_t>(a.window) + a.n_first < span)
+    span = a.window + a.n_first > 0 ? a.window + a.n_first : 1;
+  const Plan q = plan(a.B, a.T, a.H, span);
+  Params p{a.q_lat, store_of(a), mask_of(a), a.B, a.H, q.tiles, q.splits,
+           a.scale * 1.4426950408889634f, a.o_lat, a.lse, nullptr, nullptr, a.status};
+  if (q.splits > 1) {
+    const size_t rows = static_cast<size_t>(a.B) * q.tiles * q.splits * 2 * q.R;
+    if (a.scratch_bytes < rows * (kVlat + 1) * sizeof(float)) return DSA_ERR_WORKSPACE_TOO_SMALL;
+    p.part_o = static_cast<float*>(a.scratch);
+    p.part_lse = p.part_o + rows * kVlat;
+  }
+  const dsa_status_t st = q.R == 96 ? launch<96>(a, q, p, stream) : launch<48>(a, q, p, stream);
+  if (st != DSA_OK || q.splits == 1) return st;
+  combine_kernel<<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.T * a.H), 128, 0, stream>>>(p, 2 * q.R);
+  return launch_status("combine_kernel");
 }
 
 }  // namespace dsa
