@@ -59,6 +59,20 @@ bool encode_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
                    box_cols, box_rows, swizzle128);
 }
 
+bool encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t z, uint64_t rows, uint64_t cols,
+                    uint32_t box_cols, uint32_t box_rows) {
+  auto enc = encoder();
+  if (enc == nullptr || z == 0 || rows == 0 || cols == 0) return false;
+  cuuint64_t dims[3] = {cols, rows, z};
+  cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                         uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
                         bool swizzle128) {

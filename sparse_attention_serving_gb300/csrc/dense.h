@@ -6,6 +6,11 @@
 
 namespace dsa {
 
+// A dense 3D BF16 tensor map [z, rows, cols] with a {box_cols, box_rows, 1} box and
+// 128-byte swizzle: boxes end with the rows of their z.
+bool encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t z, uint64_t rows, uint64_t cols,
+                    uint32_t box_cols, uint32_t box_rows);
+
 struct AppendRopeArgs {
   const float* k_pre;
   const uint16_t* kv_new;

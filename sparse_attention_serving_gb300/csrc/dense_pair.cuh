@@ -1,0 +1,50 @@
+// dense_pair.cuh -- what the kernels of dense latent attention share beyond cluster.cuh:
+// waits by whole warps that end with their CTA, rings, the exponential.
+#pragma once
+#include "cluster.cuh"
+
+namespace dsa {
+namespace dense {
+
+constexpr int CHUNK = 64 * 128;           // 64 rows x 64 dims in shared memory
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A bounded wait by a whole warp; false (for all lanes) once the CTA has given up.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* s_abort,
+                                     uint32_t* status, uint32_t where) {
+  auto test = [&] { return CLUSTER ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity); };
+  bool ok = test();
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+      for (int k = 0; k < 16 && !ok; ++k) ok = test();
+      if (ok || *s_abort != 0) break;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        status_raise(status, DSA_ERR_DEVICE_TIMEOUT, where);
+        *s_abort = 1;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// A ring's slot and the parity of its current use.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) slot = 0, ph ^= 1;
+  }
+};
+
+}  // namespace dense
+}  // namespace dsa

@@ -34,14 +34,13 @@
 
 #include <cuda_bf16.h>
 
-#include "cluster.cuh"
 #include "dense_mask.cuh"
+#include "dense_pair.cuh"
 
 namespace dsa {
 namespace dense {
 
 constexpr int WARPS = 8, THREADS = WARPS * 32;
-constexpr int CHUNK = 64 * 128;           // 64 rows x 64 dims
 constexpr float FAR = 100.f;              // exponents that P may reach
 
 template <int R_>
@@ -88,12 +87,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // One row by a warp over pages k0..k1-1 of `pages`, in FP32 with a running maximum:
 // for what the products above cannot give.  Into o / lse, or (part) the partials.
 __device__ __noinline__ void attend_row(const Params& p, const Seq& s, const Pages& pages, int k0,
@@ -153,38 +146,6 @@ __device__ __noinline__ void attend_row(const Params& p, const Seq& s, const Pag
     if (lane == 0 && p.lse != nullptr) p.lse[at] = lse2 * 0.6931471805599453f;
   }
 }
-
-// A bounded wait by a whole warp; false (for all lanes) once the CTA has given up.
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* s_abort,
-                                     uint32_t* status, uint32_t where) {
-  auto test = [&] { return CLUSTER ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity); };
-  bool ok = test();
-  if (!ok) {
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-#pragma unroll 1
-      for (int k = 0; k < 16 && !ok; ++k) ok = test();
-      if (ok || *s_abort != 0) break;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        status_raise(status, DSA_ERR_DEVICE_TIMEOUT, where);
-        *s_abort = 1;
-        break;
-      }
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
-}
-
-// A ring's slot and the parity of its current use.
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == N) slot = 0, ph ^= 1;
-  }
-};
 
 template <int R>
 __global__ void __launch_bounds__(THREADS, 1)

@@ -1,142 +1,770 @@
 // mla_window_bwd.cu -- backward pass of windowed dense attention over latent rows.
 //
-// Given the forward's o_lat and lse, and d_o, with z and p as there:
+// Given the forward's o_lat and lse, and d_o, with z as there:
 //   p_s = exp(z_s - lse),  D = d_o . o_lat,  dz_s = scale * p_s (d_o . KV[s, 0:512] - D)
 //   dq = sum_s dz_s KV[s, :],   dkv[s] = sum over the queries that see s of dz_s q + p_s d_o
 //
-// A warp per (query, head) for dq and per row for dkv, dims over the lanes.
+// The (query, head) rows of a sequence are packed into tiles of 128; a tile sees a
+// list of pages (64 rows of the cache).  P and dZ of a (tile, page) are 128 x 64 BF16
+// blocks in the workspace, 128-byte swizzled as the tensor core reads them (rows of
+// 64 keys), so each product below takes them by plain box copies in either order.
+//   prep     D and lse (base 2) of every row
+//   pz       [S^T | dP^T] [256 keys x (128 + 128)] = K . [Q | dO]^T for a tile and four
+//            of its pages: one MMA, M = 256, N = 256 on a pair of CTAs, of which the
+//            even one holds the tile's q and the odd one its d_o (and zeros for the
+//            rotated dims, which have no value part), so neither needs room for both.
+//            A thread has a key and both of its products with a row: p and dz need
+//            no exchange.  Blocks leave from registers.
+//   product  dq: [256 rows x 256 or 320 dims] = dZ . K over the pages of two tiles;
+//            dkv: [256 keys x 256 or 320 dims] = dZ^T . q + P^T . dO over a segment of
+//            the tiles that see the keys.  M = 256 on a pair of CTAs; the 576 dims are
+//            two tasks (0..255; 256..575), as 512 TMEM columns do not hold them.
+//   reduce   dkv's segments, added in order (no atomics: equal calls give equal bits)
+// Tiles go in chunks where P and dZ of all would take more than kChunkBytes.
 #include <cmath>
 
 #include <cuda_bf16.h>
 
 #include "dense_mask.cuh"
-#include "sm103.cuh"
+#include "dense_pair.cuh"
 
 namespace dsa {
 namespace wbw {
 
 using namespace dense;
-constexpr int WARPS = 8;
+
+constexpr int X = 128;                              // rows of a tile
+constexpr int BLOCK = X * 128;                      // bytes of a block: 128 rows x 64 keys
+constexpr int64_t kChunkBytes = int64_t(4) << 30;   // P and dZ at a time
+constexpr int TASKS = 304;                          // dkv tasks aimed at: about four a pair of SMs
+
+enum : uint32_t {
+  SITE_B = 0x720, SITE_KF = 0x721, SITE_KE = 0x722, SITE_AF = 0x723, SITE_AE = 0x724,
+  SITE_F = 0x725, SITE_E = 0x726, SITE_LAND = 0x727, SITE_DONE = 0x728, SITE_DRAIN = 0x729
+};
+
+struct Plan {
+  int RT, RC, np;        // tiles of a sequence, of a chunk; pages a tile may see at most
+  int KT, KF;            // tiles of 256 keys; those that hold first tokens
+  int seg, n_long, n_short, slots;   // tiles of a segment; segments of a key tile that holds first
+                                     // tokens, of another; segments of a sequence
+};
 
 struct Params {
-  const uint16_t* q;
   Store kv;
   Mask m;
   int B, H;
-  float scale;
+  Plan q;
+  int rt0;               // first tile of the chunk
+  float scale, scale_log2;
   const uint16_t* o;
-  const float* lse;
   const uint16_t* d_o;
+  const float* lse;
+  float2* rows;          // [B, T * H] lse (base 2), D
+  uint8_t* pz;           // a block of zeros, then [B, RC, np, P | dZ] blocks
+  float* part;           // [B, slots, 256, 576]
+  float* acc;            // [B, max_kv_len, 576] between chunks
   uint16_t* dq;
   uint16_t* dkv;
+  int first_chunk, last_chunk;
   uint32_t* status;
+
+  // first row (128 bytes each) of a block in the workspace's tensor map
+  __device__ __forceinline__ int64_t block_row(int b, int rt, int k, int which) const {
+    return X + (((static_cast<int64_t>(b) * q.RC + rt - rt0) * q.np + k) * 2 + which) * X;
+  }
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+__device__ __forceinline__ Pages tile_pages(const Params& p, const Seq& s, int rt) {
+  const int rows = s.n * p.H, g = rt * X;
+  if (g >= rows) return Pages{0, 0, 0};
+  return pages_of(p.m, s, g / p.H, (min(g + X, rows) - 1) / p.H);
 }
-// C chunks of 64 dims of a row: dims 64c + 2 lane (+1)
-template <int C>
-__device__ __forceinline__ void load_row(const uint16_t* row, int lane, float (&x)[2 * C]) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(row) + lane;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const uint32_t v = __ldg(r + 32 * c);
-    x[2 * c] = __uint_as_float(v << 16), x[2 * c + 1] = __uint_as_float(v & 0xffff0000u);
-  }
+// Where a page stands in a list, or -1.
+__device__ __forceinline__ int place(const Pages& l, int pg) {
+  return pg < l.head ? pg : pg >= l.tail && pg < l.end ? l.head + pg - l.tail : -1;
 }
-template <int N, int M, int K>
-__device__ __forceinline__ float dot(const float (&x)[M], const float (&y)[K]) {
-  float z = 0.f;
-#pragma unroll
-  for (int d = 0; d < N; ++d) z = fmaf(x[d], y[d], z);
-  return warp_sum(z);
-}
-__device__ __forceinline__ void store_row(uint16_t* row, int lane, const float (&x)[18]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(row) + lane;
-#pragma unroll
-  for (int c = 0; c < 9; ++c) r[32 * c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
+// The chunk's tiles that see some of the keys 256 kt .. 256 kt + 255.
+__device__ __forceinline__ int2 tiles_of(const Params& p, const Seq& s, int kt) {
+  const int64_t s0 = 256ll * kt;
+  const int64_t n = min(s.n, s.L - s.pos0);
+  int64_t lo = max(s0 - s.pos0, int64_t(0));
+  int64_t hi = s0 < p.m.n_first ? n : min(n, s0 + 255 + p.m.window - s.pos0);
+  if (!s.ok || lo >= hi) return make_int2(0, 0);
+  lo = max(lo * p.H / X, static_cast<int64_t>(p.rt0));
+  hi = min((hi * p.H + X - 1) / X, static_cast<int64_t>(p.rt0 + p.q.RC));
+  return lo < hi ? make_int2(static_cast<int>(lo), static_cast<int>(hi)) : make_int2(0, 0);
 }
 
-__global__ void __launch_bounds__(WARPS * 32) dq_kernel(const Params p) {
+__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// A warp per row; also the block of zeros.
+__global__ void __launch_bounds__(256) prep_kernel(const Params p) {
   const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(p.B) * p.m.T * p.H) return;
-  const int64_t qi = row / p.H;
-  const int b = static_cast<int>(qi / p.m.T), i = static_cast<int>(qi % p.m.T);
-  const Seq s = seq_of(p.m, b);
-  if (row % (static_cast<int64_t>(p.m.T) * p.H) == 0 && lane == 0) report_seq(p.m, s, b, p.status);
-  float q[18], d_o[16], o[16], acc[18], x[18];
-  load_row<9>(p.q + row * kRlat, lane, q);
-  load_row<8>(p.d_o + row * kVlat, lane, d_o);
-  load_row<8>(p.o + row * kVlat, lane, o);
-#pragma unroll
-  for (int d = 0; d < 18; ++d) acc[d] = 0.f;
-  const float D = dot<16>(d_o, o), lse = __ldg(p.lse + row);
-  const Pages pages = pages_of(p.m, s, i, i);
-  for (int k = 0; k < pages.count(); ++k) {
-    const int pg = pages.page(k);
-    for (uint64_t see = row_mask(p.m, s, i, 0, pg * 64); see != 0; see &= see - 1) {
-      const int64_t r = page_row(p.kv, b, pg) + __ffsll(static_cast<long long>(see)) - 1;
-      load_row<9>(p.kv.base + r * kRlat, lane, x);
-      const float e = expf(dot<18>(q, x) * p.scale - lse);
-      const float dz = e * (dot<16>(d_o, x) - D) * p.scale;
-#pragma unroll
-      for (int d = 0; d < 18; ++d) acc[d] = fmaf(dz, x[d], acc[d]);
-    }
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (blockIdx.x < BLOCK / (256 * 16))
+    reinterpret_cast<uint4*>(p.pz)[blockIdx.x * 256 + threadIdx.x] = make_uint4(0, 0, 0, 0);
+  const int per = p.m.T * p.H;
+  if (row >= static_cast<int64_t>(p.B) * per) return;
+  if (row % per == 0 && lane == 0) {
+    const int b = static_cast<int>(row / per);
+    report_seq(p.m, seq_of(p.m, b), b, p.status);
   }
-  store_row(p.dq + row * kRlat, lane, acc);
+  const uint4* x = reinterpret_cast<const uint4*>(p.o + row * kVlat) + lane;
+  const uint4* y = reinterpret_cast<const uint4*>(p.d_o + row * kVlat) + lane;
+  float d = 0.f;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const uint4 a = x[32 * c], g = y[32 * c];
+    d = fmaf(lo_f(a.x), lo_f(g.x), fmaf(hi_f(a.x), hi_f(g.x), d));
+    d = fmaf(lo_f(a.y), lo_f(g.y), fmaf(hi_f(a.y), hi_f(g.y), d));
+    d = fmaf(lo_f(a.z), lo_f(g.z), fmaf(hi_f(a.z), hi_f(g.z), d));
+    d = fmaf(lo_f(a.w), lo_f(g.w), fmaf(hi_f(a.w), hi_f(g.w), d));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  if (lane == 0) p.rows[row] = make_float2(p.lse[row] * 1.4426950408889634f, d);
 }
 
-__global__ void __launch_bounds__(WARPS * 32) dkv_kernel(const Params p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-  const int b = static_cast<int>(w / p.m.max_kv_len), r = static_cast<int>(w % p.m.max_kv_len);
-  if (b >= p.B) return;
+// ---------------------------------------------------------------------------
+// pz
+// ---------------------------------------------------------------------------
+struct Pz {
+  static constexpr int NS = 4;                       // slots: 64 dims of 128 keys
+  static constexpr int OFF_B = 0;                    // q or d_o of the tile: 9 chunks of 128 rows
+  static constexpr int OFF_K = 9 * BLOCK;
+  static constexpr int OFF_ROW = OFF_K + NS * BLOCK;
+  static constexpr int OFF_MISC = OFF_ROW + X * 16;
+  static constexpr int SMEM = OFF_MISC + 256 + 1024;
+  static constexpr int THREADS = 384;                // 0 copies, 1 issues, 4..11 form P and dZ
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+__global__ void __launch_bounds__(Pz::THREADS, 1)
+    pz_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+              const __grid_constant__ CUtensorMap tm_kv, const Params p) {
+  using C = Pz;
+  constexpr uint32_t IDESC = idesc_bf16(256, 256, false, false);
+  const int rank = blockIdx.x & 1;
+  const int b = (blockIdx.x >> 1) / p.q.RC, rt = p.rt0 + (blockIdx.x >> 1) % p.q.RC;
   const Seq s = seq_of(p.m, b);
-  if (!s.ok || r >= s.L) return;
-  const int64_t row = static_cast<int64_t>(b) * p.kv.seq_stride + r;
-  float x[18], acc[18], q[18], d_o[16], o[16];
-  load_row<9>(p.kv.base + row * kRlat, lane, x);
+  const Pages pages = tile_pages(p, s, rt);
+  const int np = pages.count(), ng = (np + 3) / 4;
+  if (ng == 0) return;                               // both CTAs
+  const int g0 = rt * X, rows = s.n * p.H;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_align1024(smem_raw);
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);   // even CTA
+  uint64_t* kempty = kfull + C::NS;
+  uint64_t* bfull = kempty + C::NS;                                  // even CTA
+  uint64_t* afull = bfull + 1;
+  uint64_t* afree = afull + 2;                                       // even CTA
+  uint64_t* drain = afree + 2;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
+  float4* s_row = reinterpret_cast<float4*>(sm + C::OFF_ROW);        // lse, D, position
+
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (tid == 0) {
+    for (int k = 0; k < C::NS; ++k) mbar_init(&kfull[k], 1), mbar_init(&kempty[k], 1);
+    mbar_init(bfull, 1);
+    for (int k = 0; k < 2; ++k) mbar_init(&afull[k], 1), mbar_init(&afree[k], 16);
+    mbar_init(drain, 1);
+    s_abort[0] = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(rank == 0 ? &tm_q : &tm_do);
+    tma_prefetch_desc(&tm_kv);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tslot, 512);
+    tmem_relinquish_pair();
+  }
+  if (tid >= 128 && tid < 128 + X) {
+    const int g = g0 + tid - 128;
+    float4 v = make_float4(0.f, 0.f, __int_as_float(-1), 0.f);
+    if (g < rows) {
+      const float2 r = p.rows[static_cast<int64_t>(b) * p.m.T * p.H + g];
+      const int t = s.pos0 + g / p.H;
+      v = make_float4(r.x, r.y, __int_as_float(t < s.L ? t : -1), 0.f);
+    }
+    s_row[tid - 128] = v;
+  }
+  if (rank == 1) {                                   // no value part for the rotated dims
+    for (int e = tid; e < BLOCK / 16; e += C::THREADS)
+      reinterpret_cast<uint4*>(sm + C::OFF_B + 8 * BLOCK)[e] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+
+  if (warp == 0) {
+    const uint32_t bbar = mapa_u32(smem_u32(bfull), 0);
+    if (elect_one_lane()) {
+      if (rank == 0) mbar_expect_tx(bfull, 17u * BLOCK);
+#pragma unroll 1
+      for (int c = 0; c < 9 - rank; ++c)
+        tma_load_3d_pair(sm + C::OFF_B + c * BLOCK, rank == 0 ? &tm_q : &tm_do, bbar, 64 * c, g0, b);
+    }
+    __syncwarp();
+    Ring<C::NS> r;
+    int used = 0;
+    bool ok = true;
+    for (int j = 0; j < ng && ok; ++j) {
+      int row[2];
 #pragma unroll
-  for (int d = 0; d < 18; ++d) acc[d] = 0.f;
-  const int last = min(s.n, s.L - s.pos0);
-  for (int i = max(0, r - s.pos0); i < last; ++i) {
-    if (r >= p.m.n_first && s.pos0 + i - r >= p.m.window) break;
-    for (int h = 0; h < p.H; ++h) {
-      const int64_t qr = (static_cast<int64_t>(b) * p.m.T + i) * p.H + h;
-      load_row<9>(p.q + qr * kRlat, lane, q);
-      load_row<8>(p.d_o + qr * kVlat, lane, d_o);
-      load_row<8>(p.o + qr * kVlat, lane, o);
-      const float e = expf(dot<18>(q, x) * p.scale - __ldg(p.lse + qr));
-      const float dz = e * (dot<16>(d_o, x) - dot<16>(d_o, o)) * p.scale;
+      for (int h = 0; h < 2; ++h) {                  // pages that are not there: any rows
+        const int k = 4 * j + 2 * rank + h;
+        row[h] = static_cast<int>(page_row(p.kv, b, k < np ? pages.page(k) : pages.page(0)));
+      }
+      for (int c = 0; c < 9; ++c) {
+        ok = used < C::NS || wait(&kempty[r.slot], r.ph ^ 1, s_abort, p.status, SITE_KE);
+        if (!ok) break;
+        if (elect_one_lane()) {
+          uint8_t* dst = sm + C::OFF_K + r.slot * BLOCK;
+          const uint32_t bar = mapa_u32(smem_u32(&kfull[r.slot]), 0);
+          if (rank == 0) mbar_expect_tx(&kfull[r.slot], 2 * BLOCK);
+          tma_load_2d_pair(dst, &tm_kv, bar, 64 * c, row[0]);
+          tma_load_2d_pair(dst + CHUNK, &tm_kv, bar, 64 * c, row[1]);
+        }
+        __syncwarp();
+        if (used < C::NS) ++used;
+        r.next();
+      }
+    }
+    if (rank == 0) wait(bfull, 0, s_abort, p.status, SITE_B);
+    for (; used > 0; --used) {
+      if (--r.slot < 0) r.slot = C::NS - 1, r.ph ^= 1;
+      if (rank == 0) wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
+      if (ok) wait(&kempty[r.slot], r.ph, s_abort, p.status, SITE_KE);
+    }
+  } else if (warp == 1 && rank == 0) {
+    const uint64_t kd = smem_desc(smem_u32(sm + C::OFF_K), 16, 1024);
+    const uint64_t bd = smem_desc(smem_u32(sm + C::OFF_B), 16, 1024);
+    Ring<C::NS> r;
+    bool ok = wait(bfull, 0, s_abort, p.status, SITE_B);
+    for (int j = 0; j < ng && ok; ++j) {
+      const int bu = j & 1;
+      if (j > 1) ok = wait<true>(&afree[bu], ((j >> 1) - 1) & 1, s_abort, p.status, SITE_AE);
+      tc_fence_after();
+      for (int c = 0; c < 9 && ok; ++c) {
+        ok = wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one_lane()) {
+          const uint64_t a = desc_add(kd, r.slot * BLOCK), w = desc_add(bd, c * BLOCK);
 #pragma unroll
-      for (int d = 0; d < 18; ++d) acc[d] = fmaf(dz, q[d], acc[d]);
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_pair(tmem + bu * 256, desc_add(a, kk * 32), desc_add(w, kk * 32), IDESC,
+                           c > 0 || kk > 0);
+          umma_commit_pair(&kempty[r.slot]);
+          if (c == 8) umma_commit_pair(&afull[bu]);
+        }
+        __syncwarp();
+        r.next();
+      }
+    }
+    if (elect_one_lane()) umma_commit_pair(drain);
+    __syncwarp();
+    wait(drain, 0, s_abort, p.status, SITE_DRAIN);
+  } else if (warp >= 4) {
+    // ---- a key a thread, 64 of the tile's rows a warp ----
+    const int sub = warp & 3, r0 = (warp - 4) / 4 * 64, key = sub * 32 + lane;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + r0;
+    const uint32_t free_bar = mapa_u32(smem_u32(afree), 0);
+    const int t0 = s.pos0 + g0 / p.H, t1 = s.pos0 + (min(g0 + X, rows) - 1) / p.H;
+    const bool whole = g0 + X <= rows && t1 < s.L;
+    bool ok = true;
+    for (int j = 0; j < ng && ok; ++j) {
+      const int bu = j & 1, k = 4 * j + 2 * rank + (sub >> 1);
+      const int kb = k < np ? pages.page(k) * 64 + (sub & 1) * 32 : 0;   // the warp's first key
+      const int at = kb + lane;
+      const bool all = whole && kb + 31 <= t0 && (kb > t1 - p.m.window || kb + 31 < p.m.n_first);
+      ok = wait(&afull[bu], (j >> 1) & 1, s_abort, p.status, SITE_AF);
+      if (!ok) break;
+      tc_fence_after();
+      // a thread's column of the two blocks: row r at 128 r, 16-byte units xor r
+      uint8_t* dst = p.pz + 128 * p.block_row(b, rt, k, 0) + (key & 7) * 2;
+      const uint32_t unit = (key & 63) >> 3;
+#pragma unroll 1
+      for (int q = 0; q < 64; q += 32) {
+        uint32_t z[32], dp[32];
+        tmem_ld32(taddr + bu * 256 + q, z);
+        tmem_ld32(taddr + bu * 256 + 128 + q, dp);
+        tmem_ld_wait_regs(z);
+        tmem_ld_wait_regs(dp);
+        if (q == 32) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive(&afree[bu]);
+            else mbar_arrive_cluster_relaxed(free_bar + bu * 8);
+          }
+        }
+        if (k < np) {
 #pragma unroll
-      for (int d = 0; d < 16; ++d) acc[d] = fmaf(e, d_o[d], acc[d]);
+          for (int e = 0; e < 32; ++e) {
+            const int r = r0 + q + e;
+            const float4 w = s_row[r];
+            float pr = ex2(fmaf(__uint_as_float(z[e]), p.scale_log2, -w.x));
+            float dz = p.scale * pr * (__uint_as_float(dp[e]) - w.y);
+            if (!all) {
+              const int t = __float_as_int(w.z);
+              const bool sees = at <= t && (t - at < p.m.window || at < p.m.n_first);
+              pr = sees ? pr : 0.f;
+              dz = sees ? dz : 0.f;
+            }
+            uint8_t* to = dst + r * 128 + ((unit ^ (r & 7)) << 4);
+            *reinterpret_cast<uint16_t*>(to) = __bfloat16_as_ushort(__float2bfloat16_rn(pr));
+            *reinterpret_cast<uint16_t*>(to + BLOCK) = __bfloat16_as_ushort(__float2bfloat16_rn(dz));
+          }
+        }
+      }
     }
   }
-  store_row(p.dkv + row * kRlat, lane, acc);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// product
+// ---------------------------------------------------------------------------
+struct Prod {
+  static constexpr int NS = 5;
+  static constexpr int OFF_W = 2 * CHUNK;            // in a stage: A 16 KB, then 64 x 128 dims, then 64 more
+  static constexpr int STAGE = 5 * CHUNK;
+  static constexpr int OFF_MISC = NS * STAGE;
+  static constexpr int SMEM = OFF_MISC + 256 + 1024;
+  static constexpr int THREADS = 256;                // 0 copies, 1 issues, all write out
+};
+
+// Task dims: columns c of D are dims 256 * upper + c.  dkv: of a stage's 64 rows, the
+// first products take dZ and q, the second P and d_o.
+template <bool DKV>
+__global__ void __launch_bounds__(Prod::THREADS, 1)
+    product_kernel(const __grid_constant__ CUtensorMap tm_pz, const __grid_constant__ CUtensorMap tm_kv,
+                   const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                   const Params p) {
+  using C = Prod;
+  constexpr uint32_t IDESC = idesc_bf16(256, 256, DKV, true), IDESC_ROT = idesc_bf16(256, 128, DKV, true);
+  const int rank = blockIdx.x & 1, upper = (blockIdx.x >> 1) & 1;
+  int u = blockIdx.x >> 2, b, kt = 0, slot = 0, x0, x1;   // dkv: tiles x0..x1-1; dq: tiles x0, x0 + 1
+  Seq s;
+  Pages list{0, 0, 0};
+  if constexpr (DKV) {
+    b = u / p.q.slots;
+    slot = u % p.q.slots;
+    const int n_first = p.q.KF * p.q.n_long;
+    int part;
+    if (slot < n_first) {
+      kt = slot / p.q.n_long, part = slot % p.q.n_long;
+    } else {
+      kt = p.q.KF + (slot - n_first) / p.q.n_short, part = (slot - n_first) % p.q.n_short;
+    }
+    s = seq_of(p.m, b);
+    const int2 tiles = tiles_of(p, s, kt);
+    x0 = tiles.x + part * p.q.seg;
+    x1 = min(x0 + p.q.seg, tiles.y);
+    if (x0 >= x1) return;
+  } else {
+    b = u / (p.q.RC / 2);
+    x0 = p.rt0 + 2 * (u % (p.q.RC / 2));
+    x1 = x0 + 2;
+    s = seq_of(p.m, b);
+    const int rows = s.n * p.H;
+    if (x0 * X >= rows) return;
+    list = pages_of(p.m, s, x0 * X / p.H, (min(x1 * X, rows) - 1) / p.H);
+  }
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);    // even CTA
+  uint64_t* empty = full + C::NS;
+  uint64_t* land = empty + C::NS;
+  uint64_t* done = land + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
+  volatile int* s_some = reinterpret_cast<volatile int*>(tslot + 2);
+
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (tid == 0) {
+    for (int k = 0; k < C::NS; ++k) mbar_init(&full[k], 2), mbar_init(&empty[k], 1);
+    mbar_init(land, 1);
+    mbar_init(done, 1);
+    s_abort[0] = 0;
+    s_some[0] = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_pz);
+    tma_prefetch_desc(DKV ? &tm_q : &tm_kv);
+    if (DKV) tma_prefetch_desc(&tm_do);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tslot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+
+  // dkv: whether a tile sees any of the task's keys
+  auto sees = [&](const Pages& l) {
+    return place(l, 4 * kt) >= 0 || place(l, 4 * kt + 1) >= 0 || place(l, 4 * kt + 2) >= 0 ||
+           place(l, 4 * kt + 3) >= 0;
+  };
+  const int col = 256 * upper + 128 * rank;
+  if (warp == 0) {
+    Ring<C::NS> r;
+    int used = 0;
+    uint32_t lph = 0;
+    bool ok = true;
+    auto acquire = [&] {
+      ok = used < C::NS || wait(&empty[r.slot], r.ph ^ 1, s_abort, p.status, SITE_E);
+      return ok;
+    };
+    auto advance = [&] {
+      __syncwarp();
+      if (used < C::NS) ++used;
+      r.next();
+    };
+    if constexpr (DKV) {
+      for (int x = x0; x < x1 && ok; ++x) {
+        const Pages l = tile_pages(p, s, x);
+        if (!sees(l)) continue;
+        const int c0 = place(l, 4 * kt + 2 * rank), c1 = place(l, 4 * kt + 2 * rank + 1);
+#pragma unroll 1
+        for (int st = 0; st < 4 && ok; ++st) {       // rows 64 (st >> 1), dZ and q or P and d_o
+          const int which = 1 - (st & 1), y = 64 * (st >> 1);
+          if (!acquire()) break;
+          if (elect_one_lane()) {
+            uint8_t* a = sm + r.slot * C::STAGE;
+            uint8_t* w = a + C::OFF_W;
+            const uint32_t bar = mapa_u32(smem_u32(&full[r.slot]), 0);
+            const bool rot = upper && which && rank == 0;
+            mbar_expect_tx_cluster(bar, (rot ? 5 : 4) * CHUNK);
+            tma_load_2d_pair(a, &tm_pz, bar, 0, c0 < 0 ? 0 : static_cast<int>(p.block_row(b, x, c0, which)) + y);
+            tma_load_2d_pair(a + CHUNK, &tm_pz, bar, 0,
+                             c1 < 0 ? 0 : static_cast<int>(p.block_row(b, x, c1, which)) + y);
+            const CUtensorMap* tm = which ? &tm_q : &tm_do;
+            tma_load_3d_pair(w, tm, bar, col, x * X + y, b);
+            tma_load_3d_pair(w + CHUNK, tm, bar, col + 64, x * X + y, b);
+            if (rot) tma_load_3d_pair(w + 2 * CHUNK, tm, bar, kVlat, x * X + y, b);
+          }
+          advance();
+        }
+      }
+    } else {
+      const Pages l = tile_pages(p, s, x0 + rank);
+      const int rows = s.n * p.H, i0 = x0 * X / p.H, i1 = (min(x1 * X, rows) - 1) / p.H;
+      for (int k = 0; k < list.count() && ok; ++k) {
+        const int pg = list.page(k), c = place(l, pg), row = static_cast<int>(page_row(p.kv, b, pg));
+        const uint64_t any = span_mask(p.m, s, i0, i1, pg * 64);
+        if (!acquire()) break;
+        uint8_t* a = sm + r.slot * C::STAGE;
+        uint8_t* w = a + C::OFF_W;
+        const uint32_t bar = mapa_u32(smem_u32(&full[r.slot]), 0);
+        const bool rot = upper && rank == 0;
+        const int n = rot ? 3 : 2;
+        if (any != ~0ull) {
+          // rows that nobody sees become zeros: whatever they hold must not meet
+          // the zeros of dZ
+          if (elect_one_lane()) {
+            mbar_expect_tx(land, n * CHUNK);
+            tma_load_2d(w, &tm_kv, land, col, row);
+            tma_load_2d(w + CHUNK, &tm_kv, land, col + 64, row);
+            if (rot) tma_load_2d(w + 2 * CHUNK, &tm_kv, land, kVlat, row);
+          }
+          __syncwarp();
+          ok = wait(land, lph, s_abort, p.status, SITE_LAND);
+          lph ^= 1;
+          if (!ok) break;
+          for (int e = lane; e < n * CHUNK / 16; e += 32)
+            if (!(any >> ((e >> 3) & 63) & 1)) reinterpret_cast<uint4*>(w)[e] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (elect_one_lane()) {
+          mbar_expect_tx_cluster(bar, (2 + (any == ~0ull ? n : 0)) * CHUNK);
+          const int br = c < 0 ? 0 : static_cast<int>(p.block_row(b, x0 + rank, c, 1));
+          tma_load_2d_pair(a, &tm_pz, bar, 0, br);
+          tma_load_2d_pair(a + CHUNK, &tm_pz, bar, 0, br + 64);
+          if (any == ~0ull) {
+            tma_load_2d_pair(w, &tm_kv, bar, col, row);
+            tma_load_2d_pair(w + CHUNK, &tm_kv, bar, col + 64, row);
+            if (rot) tma_load_2d_pair(w + 2 * CHUNK, &tm_kv, bar, kVlat, row);
+          }
+        }
+        advance();
+      }
+    }
+    if (lane == 0 && used > 0) s_some[0] = 1;
+    for (; used > 0; --used) {
+      if (--r.slot < 0) r.slot = C::NS - 1, r.ph ^= 1;
+      if (rank == 0) wait<true>(&full[r.slot], r.ph, s_abort, p.status, SITE_F);
+      if (ok) wait(&empty[r.slot], r.ph, s_abort, p.status, SITE_E);
+    }
+  } else if (warp == 1 && rank == 0) {
+    const uint64_t ad = DKV ? smem_desc(smem_u32(sm), CHUNK, 1024) : smem_desc(smem_u32(sm), 16, 1024);
+    const uint64_t wd = smem_desc(smem_u32(sm + C::OFF_W), CHUNK, 1024);
+    Ring<C::NS> r;
+    bool ok = true;
+    uint32_t more = 0;                               // accumulate
+    auto multiply = [&](bool rot) {
+      ok = wait<true>(&full[r.slot], r.ph, s_abort, p.status, SITE_F);
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one_lane()) {
+        const uint64_t a = desc_add(ad, r.slot * C::STAGE), w = desc_add(wd, r.slot * C::STAGE);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t ak = desc_add(a, kk * (DKV ? 2048 : 32));
+          umma_bf16_pair(tmem, ak, desc_add(w, kk * 2048), IDESC, more | (kk > 0));
+          if (rot)
+            umma_bf16_pair(tmem + 256, ak, desc_add(w, 2 * CHUNK + kk * 2048), IDESC_ROT, more | (kk > 0));
+        }
+        umma_commit_pair(&empty[r.slot]);
+      }
+      __syncwarp();
+      more = 1;
+      r.next();
+    };
+    if constexpr (DKV) {
+      for (int x = x0; x < x1 && ok; ++x) {
+        if (!sees(tile_pages(p, s, x))) continue;
+        for (int st = 0; st < 4 && ok; ++st) multiply(upper && !(st & 1));
+      }
+    } else {
+      for (int k = 0; k < list.count() && ok; ++k) multiply(upper);
+    }
+    if (elect_one_lane()) umma_commit_pair(done);
+    __syncwarp();
+    wait(done, 0, s_abort, p.status, SITE_DONE);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+
+  // ---- out: a row (key) a thread; warps 0-3 the lower half of the columns ----
+  const bool some = s_some[0] != 0;
+  const int sub = warp & 3, half = warp >> 2, r = 128 * rank + 32 * sub + lane;
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16);
+  const int rows = s.n * p.H, g = x0 * X + r;
+#pragma unroll 1
+  for (int q = 0; q < (upper ? 5 : 4); ++q) {
+    const int c = q < 4 ? 128 * half + 32 * q : 256 + 32 * half;
+    uint32_t v[32];
+    if (some) {
+      tmem_ld32(taddr + c, v);
+      tmem_ld_wait_regs(v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = 0;
+    }
+    if constexpr (DKV) {
+      float4* to = reinterpret_cast<float4*>(
+          p.part + ((static_cast<int64_t>(b) * p.q.slots + slot) * 256 + r) * kRlat + 256 * upper + c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        to[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                            __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+    } else if (g < rows) {
+      uint4* to = reinterpret_cast<uint4*>(
+          p.dq + (static_cast<int64_t>(b) * p.m.T * p.H + g) * kRlat + 256 * upper + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t w[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          w[f] = pack_bf16x2(__uint_as_float(v[8 * e + 2 * f]), __uint_as_float(v[8 * e + 2 * f + 1]));
+        to[e] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// dkv of a row: its segments in order (and what earlier chunks left), four dims a thread.
+__global__ void __launch_bounds__(144) reduce_kernel(const Params p) {
+  const int b = blockIdx.x / p.m.max_kv_len, key = blockIdx.x % p.m.max_kv_len, kt = key >> 8;
+  const Seq s = seq_of(p.m, b);
+  if (!s.ok || key >= s.L) return;
+  const int2 tiles = tiles_of(p, s, kt);
+  const int n = (tiles.y - tiles.x + p.q.seg - 1) / p.q.seg;
+  const int first = kt < p.q.KF ? kt * p.q.n_long : p.q.KF * p.q.n_long + (kt - p.q.KF) * p.q.n_short;
+  const float4* at = reinterpret_cast<const float4*>(
+      p.part + ((static_cast<int64_t>(b) * p.q.slots + first) * 256 + (key & 255)) * kRlat) + threadIdx.x;
+  float4* acc = reinterpret_cast<float4*>(p.acc + (static_cast<int64_t>(b) * p.m.max_kv_len + key) * kRlat) +
+                threadIdx.x;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!p.first_chunk) v = *acc;
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float4 w = at[static_cast<int64_t>(k) * 256 * (kRlat / 4)];
+    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+  }
+  if (!p.last_chunk) {
+    *acc = v;
+    return;
+  }
+  reinterpret_cast<uint2*>(p.dkv + (static_cast<int64_t>(b) * p.kv.seq_stride + key) * kRlat)[threadIdx.x] =
+      make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+// span: keys that one query may see at most (window + n_first, or every row)
+Plan plan(int B, int T, int H, int max_kv_len, int64_t span, int64_t window, int64_t n_first) {
+  Plan q{};
+  const int64_t rows = static_cast<int64_t>(T) * H, S = max_kv_len;
+  q.RT = static_cast<int>((rows + 2 * X - 1) / (2 * X) * 2);
+  const int64_t tokens = (X + H - 2) / H + 1;
+  const int64_t np = (span + tokens) / 64 + 4, most = (S + 63) / 64;
+  q.np = static_cast<int>(np < most ? np : most);
+  int64_t rc = kChunkBytes / (static_cast<int64_t>(B) * q.np * 2 * BLOCK) / 2 * 2;
+  if (rc < 2) rc = 2;
+  q.RC = static_cast<int>(rc < q.RT ? rc : q.RT);
+  q.KT = static_cast<int>((S + 255) / 256);
+  const int64_t kf = (n_first + 255) / 256;
+  q.KF = static_cast<int>(kf < q.KT ? kf : q.KT);
+  // tiles that see a key tile
+  int64_t few = ((window + 255) * H + X - 1) / X + 1;
+  if (few > q.RC) few = q.RC;
+  const int64_t all = q.KF * static_cast<int64_t>(q.RC) + (q.KT - q.KF) * few;
+  int64_t seg = (2 * B * all + TASKS - 1) / TASKS;
+  if (seg < 16) seg = 16;
+  q.seg = static_cast<int>(seg < q.RC ? seg : q.RC);
+  q.n_long = (q.RC + q.seg - 1) / q.seg;
+  q.n_short = static_cast<int>((few + q.seg - 1) / q.seg);
+  q.slots = q.KF * q.n_long + (q.KT - q.KF) * q.n_short;
+  return q;
+}
+
+// Bytes by part, from the sizes and the span alone (never less for a longer span).
+struct Sizes {
+  size_t rows, pz, part, acc;
+  size_t total() const { return rows + pz + part + acc; }
+};
+Sizes sizes(const Plan& q, int B, int T, int H, int max_kv_len) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  auto least = [](size_t x, size_t y) { return x < y ? x : y; };
+  Sizes z{};
+  z.rows = up(static_cast<size_t>(B) * T * H * sizeof(float2));
+  const size_t two = static_cast<size_t>(B) * 2 * q.np * 2 * BLOCK;
+  const size_t chunk = two > static_cast<size_t>(kChunkBytes) ? two : static_cast<size_t>(kChunkBytes);
+  z.pz = BLOCK + least(two / 2 * q.RT, chunk);
+  // B * slots <= TASKS / 2 + B * KT: every key tile rounds its segments up once
+  z.part = (TASKS / 2 + 1 + static_cast<size_t>(B) * q.KT) * 256 * kRlat * sizeof(float);
+  z.acc = two / 2 * q.RT > static_cast<size_t>(kChunkBytes)
+              ? up(static_cast<size_t>(B) * max_kv_len * kRlat * sizeof(float))
+              : 0;
+  return z;
+}
+
+template <typename Kernel, typename... Args>
+dsa_status_t launch_pairs(const char* what, Kernel kernel, int64_t pairs, int threads, int smem,
+                          cudaStream_t stream, Args... args) {
+  if (pairs > (1 << 30) - 1) return DSA_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return launch_status("cudaFuncSetAttribute");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, args...);
+  return launch_status(what);
 }
 
 }  // namespace wbw
 
 size_t window_bwd_scratch_bytes(int B, int T, int H, int max_kv_len, int64_t span) {
-  (void)B, (void)T, (void)H, (void)max_kv_len, (void)span;
-  return 0;
+  return wbw::sizes(wbw::plan(B, T, H, max_kv_len, span, span, 0), B, T, H, max_kv_len).total();
 }
 
 dsa_status_t window_bwd_launch(const WindowBwdArgs& a, cudaStream_t stream) {
   using namespace wbw;
-  const Params p{a.f.q_lat, store_of(a.f), mask_of(a.f), a.f.B, a.f.H, a.f.scale, a.f.o_lat,
-                 a.f.lse, a.d_o, a.dq, a.dkv, a.f.status};
-  const int64_t rows = static_cast<int64_t>(a.f.B) * a.f.T * a.f.H;
-  const int64_t keys = static_cast<int64_t>(a.f.B) * a.f.max_kv_len;
-  dq_kernel<<<static_cast<unsigned>((rows + WARPS - 1) / WARPS), WARPS * 32, 0, stream>>>(p);
-  dkv_kernel<<<static_cast<unsigned>((keys + WARPS - 1) / WARPS), WARPS * 32, 0, stream>>>(p);
-  return launch_status("dkv_kernel");
+  const DenseArgs& f = a.f;
+  const int64_t S = f.max_kv_len, both = static_cast<int64_t>(f.window) + f.n_first;
+  const int64_t span = both == 0 ? 1 : both < S ? both : S;
+  const Plan q = plan(f.B, f.T, f.H, f.max_kv_len, span, f.window < S ? f.window : S,
+                      f.n_first < S ? f.n_first : S);
+  const Sizes z = sizes(q, f.B, f.T, f.H, f.max_kv_len);
+  if (f.scratch_bytes < z.total()) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t per = static_cast<int64_t>(f.T) * f.H;
+  uint8_t* ws = static_cast<uint8_t*>(f.scratch);
+  Params p{};
+  p.kv = store_of(f);
+  p.m = mask_of(f);
+  p.B = f.B;
+  p.H = f.H;
+  p.q = q;
+  p.scale = f.scale;
+  p.scale_log2 = f.scale * 1.4426950408889634f;
+  p.o = f.o_lat;
+  p.d_o = a.d_o;
+  p.lse = f.lse;
+  p.rows = reinterpret_cast<float2*>(ws);
+  p.pz = ws + z.rows;
+  p.part = reinterpret_cast<float*>(p.pz + z.pz);
+  p.acc = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.part) + z.part);
+  p.dq = a.dq;
+  p.dkv = a.dkv;
+  p.status = f.status;
+  const uint64_t pz_rows = z.pz / 128;
+  if (pz_rows >= (uint64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
+  // boxes of 64 rows for the products, of a tile for pz
+  CUtensorMap tq, td, tq_tile, td_tile, tk, tp;
+  const uint64_t kv_rows = static_cast<uint64_t>((f.B - 1) * f.kv.seq_stride + f.max_kv_len);
+  if (!encode_tmap_2d(&tk, f.kv.base, kv_rows, kRlat, kRlat * 2, 64, 64, true) ||
+      !encode_tmap_2d(&tp, p.pz, pz_rows, 64, 128, 64, 64, false) ||
+      !encode_tmap_3d(&tq, f.q_lat, f.B, per, kRlat, 64, 64) ||
+      !encode_tmap_3d(&td, a.d_o, f.B, per, kVlat, 64, 64) ||
+      !encode_tmap_3d(&tq_tile, f.q_lat, f.B, per, kRlat, 64, X) ||
+      !encode_tmap_3d(&td_tile, a.d_o, f.B, per, kVlat, 64, X))
+    return DSA_ERR_CUDA;
+  const int64_t ctas = (f.B * per + 7) / 8;
+  prep_kernel<<<static_cast<unsigned>(ctas > 4 ? ctas : 4), 256, 0, stream>>>(p);
+  if (launch_status("prep_kernel") != DSA_OK) return DSA_ERR_CUDA;
+  for (int rt0 = 0; rt0 < q.RT; rt0 += q.RC) {
+    p.rt0 = rt0;
+    p.first_chunk = rt0 == 0;
+    p.last_chunk = rt0 + q.RC >= q.RT;
+    const int64_t tiles = static_cast<int64_t>(f.B) * q.RC;
+    dsa_status_t st = launch_pairs("pz_kernel", pz_kernel, tiles, Pz::THREADS, Pz::SMEM, stream, tq_tile,
+                                   td_tile, tk, p);
+    if (st == DSA_OK)
+      st = launch_pairs("product_kernel", product_kernel<false>, tiles, Prod::THREADS, Prod::SMEM, stream,
+                        tp, tk, tq, td, p);
+    if (st == DSA_OK)
+      st = launch_pairs("product_kernel", product_kernel<true>, 2ll * f.B * q.slots, Prod::THREADS,
+                        Prod::SMEM, stream, tp, tk, tq, td, p);
+    if (st != DSA_OK) return st;
+    reduce_kernel<<<static_cast<unsigned>(static_cast<int64_t>(f.B) * f.max_kv_len), 144, 0, stream>>>(p);
+    if (launch_status("reduce_kernel") != DSA_OK) return DSA_ERR_CUDA;
+  }
+  return DSA_OK;
 }
 
 }  // namespace dsa
