@@ -15,16 +15,18 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // A bounded wait by a whole warp; false (for all lanes) once the CTA has given up.
+// CLUSTER: what the other CTA's threads wrote before they arrived is read next (by
+// loads: what the tensor core reads, its own CTA's copies and fences have ordered).
+// One fence after the wait, not an acquire at cluster scope in every poll.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* s_abort,
                                      uint32_t* status, uint32_t where) {
-  auto test = [&] { return CLUSTER ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity); };
-  bool ok = test();
+  bool ok = mbar_test(bar, parity);
   if (!ok) {
     const uint64_t t0 = globaltimer_ns();
     while (true) {
 #pragma unroll 1
-      for (int k = 0; k < 16 && !ok; ++k) ok = test();
+      for (int k = 0; k < 16 && !ok; ++k) ok = mbar_test(bar, parity);
       if (ok || *s_abort != 0) break;
       if (globaltimer_ns() - t0 > kWaitLimitNs) {
         status_raise(status, DSA_ERR_DEVICE_TIMEOUT, where);
@@ -33,6 +35,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
       }
     }
   }
+  if (CLUSTER) asm volatile("fence.acq_rel.cluster;" ::: "memory");
   return __all_sync(0xffffffffu, ok);
 }
 

@@ -20,16 +20,19 @@
 // read, 136 KB copied in and 24 KB of P written, about 3,800 cycles at 128 bytes,
 // beside 3,840 cycles of MMAs (R = 96).
 //
-// Roles (8 warps): 0 copies Q and K, 1 copies V, 2 and 3 of the even CTA issue the
+// Roles (12 warps): 0 copies Q and K, 1 copies V, 2 and 3 of the even CTA issue the
 // two products, 4..7 hold a row a thread: its 128 scores, P = 2^(z - m) to BF16 in
-// shared memory.  m is the maximum of the first block in which the row sees
-// anything, so O^T is never rescaled; a row whose later scores exceed it by 2^100
-// sends its unit to attend_row.  So does a row that one query of the unit sees and
-// another does not and that holds an infinity or a NaN (0 * NaN would reach both).
-// Rows of a page that nobody in the unit sees are zeroed in V before use.
+// shared memory; 8..11 write O^T / l out while the next unit's first products run.
+// m is the maximum of the first block in which the row sees anything, so O^T is
+// never rescaled; a row whose later scores exceed it by 2^100 sends its unit to
+// attend_row.  So does a row that one query of the unit sees and another does not
+// and that holds an infinity or a NaN (0 * NaN would reach both).  Rows of a page
+// that nobody in the unit sees are zeroed in V before use.
 //
-// Few units: the blocks of a unit are split over several pairs, and combine_kernel
-// joins their normalised FP32 outputs by their log-sum-exps, in order.
+// Persistent: the blocks of all units stand in one line, and every pair of SMs takes
+// an equal stretch of it (whole units where there are many).  A unit that is cut has
+// its pieces' normalised FP32 outputs joined by their log-sum-exps, in order, by
+// combine_kernel.
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -40,7 +43,7 @@
 namespace dsa {
 namespace dense {
 
-constexpr int WARPS = 8, THREADS = WARPS * 32;
+constexpr int THREADS = 384;
 constexpr float FAR = 100.f;              // exponents that P may reach
 
 template <int R_>
@@ -54,7 +57,8 @@ struct Cfg {
   static constexpr int OFF_K = OFF_P + 2 * QCH;
   static constexpr int OFF_V = OFF_K + NK * CHUNK;
   static constexpr int OFF_MISC = OFF_V + NV * 2 * CHUNK;
-  static constexpr int SMEM = OFF_MISC + 1536 + 1024;
+  static constexpr int MISC = 512 + 16 * R;
+  static constexpr int SMEM = OFF_MISC + MISC + 1024;
   static constexpr uint32_t S_COL = 4 * R;
   static_assert(SMEM <= 232448, "shared memory");
   static_assert(OFF_Q + 8 * QCH + 128 * 128 <= OFF_K, "the aliased rows stay inside Q and P");
@@ -64,19 +68,29 @@ struct Cfg {
 enum : uint32_t {
   SITE_Q = 0x710, SITE_KF = 0x711, SITE_KE = 0x712, SITE_VF = 0x713, SITE_VE = 0x714,
   SITE_SF = 0x715, SITE_SE = 0x716, SITE_P = 0x717, SITE_O = 0x718, SITE_VT = 0x719,
-  SITE_DRAIN = 0x71a
+  SITE_DRAIN = 0x71a, SITE_OE = 0x71b, SITE_L = 0x71c
+};
+
+// A pair's stretch of the line, as combine_kernel needs it: the unit and the block
+// that it starts with, the unit that it begins but does not end (or -1) and the slot
+// of that piece.
+struct Stretch {
+  int first, j0, head, slot;
 };
 
 struct Params {
   const uint16_t* q;
   Store kv;
   Mask m;
-  int B, H, tiles, splits;
+  int B, H, tiles, pairs;
+  int nominal;        // window: blocks that a unit counts for; tree: 0, what it has
+  int cut;            // units may be cut
   float scale_log2;
   uint16_t* o;
   float* lse;
-  float* part_o;      // [unit, split, 2R, 512] normalised
-  float* part_lse;    // [unit, split, 2R] base 2
+  float* part_o;      // [pairs, 2, 2R, 512] normalised
+  float* part_lse;    // [pairs, 2, 2R] base 2
+  Stretch* stretch;   // [pairs]
   uint32_t* status;
 };
 
@@ -147,6 +161,120 @@ __device__ __noinline__ void attend_row(const Params& p, const Seq& s, const Pag
   }
 }
 
+// A piece of a unit: its pages k0 .. k1-1, nb blocks.
+struct Unit {
+  int b, id, g0, rows, i0, i1;    // rows: of the sequence
+  Seq s;
+  Pages pages;
+  int k0, k1, nb;
+  int j0, j1, of;                 // blocks j0 .. j1-1 of `of`
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == of; }
+};
+
+// A pair's stretch of the line, unit by unit.  Every warp walks it by itself (all
+// lanes alike); the sequences' lengths stay in L1.
+template <int R>
+struct Line {
+  const Params& p;
+  int b = 0, tile = 0, j = 0, tiles = 0, cost = 0;   // tiles and blocks per tile of sequence b
+  int64_t left = 0;
+  Seq s;
+
+  __device__ __forceinline__ void measure(int at, Seq& sq, int& n_tiles, int& n_blocks) const {
+    sq = seq_of(p.m, at);
+    n_tiles = (sq.n * p.H + 2 * R - 1) / (2 * R);
+    n_blocks = p.nominal;
+    if (p.nominal == 0) n_blocks = sq.ok ? max(((sq.L + 63) / 64 + 1) / 2, 1) : 1;
+  }
+  // The sequence, tile and block at x (or behind the last sequence).
+  __device__ __forceinline__ void seek(int64_t x) {
+    if (p.nominal > 0) {
+      const int64_t u = x / p.nominal;
+      j = static_cast<int>(x - u * p.nominal);
+      b = static_cast<int>(u / p.tiles);
+      tile = static_cast<int>(u % p.tiles);
+      if (b < p.B) measure(b, s, tiles, cost);
+      return;
+    }
+    const int lane = threadIdx.x & 31;
+    for (b = 0; b < p.B; b += 32) {
+      Seq sq;
+      int n = 0, c = 0;
+      if (b + lane < p.B) measure(b + lane, sq, n, c);
+      int64_t sum = static_cast<int64_t>(n) * c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const unsigned over = __ballot_sync(0xffffffffu, sum > x);
+      if (over != 0) {
+        const int at = __ffs(over) - 1;
+        x -= __shfl_sync(0xffffffffu, sum - static_cast<int64_t>(n) * c, at);
+        b += at;
+        measure(b, s, tiles, cost);
+        tile = static_cast<int>(x / cost);
+        j = static_cast<int>(x % cost);
+        return;
+      }
+      x -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  __device__ __forceinline__ int64_t total() const {
+    if (p.nominal > 0) return static_cast<int64_t>(p.B) * p.tiles * p.nominal;
+    int64_t sum = 0;
+    for (int at = threadIdx.x & 31; at < p.B; at += 32) {
+      Seq sq;
+      int n, c;
+      measure(at, sq, n, c);
+      sum += static_cast<int64_t>(n) * c;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+  }
+  __device__ __forceinline__ Line(const Params& pp, int pair) : p(pp) {
+    const int64_t all = total(), n = min(all, static_cast<int64_t>(p.pairs));
+    if (pair >= n) return;        // a block each: the last pairs have nothing
+    int64_t x0 = all * pair / n, x1 = all * (pair + 1) / n;
+    if (!p.cut) {                 // whole units: to the next unit's start
+      seek(x1);
+      if (x1 < all && j > 0) x1 += cost - j;
+      seek(x0);
+      if (x0 < all && j > 0) x0 += cost - j;
+    }
+    if (x0 < x1) seek(x0);
+    left = x1 - x0;
+  }
+  __device__ __forceinline__ bool next(Unit& u) {
+    if (left <= 0) return false;
+    while (tile >= tiles) {
+      if (++b >= p.B) return false;
+      tile = j = 0;
+      measure(b, s, tiles, cost);
+    }
+    u.b = b;
+    u.id = b * p.tiles + tile;
+    u.s = s;
+    u.g0 = tile * 2 * R;
+    u.rows = s.n * p.H;
+    u.i0 = u.g0 / p.H;
+    u.i1 = (min(u.g0 + 2 * R, u.rows) - 1) / p.H;
+    u.pages = pages_of(p.m, s, u.i0, u.i1);
+    u.of = cost;
+    u.j0 = j;
+    u.j1 = static_cast<int>(min(static_cast<int64_t>(cost), j + left));
+    const int np = u.pages.count();
+    u.k0 = min(2 * u.j0, np);
+    u.k1 = min(2 * u.j1, np);
+    u.nb = (u.k1 - u.k0 + 1) / 2;
+    left -= u.j1 - u.j0;
+    j = 0;
+    ++tile;
+    return true;
+  }
+};
+
 template <int R>
 __global__ void __launch_bounds__(THREADS, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
@@ -161,37 +289,41 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* vfull = kempty + C::NK;                                  // even CTA
   uint64_t* vempty = vfull + C::NV;
   uint64_t* qfull = vempty + C::NV;                                  // even CTA
-  uint64_t* sfull = qfull + 1;
-  uint64_t* sfree = qfull + 2;                                       // even CTA
-  uint64_t* pready = qfull + 3;                                      // even CTA
-  uint64_t* odone = qfull + 4;
-  uint64_t* vland = qfull + 5;                                       // this CTA's own copies
-  uint64_t* drain = qfull + 6;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(qfull + 7);
+  uint64_t* qempty = qfull + 1;
+  uint64_t* sfull = qfull + 2;
+  uint64_t* sfree = qfull + 3;                                       // even CTA
+  uint64_t* pready = qfull + 4;                                      // even CTA
+  uint64_t* odone = qfull + 5;                                       // a block's values added
+  uint64_t* ofull = qfull + 6;                                       // a unit's
+  uint64_t* ofree = qfull + 7;                                       // even CTA
+  uint64_t* lfull = qfull + 8;                                       // [2] a unit's sums, of both CTAs
+  uint64_t* lfree = qfull + 10;                                      // [2]
+  uint64_t* vland = qfull + 12;                                      // [2] this CTA's own copies
+  uint64_t* drain = qfull + 14;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(qfull + 15);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
-  int* s_slow = reinterpret_cast<int*>(tslot + 2);
-  float* s_inv = reinterpret_cast<float*>(tslot + 4);                // [2R]
-  static_assert((2 * C::NK + 2 * C::NV + 7) * 8 + 16 + 8 * R <= 1536, "misc");
+  int* s_slow = reinterpret_cast<int*>(tslot + 2);                   // [2]
+  float* s_inv = reinterpret_cast<float*>(sm + C::OFF_MISC + 512);   // [2][2R]
+  static_assert((2 * C::NK + 2 * C::NV + 15) * 8 + 16 <= 512, "misc");
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int rank = blockIdx.x & 1;
-  int u = blockIdx.x >> 1;
-  const int sp = u % p.splits;
-  u /= p.splits;
-  const int tile = u % p.tiles, b = u / p.tiles;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
 
   if (tid == 0) {
     for (int k = 0; k < C::NK; ++k) mbar_init(&kfull[k], 1), mbar_init(&kempty[k], 1);
     for (int k = 0; k < C::NV; ++k) mbar_init(&vfull[k], 2), mbar_init(&vempty[k], 1);
     mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
     mbar_init(sfull, 1);
     mbar_init(sfree, 8);
     mbar_init(pready, 8);
     mbar_init(odone, 1);
-    mbar_init(vland, 1);
+    mbar_init(ofull, 1);
+    mbar_init(ofree, 8);
+    for (int k = 0; k < 2; ++k) mbar_init(&lfull[k], 8), mbar_init(&lfree[k], 8), mbar_init(&vland[k], 1);
     mbar_init(drain, 2);
     s_abort[0] = 0;
-    s_slow[0] = 0;
+    s_slow[0] = s_slow[1] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_kv);
@@ -200,63 +332,67 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc_pair(tslot, 512);
     tmem_relinquish_pair();
   }
-  const Seq s = seq_of(p.m, b);
-  const int g0 = tile * 2 * R, rows = s.n * p.H;        // rows of the sequence: T * H < 2^31
-  const int i0 = g0 / p.H, i1 = (min(g0 + 2 * R, rows) - 1) / p.H;
-  Pages pages{0, 0, 0};
-  if (g0 < rows) pages = pages_of(p.m, s, i0, i1);
-  const int np = pages.count();
-  const int bps = ((np + 1) / 2 + p.splits - 1) / p.splits;
-  const int k0 = min(2 * sp * bps, np), k1 = min(k0 + 2 * bps, np);   // this unit's pages
-  const int nb = (k1 - k0 + 1) / 2;
-  if (rank == 0 && tid == 0 && tile == 0 && sp == 0) report_seq(p.m, s, b, p.status);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tslot;
 
-  float l_sum = 0.f, m_ref = -INFINITY;                  // softmax threads
-  if (nb > 0) {
+  if (warp < 4) {
+    regs_dec<128>();
     if (warp == 0) {
       // ---- Q, then the own page's K, chunk by chunk ----
       const uint32_t qbar = mapa_u32(smem_u32(qfull), 0);
-      if (elect_one_lane()) {
-        if (rank == 0) mbar_expect_tx(qfull, 2u * 9u * C::QCH);
-        const int row = static_cast<int>(static_cast<int64_t>(b) * p.m.T * p.H) + g0 + rank * R;
-#pragma unroll 1
-        for (int c = 0; c < 9; ++c)
-          tma_load_2d_pair(sm + C::OFF_Q + c * C::QCH, &tm_q, qbar, 64 * c, row);
-      }
-      __syncwarp();
+      Line<R> line(p, pair);
+      Unit u;
       Ring<C::NK> r;
-      int used = 0;
+      Stretch mine{-1, 0, -1, 0};
+      int used = 0, n = 0;
       bool ok = true;
-      for (int j = 0; j < nb && ok; ++j) {
-        const int k = k0 + 2 * j + rank;
-        int64_t row = -1;
-        if (k < k1) {
-          row = page_row(p.kv, b, pages.page(k));
-          if (row < 0 && lane == 0)
-            status_raise(p.status, DSA_ERR_BAD_INDEX, SITE_PAGE, static_cast<uint32_t>(pages.page(k)));
+      for (int at = 0; ok && line.next(u); ++at) {
+        if (at == 0) mine.first = u.id, mine.j0 = u.j0;
+        if (u.j0 == 0 && u.j1 < u.of) mine.head = u.id, mine.slot = 2 * pair + (at > 0);
+        if (rank == 0 && lane == 0 && u.g0 == 0 && u.j0 == 0) report_seq(p.m, u.s, u.b, p.status);
+        if (u.nb == 0) continue;
+        if (n > 0) ok = wait(qempty, (n - 1) & 1, s_abort, p.status, SITE_Q);
+        ++n;
+        if (!ok) break;
+        if (elect_one_lane()) {
+          if (rank == 0) mbar_expect_tx(qfull, 2u * 9u * C::QCH);
+          const int row = static_cast<int>(static_cast<int64_t>(u.b) * p.m.T * p.H) + u.g0 + rank * R;
+#pragma unroll 1
+          for (int c = 0; c < 9; ++c)
+            tma_load_2d_pair(sm + C::OFF_Q + c * C::QCH, &tm_q, qbar, 64 * c, row);
         }
-        if (row < 0) row = 0;                            // nobody sees it
-        for (int c = 0; c < 9; ++c) {
-          ok = used < C::NK || wait(&kempty[r.slot], r.ph ^ 1, s_abort, p.status, SITE_KE);
-          if (!ok) break;
-          if (elect_one_lane()) {
-            if (rank == 0) mbar_expect_tx(&kfull[r.slot], 2 * CHUNK);
-            tma_load_2d_pair(sm + C::OFF_K + r.slot * CHUNK, &tm_kv, mapa_u32(smem_u32(&kfull[r.slot]), 0),
-                             64 * c, static_cast<int>(row));
+        __syncwarp();
+        for (int j = 0; j < u.nb && ok; ++j) {
+          const int k = u.k0 + 2 * j + rank;
+          int64_t row = -1;
+          if (k < u.k1) {
+            row = page_row(p.kv, u.b, u.pages.page(k));
+            if (row < 0 && lane == 0)
+              status_raise(p.status, DSA_ERR_BAD_INDEX, SITE_PAGE, static_cast<uint32_t>(u.pages.page(k)));
           }
-          __syncwarp();
-          if (used < C::NK) ++used;
-          r.next();
+          if (row < 0) row = 0;                            // nobody sees it
+          for (int c = 0; c < 9; ++c) {
+            ok = used < C::NK || wait(&kempty[r.slot], r.ph ^ 1, s_abort, p.status, SITE_KE);
+            if (!ok) break;
+            if (elect_one_lane()) {
+              if (rank == 0) mbar_expect_tx(&kfull[r.slot], 2 * CHUNK);
+              tma_load_2d_pair(sm + C::OFF_K + r.slot * CHUNK, &tm_kv,
+                               mapa_u32(smem_u32(&kfull[r.slot]), 0), 64 * c, static_cast<int>(row));
+            }
+            __syncwarp();
+            if (used < C::NK) ++used;
+            r.next();
+          }
         }
       }
+      if (rank == 0 && lane == 0 && p.cut) p.stretch[pair] = mine;
       // the pair's copies have landed and the last arrivals of the MMAs have come
       // before either CTA leaves
-      if (rank == 0) wait(qfull, 0, s_abort, p.status, SITE_Q);
+      if (rank == 0 && n > 0) wait(qfull, (n - 1) & 1, s_abort, p.status, SITE_Q);
+      if (ok && n > 0) wait(qempty, (n - 1) & 1, s_abort, p.status, SITE_Q);
       for (; used > 0; --used) {
         if (--r.slot < 0) r.slot = C::NK - 1, r.ph ^= 1;
         if (rank == 0) wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
@@ -264,59 +400,64 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     } else if (warp == 1) {
       // ---- V: the own 256 dims of both pages, 128 at a time ----
+      Line<R> line(p, pair);
+      Unit u;
       Ring<C::NV> r;
       int used = 0;
       uint32_t vph = 0;
       bool ok = true;
-      for (int j = 0; j < nb && ok; ++j) {
+      while (ok && line.next(u)) {
 #pragma unroll 1
-        for (int half = 0; half < 2 && ok; ++half) {
-          const int k = k0 + 2 * j + half;
+        for (int k = u.k0; k < u.k0 + 2 * u.nb && ok; ++k) {
           int64_t row = -1;
           uint64_t any = 0;
-          if (k < k1) {
-            row = page_row(p.kv, b, pages.page(k));
-            if (row >= 0) any = span_mask(p.m, s, i0, i1, pages.page(k) * 64);
+          if (k < u.k1) {
+            row = page_row(p.kv, u.b, u.pages.page(k));
+            if (row >= 0) any = span_mask(p.m, u.s, u.i0, u.i1, u.pages.page(k) * 64);
           }
+          Ring<C::NV> z = r;
 #pragma unroll 1
           for (int m = 0; m < 2; ++m) {
             ok = used < C::NV || wait(&vempty[r.slot], r.ph ^ 1, s_abort, p.status, SITE_VE);
             if (!ok) break;
             uint8_t* dst = sm + C::OFF_V + r.slot * 2 * CHUNK;
-            const uint32_t bar = mapa_u32(smem_u32(&vfull[r.slot]), 0);
             const int col = 256 * rank + 128 * m;
-            if (any == ~0ull) {
-              if (elect_one_lane()) {
+            if (any != 0 && elect_one_lane()) {
+              if (any == ~0ull) {
+                const uint32_t bar = mapa_u32(smem_u32(&vfull[r.slot]), 0);
                 mbar_expect_tx_cluster(bar, 2 * CHUNK);
                 tma_load_2d_pair(dst, &tm_kv, bar, col, static_cast<int>(row));
                 tma_load_2d_pair(dst + CHUNK, &tm_kv, bar, col + 64, static_cast<int>(row));
+              } else {
+                mbar_expect_tx(&vland[m], 2 * CHUNK);
+                tma_load_2d(dst, &tm_kv, &vland[m], col, static_cast<int>(row));
+                tma_load_2d(dst + CHUNK, &tm_kv, &vland[m], col + 64, static_cast<int>(row));
               }
-              __syncwarp();
-            } else {
-              // rows that nobody sees become zeros: whatever they hold must not
-              // meet the zeros of P
-              if (any != 0) {
-                if (elect_one_lane()) {
-                  mbar_expect_tx(vland, 2 * CHUNK);
-                  tma_load_2d(dst, &tm_kv, vland, col, static_cast<int>(row));
-                  tma_load_2d(dst + CHUNK, &tm_kv, vland, col + 64, static_cast<int>(row));
-                }
-                __syncwarp();
-                ok = wait(vland, vph, s_abort, p.status, SITE_VT);
-                vph ^= 1;
-                if (!ok) break;
-              }
-#pragma unroll 4
-              for (int e = lane; e < 1024; e += 32)     // 16 bytes of row (e >> 3) & 63
-                if (!(any >> ((e >> 3) & 63) & 1))
-                  reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(bar);
             }
+            __syncwarp();
             if (used < C::NV) ++used;
             r.next();
           }
+          if (!ok || any == ~0ull) continue;
+          // rows that nobody sees become zeros: whatever they hold must not meet the
+          // zeros of P
+#pragma unroll 1
+          for (int m = 0; m < 2; ++m) {
+            if (any != 0) {
+              ok = wait(&vland[m], vph, s_abort, p.status, SITE_VT);
+              if (!ok) break;
+            }
+            uint8_t* dst = sm + C::OFF_V + z.slot * 2 * CHUNK;
+#pragma unroll 4
+            for (int e = lane; e < 1024; e += 32)       // 16 bytes of row (e >> 3) & 63
+              if (!(any >> ((e >> 3) & 63) & 1))
+                reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_u32(smem_u32(&vfull[z.slot]), 0));
+            z.next();
+          }
+          if (any != 0) vph ^= 1;
         }
       }
       for (; used > 0; --used) {
@@ -329,42 +470,57 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ---- scores ----
         const uint64_t qd = smem_desc(smem_u32(sm + C::OFF_Q), 16, 1024);
         const uint64_t kd = smem_desc(smem_u32(sm + C::OFF_K), 16, 1024);
+        Line<R> line(p, pair);
+        Unit u;
         Ring<C::NK> r;
-        bool ok = wait(qfull, 0, s_abort, p.status, SITE_Q);
-        for (int j = 0; j < nb && ok; ++j) {
-          if (j > 0) ok = wait<true>(sfree, (j - 1) & 1, s_abort, p.status, SITE_SE);
-          tc_fence_after();
-          for (int c = 0; c < 9 && ok; ++c) {
-            ok = wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
-            if (!ok) break;
+        int n = 0, blk = 0;
+        bool ok = true;
+        while (ok && line.next(u)) {
+          if (u.nb == 0) continue;
+          ok = wait(qfull, n & 1, s_abort, p.status, SITE_Q);
+          ++n;
+          for (int j = 0; j < u.nb && ok; ++j, ++blk) {
+            if (blk > 0) ok = wait(sfree, (blk - 1) & 1, s_abort, p.status, SITE_SE);
             tc_fence_after();
-            if (elect_one_lane()) {
-              const uint64_t a = desc_add(qd, c * C::QCH), w = desc_add(kd, r.slot * CHUNK);
+            for (int c = 0; c < 9 && ok; ++c) {
+              ok = wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one_lane()) {
+                const uint64_t a = desc_add(qd, c * C::QCH), w = desc_add(kd, r.slot * CHUNK);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_bf16_pair(tmem + C::S_COL, desc_add(a, kk * 32), desc_add(w, kk * 32), IDESC_S,
-                               c > 0 || kk > 0);
-              umma_commit_pair(&kempty[r.slot]);
-              if (c == 8) umma_commit_pair(sfull);
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_bf16_pair(tmem + C::S_COL, desc_add(a, kk * 32), desc_add(w, kk * 32), IDESC_S,
+                                 c > 0 || kk > 0);
+                umma_commit_pair(&kempty[r.slot]);
+                if (c == 8) umma_commit_pair(sfull);
+                if (c == 8 && j == u.nb - 1) umma_commit_pair(qempty);
+              }
+              __syncwarp();
+              r.next();
             }
-            __syncwarp();
-            r.next();
           }
         }
         if (elect_one_lane()) umma_commit_pair(drain);
         __syncwarp();
       }
-    } else if (warp == 3) {
-      if (rank == 0) {
-        // ---- values ----
-        const uint64_t pd = smem_desc(smem_u32(sm + C::OFF_P), 16, 1024);
-        const uint64_t vd = smem_desc(smem_u32(sm + C::OFF_V), CHUNK, 1024);
-        Ring<C::NV> r;
-        bool ok = true;
-        for (int j = 0; j < nb && ok; ++j) {
-          ok = wait<true>(pready, j & 1, s_abort, p.status, SITE_P);
+    } else if (rank == 0) {
+      // ---- values ----
+      const uint64_t pd = smem_desc(smem_u32(sm + C::OFF_P), 16, 1024);
+      const uint64_t vd = smem_desc(smem_u32(sm + C::OFF_V), CHUNK, 1024);
+      Line<R> line(p, pair);
+      Unit u;
+      Ring<C::NV> r;
+      int n = 0, blk = 0;
+      bool ok = true;
+      while (ok && line.next(u)) {
+        if (u.nb == 0) continue;
+        for (int j = 0; j < u.nb && ok; ++j, ++blk) {
+          ok = wait(pready, blk & 1, s_abort, p.status, SITE_P);
+          // the unit before has been read out
+          if (ok && j == 0 && n > 0) ok = wait(ofree, (n - 1) & 1, s_abort, p.status, SITE_OE);
           for (int t = 0; t < 4 && ok; ++t) {            // page t >> 1, dims 128 (t & 1)
-            ok = wait<true>(&vfull[r.slot], r.ph, s_abort, p.status, SITE_VF);
+            ok = wait(&vfull[r.slot], r.ph, s_abort, p.status, SITE_VF);
             if (!ok) break;
             tc_fence_after();
             if (elect_one_lane()) {
@@ -375,40 +531,51 @@ __global__ void __launch_bounds__(THREADS, 1)
                                IDESC_O, j > 0 || t > 1 || kk > 0);
               umma_commit_pair(&vempty[r.slot]);
               if (t == 3) umma_commit_pair(odone);
+              if (t == 3 && j == u.nb - 1) umma_commit_pair(ofull);
             }
             __syncwarp();
             r.next();
           }
         }
-        if (elect_one_lane()) umma_commit_pair(drain);
-        __syncwarp();
-        // every MMA of the pair is complete before anything is given up
-        wait(drain, 0, s_abort, p.status, SITE_DRAIN);
+        ++n;
       }
-    } else {
-      // ---- softmax: a row a thread ----
-      const int sub = warp & 3, r = sub * 32 + lane, g = g0 + rank * R + r;
-      const bool live = r < R && g < rows;
+      if (elect_one_lane()) umma_commit_pair(drain);
+      __syncwarp();
+      // every MMA of the pair is complete before anything is given up
+      wait(drain, 0, s_abort, p.status, SITE_DRAIN);
+    }
+  } else if (warp < 8) {
+    regs_inc<216>();
+    // ---- softmax: a row a thread ----
+    const int sub = warp & 3, r = sub * 32 + lane;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + C::S_COL;
+    const uint32_t free_bar = mapa_u32(smem_u32(sfree), 0), p_bar = mapa_u32(smem_u32(pready), 0);
+    uint8_t* prow = sm + C::OFF_P + (r >> 3) * 1024 + (r & 7) * 128;
+    Line<R> line(p, pair);
+    Unit u;
+    int blk = 0;
+    bool ok = true;
+    for (int at = 0; ok && line.next(u); ++at) {
+      const int g = u.g0 + rank * R + r;
+      const bool live = r < R && g < u.rows;
       const int i = live ? g / p.H : 0;
       const uint64_t bits =
-          live && p.m.tree != nullptr ? __ldg(p.m.tree + static_cast<int64_t>(b) * p.m.T + i) : 0;
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + C::S_COL;
-      const uint32_t free_bar = mapa_u32(smem_u32(sfree), 0), p_bar = mapa_u32(smem_u32(pready), 0);
-      uint8_t* prow = sm + C::OFF_P + (r >> 3) * 1024 + (r & 7) * 128;
-      bool slow = false, ok = true;
-      for (int j = 0; j < nb && ok; ++j) {
+          live && p.m.tree != nullptr ? __ldg(p.m.tree + static_cast<int64_t>(u.b) * p.m.T + i) : 0;
+      float l_sum = 0.f, m_ref = -INFINITY;
+      bool slow = false;
+      for (int j = 0; j < u.nb && ok; ++j, ++blk) {
         // who sees what of the block's two pages (a row that is not there: all)
         uint64_t see[2], any[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int k = k0 + 2 * j + h;
+          const int k = u.k0 + 2 * j + h;
           see[h] = any[h] = 0;
-          if (k < k1 && page_row(p.kv, b, pages.page(k)) >= 0) {
-            any[h] = span_mask(p.m, s, i0, i1, pages.page(k) * 64);
-            see[h] = live ? row_mask(p.m, s, i, bits, pages.page(k) * 64) : any[h];
+          if (k < u.k1 && page_row(p.kv, u.b, u.pages.page(k)) >= 0) {
+            any[h] = span_mask(p.m, u.s, u.i0, u.i1, u.pages.page(k) * 64);
+            see[h] = live ? row_mask(p.m, u.s, i, bits, u.pages.page(k) * 64) : any[h];
           }
         }
-        ok = wait(sfull, j & 1, s_abort, p.status, SITE_SF);
+        ok = wait(sfull, blk & 1, s_abort, p.status, SITE_SF);
         if (!ok) break;
         tc_fence_after();
         uint32_t z[4][32];
@@ -461,7 +628,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (most > FAR) slow = true;
         l_sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
         // P is free once the block before has been multiplied
-        if (j > 0) ok = wait(odone, (j - 1) & 1, s_abort, p.status, SITE_O);
+        if (blk > 0) ok = wait(odone, (blk - 1) & 1, s_abort, p.status, SITE_O);
         if (!ok) break;
         if (r < R) {
 #pragma unroll
@@ -478,63 +645,104 @@ __global__ void __launch_bounds__(THREADS, 1)
           else mbar_arrive_cluster(p_bar);
         }
       }
-      if (ok) ok = wait(odone, (nb - 1) & 1, s_abort, p.status, SITE_O);
-      tc_fence_after();
-      // what the epilogues of both CTAs need of this row
+      // what the epilogues of both CTAs need of this row, once they are done with the
+      // unit before the last
+      const int bu = at & 1;
+      if (ok && at > 1) ok = wait(&lfree[bu], ((at >> 1) - 1) & 1, s_abort, p.status, SITE_L);
+      if (!ok) break;
+      if (live) {
+        const float lse2 = l_sum == 0.f ? -INFINITY : m_ref + log2f(l_sum);
+        if (!u.whole())
+          p.part_lse[(2 * pair + (at > 0)) * 2 * R + rank * R + r] = lse2;
+        else if (p.lse != nullptr)
+          p.lse[static_cast<int64_t>(u.b) * p.m.T * p.H + g] = lse2 * 0.6931471805599453f;
+      }
       if (r < R) {
-        const float inv = ok && l_sum != 0.f ? 1.f / l_sum : 0.f;
-        s_inv[rank * R + r] = inv;
-        st_cluster_u32(smem_u32(&s_inv[rank * R + r]), rank ^ 1, __float_as_uint(inv));
+        const float inv = l_sum != 0.f ? 1.f / l_sum : 0.f;
+        float* to = &s_inv[bu * 2 * R + rank * R + r];
+        *to = inv;
+        st_cluster_u32(smem_u32(to), rank ^ 1, __float_as_uint(inv));
       }
       if (__any_sync(0xffffffffu, slow && live) && lane == 0) {
-        s_slow[0] = 1;
-        st_cluster_u32(smem_u32(s_slow), rank ^ 1, 1);
+        s_slow[bu] = 1;
+        st_cluster_u32(smem_u32(&s_slow[bu]), rank ^ 1, 1);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_cluster(mapa_u32(smem_u32(&lfull[bu]), rank));
+        mbar_arrive_cluster(mapa_u32(smem_u32(&lfull[bu]), rank ^ 1));
+      }
+    }
+  } else {
+    regs_dec<160>();
+    // ---- out: lane = dim 256 rank + 128 m + 32 sub + lane, a row a column ----
+    const int sub = warp & 3;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16);
+    const uint32_t free_bar = mapa_u32(smem_u32(ofree), 0);
+    Line<R> line(p, pair);
+    Unit u;
+    int n = 0;
+    bool ok = true;
+    for (int at = 0; ok && line.next(u); ++at) {
+      const int bu = at & 1, here = min(2 * R, u.rows - u.g0);   // rows that are there
+      const int64_t first = static_cast<int64_t>(u.b) * p.m.T * p.H + u.g0;
+      const int64_t part = static_cast<int64_t>(2 * pair + (at > 0)) * 2 * R;
+      const bool parts = !u.whole();
+      const float* inv = s_inv + bu * 2 * R;
+      ok = wait<true>(&lfull[bu], (at >> 1) & 1, s_abort, p.status, SITE_L);
+      if (ok && u.nb > 0) ok = wait(ofull, n & 1, s_abort, p.status, SITE_O);
+      if (!ok) break;
+      tc_fence_after();
+      const bool slow = reinterpret_cast<volatile int*>(s_slow)[bu] != 0;
+      if (!slow) {
+#pragma unroll 1
+        for (int m = 0; m < 2; ++m) {
+          const int dim = 256 * rank + 128 * m + 32 * sub + lane;
+#pragma unroll 1
+          for (int c0 = 0; c0 < here; c0 += 32) {
+            uint32_t x[32];
+            if (u.nb > 0) {
+              tmem_ld32(taddr + m * 2 * R + c0, x);
+              tmem_ld_wait_regs(x);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = u.nb > 0 ? __float_as_uint(__uint_as_float(x[e]) * inv[c0 + e]) : 0;
+            if (parts) {
+              float* to = p.part_o + (part + c0) * kVlat + dim;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c0 + e < here) to[e * kVlat] = __uint_as_float(x[e]);
+            } else {
+              uint16_t* to = p.o + (first + c0) * kVlat + dim;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c0 + e < here) to[e * kVlat] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(x[e])));
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (u.nb > 0 && lane == 0) {                       // O^T may be overwritten
+        if (rank == 0) mbar_arrive(ofree);
+        else mbar_arrive_cluster_relaxed(free_bar);
+      }
+      if (u.nb > 0) ++n;
+      if (slow) {
+        for (int r = rank * R + sub; r < min(here, rank * R + R); r += 4)
+          attend_row(p, u.s, u.pages, u.k0, u.k1, u.b, u.g0 + r, parts ? p.part_o + (part + r) * kVlat : nullptr,
+                     parts ? p.part_lse + part + r : nullptr);
+        named_bar_sync(1, 128);                          // all of them have read the flag
+        if (sub == 0 && lane == 0) s_slow[bu] = 0;
+        __syncwarp();
+      }
+      if (lane == 0) {
+        mbar_arrive_cluster(mapa_u32(smem_u32(&lfree[bu]), rank));
+        mbar_arrive_cluster(mapa_u32(smem_u32(&lfree[bu]), rank ^ 1));
       }
     }
   }
   __syncwarp();
-  tc_fence_before();
-  cluster_sync();
-  tc_fence_after();
-
-  // ---- epilogue: warp w has dims 256 rank + 128 (w / 4) + 32 (w % 4) + lane ----
-  const int64_t first = static_cast<int64_t>(b) * p.m.T * p.H + g0;
-  const int64_t part = static_cast<int64_t>(blockIdx.x >> 1) * 2 * R;
-  const bool parts = p.splits > 1;
-  const int here = min(2 * R, rows - g0);                // rows of the unit that are there
-  if (s_slow[0]) {
-    for (int r = rank * R + warp; r < min(here, rank * R + R); r += WARPS)
-      attend_row(p, s, pages, k0, k1, b, g0 + r, parts ? p.part_o + (part + r) * kVlat : nullptr,
-                 parts ? p.part_lse + part + r : nullptr);
-  } else {
-    const int sub = warp & 3, m = warp >> 2, dim = 256 * rank + 128 * m + 32 * sub + lane;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + m * 2 * R;
-#pragma unroll 1
-    for (int c0 = 0; c0 < here; c0 += 32) {
-      uint32_t x[32];
-      if (nb > 0) {
-        tmem_ld32(taddr + c0, x);
-        tmem_ld_wait_regs(x);
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        if (c0 + e >= here) break;
-        const float v = nb > 0 ? __uint_as_float(x[e]) * s_inv[c0 + e] : 0.f;
-        if (parts)
-          p.part_o[(part + c0 + e) * kVlat + dim] = v;
-        else
-          p.o[(first + c0 + e) * kVlat + dim] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-      }
-    }
-    const int r = sub * 32 + lane, at = rank * R + r;
-    if (m == 1 && r < R && at < here) {
-      const float lse2 = l_sum == 0.f ? -INFINITY : m_ref + log2f(l_sum);
-      if (parts)
-        p.part_lse[part + at] = lse2;
-      else if (p.lse != nullptr)
-        p.lse[first + at] = lse2 * 0.6931471805599453f;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -544,23 +752,27 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Joins the splits of a row: lse = log2 sum 2^lse_k, o = sum 2^(lse_k - lse) o_k, in
-// FP32 and in order.  A CTA per row, four dims a thread.
-__global__ void __launch_bounds__(128) combine_kernel(const Params p, int R2) {
-  const int64_t row = blockIdx.x;                        // of all sequences
-  const int per = p.m.T * p.H, b = static_cast<int>(row / per), g = static_cast<int>(row % per);
+// Joins the pieces of the unit that pair blockIdx.x / 2R begins and does not end:
+// lse = log2 sum 2^lse_k, o = sum 2^(lse_k - lse) o_k, in FP32 and in order.  A CTA
+// per row, four dims a thread.
+template <int R>
+__global__ void __launch_bounds__(128) combine_kernel(const Params p) {
+  const int pair = blockIdx.x / (2 * R), r = blockIdx.x % (2 * R);
+  const Stretch mine = p.stretch[pair];
+  if (mine.head < 0) return;
+  const int b = mine.head / p.tiles, g = mine.head % p.tiles * 2 * R + r;
   if (g >= seq_of(p.m, b).n * p.H) return;
-  const int64_t unit = static_cast<int64_t>(b) * p.tiles + g / R2;
-  const int64_t at = unit * p.splits * R2 + g % R2;
+  int last = pair;                                       // the pieces: mine.slot, then 2k for k up to last
+  while (last + 1 < p.pairs && p.stretch[last + 1].first == mine.head && p.stretch[last + 1].j0 > 0) ++last;
+  auto at = [&](int k) { return static_cast<int64_t>(k == pair ? mine.slot : 2 * k) * 2 * R + r; };
   float top = -INFINITY;
-  for (int k = 0; k < p.splits; ++k) top = fmaxf(top, p.part_lse[at + static_cast<int64_t>(k) * R2]);
+  for (int k = pair; k <= last; ++k) top = fmaxf(top, p.part_lse[at(k)]);
   float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int k = 0; k < p.splits; ++k) {
-    const int64_t a = at + static_cast<int64_t>(k) * R2;
-    const float l = p.part_lse[a];
-    const float4 v = reinterpret_cast<const float4*>(p.part_o + a * kVlat)[threadIdx.x];
+  for (int k = pair; k <= last; ++k) {
+    const float l = p.part_lse[at(k)];
+    const float4 v = reinterpret_cast<const float4*>(p.part_o + at(k) * kVlat)[threadIdx.x];
     if (l == -INFINITY) continue;
     const float w = exp2f(l - top);
     sum += w;
@@ -568,28 +780,36 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p, int R2) {
     acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t row = static_cast<int64_t>(b) * p.m.T * p.H + g;
   reinterpret_cast<uint2*>(p.o + row * kVlat)[threadIdx.x] =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   if (threadIdx.x == 0 && p.lse != nullptr)
     p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Rows per CTA, units and splits.  A unit's blocks are split where the units leave
-// pairs of SMs idle, into parts of at least two blocks.
 struct Plan {
-  int R, tiles, splits;
+  int R, tiles, blocks, pairs;      // blocks: of a unit, at most
+  bool cut;
 };
+// span: the keys that one query may see at most.  Units are cut where the pair with
+// the most whole ones would have three blocks more to do than the mean: the pieces'
+// outputs and their joining take about as long (9 us).
 Plan plan(int B, int T, int H, int64_t span) {
   Plan q{};
   const int64_t rows = static_cast<int64_t>(T) * H;
   q.R = rows <= 96 ? 48 : 96;
   q.tiles = static_cast<int>((rows + 2 * q.R - 1) / (2 * q.R));
-  const int64_t units = static_cast<int64_t>(B) * q.tiles, pairs = num_sms() / 2;
-  const int64_t blocks = (span + 2 * q.R / H + 2 + 128) / 128 + 1;
-  int64_t n = pairs / units;
-  if (n > blocks / 2) n = blocks / 2;
-  q.splits = n < 1 ? 1 : static_cast<int>(n);
+  const int64_t tokens = (2 * q.R + H - 2) / H + 1;      // of a unit
+  q.blocks = static_cast<int>((span + tokens + 64) / 128 + 2);
+  const int64_t units = static_cast<int64_t>(B) * q.tiles, most = num_sms() / 2;
+  q.cut = (units + most - 1) / most * q.blocks * most > units * q.blocks + 3 * most;
+  const int64_t pieces = units * (q.cut ? q.blocks : 1);
+  q.pairs = static_cast<int>(pieces < most ? pieces : most);
   return q;
+}
+size_t part_bytes(const Plan& q) {
+  if (!q.cut) return 0;
+  return static_cast<size_t>(q.pairs) * (2 * 2 * q.R * (kVlat + 1) * sizeof(float) + sizeof(Stretch));
 }
 
 template <int R>
@@ -607,7 +827,7 @@ dsa_status_t launch(const DenseArgs& a, const Plan& q, const Params& p, cudaStre
       cudaSuccess)
     return launch_status("cudaFuncSetAttribute");
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2ll * a.B * q.tiles * q.splits));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * q.pairs));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
@@ -618,15 +838,16 @@ dsa_status_t launch(const DenseArgs& a, const Plan& q, const Params& p, cudaStre
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   cudaLaunchKernelEx(&cfg, pair_kernel<R>, tq, tk, p);
-  return launch_status("pair_kernel");
+  const dsa_status_t st = launch_status("pair_kernel");
+  if (st != DSA_OK || !q.cut) return st;
+  combine_kernel<R><<<static_cast<unsigned>(q.pairs * 2 * R), 128, 0, stream>>>(p);
+  return launch_status("combine_kernel");
 }
 
 }  // namespace dense
 
 size_t dense_scratch_bytes(int B, int T, int H, int64_t span) {
-  const dense::Plan q = dense::plan(B, T, H, span);
-  if (q.splits == 1) return 0;
-  return static_cast<size_t>(B) * q.tiles * q.splits * 2 * q.R * (kVlat + 1) * sizeof(float);
+  return dense::part_bytes(dense::plan(B, T, H, span));
 }
 
 dsa_status_t dense_fwd_launch(const DenseArgs& a, cudaStream_t stream) {
@@ -635,18 +856,26 @@ dsa_status_t dense_fwd_launch(const DenseArgs& a, cudaStream_t stream) {
   if (a.tree == nullptr && static_cast<int64_t>(a.window) + a.n_first < span)
     span = a.window + a.n_first > 0 ? a.window + a.n_first : 1;
   const Plan q = plan(a.B, a.T, a.H, span);
-  Params p{a.q_lat, store_of(a), mask_of(a), a.B, a.H, q.tiles, q.splits,
-           a.scale * 1.4426950408889634f, a.o_lat, a.lse, nullptr, nullptr, a.status};
-  if (q.splits > 1) {
-    const size_t rows = static_cast<size_t>(a.B) * q.tiles * q.splits * 2 * q.R;
-    if (a.scratch_bytes < rows * (kVlat + 1) * sizeof(float)) return DSA_ERR_WORKSPACE_TOO_SMALL;
-    p.part_o = static_cast<float*>(a.scratch);
-    p.part_lse = p.part_o + rows * kVlat;
-  }
-  const dsa_status_t st = q.R == 96 ? launch<96>(a, q, p, stream) : launch<48>(a, q, p, stream);
-  if (st != DSA_OK || q.splits == 1) return st;
-  combine_kernel<<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.T * a.H), 128, 0, stream>>>(p, 2 * q.R);
-  return launch_status("combine_kernel");
+  if (a.scratch_bytes < part_bytes(q)) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  Params p{};
+  p.q = a.q_lat;
+  p.kv = store_of(a);
+  p.m = mask_of(a);
+  p.B = a.B;
+  p.H = a.H;
+  p.tiles = q.tiles;
+  p.pairs = q.pairs;
+  p.nominal = a.tree != nullptr ? 0 : q.blocks;
+  p.cut = q.cut;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.o = a.o_lat;
+  p.lse = a.lse;
+  p.part_o = static_cast<float*>(a.scratch);
+  const size_t rows = static_cast<size_t>(q.pairs) * 2 * 2 * q.R;
+  p.part_lse = p.part_o + rows * kVlat;
+  p.stretch = reinterpret_cast<Stretch*>(p.part_lse + rows);
+  p.status = a.status;
+  return q.R == 96 ? launch<96>(a, q, p, stream) : launch<48>(a, q, p, stream);
 }
 
 }  // namespace dsa

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
     bool ok = wait(bfull, 0, s_abort, p.status, SITE_B);
     for (int j = 0; j < ng && ok; ++j) {
       const int bu = j & 1;
-      if (j > 1) ok = wait<true>(&afree[bu], ((j >> 1) - 1) & 1, s_abort, p.status, SITE_AE);
+      if (j > 1) ok = wait(&afree[bu], ((j >> 1) - 1) & 1, s_abort, p.status, SITE_AE);
       tc_fence_after();
       for (int c = 0; c < 9 && ok; ++c) {
         ok = wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
@@ -494,7 +494,11 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
           __syncwarp();
         }
         if (elect_one_lane()) {
-          mbar_expect_tx_cluster(bar, (2 + (any == ~0ull ? n : 0)) * CHUNK);
+          if (any == ~0ull) {
+            mbar_expect_tx_cluster(bar, (2 + n) * CHUNK);
+          } else {
+            mbar_expect_tx_cluster_release(bar, 2 * CHUNK);
+          }
           const int br = c < 0 ? 0 : static_cast<int>(p.block_row(b, x0 + rank, c, 1));
           tma_load_2d_pair(a, &tm_pz, bar, 0, br);
           tma_load_2d_pair(a + CHUNK, &tm_pz, bar, 0, br + 64);
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
     if (lane == 0 && used > 0) s_some[0] = 1;
     for (; used > 0; --used) {
       if (--r.slot < 0) r.slot = C::NS - 1, r.ph ^= 1;
-      if (rank == 0) wait<true>(&full[r.slot], r.ph, s_abort, p.status, SITE_F);
+      if (rank == 0) wait(&full[r.slot], r.ph, s_abort, p.status, SITE_F);
       if (ok) wait(&empty[r.slot], r.ph, s_abort, p.status, SITE_E);
     }
   } else if (warp == 1 && rank == 0) {
@@ -520,7 +524,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
     bool ok = true;
     uint32_t more = 0;                               // accumulate
     auto multiply = [&](bool rot) {
-      ok = wait<true>(&full[r.slot], r.ph, s_abort, p.status, SITE_F);
+      ok = wait(&full[r.slot], r.ph, s_abort, p.status, SITE_F);
       if (!ok) return;
       tc_fence_after();
       if (elect_one_lane()) {
