@@ -466,9 +466,9 @@ dsa_status_t dsa_cache_append_rope(const float* k_pre, const uint16_t* kv_new,
  *   n_draft [B] int32             drafted tokens of each sequence, or NULL: T.  The
  *           outputs of the tokens behind them are left as they were.
  *   scale, o_lat [B, T, H, 512] BF16, lse [B, T, H] FP32 or NULL   as sparse_mla_fwd
- * A token that sees nothing gets o_lat = 0 and lse = -inf.  Rows that no token of
- * the sequence sees may hold anything, and what a row holds (an infinity or a NaN
- * too) reaches only the tokens that see it.
+ * A token that sees nothing gets o_lat = 0 and lse = -inf.  What a row holds (an
+ * infinity or a NaN too) reaches only the tokens that see it; such a row is fast
+ * behind the sequence's last, and slow where some tokens do not see it.
  * kv_len[b] < 0, kv_len[b] + n_draft[b] > max_kv_len (the sequence's tokens then see
  * nothing), n_draft outside [0, T] (taken as the nearer bound) and pages outside the
  * pool (not seen) are recorded as DSA_ERR_BAD_INDEX.
@@ -508,7 +508,9 @@ dsa_status_t mla_window_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const i
  *   q_lat, kv, q_start, kv_len, window, n_first, scale   as for mla_window_fwd;
  *                       kv contiguous, its sequences in separate rows
  *   o_lat, lse          the forward's outputs
- *   d_o   [B,Tq,H,512]  BF16   upstream gradient of o_lat
+ *                       (these, q_lat and kv's rows below kv_len[b] finite; lse of a
+ *                       query that sees nothing -inf, as the forward gives it)
+ *   d_o   [B,Tq,H,512]  BF16   upstream gradient of o_lat, finite
  *   dq    [B,Tq,H,576]  BF16   written; 0 for a query that sees nothing
  *   dkv                 BF16   rows numbered like kv's ([B, seq_stride, 576]):
  *                       rows 0 .. kv_len[b]-1 are written (0 where no query of the

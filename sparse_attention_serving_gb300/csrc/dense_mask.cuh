@@ -25,15 +25,15 @@ struct Seq {
 };
 __device__ __forceinline__ Seq seq_of(const Mask& m, int b) {
   Seq s;
-  s.pos0 = __ldg(m.pos0 + b);
+  s.pos0 = m.pos0[b];
   if (m.tree != nullptr) {
-    const int n = m.lim != nullptr ? __ldg(m.lim + b) : m.T;
+    const int n = m.lim != nullptr ? m.lim[b] : m.T;
     s.n = min(max(n, 0), m.T);
     s.ok = s.pos0 >= 0 && s.pos0 <= m.max_kv_len - s.n;
     s.L = s.pos0 + s.n;
   } else {
     s.n = m.T;
-    s.L = __ldg(m.lim + b);
+    s.L = m.lim[b];
     s.ok = s.pos0 >= 0 && s.L <= m.max_kv_len && s.pos0 < s.L;
   }
   return s;
@@ -41,7 +41,7 @@ __device__ __forceinline__ Seq seq_of(const Mask& m, int b) {
 // What is wrong with the sequence, if anything: said once, by one thread.
 __device__ __forceinline__ void report_seq(const Mask& m, const Seq& s, int b, uint32_t* status) {
   if (m.tree != nullptr) {
-    if (m.lim != nullptr && s.n != __ldg(m.lim + b))
+    if (m.lim != nullptr && s.n != m.lim[b])
       status_raise(status, DSA_ERR_BAD_INDEX, SITE_DRAFT, static_cast<uint32_t>(b));
     if (!s.ok && s.n > 0) status_raise(status, DSA_ERR_BAD_INDEX, SITE_SEQ, static_cast<uint32_t>(b));
   } else if (!s.ok || s.pos0 > s.L - s.n) {
@@ -101,15 +101,6 @@ __device__ __forceinline__ Pages pages_of(const Mask& m, const Seq& s, int i0, i
   return p;
 }
 
-// The rows kb..kb+63 that any of the queries i0..i1 may see.
-__device__ __forceinline__ uint64_t span_mask(const Mask& m, const Seq& s, int i0, int i1, int kb) {
-  if (!s.ok) return 0;
-  if (m.tree != nullptr) return range_bits(0, s.L, kb);
-  const int t0 = s.pos0 + i0, t1 = min(s.pos0 + i1, s.L - 1);
-  return range_bits(t0 - m.window + 1, m.window > 0 ? t1 + 1 : 0, kb) |
-         range_bits(0, min(m.n_first, t1 + 1), kb);
-}
-
 struct Store {
   const uint16_t* base;
   int64_t seq_stride;
@@ -120,7 +111,7 @@ struct Store {
 __device__ __forceinline__ int64_t page_row(const Store& kv, int b, int pg) {
   if (kv.block_table == nullptr) return static_cast<int64_t>(b) * kv.seq_stride + pg * 64;
   if (pg >= kv.max_pages) return -1;
-  const int id = __ldg(kv.block_table + static_cast<int64_t>(b) * kv.max_pages + pg);
+  const int id = kv.block_table[static_cast<int64_t>(b) * kv.max_pages + pg];
   return id < 0 || id >= kv.num_pages ? -1 : static_cast<int64_t>(id) * kPage;
 }
 

@@ -20,14 +20,14 @@
 // read, 136 KB copied in and 24 KB of P written, about 3,800 cycles at 128 bytes,
 // beside 3,840 cycles of MMAs (R = 96).
 //
-// Roles (12 warps): 0 copies Q and K, 1 copies V, 2 and 3 of the even CTA issue the
+// Roles (12 warps): 0 copies Q (chunk by chunk beside a unit's first K) and K, 1 copies V, 2 and 3 of the even CTA issue the
 // two products, 4..7 hold a row a thread: its 128 scores, P = 2^(z - m) to BF16 in
 // shared memory; 8..11 write O^T / l out while the next unit's first products run.
 // m is the maximum of the first block in which the row sees anything, so O^T is
 // never rescaled; a row whose later scores exceed it by 2^100 sends its unit to
-// attend_row.  So does a row that one query of the unit sees and another does not
-// and that holds an infinity or a NaN (0 * NaN would reach both).  Rows of a page
-// that nobody in the unit sees are zeroed in V before use.
+// attend_row.  So does a row of the sequence that holds an infinity or a NaN and that
+// some query of the unit does not see (0 * NaN would reach it).  Rows behind the
+// sequence, in its last page, are zeroed in V before use.
 //
 // Persistent: the blocks of all units stand in one line, and every pair of SMs takes
 // an equal stretch of it (whole units where there are many).  A unit that is cut has
@@ -57,7 +57,7 @@ struct Cfg {
   static constexpr int OFF_K = OFF_P + 2 * QCH;
   static constexpr int OFF_V = OFF_K + NK * CHUNK;
   static constexpr int OFF_MISC = OFF_V + NV * 2 * CHUNK;
-  static constexpr int MISC = 512 + 16 * R;
+  static constexpr int MISC = 1024 + 16 * R;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   static constexpr uint32_t S_COL = 4 * R;
   static_assert(SMEM <= 232448, "shared memory");
@@ -68,7 +68,7 @@ struct Cfg {
 enum : uint32_t {
   SITE_Q = 0x710, SITE_KF = 0x711, SITE_KE = 0x712, SITE_VF = 0x713, SITE_VE = 0x714,
   SITE_SF = 0x715, SITE_SE = 0x716, SITE_P = 0x717, SITE_O = 0x718, SITE_VT = 0x719,
-  SITE_DRAIN = 0x71a, SITE_OE = 0x71b, SITE_L = 0x71c
+  SITE_DRAIN = 0x71a, SITE_OE = 0x71b, SITE_L = 0x71c, SITE_U = 0x71d
 };
 
 // A pair's stretch of the line, as combine_kernel needs it: the unit and the block
@@ -275,6 +275,26 @@ struct Line {
   }
 };
 
+// The units of a CTA's stretch in shared memory: the K warp walks the line and
+// publishes them, the others read them there (and keep their registers).
+constexpr int UNITS = 4;
+struct Feed {
+  const Unit* ring;
+  uint64_t* full;
+  uint64_t* empty;
+  volatile int* s_abort;
+  uint32_t* status;
+  int at = -1;
+  // The next unit, the one before given back; null at the end or once the CTA has given up.
+  __device__ __forceinline__ const Unit* next() {
+    if (at >= 0) mbar_arrive_warp(&empty[at % UNITS]);
+    ++at;
+    if (!wait(&full[at % UNITS], (at / UNITS) & 1, s_abort, status, SITE_U)) return nullptr;
+    const Unit* u = ring + at % UNITS;
+    return u->b >= 0 ? u : nullptr;
+  }
+};
+
 template <int R>
 __global__ void __launch_bounds__(THREADS, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
@@ -288,23 +308,25 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* kempty = kfull + C::NK;
   uint64_t* vfull = kempty + C::NK;                                  // even CTA
   uint64_t* vempty = vfull + C::NV;
-  uint64_t* qfull = vempty + C::NV;                                  // even CTA
-  uint64_t* qempty = qfull + 1;
-  uint64_t* sfull = qfull + 2;
-  uint64_t* sfree = qfull + 3;                                       // even CTA
-  uint64_t* pready = qfull + 4;                                      // even CTA
-  uint64_t* odone = qfull + 5;                                       // a block's values added
-  uint64_t* ofull = qfull + 6;                                       // a unit's
-  uint64_t* ofree = qfull + 7;                                       // even CTA
-  uint64_t* lfull = qfull + 8;                                       // [2] a unit's sums, of both CTAs
-  uint64_t* lfree = qfull + 10;                                      // [2]
-  uint64_t* vland = qfull + 12;                                      // [2] this CTA's own copies
-  uint64_t* drain = qfull + 14;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(qfull + 15);
+  uint64_t* sfull = vempty + C::NV;
+  uint64_t* sfree = sfull + 1;                                       // even CTA
+  uint64_t* pready = sfull + 2;                                      // even CTA
+  uint64_t* odone = sfull + 3;                                       // a block's values added
+  uint64_t* ofull = sfull + 4;                                       // a unit's
+  uint64_t* ofree = sfull + 5;                                       // [2] even CTA: 2R columns read
+  uint64_t* lfull = sfull + 7;                                       // [2] a unit's sums, of both CTAs
+  uint64_t* lfree = sfull + 9;                                       // [2]
+  uint64_t* vland = sfull + 11;                                      // [2] this CTA's own copies
+  uint64_t* drain = sfull + 13;
+  uint64_t* ufull = sfull + 14;                                      // [UNITS]
+  uint64_t* uempty = ufull + UNITS;                                  // [UNITS]
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(uempty + UNITS);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
   int* s_slow = reinterpret_cast<int*>(tslot + 2);                   // [2]
-  float* s_inv = reinterpret_cast<float*>(sm + C::OFF_MISC + 512);   // [2][2R]
-  static_assert((2 * C::NK + 2 * C::NV + 15) * 8 + 16 <= 512, "misc");
+  Unit* s_unit = reinterpret_cast<Unit*>(sm + C::OFF_MISC + 512);    // [UNITS]
+  float* s_inv = reinterpret_cast<float*>(sm + C::OFF_MISC + 1024);  // [2][2R]
+  static_assert((2 * C::NK + 2 * C::NV + 14 + 2 * UNITS) * 8 + 16 <= 512, "misc");
+  static_assert(UNITS * sizeof(Unit) <= 512, "misc");
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
@@ -312,15 +334,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (tid == 0) {
     for (int k = 0; k < C::NK; ++k) mbar_init(&kfull[k], 1), mbar_init(&kempty[k], 1);
     for (int k = 0; k < C::NV; ++k) mbar_init(&vfull[k], 2), mbar_init(&vempty[k], 1);
-    mbar_init(qfull, 1);
-    mbar_init(qempty, 1);
     mbar_init(sfull, 1);
     mbar_init(sfree, 8);
     mbar_init(pready, 8);
     mbar_init(odone, 1);
     mbar_init(ofull, 1);
-    mbar_init(ofree, 8);
-    for (int k = 0; k < 2; ++k) mbar_init(&lfull[k], 8), mbar_init(&lfree[k], 8), mbar_init(&vland[k], 1);
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&ofree[k], 8);
+      mbar_init(&lfull[k], 8);
+      mbar_init(&lfree[k], 8);
+      mbar_init(&vland[k], 1);
+    }
+    for (int k = 0; k < UNITS; ++k) mbar_init(&ufull[k], 1), mbar_init(&uempty[k], rank == 0 ? 11 : 9);
     mbar_init(drain, 2);
     s_abort[0] = 0;
     s_slow[0] = s_slow[1] = 0;
@@ -337,62 +362,67 @@ __global__ void __launch_bounds__(THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  pdl_wait();
+  pdl_start_next();
+  Feed feed{s_unit, ufull, uempty, s_abort, p.status};
 
   if (warp < 4) {
-    regs_dec<128>();
     if (warp == 0) {
-      // ---- Q, then the own page's K, chunk by chunk ----
-      const uint32_t qbar = mapa_u32(smem_u32(qfull), 0);
+      // ---- the own page's K, chunk by chunk; beside the first block's, Q's: the
+      // products that read a chunk of the unit before are those that free K's slot ----
       Line<R> line(p, pair);
       Unit u;
       Ring<C::NK> r;
       Stretch mine{-1, 0, -1, 0};
-      int used = 0, n = 0;
+      int used = 0;
       bool ok = true;
-      for (int at = 0; ok && line.next(u); ++at) {
+      for (int at = 0;; ++at) {
+        const bool more = line.next(u);
+        if (!more) u.b = -1;
+        if (at >= UNITS) ok = wait(&uempty[at % UNITS], (at / UNITS - 1) & 1, s_abort, p.status, SITE_U);
+        if (!ok) break;
+        if (lane == 0) {
+          s_unit[at % UNITS] = u;
+          mbar_arrive(&ufull[at % UNITS]);
+        }
+        __syncwarp();
+        if (!more) break;
         if (at == 0) mine.first = u.id, mine.j0 = u.j0;
         if (u.j0 == 0 && u.j1 < u.of) mine.head = u.id, mine.slot = 2 * pair + (at > 0);
         if (rank == 0 && lane == 0 && u.g0 == 0 && u.j0 == 0) report_seq(p.m, u.s, u.b, p.status);
-        if (u.nb == 0) continue;
-        if (n > 0) ok = wait(qempty, (n - 1) & 1, s_abort, p.status, SITE_Q);
-        ++n;
-        if (!ok) break;
-        if (elect_one_lane()) {
-          if (rank == 0) mbar_expect_tx(qfull, 2u * 9u * C::QCH);
-          const int row = static_cast<int>(static_cast<int64_t>(u.b) * p.m.T * p.H) + u.g0 + rank * R;
-#pragma unroll 1
-          for (int c = 0; c < 9; ++c)
-            tma_load_2d_pair(sm + C::OFF_Q + c * C::QCH, &tm_q, qbar, 64 * c, row);
-        }
-        __syncwarp();
+        const int qrow = static_cast<int>(static_cast<int64_t>(u.b) * p.m.T * p.H) + u.g0 + rank * R;
         for (int j = 0; j < u.nb && ok; ++j) {
           const int k = u.k0 + 2 * j + rank;
-          int64_t row = -1;
+          const bool both = u.k0 + 2 * j + 1 < u.k1;       // else the odd CTA's slots keep what they hold
+          int64_t row = 0;
           if (k < u.k1) {
             row = page_row(p.kv, u.b, u.pages.page(k));
-            if (row < 0 && lane == 0)
-              status_raise(p.status, DSA_ERR_BAD_INDEX, SITE_PAGE, static_cast<uint32_t>(u.pages.page(k)));
+            if (row < 0) {                                 // nobody sees it
+              if (lane == 0)
+                status_raise(p.status, DSA_ERR_BAD_INDEX, SITE_PAGE, static_cast<uint32_t>(u.pages.page(k)));
+              row = 0;
+            }
           }
-          if (row < 0) row = 0;                            // nobody sees it
           for (int c = 0; c < 9; ++c) {
             ok = used < C::NK || wait(&kempty[r.slot], r.ph ^ 1, s_abort, p.status, SITE_KE);
             if (!ok) break;
             if (elect_one_lane()) {
-              if (rank == 0) mbar_expect_tx(&kfull[r.slot], 2 * CHUNK);
-              tma_load_2d_pair(sm + C::OFF_K + r.slot * CHUNK, &tm_kv,
-                               mapa_u32(smem_u32(&kfull[r.slot]), 0), 64 * c, static_cast<int>(row));
+              const uint32_t bar = mapa_u32(smem_u32(&kfull[r.slot]), 0);
+              if (rank == 0) mbar_expect_tx(&kfull[r.slot], (both ? 2 : 1) * CHUNK + (j == 0 ? 2 * C::QCH : 0));
+              if (j == 0) tma_load_2d_pair(sm + C::OFF_Q + c * C::QCH, &tm_q, bar, 64 * c, qrow);
+              if (k < u.k1)
+                tma_load_2d_pair(sm + C::OFF_K + r.slot * CHUNK, &tm_kv, bar, 64 * c, static_cast<int>(row));
             }
             __syncwarp();
             if (used < C::NK) ++used;
             r.next();
           }
         }
+        if (!ok) break;
       }
       if (rank == 0 && lane == 0 && p.cut) p.stretch[pair] = mine;
       // the pair's copies have landed and the last arrivals of the MMAs have come
       // before either CTA leaves
-      if (rank == 0 && n > 0) wait(qfull, (n - 1) & 1, s_abort, p.status, SITE_Q);
-      if (ok && n > 0) wait(qempty, (n - 1) & 1, s_abort, p.status, SITE_Q);
       for (; used > 0; --used) {
         if (--r.slot < 0) r.slot = C::NK - 1, r.ph ^= 1;
         if (rank == 0) wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
@@ -400,21 +430,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     } else if (warp == 1) {
       // ---- V: the own 256 dims of both pages, 128 at a time ----
-      Line<R> line(p, pair);
-      Unit u;
       Ring<C::NV> r;
       int used = 0;
       uint32_t vph = 0;
       bool ok = true;
-      while (ok && line.next(u)) {
+      while (const Unit* up = ok ? feed.next() : nullptr) {
+        const Unit& u = *up;
 #pragma unroll 1
-        for (int k = u.k0; k < u.k0 + 2 * u.nb && ok; ++k) {
-          int64_t row = -1;
-          uint64_t any = 0;
-          if (k < u.k1) {
-            row = page_row(p.kv, u.b, u.pages.page(k));
-            if (row >= 0) any = span_mask(p.m, u.s, u.i0, u.i1, u.pages.page(k) * 64);
-          }
+        for (int k = u.k0; k < u.k1 && ok; ++k) {
+          const int64_t row = page_row(p.kv, u.b, u.pages.page(k));
+          const uint64_t any = row < 0 ? 0 : range_bits(0, u.s.L, u.pages.page(k) * 64);
           Ring<C::NV> z = r;
 #pragma unroll 1
           for (int m = 0; m < 2; ++m) {
@@ -439,8 +464,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             r.next();
           }
           if (!ok || any == ~0ull) continue;
-          // rows that nobody sees become zeros: whatever they hold must not meet the
-          // zeros of P
+          // rows behind the sequence become zeros: whatever they hold must not meet
+          // the zeros of P
 #pragma unroll 1
           for (int m = 0; m < 2; ++m) {
             if (any != 0) {
@@ -470,15 +495,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ---- scores ----
         const uint64_t qd = smem_desc(smem_u32(sm + C::OFF_Q), 16, 1024);
         const uint64_t kd = smem_desc(smem_u32(sm + C::OFF_K), 16, 1024);
-        Line<R> line(p, pair);
-        Unit u;
         Ring<C::NK> r;
-        int n = 0, blk = 0;
+        int blk = 0;
         bool ok = true;
-        while (ok && line.next(u)) {
-          if (u.nb == 0) continue;
-          ok = wait(qfull, n & 1, s_abort, p.status, SITE_Q);
-          ++n;
+        while (const Unit* up = ok ? feed.next() : nullptr) {
+        const Unit& u = *up;
           for (int j = 0; j < u.nb && ok; ++j, ++blk) {
             if (blk > 0) ok = wait(sfree, (blk - 1) & 1, s_abort, p.status, SITE_SE);
             tc_fence_after();
@@ -494,7 +515,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                                  c > 0 || kk > 0);
                 umma_commit_pair(&kempty[r.slot]);
                 if (c == 8) umma_commit_pair(sfull);
-                if (c == 8 && j == u.nb - 1) umma_commit_pair(qempty);
               }
               __syncwarp();
               r.next();
@@ -508,19 +528,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       // ---- values ----
       const uint64_t pd = smem_desc(smem_u32(sm + C::OFF_P), 16, 1024);
       const uint64_t vd = smem_desc(smem_u32(sm + C::OFF_V), CHUNK, 1024);
-      Line<R> line(p, pair);
-      Unit u;
       Ring<C::NV> r;
       int n = 0, blk = 0;
       bool ok = true;
-      while (ok && line.next(u)) {
+      while (const Unit* up = ok ? feed.next() : nullptr) {
+        const Unit& u = *up;
         if (u.nb == 0) continue;
         for (int j = 0; j < u.nb && ok; ++j, ++blk) {
           ok = wait(pready, blk & 1, s_abort, p.status, SITE_P);
-          // the unit before has been read out
-          if (ok && j == 0 && n > 0) ok = wait(ofree, (n - 1) & 1, s_abort, p.status, SITE_OE);
-          for (int t = 0; t < 4 && ok; ++t) {            // page t >> 1, dims 128 (t & 1)
-            ok = wait(&vfull[r.slot], r.ph, s_abort, p.status, SITE_VF);
+          const int nt = u.k0 + 2 * j + 1 < u.k1 ? 4 : 2;
+          for (int t = 0; t < nt && ok; ++t) {           // page t >> 1, dims 128 (t & 1)
+            // the unit before has been read out
+            if (j == 0 && t < 2 && n > 0) ok = wait(&ofree[t], (n - 1) & 1, s_abort, p.status, SITE_OE);
+            ok = ok && wait(&vfull[r.slot], r.ph, s_abort, p.status, SITE_VF);
             if (!ok) break;
             tc_fence_after();
             if (elect_one_lane()) {
@@ -530,8 +550,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 umma_bf16_pair(tmem + (t & 1) * 2 * R, desc_add(a, kk * 2048), desc_add(w, kk * 32),
                                IDESC_O, j > 0 || t > 1 || kk > 0);
               umma_commit_pair(&vempty[r.slot]);
-              if (t == 3) umma_commit_pair(odone);
-              if (t == 3 && j == u.nb - 1) umma_commit_pair(ofull);
+              if (t == nt - 1) umma_commit_pair(odone);
+              if (t == nt - 1 && j == u.nb - 1) umma_commit_pair(ofull);
             }
             __syncwarp();
             r.next();
@@ -545,22 +565,21 @@ __global__ void __launch_bounds__(THREADS, 1)
       wait(drain, 0, s_abort, p.status, SITE_DRAIN);
     }
   } else if (warp < 8) {
-    regs_inc<216>();
     // ---- softmax: a row a thread ----
     const int sub = warp & 3, r = sub * 32 + lane;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + C::S_COL;
     const uint32_t free_bar = mapa_u32(smem_u32(sfree), 0), p_bar = mapa_u32(smem_u32(pready), 0);
     uint8_t* prow = sm + C::OFF_P + (r >> 3) * 1024 + (r & 7) * 128;
-    Line<R> line(p, pair);
-    Unit u;
     int blk = 0;
     bool ok = true;
-    for (int at = 0; ok && line.next(u); ++at) {
+    while (const Unit* up = ok ? feed.next() : nullptr) {
+      const Unit& u = *up;
+      const int at = feed.at;
       const int g = u.g0 + rank * R + r;
       const bool live = r < R && g < u.rows;
       const int i = live ? g / p.H : 0;
       const uint64_t bits =
-          live && p.m.tree != nullptr ? __ldg(p.m.tree + static_cast<int64_t>(u.b) * p.m.T + i) : 0;
+          live && p.m.tree != nullptr ? p.m.tree[static_cast<int64_t>(u.b) * p.m.T + i] : 0;
       float l_sum = 0.f, m_ref = -INFINITY;
       bool slow = false;
       for (int j = 0; j < u.nb && ok; ++j, ++blk) {
@@ -571,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int k = u.k0 + 2 * j + h;
           see[h] = any[h] = 0;
           if (k < u.k1 && page_row(p.kv, u.b, u.pages.page(k)) >= 0) {
-            any[h] = span_mask(p.m, u.s, u.i0, u.i1, u.pages.page(k) * 64);
+            any[h] = range_bits(0, u.s.L, u.pages.page(k) * 64);
             see[h] = live ? row_mask(p.m, u.s, i, bits, u.pages.page(k) * 64) : any[h];
           }
         }
@@ -674,16 +693,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   } else {
-    regs_dec<160>();
     // ---- out: lane = dim 256 rank + 128 m + 32 sub + lane, a row a column ----
     const int sub = warp & 3;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16);
     const uint32_t free_bar = mapa_u32(smem_u32(ofree), 0);
-    Line<R> line(p, pair);
-    Unit u;
     int n = 0;
     bool ok = true;
-    for (int at = 0; ok && line.next(u); ++at) {
+    while (const Unit* up = ok ? feed.next() : nullptr) {
+      const Unit& u = *up;
+      const int at = feed.at;
       const int bu = at & 1, here = min(2 * R, u.rows - u.g0);   // rows that are there
       const int64_t first = static_cast<int64_t>(u.b) * p.m.T * p.H + u.g0;
       const int64_t part = static_cast<int64_t>(2 * pair + (at > 0)) * 2 * R;
@@ -694,38 +711,43 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       const bool slow = reinterpret_cast<volatile int*>(s_slow)[bu] != 0;
-      if (!slow) {
 #pragma unroll 1
-        for (int m = 0; m < 2; ++m) {
-          const int dim = 256 * rank + 128 * m + 32 * sub + lane;
+      for (int m = 0; m < 2; ++m) {
+        const int dim = 256 * rank + 128 * m + 32 * sub + lane;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + m * 2 * R;
 #pragma unroll 1
-          for (int c0 = 0; c0 < here; c0 += 32) {
-            uint32_t x[32];
-            if (u.nb > 0) {
-              tmem_ld32(taddr + m * 2 * R + c0, x);
-              tmem_ld_wait_regs(x);
-            }
+        for (int c0 = 0; c0 < here && !slow; c0 += 32) {
+          uint32_t x[32];
+          if (u.nb > 0) {
+            tmem_ld32(taddr + c0, x);
+            tmem_ld_wait_regs(x);
+          }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = u.nb > 0 ? __float_as_uint(__uint_as_float(x[e]) * inv[c0 + e]) : 0;
-            if (parts) {
-              float* to = p.part_o + (part + c0) * kVlat + dim;
+          for (int e = 0; e < 32; e += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(inv + c0 + e);
+            x[e] = u.nb > 0 ? __float_as_uint(__uint_as_float(x[e]) * w.x) : 0;
+            x[e + 1] = u.nb > 0 ? __float_as_uint(__uint_as_float(x[e + 1]) * w.y) : 0;
+            x[e + 2] = u.nb > 0 ? __float_as_uint(__uint_as_float(x[e + 2]) * w.z) : 0;
+            x[e + 3] = u.nb > 0 ? __float_as_uint(__uint_as_float(x[e + 3]) * w.w) : 0;
+          }
+          if (parts) {
+            float* to = p.part_o + (part + c0) * kVlat + dim;
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c0 + e < here) to[e * kVlat] = __uint_as_float(x[e]);
-            } else {
-              uint16_t* to = p.o + (first + c0) * kVlat + dim;
+            for (int e = 0; e < 32; ++e)
+              if (c0 + e < here) to[e * kVlat] = __uint_as_float(x[e]);
+          } else {
+            uint16_t* to = p.o + (first + c0) * kVlat + dim;
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c0 + e < here) to[e * kVlat] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(x[e])));
-            }
+            for (int e = 0; e < 32; ++e)
+              if (c0 + e < here) to[e * kVlat] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(x[e])));
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (u.nb > 0 && lane == 0) {                       // O^T may be overwritten
-        if (rank == 0) mbar_arrive(ofree);
-        else mbar_arrive_cluster_relaxed(free_bar);
+        tc_fence_before();
+        __syncwarp();
+        if (u.nb > 0 && lane == 0) {                     // these columns may be overwritten
+          if (rank == 0) mbar_arrive(&ofree[m]);
+          else mbar_arrive_cluster_relaxed(free_bar + 8 * m);
+        }
       }
       if (u.nb > 0) ++n;
       if (slow) {
@@ -758,6 +780,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <int R>
 __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
   const int pair = blockIdx.x / (2 * R), r = blockIdx.x % (2 * R);
+  pdl_wait();
+  pdl_start_next();
   const Stretch mine = p.stretch[pair];
   if (mine.head < 0) return;
   const int b = mine.head / p.tiles, g = mine.head % p.tiles * 2 * R + r;
@@ -826,21 +850,10 @@ dsa_status_t launch(const DenseArgs& a, const Plan& q, const Params& p, cudaStre
   if (cudaFuncSetAttribute(pair_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
       cudaSuccess)
     return launch_status("cudaFuncSetAttribute");
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * q.pairs));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 2;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, pair_kernel<R>, tq, tk, p);
+  launch_overlapped(pair_kernel<R>, static_cast<unsigned>(2 * q.pairs), THREADS, C::SMEM, 2, stream, tq, tk, p);
   const dsa_status_t st = launch_status("pair_kernel");
   if (st != DSA_OK || !q.cut) return st;
-  combine_kernel<R><<<static_cast<unsigned>(q.pairs * 2 * R), 128, 0, stream>>>(p);
+  launch_overlapped(combine_kernel<R>, static_cast<unsigned>(q.pairs * 2 * R), 128, 0, 0, stream, p);
   return launch_status("combine_kernel");
 }
 

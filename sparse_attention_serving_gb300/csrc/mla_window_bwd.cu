@@ -465,10 +465,9 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       }
     } else {
       const Pages l = tile_pages(p, s, x0 + rank);
-      const int rows = s.n * p.H, i0 = x0 * X / p.H, i1 = (min(x1 * X, rows) - 1) / p.H;
       for (int k = 0; k < list.count() && ok; ++k) {
         const int pg = list.page(k), c = place(l, pg), row = static_cast<int>(page_row(p.kv, b, pg));
-        const uint64_t any = span_mask(p.m, s, i0, i1, pg * 64);
+        const uint64_t any = range_bits(0, s.L, pg * 64);
         if (!acquire()) break;
         uint8_t* a = sm + r.slot * C::STAGE;
         uint8_t* w = a + C::OFF_W;
@@ -476,7 +475,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
         const bool rot = upper && rank == 0;
         const int n = rot ? 3 : 2;
         if (any != ~0ull) {
-          // rows that nobody sees become zeros: whatever they hold must not meet
+          // rows behind the sequence become zeros: whatever they hold must not meet
           // the zeros of dZ
           if (elect_one_lane()) {
             mbar_expect_tx(land, n * CHUNK);
