@@ -16,10 +16,17 @@
 //            A thread has a key and both of its products with a row: p and dz need
 //            no exchange.  Blocks leave from registers.
 //   product  dq: [256 rows x 256 or 320 dims] = dZ . K over the pages of two tiles;
-//            dkv: [256 keys x 256 or 320 dims] = dZ^T . q + P^T . dO over a segment of
-//            the tiles that see the keys.  M = 256 on a pair of CTAs; the 576 dims are
+//            dkv: [256 keys x 256 or 320 dims] = dZ^T . q + P^T . dO over those tiles of
+//            a segment that see the keys.  M = 256 on a pair of CTAs; the 576 dims are
 //            two tasks (0..255; 256..575), as 512 TMEM columns do not hold them.
 //   reduce   dkv's segments, added in order (no atomics: equal calls give equal bits)
+// dkv's tasks stand in the order of the segments, so that the key tiles that see a
+// segment run through its q and d_o at the same time and read them from L2 (by key
+// tile they came from HBM for each: 5.5 GB instead of 2.7 at 4096 tokens x 96 heads,
+// window 1024, and 0.88 ms at 6.4 TB/s).  pz and dq are persistent (dkv's tasks differ
+// in length and are dealt out as SMs fall free): the next task's
+// copies (pz: of its q and d_o too, chunk by chunk beside the first keys) and first
+// products run while the last one's results are written out.
 // Tiles go in chunks where P and dZ of all would take more than kChunkBytes.
 #include <cmath>
 
@@ -36,18 +43,20 @@ using namespace dense;
 constexpr int X = 128;                              // rows of a tile
 constexpr int BLOCK = X * 128;                      // bytes of a block: 128 rows x 64 keys
 constexpr int64_t kChunkBytes = int64_t(4) << 30;   // P and dZ at a time
-constexpr int TASKS = 304;                          // dkv tasks aimed at: about four a pair of SMs
+constexpr int TASKS = 600;                          // dkv tasks aimed at: about eight a pair of SMs
 
 enum : uint32_t {
   SITE_B = 0x720, SITE_KF = 0x721, SITE_KE = 0x722, SITE_AF = 0x723, SITE_AE = 0x724,
-  SITE_F = 0x725, SITE_E = 0x726, SITE_LAND = 0x727, SITE_DONE = 0x728, SITE_DRAIN = 0x729
+  SITE_F = 0x725, SITE_E = 0x726, SITE_LAND = 0x727, SITE_DONE = 0x728, SITE_DRAIN = 0x729,
+  SITE_DF = 0x72a
 };
 
 struct Plan {
   int RT, RC, np;        // tiles of a sequence, of a chunk; pages a tile may see at most
   int KT, KF;            // tiles of 256 keys; those that hold first tokens
-  int seg, n_long, n_short, slots;   // tiles of a segment; segments of a key tile that holds first
-                                     // tokens, of another; segments of a sequence
+  int seg, G, nk;        // tiles of a segment; segments of a chunk; key tiles that a segment's
+                         // windows reach
+  __host__ __device__ int per_seg() const { return nk + KF; }
 };
 
 struct Params {
@@ -62,7 +71,7 @@ struct Params {
   const float* lse;
   float2* rows;          // [B, T * H] lse (base 2), D
   uint8_t* pz;           // a block of zeros, then [B, RC, np, P | dZ] blocks
-  float* part;           // [B, slots, 256, 576]
+  float* part;           // [B, G, nk + KF, 256, 576]
   float* acc;            // [B, max_kv_len, 576] between chunks
   uint16_t* dq;
   uint16_t* dkv;
@@ -95,6 +104,18 @@ __device__ __forceinline__ int2 tiles_of(const Params& p, const Seq& s, int kt) 
   hi = min((hi * p.H + X - 1) / X, static_cast<int64_t>(p.rt0 + p.q.RC));
   return lo < hi ? make_int2(static_cast<int>(lo), static_cast<int>(hi)) : make_int2(0, 0);
 }
+// The first key tile that the windows of segment g reach.
+__device__ __forceinline__ int first_key_tile(const Params& p, const Seq& s, int g) {
+  const int t = s.pos0 + (p.rt0 + g * p.q.seg) * X / p.H;
+  return max(t - p.m.window + 1, 0) >> 8;
+}
+// Where the sums of segment g for key tile kt stand: the windows' key tiles, then those
+// of first tokens that no window reaches.
+__device__ __forceinline__ int64_t part_row(const Params& p, const Seq& s, int b, int g, int kt) {
+  const int k0 = first_key_tile(p, s, g);
+  const int at = kt >= k0 ? kt - k0 : p.q.nk + kt;
+  return ((static_cast<int64_t>(b) * p.q.G + g) * p.q.per_seg() + at) * 256;
+}
 
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
@@ -103,6 +124,8 @@ __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0
 __global__ void __launch_bounds__(256) prep_kernel(const Params p) {
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_start_next();
   if (blockIdx.x < BLOCK / (256 * 16))
     reinterpret_cast<uint4*>(p.pz)[blockIdx.x * 256 + threadIdx.x] = make_uint4(0, 0, 0, 0);
   const int per = p.m.T * p.H;
@@ -135,41 +158,53 @@ struct Pz {
   static constexpr int OFF_B = 0;                    // q or d_o of the tile: 9 chunks of 128 rows
   static constexpr int OFF_K = 9 * BLOCK;
   static constexpr int OFF_ROW = OFF_K + NS * BLOCK;
-  static constexpr int OFF_MISC = OFF_ROW + X * 16;
+  static constexpr int OFF_MISC = OFF_ROW + 2 * X * 16;
   static constexpr int SMEM = OFF_MISC + 256 + 1024;
   static constexpr int THREADS = 384;                // 0 copies, 1 issues, 4..11 form P and dZ
   static_assert(SMEM <= 232448, "shared memory");
 };
+
+// A tile of the chunk and what it sees.
+struct Tile {
+  int b, rt, g0, rows;   // rows: of the sequence
+  Seq s;
+  Pages pages;
+  int np, ng;            // pages, groups of four
+};
+__device__ __forceinline__ Tile tile_at(const Params& p, int task) {
+  Tile t;
+  t.b = task / p.q.RC;
+  t.rt = p.rt0 + task % p.q.RC;
+  t.s = seq_of(p.m, t.b);
+  t.pages = tile_pages(p, t.s, t.rt);
+  t.np = t.pages.count();
+  t.ng = (t.np + 3) / 4;
+  t.g0 = t.rt * X;
+  t.rows = t.s.n * p.H;
+  return t;
+}
 
 __global__ void __launch_bounds__(Pz::THREADS, 1)
     pz_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
               const __grid_constant__ CUtensorMap tm_kv, const Params p) {
   using C = Pz;
   constexpr uint32_t IDESC = idesc_bf16(256, 256, false, false);
-  const int rank = blockIdx.x & 1;
-  const int b = (blockIdx.x >> 1) / p.q.RC, rt = p.rt0 + (blockIdx.x >> 1) % p.q.RC;
-  const Seq s = seq_of(p.m, b);
-  const Pages pages = tile_pages(p, s, rt);
-  const int np = pages.count(), ng = (np + 3) / 4;
-  if (ng == 0) return;                               // both CTAs
-  const int g0 = rt * X, rows = s.n * p.H;
+  const int rank = blockIdx.x & 1, tasks = p.B * p.q.RC, step = gridDim.x >> 1;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_align1024(smem_raw);
   uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);   // even CTA
   uint64_t* kempty = kfull + C::NS;
-  uint64_t* bfull = kempty + C::NS;                                  // even CTA
-  uint64_t* afull = bfull + 1;
+  uint64_t* afull = kempty + C::NS;
   uint64_t* afree = afull + 2;                                       // even CTA
   uint64_t* drain = afree + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
-  float4* s_row = reinterpret_cast<float4*>(sm + C::OFF_ROW);        // lse, D, position
+  float4* s_row = reinterpret_cast<float4*>(sm + C::OFF_ROW);        // [2][X] lse, D, position
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int k = 0; k < C::NS; ++k) mbar_init(&kfull[k], 1), mbar_init(&kempty[k], 1);
-    mbar_init(bfull, 1);
     for (int k = 0; k < 2; ++k) mbar_init(&afull[k], 1), mbar_init(&afree[k], 16);
     mbar_init(drain, 1);
     s_abort[0] = 0;
@@ -181,16 +216,6 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
     tmem_alloc_pair(tslot, 512);
     tmem_relinquish_pair();
   }
-  if (tid >= 128 && tid < 128 + X) {
-    const int g = g0 + tid - 128;
-    float4 v = make_float4(0.f, 0.f, __int_as_float(-1), 0.f);
-    if (g < rows) {
-      const float2 r = p.rows[static_cast<int64_t>(b) * p.m.T * p.H + g];
-      const int t = s.pos0 + g / p.H;
-      v = make_float4(r.x, r.y, __int_as_float(t < s.L ? t : -1), 0.f);
-    }
-    s_row[tid - 128] = v;
-  }
   if (rank == 1) {                                   // no value part for the rotated dims
     for (int e = tid; e < BLOCK / 16; e += C::THREADS)
       reinterpret_cast<uint4*>(sm + C::OFF_B + 8 * BLOCK)[e] = make_uint4(0, 0, 0, 0);
@@ -201,42 +226,43 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  pdl_wait();
+  pdl_start_next();
 
   if (warp == 0) {
-    const uint32_t bbar = mapa_u32(smem_u32(bfull), 0);
-    if (elect_one_lane()) {
-      if (rank == 0) mbar_expect_tx(bfull, 17u * BLOCK);
-#pragma unroll 1
-      for (int c = 0; c < 9 - rank; ++c)
-        tma_load_3d_pair(sm + C::OFF_B + c * BLOCK, rank == 0 ? &tm_q : &tm_do, bbar, 64 * c, g0, b);
-    }
-    __syncwarp();
     Ring<C::NS> r;
     int used = 0;
     bool ok = true;
-    for (int j = 0; j < ng && ok; ++j) {
-      int row[2];
+    for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
+      const Tile t = tile_at(p, task);
+      for (int j = 0; j < t.ng && ok; ++j) {
+        int row[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {                  // pages that are not there: any rows
-        const int k = 4 * j + 2 * rank + h;
-        row[h] = static_cast<int>(page_row(p.kv, b, k < np ? pages.page(k) : pages.page(0)));
-      }
-      for (int c = 0; c < 9; ++c) {
-        ok = used < C::NS || wait(&kempty[r.slot], r.ph ^ 1, s_abort, p.status, SITE_KE);
-        if (!ok) break;
-        if (elect_one_lane()) {
-          uint8_t* dst = sm + C::OFF_K + r.slot * BLOCK;
-          const uint32_t bar = mapa_u32(smem_u32(&kfull[r.slot]), 0);
-          if (rank == 0) mbar_expect_tx(&kfull[r.slot], 2 * BLOCK);
-          tma_load_2d_pair(dst, &tm_kv, bar, 64 * c, row[0]);
-          tma_load_2d_pair(dst + CHUNK, &tm_kv, bar, 64 * c, row[1]);
+        for (int h = 0; h < 2; ++h) {                // pages that are not there: any rows
+          const int k = 4 * j + 2 * rank + h;
+          row[h] = static_cast<int>(page_row(p.kv, t.b, t.pages.page(k < t.np ? k : 0)));
         }
-        __syncwarp();
-        if (used < C::NS) ++used;
-        r.next();
+        for (int c = 0; c < 9; ++c) {
+          // a tile's first keys bring its q and d_o along: the products that read the
+          // last tile's chunk c came before those that free this slot
+          ok = used < C::NS || wait(&kempty[r.slot], r.ph ^ 1, s_abort, p.status, SITE_KE);
+          if (!ok) break;
+          if (elect_one_lane()) {
+            uint8_t* dst = sm + C::OFF_K + r.slot * BLOCK;
+            const uint32_t bar = mapa_u32(smem_u32(&kfull[r.slot]), 0);
+            if (rank == 0)
+              mbar_expect_tx(&kfull[r.slot], (2 + (j > 0 ? 0 : c < 8 ? 2 : 1)) * BLOCK);
+            if (j == 0 && (c < 8 || rank == 0))
+              tma_load_3d_pair(sm + C::OFF_B + c * BLOCK, rank == 0 ? &tm_q : &tm_do, bar, 64 * c, t.g0, t.b);
+            tma_load_2d_pair(dst, &tm_kv, bar, 64 * c, row[0]);
+            tma_load_2d_pair(dst + CHUNK, &tm_kv, bar, 64 * c, row[1]);
+          }
+          __syncwarp();
+          if (used < C::NS) ++used;
+          r.next();
+        }
       }
     }
-    if (rank == 0) wait(bfull, 0, s_abort, p.status, SITE_B);
     for (; used > 0; --used) {
       if (--r.slot < 0) r.slot = C::NS - 1, r.ph ^= 1;
       if (rank == 0) wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
@@ -246,26 +272,30 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
     const uint64_t kd = smem_desc(smem_u32(sm + C::OFF_K), 16, 1024);
     const uint64_t bd = smem_desc(smem_u32(sm + C::OFF_B), 16, 1024);
     Ring<C::NS> r;
-    bool ok = wait(bfull, 0, s_abort, p.status, SITE_B);
-    for (int j = 0; j < ng && ok; ++j) {
-      const int bu = j & 1;
-      if (j > 1) ok = wait(&afree[bu], ((j >> 1) - 1) & 1, s_abort, p.status, SITE_AE);
-      tc_fence_after();
-      for (int c = 0; c < 9 && ok; ++c) {
-        ok = wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
-        if (!ok) break;
+    int n = 0;                                       // groups so far
+    bool ok = true;
+    for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
+      const int ng = tile_at(p, task).ng;
+      for (int j = 0; j < ng && ok; ++j, ++n) {
+        const int bu = n & 1;
+        if (n > 1) ok = wait(&afree[bu], ((n >> 1) - 1) & 1, s_abort, p.status, SITE_AE);
         tc_fence_after();
-        if (elect_one_lane()) {
-          const uint64_t a = desc_add(kd, r.slot * BLOCK), w = desc_add(bd, c * BLOCK);
+        for (int c = 0; c < 9 && ok; ++c) {
+          ok = wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one_lane()) {
+            const uint64_t a = desc_add(kd, r.slot * BLOCK), w = desc_add(bd, c * BLOCK);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_bf16_pair(tmem + bu * 256, desc_add(a, kk * 32), desc_add(w, kk * 32), IDESC,
-                           c > 0 || kk > 0);
-          umma_commit_pair(&kempty[r.slot]);
-          if (c == 8) umma_commit_pair(&afull[bu]);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16_pair(tmem + bu * 256, desc_add(a, kk * 32), desc_add(w, kk * 32), IDESC,
+                             c > 0 || kk > 0);
+            umma_commit_pair(&kempty[r.slot]);
+            if (c == 8) umma_commit_pair(&afull[bu]);
+          }
+          __syncwarp();
+          r.next();
         }
-        __syncwarp();
-        r.next();
       }
     }
     if (elect_one_lane()) umma_commit_pair(drain);
@@ -276,51 +306,74 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
     const int sub = warp & 3, r0 = (warp - 4) / 4 * 64, key = sub * 32 + lane;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + r0;
     const uint32_t free_bar = mapa_u32(smem_u32(afree), 0);
-    const int t0 = s.pos0 + g0 / p.H, t1 = s.pos0 + (min(g0 + X, rows) - 1) / p.H;
-    const bool whole = g0 + X <= rows && t1 < s.L;
-    bool ok = true;
-    for (int j = 0; j < ng && ok; ++j) {
-      const int bu = j & 1, k = 4 * j + 2 * rank + (sub >> 1);
-      const int kb = k < np ? pages.page(k) * 64 + (sub & 1) * 32 : 0;   // the warp's first key
-      const int at = kb + lane;
-      const bool all = whole && kb + 31 <= t0 && (kb > t1 - p.m.window || kb + 31 < p.m.n_first);
-      ok = wait(&afull[bu], (j >> 1) & 1, s_abort, p.status, SITE_AF);
-      if (!ok) break;
-      tc_fence_after();
-      // a thread's column of the two blocks: row r at 128 r, 16-byte units xor r
-      uint8_t* dst = p.pz + 128 * p.block_row(b, rt, k, 0) + (key & 7) * 2;
-      const uint32_t unit = (key & 63) >> 3;
-#pragma unroll 1
-      for (int q = 0; q < 64; q += 32) {
-        uint32_t z[32], dp[32];
-        tmem_ld32(taddr + bu * 256 + q, z);
-        tmem_ld32(taddr + bu * 256 + 128 + q, dp);
-        tmem_ld_wait_regs(z);
-        tmem_ld_wait_regs(dp);
-        if (q == 32) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (rank == 0) mbar_arrive(&afree[bu]);
-            else mbar_arrive_cluster_relaxed(free_bar + bu * 8);
-          }
+    const uint32_t unit = (key & 63) >> 3;
+    const int mine = tid - 128;                      // a row of the tile for the first half of the threads
+    auto row_at = [&](int task) {                    // lse, D and position of that row
+      float4 v = make_float4(0.f, 0.f, __int_as_float(-1), 0.f);
+      if (task < tasks && mine < X) {
+        const int b = task / p.q.RC, g = (p.rt0 + task % p.q.RC) * X + mine;
+        const Seq s = seq_of(p.m, b);
+        if (g < s.n * p.H) {
+          const float2 r = p.rows[static_cast<int64_t>(b) * p.m.T * p.H + g];
+          const int t = s.pos0 + g / p.H;
+          v = make_float4(r.x, r.y, __int_as_float(t < s.L ? t : -1), 0.f);
         }
-        if (k < np) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int r = r0 + q + e;
-            const float4 w = s_row[r];
-            float pr = ex2(fmaf(__uint_as_float(z[e]), p.scale_log2, -w.x));
-            float dz = p.scale * pr * (__uint_as_float(dp[e]) - w.y);
-            if (!all) {
-              const int t = __float_as_int(w.z);
-              const bool sees = at <= t && (t - at < p.m.window || at < p.m.n_first);
-              pr = sees ? pr : 0.f;
-              dz = sees ? dz : 0.f;
+      }
+      return v;
+    };
+    float4 next = row_at(blockIdx.x >> 1);
+    int n = 0, at = 0;
+    bool ok = true;
+    for (int task = blockIdx.x >> 1; task < tasks; task += step, at ^= 1) {
+      const Tile t = tile_at(p, task);
+      const float4* rows = s_row + at * X;
+      if (mine < X) s_row[at * X + mine] = next;
+      if (named_bar_or(1, 256, !ok)) break;          // rows written; two tiles back: read
+      next = row_at(task + step);
+      const int t0 = t.s.pos0 + t.g0 / p.H, t1 = t.s.pos0 + (min(t.g0 + X, t.rows) - 1) / p.H;
+      const bool whole = t.g0 + X <= t.rows && t1 < t.s.L;
+      for (int j = 0; j < t.ng && ok; ++j, ++n) {
+        const int bu = n & 1, k = 4 * j + 2 * rank + (sub >> 1);
+        const int kb = k < t.np ? t.pages.page(k) * 64 + (sub & 1) * 32 : 0;   // the warp's first key
+        const int kp = kb + lane;
+        const bool all = whole && kb + 31 <= t0 && (kb > t1 - p.m.window || kb + 31 < p.m.n_first);
+        ok = wait(&afull[bu], (n >> 1) & 1, s_abort, p.status, SITE_AF);
+        if (!ok) break;
+        tc_fence_after();
+        // a thread's column of the two blocks: row r at 128 r, 16-byte units xor r
+        uint8_t* dst = p.pz + 128 * p.block_row(t.b, t.rt, k, 0) + (key & 7) * 2;
+#pragma unroll 1
+        for (int q = 0; q < 64; q += 32) {
+          uint32_t z[32], dp[32];
+          tmem_ld32(taddr + bu * 256 + q, z);
+          tmem_ld32(taddr + bu * 256 + 128 + q, dp);
+          tmem_ld_wait_regs(z);
+          tmem_ld_wait_regs(dp);
+          if (q == 32) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (rank == 0) mbar_arrive(&afree[bu]);
+              else mbar_arrive_cluster_relaxed(free_bar + bu * 8);
             }
-            uint8_t* to = dst + r * 128 + ((unit ^ (r & 7)) << 4);
-            *reinterpret_cast<uint16_t*>(to) = __bfloat16_as_ushort(__float2bfloat16_rn(pr));
-            *reinterpret_cast<uint16_t*>(to + BLOCK) = __bfloat16_as_ushort(__float2bfloat16_rn(dz));
+          }
+          if (k < t.np) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int r = r0 + q + e;
+              const float4 w = rows[r];
+              float pr = ex2(fmaf(__uint_as_float(z[e]), p.scale_log2, -w.x));
+              float dz = p.scale * pr * (__uint_as_float(dp[e]) - w.y);
+              if (!all) {
+                const int tt = __float_as_int(w.z);
+                const bool sees = kp <= tt && (tt - kp < p.m.window || kp < p.m.n_first);
+                pr = sees ? pr : 0.f;
+                dz = sees ? dz : 0.f;
+              }
+              uint8_t* to = dst + r * 128 + ((unit ^ (r & 7)) << 4);
+              *reinterpret_cast<uint16_t*>(to) = __bfloat16_as_ushort(__float2bfloat16_rn(pr));
+              *reinterpret_cast<uint16_t*>(to + BLOCK) = __bfloat16_as_ushort(__float2bfloat16_rn(dz));
+            }
           }
         }
       }
@@ -345,63 +398,89 @@ struct Prod {
   static constexpr int STAGE = 5 * CHUNK;
   static constexpr int OFF_MISC = NS * STAGE;
   static constexpr int SMEM = OFF_MISC + 256 + 1024;
-  static constexpr int THREADS = 256;                // 0 copies, 1 issues, all write out
+  static constexpr int THREADS = 384;                // 0 copies, 1 issues, 4..11 write out
 };
 
-// Task dims: columns c of D are dims 256 * upper + c.  dkv: of a stage's 64 rows, the
-// first products take dZ and q, the second P and d_o.
+// Columns c of D are dims 256 * upper + c.  dkv: of a stage's 64 rows, the first
+// products take dZ and q, the second P and d_o.
+template <bool DKV>
+struct Task {
+  int b, upper, kt, g, x0, x1;   // dkv: tiles x0..x1-1 of segment g; dq: tiles x0, x0 + 1
+  Seq s;
+  Pages list;                    // dq: pages of the two tiles
+  bool there;
+
+  __device__ __forceinline__ Task(const Params& p, int task) {
+    upper = task & 1;
+    int u = task >> 1;
+    kt = g = 0;
+    list = Pages{0, 0, 0};
+    if constexpr (DKV) {
+      const int at = u % p.q.per_seg();
+      u /= p.q.per_seg();
+      g = u % p.q.G;
+      b = u / p.q.G;
+      s = seq_of(p.m, b);
+      const int k0 = first_key_tile(p, s, g);
+      kt = at < p.q.nk ? k0 + at : at - p.q.nk;
+      there = s.ok && kt < p.q.KT && (at < p.q.nk || kt < k0);
+      const int2 tiles = there ? tiles_of(p, s, kt) : make_int2(0, 0);
+      x0 = max(tiles.x, p.rt0 + g * p.q.seg);
+      x1 = min(tiles.y, p.rt0 + (g + 1) * p.q.seg);
+      there = x0 < x1;
+    } else {
+      b = u / (p.q.RC / 2);
+      x0 = p.rt0 + 2 * (u % (p.q.RC / 2));
+      x1 = x0 + 2;
+      s = seq_of(p.m, b);
+      const int rows = s.n * p.H;
+      there = x0 * X < rows;
+      if (there) list = pages_of(p.m, s, x0 * X / p.H, (min(x1 * X, rows) - 1) / p.H);
+    }
+  }
+  // dkv: whether a tile sees any of the task's keys
+  __device__ __forceinline__ bool sees(const Pages& l) const {
+    return place(l, 4 * kt) >= 0 || place(l, 4 * kt + 1) >= 0 || place(l, 4 * kt + 2) >= 0 ||
+           place(l, 4 * kt + 3) >= 0;
+  }
+  // Whether there is anything to add up.
+  __device__ __forceinline__ bool some(const Params& p) const {
+    if constexpr (DKV) {
+      for (int x = x0; x < x1; ++x)
+        if (sees(tile_pages(p, s, x))) return true;
+      return false;
+    }
+    return list.count() > 0;
+  }
+};
+
 template <bool DKV>
 __global__ void __launch_bounds__(Prod::THREADS, 1)
     product_kernel(const __grid_constant__ CUtensorMap tm_pz, const __grid_constant__ CUtensorMap tm_kv,
                    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                   const Params p) {
+                   const Params p, int tasks) {
   using C = Prod;
   constexpr uint32_t IDESC = idesc_bf16(256, 256, DKV, true), IDESC_ROT = idesc_bf16(256, 128, DKV, true);
-  const int rank = blockIdx.x & 1, upper = (blockIdx.x >> 1) & 1;
-  int u = blockIdx.x >> 2, b, kt = 0, slot = 0, x0, x1;   // dkv: tiles x0..x1-1; dq: tiles x0, x0 + 1
-  Seq s;
-  Pages list{0, 0, 0};
-  if constexpr (DKV) {
-    b = u / p.q.slots;
-    slot = u % p.q.slots;
-    const int n_first = p.q.KF * p.q.n_long;
-    int part;
-    if (slot < n_first) {
-      kt = slot / p.q.n_long, part = slot % p.q.n_long;
-    } else {
-      kt = p.q.KF + (slot - n_first) / p.q.n_short, part = (slot - n_first) % p.q.n_short;
-    }
-    s = seq_of(p.m, b);
-    const int2 tiles = tiles_of(p, s, kt);
-    x0 = tiles.x + part * p.q.seg;
-    x1 = min(x0 + p.q.seg, tiles.y);
-    if (x0 >= x1) return;
-  } else {
-    b = u / (p.q.RC / 2);
-    x0 = p.rt0 + 2 * (u % (p.q.RC / 2));
-    x1 = x0 + 2;
-    s = seq_of(p.m, b);
-    const int rows = s.n * p.H;
-    if (x0 * X >= rows) return;
-    list = pages_of(p.m, s, x0 * X / p.H, (min(x1 * X, rows) - 1) / p.H);
-  }
+  const int rank = blockIdx.x & 1, step = gridDim.x >> 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);    // even CTA
   uint64_t* empty = full + C::NS;
   uint64_t* land = empty + C::NS;
-  uint64_t* done = land + 1;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* done = land + 1;                                         // a task's sums are complete
+  uint64_t* dfree = done + 1;                                        // even CTA: and read
+  uint64_t* drain = dfree + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
-  volatile int* s_some = reinterpret_cast<volatile int*>(tslot + 2);
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int k = 0; k < C::NS; ++k) mbar_init(&full[k], 2), mbar_init(&empty[k], 1);
     mbar_init(land, 1);
     mbar_init(done, 1);
+    mbar_init(dfree, 16);
+    mbar_init(drain, 1);
     s_abort[0] = 0;
-    s_some[0] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_pz);
     tma_prefetch_desc(DKV ? &tm_q : &tm_kv);
@@ -416,13 +495,9 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  pdl_wait();
+  pdl_start_next();
 
-  // dkv: whether a tile sees any of the task's keys
-  auto sees = [&](const Pages& l) {
-    return place(l, 4 * kt) >= 0 || place(l, 4 * kt + 1) >= 0 || place(l, 4 * kt + 2) >= 0 ||
-           place(l, 4 * kt + 3) >= 0;
-  };
-  const int col = 256 * upper + 128 * rank;
   if (warp == 0) {
     Ring<C::NS> r;
     int used = 0;
@@ -437,80 +512,85 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       if (used < C::NS) ++used;
       r.next();
     };
-    if constexpr (DKV) {
-      for (int x = x0; x < x1 && ok; ++x) {
-        const Pages l = tile_pages(p, s, x);
-        if (!sees(l)) continue;
-        const int c0 = place(l, 4 * kt + 2 * rank), c1 = place(l, 4 * kt + 2 * rank + 1);
+    for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
+      const Task<DKV> t(p, task);
+      if (!t.there) continue;
+      const int col = 256 * t.upper + 128 * rank;
+      if constexpr (DKV) {
+        for (int x = t.x0; x < t.x1 && ok; ++x) {
+          const Pages l = tile_pages(p, t.s, x);
+          if (!t.sees(l)) continue;
+          const int c0 = place(l, 4 * t.kt + 2 * rank), c1 = place(l, 4 * t.kt + 2 * rank + 1);
 #pragma unroll 1
-        for (int st = 0; st < 4 && ok; ++st) {       // rows 64 (st >> 1), dZ and q or P and d_o
-          const int which = 1 - (st & 1), y = 64 * (st >> 1);
+          for (int st = 0; st < 4 && ok; ++st) {     // rows 64 (st >> 1), dZ and q or P and d_o
+            const int which = 1 - (st & 1), y = 64 * (st >> 1);
+            if (!acquire()) break;
+            if (elect_one_lane()) {
+              uint8_t* a = sm + r.slot * C::STAGE;
+              uint8_t* w = a + C::OFF_W;
+              const uint32_t bar = mapa_u32(smem_u32(&full[r.slot]), 0);
+              const bool rot = t.upper && which && rank == 0;
+              mbar_expect_tx_cluster(bar, (rot ? 5 : 4) * CHUNK);
+              tma_load_2d_pair(a, &tm_pz, bar, 0,
+                               c0 < 0 ? 0 : static_cast<int>(p.block_row(t.b, x, c0, which)) + y);
+              tma_load_2d_pair(a + CHUNK, &tm_pz, bar, 0,
+                               c1 < 0 ? 0 : static_cast<int>(p.block_row(t.b, x, c1, which)) + y);
+              const CUtensorMap* tm = which ? &tm_q : &tm_do;
+              tma_load_3d_pair(w, tm, bar, col, x * X + y, t.b);
+              tma_load_3d_pair(w + CHUNK, tm, bar, col + 64, x * X + y, t.b);
+              if (rot) tma_load_3d_pair(w + 2 * CHUNK, tm, bar, kVlat, x * X + y, t.b);
+            }
+            advance();
+          }
+        }
+      } else {
+        const Pages l = tile_pages(p, t.s, t.x0 + rank);
+        for (int k = 0; k < t.list.count() && ok; ++k) {
+          const int pg = t.list.page(k), c = place(l, pg), row = static_cast<int>(page_row(p.kv, t.b, pg));
+          const uint64_t any = range_bits(0, t.s.L, pg * 64);
           if (!acquire()) break;
+          uint8_t* a = sm + r.slot * C::STAGE;
+          uint8_t* w = a + C::OFF_W;
+          const uint32_t bar = mapa_u32(smem_u32(&full[r.slot]), 0);
+          const bool rot = t.upper && rank == 0;
+          const int n = rot ? 3 : 2;
+          if (any != ~0ull) {
+            // rows behind the sequence become zeros: whatever they hold must not meet
+            // the zeros of dZ
+            if (elect_one_lane()) {
+              mbar_expect_tx(land, n * CHUNK);
+              tma_load_2d(w, &tm_kv, land, col, row);
+              tma_load_2d(w + CHUNK, &tm_kv, land, col + 64, row);
+              if (rot) tma_load_2d(w + 2 * CHUNK, &tm_kv, land, kVlat, row);
+            }
+            __syncwarp();
+            ok = wait(land, lph, s_abort, p.status, SITE_LAND);
+            lph ^= 1;
+            if (!ok) break;
+            for (int e = lane; e < n * CHUNK / 16; e += 32)
+              if (!(any >> ((e >> 3) & 63) & 1)) reinterpret_cast<uint4*>(w)[e] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
           if (elect_one_lane()) {
-            uint8_t* a = sm + r.slot * C::STAGE;
-            uint8_t* w = a + C::OFF_W;
-            const uint32_t bar = mapa_u32(smem_u32(&full[r.slot]), 0);
-            const bool rot = upper && which && rank == 0;
-            mbar_expect_tx_cluster(bar, (rot ? 5 : 4) * CHUNK);
-            tma_load_2d_pair(a, &tm_pz, bar, 0, c0 < 0 ? 0 : static_cast<int>(p.block_row(b, x, c0, which)) + y);
-            tma_load_2d_pair(a + CHUNK, &tm_pz, bar, 0,
-                             c1 < 0 ? 0 : static_cast<int>(p.block_row(b, x, c1, which)) + y);
-            const CUtensorMap* tm = which ? &tm_q : &tm_do;
-            tma_load_3d_pair(w, tm, bar, col, x * X + y, b);
-            tma_load_3d_pair(w + CHUNK, tm, bar, col + 64, x * X + y, b);
-            if (rot) tma_load_3d_pair(w + 2 * CHUNK, tm, bar, kVlat, x * X + y, b);
+            if (any == ~0ull) {
+              mbar_expect_tx_cluster(bar, (2 + n) * CHUNK);
+            } else {
+              mbar_expect_tx_cluster_release(bar, 2 * CHUNK);
+            }
+            const int br = c < 0 ? 0 : static_cast<int>(p.block_row(t.b, t.x0 + rank, c, 1));
+            tma_load_2d_pair(a, &tm_pz, bar, 0, br);
+            tma_load_2d_pair(a + CHUNK, &tm_pz, bar, 0, br + 64);
+            if (any == ~0ull) {
+              tma_load_2d_pair(w, &tm_kv, bar, col, row);
+              tma_load_2d_pair(w + CHUNK, &tm_kv, bar, col + 64, row);
+              if (rot) tma_load_2d_pair(w + 2 * CHUNK, &tm_kv, bar, kVlat, row);
+            }
           }
           advance();
         }
       }
-    } else {
-      const Pages l = tile_pages(p, s, x0 + rank);
-      for (int k = 0; k < list.count() && ok; ++k) {
-        const int pg = list.page(k), c = place(l, pg), row = static_cast<int>(page_row(p.kv, b, pg));
-        const uint64_t any = range_bits(0, s.L, pg * 64);
-        if (!acquire()) break;
-        uint8_t* a = sm + r.slot * C::STAGE;
-        uint8_t* w = a + C::OFF_W;
-        const uint32_t bar = mapa_u32(smem_u32(&full[r.slot]), 0);
-        const bool rot = upper && rank == 0;
-        const int n = rot ? 3 : 2;
-        if (any != ~0ull) {
-          // rows behind the sequence become zeros: whatever they hold must not meet
-          // the zeros of dZ
-          if (elect_one_lane()) {
-            mbar_expect_tx(land, n * CHUNK);
-            tma_load_2d(w, &tm_kv, land, col, row);
-            tma_load_2d(w + CHUNK, &tm_kv, land, col + 64, row);
-            if (rot) tma_load_2d(w + 2 * CHUNK, &tm_kv, land, kVlat, row);
-          }
-          __syncwarp();
-          ok = wait(land, lph, s_abort, p.status, SITE_LAND);
-          lph ^= 1;
-          if (!ok) break;
-          for (int e = lane; e < n * CHUNK / 16; e += 32)
-            if (!(any >> ((e >> 3) & 63) & 1)) reinterpret_cast<uint4*>(w)[e] = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (elect_one_lane()) {
-          if (any == ~0ull) {
-            mbar_expect_tx_cluster(bar, (2 + n) * CHUNK);
-          } else {
-            mbar_expect_tx_cluster_release(bar, 2 * CHUNK);
-          }
-          const int br = c < 0 ? 0 : static_cast<int>(p.block_row(b, x0 + rank, c, 1));
-          tma_load_2d_pair(a, &tm_pz, bar, 0, br);
-          tma_load_2d_pair(a + CHUNK, &tm_pz, bar, 0, br + 64);
-          if (any == ~0ull) {
-            tma_load_2d_pair(w, &tm_kv, bar, col, row);
-            tma_load_2d_pair(w + CHUNK, &tm_kv, bar, col + 64, row);
-            if (rot) tma_load_2d_pair(w + 2 * CHUNK, &tm_kv, bar, kVlat, row);
-          }
-        }
-        advance();
-      }
     }
-    if (lane == 0 && used > 0) s_some[0] = 1;
     for (; used > 0; --used) {
       if (--r.slot < 0) r.slot = C::NS - 1, r.ph ^= 1;
       if (rank == 0) wait(&full[r.slot], r.ph, s_abort, p.status, SITE_F);
@@ -520,6 +600,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
     const uint64_t ad = DKV ? smem_desc(smem_u32(sm), CHUNK, 1024) : smem_desc(smem_u32(sm), 16, 1024);
     const uint64_t wd = smem_desc(smem_u32(sm + C::OFF_W), CHUNK, 1024);
     Ring<C::NS> r;
+    int n = 0;                                       // tasks so far
     bool ok = true;
     uint32_t more = 0;                               // accumulate
     auto multiply = [&](bool rot) {
@@ -541,60 +622,83 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       more = 1;
       r.next();
     };
-    if constexpr (DKV) {
-      for (int x = x0; x < x1 && ok; ++x) {
-        if (!sees(tile_pages(p, s, x))) continue;
-        for (int st = 0; st < 4 && ok; ++st) multiply(upper && !(st & 1));
+    for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
+      const Task<DKV> t(p, task);
+      if (!t.there) continue;
+      if (n > 0) ok = wait(dfree, (n - 1) & 1, s_abort, p.status, SITE_DF);
+      tc_fence_after();
+      ++n;
+      more = 0;
+      if constexpr (DKV) {
+        for (int x = t.x0; x < t.x1 && ok; ++x) {
+          if (!t.sees(tile_pages(p, t.s, x))) continue;
+          for (int st = 0; st < 4 && ok; ++st) multiply(t.upper && !(st & 1));
+        }
+      } else {
+        for (int k = 0; k < t.list.count() && ok; ++k) multiply(t.upper);
       }
-    } else {
-      for (int k = 0; k < list.count() && ok; ++k) multiply(upper);
+      if (elect_one_lane()) umma_commit_pair(done);
+      __syncwarp();
     }
-    if (elect_one_lane()) umma_commit_pair(done);
+    if (elect_one_lane()) umma_commit_pair(drain);
     __syncwarp();
-    wait(done, 0, s_abort, p.status, SITE_DONE);
+    wait(drain, 0, s_abort, p.status, SITE_DRAIN);
+  } else if (warp >= 4) {
+    // ---- out: a row (key) a thread; warps 4..7 the lower half of the columns ----
+    const int sub = warp & 3, half = (warp >> 2) - 1, r = 128 * rank + 32 * sub + lane;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16);
+    const uint32_t free_bar = mapa_u32(smem_u32(dfree), 0);
+    int n = 0;
+    bool ok = true;
+    for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
+      const Task<DKV> t(p, task);
+      if (!t.there) continue;
+      const bool some = t.some(p);
+      const int g = t.x0 * X + r;                    // dq: row of the sequence
+      ok = wait(done, n & 1, s_abort, p.status, SITE_DONE);
+      if (!ok) break;
+      ++n;
+      tc_fence_after();
+#pragma unroll 1
+      for (int q = 0; q < (t.upper ? 5 : 4); ++q) {
+        const int c = q < 4 ? 128 * half + 32 * q : 256 + 32 * half;
+        uint32_t v[32];
+        if (some) {
+          tmem_ld32(taddr + c, v);
+          tmem_ld_wait_regs(v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0;
+        }
+        if constexpr (DKV) {
+          float4* to = reinterpret_cast<float4*>(
+              p.part + (part_row(p, t.s, t.b, t.g, t.kt) + r) * kRlat + 256 * t.upper + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            to[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+        } else if (g < t.s.n * p.H) {
+          uint4* to = reinterpret_cast<uint4*>(
+              p.dq + (static_cast<int64_t>(t.b) * p.m.T * p.H + g) * kRlat + 256 * t.upper + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+              w[f] = pack_bf16x2(__uint_as_float(v[8 * e + 2 * f]), __uint_as_float(v[8 * e + 2 * f + 1]));
+            to[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(dfree);
+        else mbar_arrive_cluster_relaxed(free_bar);
+      }
+    }
   }
   __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();
-  tc_fence_after();
-
-  // ---- out: a row (key) a thread; warps 0-3 the lower half of the columns ----
-  const bool some = s_some[0] != 0;
-  const int sub = warp & 3, half = warp >> 2, r = 128 * rank + 32 * sub + lane;
-  const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16);
-  const int rows = s.n * p.H, g = x0 * X + r;
-#pragma unroll 1
-  for (int q = 0; q < (upper ? 5 : 4); ++q) {
-    const int c = q < 4 ? 128 * half + 32 * q : 256 + 32 * half;
-    uint32_t v[32];
-    if (some) {
-      tmem_ld32(taddr + c, v);
-      tmem_ld_wait_regs(v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = 0;
-    }
-    if constexpr (DKV) {
-      float4* to = reinterpret_cast<float4*>(
-          p.part + ((static_cast<int64_t>(b) * p.q.slots + slot) * 256 + r) * kRlat + 256 * upper + c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        to[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                            __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-    } else if (g < rows) {
-      uint4* to = reinterpret_cast<uint4*>(
-          p.dq + (static_cast<int64_t>(b) * p.m.T * p.H + g) * kRlat + 256 * upper + c);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t w[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-          w[f] = pack_bf16x2(__uint_as_float(v[8 * e + 2 * f]), __uint_as_float(v[8 * e + 2 * f + 1]));
-        to[e] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -607,21 +711,23 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
 // dkv of a row: its segments in order (and what earlier chunks left), four dims a thread.
 __global__ void __launch_bounds__(144) reduce_kernel(const Params p) {
   const int b = blockIdx.x / p.m.max_kv_len, key = blockIdx.x % p.m.max_kv_len, kt = key >> 8;
+  pdl_wait();
+  pdl_start_next();
   const Seq s = seq_of(p.m, b);
   if (!s.ok || key >= s.L) return;
   const int2 tiles = tiles_of(p, s, kt);
-  const int n = (tiles.y - tiles.x + p.q.seg - 1) / p.q.seg;
-  const int first = kt < p.q.KF ? kt * p.q.n_long : p.q.KF * p.q.n_long + (kt - p.q.KF) * p.q.n_short;
-  const float4* at = reinterpret_cast<const float4*>(
-      p.part + ((static_cast<int64_t>(b) * p.q.slots + first) * 256 + (key & 255)) * kRlat) + threadIdx.x;
   float4* acc = reinterpret_cast<float4*>(p.acc + (static_cast<int64_t>(b) * p.m.max_kv_len + key) * kRlat) +
                 threadIdx.x;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (!p.first_chunk) v = *acc;
+  if (tiles.x < tiles.y) {
+    const int g1 = (tiles.y - 1 - p.rt0) / p.q.seg;
 #pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float4 w = at[static_cast<int64_t>(k) * 256 * (kRlat / 4)];
-    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    for (int g = (tiles.x - p.rt0) / p.q.seg; g <= g1; ++g) {
+      const float4 w = reinterpret_cast<const float4*>(
+          p.part + (part_row(p, s, b, g, kt) + (key & 255)) * kRlat)[threadIdx.x];
+      v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    }
   }
   if (!p.last_chunk) {
     *acc = v;
@@ -631,7 +737,11 @@ __global__ void __launch_bounds__(144) reduce_kernel(const Params p) {
       make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-// span: keys that one query may see at most (window + n_first, or every row)
+// span: keys that one query may see at most (window + n_first, or every row).  All but
+// KF and nk follow from the sizes and the span alone, and nk + KF stays within
+// most_key_tiles().
+int64_t seg_tokens(int seg, int H) { return (static_cast<int64_t>(seg) * X + H - 2) / H + 1; }
+int64_t most_key_tiles(int seg, int H, int64_t span) { return (span + seg_tokens(seg, H) + 509) / 256 + 2; }
 Plan plan(int B, int T, int H, int max_kv_len, int64_t span, int64_t window, int64_t n_first) {
   Plan q{};
   const int64_t rows = static_cast<int64_t>(T) * H, S = max_kv_len;
@@ -643,39 +753,31 @@ Plan plan(int B, int T, int H, int max_kv_len, int64_t span, int64_t window, int
   if (rc < 2) rc = 2;
   q.RC = static_cast<int>(rc < q.RT ? rc : q.RT);
   q.KT = static_cast<int>((S + 255) / 256);
-  const int64_t kf = (n_first + 255) / 256;
-  q.KF = static_cast<int>(kf < q.KT ? kf : q.KT);
-  // tiles that see a key tile
-  int64_t few = ((window + 255) * H + X - 1) / X + 1;
-  if (few > q.RC) few = q.RC;
-  const int64_t all = q.KF * static_cast<int64_t>(q.RC) + (q.KT - q.KF) * few;
-  int64_t seg = (2 * B * all + TASKS - 1) / TASKS;
-  if (seg < 16) seg = 16;
+  // segments: as many tasks as keep the pairs evenly busy, but the sums of each are
+  // 590 KB to write and add
+  int64_t seg = (2ll * B * q.RC * (span / 256 + 2) + TASKS - 1) / TASKS;
+  if (seg < 2) seg = 2;
   q.seg = static_cast<int>(seg < q.RC ? seg : q.RC);
-  q.n_long = (q.RC + q.seg - 1) / q.seg;
-  q.n_short = static_cast<int>((few + q.seg - 1) / q.seg);
-  q.slots = q.KF * q.n_long + (q.KT - q.KF) * q.n_short;
+  q.G = (q.RC + q.seg - 1) / q.seg;
+  const int64_t kf = (n_first + 255) / 256, nk = (window + seg_tokens(q.seg, H) + 254) / 256 + 1;
+  q.KF = static_cast<int>(kf < q.KT ? kf : q.KT);
+  q.nk = static_cast<int>(nk < q.KT ? nk : q.KT);
   return q;
 }
 
-// Bytes by part, from the sizes and the span alone (never less for a longer span).
+// Bytes by part, from the sizes and the span alone.
 struct Sizes {
   size_t rows, pz, part, acc;
   size_t total() const { return rows + pz + part + acc; }
 };
-Sizes sizes(const Plan& q, int B, int T, int H, int max_kv_len) {
+Sizes sizes(const Plan& q, int B, int T, int H, int max_kv_len, int64_t span) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  auto least = [](size_t x, size_t y) { return x < y ? x : y; };
   Sizes z{};
   z.rows = up(static_cast<size_t>(B) * T * H * sizeof(float2));
-  const size_t two = static_cast<size_t>(B) * 2 * q.np * 2 * BLOCK;
-  const size_t chunk = two > static_cast<size_t>(kChunkBytes) ? two : static_cast<size_t>(kChunkBytes);
-  z.pz = BLOCK + least(two / 2 * q.RT, chunk);
-  // B * slots <= TASKS / 2 + B * KT: every key tile rounds its segments up once
-  z.part = (TASKS / 2 + 1 + static_cast<size_t>(B) * q.KT) * 256 * kRlat * sizeof(float);
-  z.acc = two / 2 * q.RT > static_cast<size_t>(kChunkBytes)
-              ? up(static_cast<size_t>(B) * max_kv_len * kRlat * sizeof(float))
-              : 0;
+  z.pz = BLOCK + static_cast<size_t>(B) * q.RC * q.np * 2 * BLOCK;
+  const int64_t all = most_key_tiles(q.seg, H, span), twice = 2ll * q.KT;
+  z.part = static_cast<size_t>(B) * q.G * (all < twice ? all : twice) * 256 * kRlat * sizeof(float);
+  z.acc = q.RC < q.RT ? up(static_cast<size_t>(B) * max_kv_len * kRlat * sizeof(float)) : 0;
   return z;
 }
 
@@ -685,25 +787,14 @@ dsa_status_t launch_pairs(const char* what, Kernel kernel, int64_t pairs, int th
   if (pairs > (1 << 30) - 1) return DSA_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return launch_status("cudaFuncSetAttribute");
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 2;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, args...);
+  launch_overlapped(kernel, static_cast<unsigned>(2 * pairs), threads, smem, 2, stream, args...);
   return launch_status(what);
 }
 
 }  // namespace wbw
 
 size_t window_bwd_scratch_bytes(int B, int T, int H, int max_kv_len, int64_t span) {
-  return wbw::sizes(wbw::plan(B, T, H, max_kv_len, span, span, 0), B, T, H, max_kv_len).total();
+  return wbw::sizes(wbw::plan(B, T, H, max_kv_len, span, span, 0), B, T, H, max_kv_len, span).total();
 }
 
 dsa_status_t window_bwd_launch(const WindowBwdArgs& a, cudaStream_t stream) {
@@ -711,15 +802,18 @@ dsa_status_t window_bwd_launch(const WindowBwdArgs& a, cudaStream_t stream) {
   const DenseArgs& f = a.f;
   const int64_t S = f.max_kv_len, both = static_cast<int64_t>(f.window) + f.n_first;
   const int64_t span = both == 0 ? 1 : both < S ? both : S;
-  const Plan q = plan(f.B, f.T, f.H, f.max_kv_len, span, f.window < S ? f.window : S,
-                      f.n_first < S ? f.n_first : S);
-  const Sizes z = sizes(q, f.B, f.T, f.H, f.max_kv_len);
+  // a window and first tokens that meet at every position: the window alone
+  const int window = both >= S ? f.max_kv_len : f.window, n_first = both >= S ? 0 : f.n_first;
+  const Plan q = plan(f.B, f.T, f.H, f.max_kv_len, span, window, n_first);
+  const Sizes z = sizes(q, f.B, f.T, f.H, f.max_kv_len, span);
   if (f.scratch_bytes < z.total()) return DSA_ERR_WORKSPACE_TOO_SMALL;
   const int64_t per = static_cast<int64_t>(f.T) * f.H;
   uint8_t* ws = static_cast<uint8_t*>(f.scratch);
   Params p{};
   p.kv = store_of(f);
   p.m = mask_of(f);
+  p.m.window = window;
+  p.m.n_first = n_first;
   p.B = f.B;
   p.H = f.H;
   p.q = q;
@@ -748,23 +842,27 @@ dsa_status_t window_bwd_launch(const WindowBwdArgs& a, cudaStream_t stream) {
       !encode_tmap_3d(&td_tile, a.d_o, f.B, per, kVlat, 64, X))
     return DSA_ERR_CUDA;
   const int64_t ctas = (f.B * per + 7) / 8;
-  prep_kernel<<<static_cast<unsigned>(ctas > 4 ? ctas : 4), 256, 0, stream>>>(p);
+  launch_overlapped(prep_kernel, static_cast<unsigned>(ctas > 4 ? ctas : 4), 256, 0, 0, stream, p);
   if (launch_status("prep_kernel") != DSA_OK) return DSA_ERR_CUDA;
   for (int rt0 = 0; rt0 < q.RT; rt0 += q.RC) {
     p.rt0 = rt0;
     p.first_chunk = rt0 == 0;
     p.last_chunk = rt0 + q.RC >= q.RT;
-    const int64_t tiles = static_cast<int64_t>(f.B) * q.RC;
-    dsa_status_t st = launch_pairs("pz_kernel", pz_kernel, tiles, Pz::THREADS, Pz::SMEM, stream, tq_tile,
+    const int64_t pairs = num_sms() / 2, tiles = static_cast<int64_t>(f.B) * q.RC;
+    const int64_t sums = 2ll * f.B * q.G * q.per_seg();
+    if (sums > (1 << 30) || tiles > (1 << 30)) return DSA_ERR_UNSUPPORTED;
+    const int64_t some = tiles < pairs ? tiles : pairs;
+    dsa_status_t st = launch_pairs("pz_kernel", pz_kernel, some, Pz::THREADS, Pz::SMEM, stream, tq_tile,
                                    td_tile, tk, p);
     if (st == DSA_OK)
-      st = launch_pairs("product_kernel", product_kernel<false>, tiles, Prod::THREADS, Prod::SMEM, stream,
-                        tp, tk, tq, td, p);
+      st = launch_pairs("product_kernel", product_kernel<false>, some, Prod::THREADS, Prod::SMEM, stream,
+                        tp, tk, tq, td, p, static_cast<int>(tiles));
     if (st == DSA_OK)
-      st = launch_pairs("product_kernel", product_kernel<true>, 2ll * f.B * q.slots, Prod::THREADS,
-                        Prod::SMEM, stream, tp, tk, tq, td, p);
+      st = launch_pairs("product_kernel", product_kernel<true>, sums, Prod::THREADS,
+                        Prod::SMEM, stream, tp, tk, tq, td, p, static_cast<int>(sums));
     if (st != DSA_OK) return st;
-    reduce_kernel<<<static_cast<unsigned>(static_cast<int64_t>(f.B) * f.max_kv_len), 144, 0, stream>>>(p);
+    launch_overlapped(reduce_kernel, static_cast<unsigned>(static_cast<int64_t>(f.B) * f.max_kv_len), 144, 0,
+                      0, stream, p);
     if (launch_status("reduce_kernel") != DSA_OK) return DSA_ERR_CUDA;
   }
   return DSA_OK;
