@@ -409,8 +409,10 @@ struct Prod {
   static constexpr int THREADS = 384;                // 0 copies, 1 issues, 4..11 write out
 };
 
-// Columns c of D are dims 256 * upper + c.  dkv: of a stage's 64 rows, the first
-// products take dZ and q, the second P and d_o.
+// Columns c of D are dims 256 * upper + c, in TMEM columns c or (upper) 192 + c: the
+// next task's products may start once the 64 columns that both use have been read.
+// The rotated dims are an MMA of their own, N = 64, 32 dims from each CTA.
+// dkv: of a stage's 64 rows, the first products take dZ and q, the second P and d_o.
 template <bool DKV>
 struct Task {
   int b, upper, kt, g, x0, x1;   // dkv: tiles x0..x1-1 of segment g; dq: tiles x0, x0 + 1
@@ -418,8 +420,9 @@ struct Task {
   Pages list;                    // dq: pages of the two tiles
   bool there;
 
-  __device__ __forceinline__ Task(const Params& p, int task) {
-    upper = task & 1;
+  // The pair's tasks are `first` + k * step; their dims alternate whatever the step.
+  __device__ __forceinline__ Task(const Params& p, int task, int first, int step) {
+    upper = (task ^ (step & 1 ? 0 : (task - first) / step)) & 1;
     int u = task >> 1;
     kt = g = 0;
     list = Pages{0, 0, 0};
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
                    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                    const Params p, int tasks) {
   using C = Prod;
-  constexpr uint32_t IDESC = idesc_bf16(256, 256, DKV, true), IDESC_ROT = idesc_bf16(256, 128, DKV, true);
+  constexpr uint32_t IDESC = idesc_bf16(256, 256, DKV, true), IDESC_ROT = idesc_bf16(256, 64, DKV, true);
   const int rank = blockIdx.x & 1, step = gridDim.x >> 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_align1024(smem_raw);
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
   uint64_t* empty = full + C::NS;
   uint64_t* land = empty + C::NS;
   uint64_t* done = land + 1;                                         // a task's sums are complete
-  uint64_t* dfree = done + 1;                                        // even CTA: and read
+  uint64_t* dfree = done + 1;                                        // even CTA: and those that the next uses read
   uint64_t* drain = dfree + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
@@ -521,7 +524,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       r.next();
     };
     for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
-      const Task<DKV> t(p, task);
+      const Task<DKV> t(p, task, blockIdx.x >> 1, step);
       if (!t.there) continue;
       const int col = 256 * t.upper + 128 * rank;
       if constexpr (DKV) {
@@ -537,7 +540,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
               uint8_t* a = sm + r.slot * C::STAGE;
               uint8_t* w = a + C::OFF_W;
               const uint32_t bar = mapa_u32(smem_u32(&full[r.slot]), 0);
-              const bool rot = t.upper && which && rank == 0;
+              const bool rot = t.upper && which;
               mbar_expect_tx_cluster(bar, (rot ? 5 : 4) * CHUNK);
               tma_load_2d_pair(a, &tm_pz, bar, 0,
                                c0 < 0 ? 0 : static_cast<int>(p.block_row(t.b, x, c0, which)) + y);
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
               const CUtensorMap* tm = which ? &tm_q : &tm_do;
               tma_load_3d_pair(w, tm, bar, col, x * X + y, t.b);
               tma_load_3d_pair(w + CHUNK, tm, bar, col + 64, x * X + y, t.b);
-              if (rot) tma_load_3d_pair(w + 2 * CHUNK, tm, bar, kVlat, x * X + y, t.b);
+              if (rot) tma_load_3d_pair(w + 2 * CHUNK, tm, bar, kVlat + 32 * rank, x * X + y, t.b);
             }
             advance();
           }
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
           uint8_t* a = sm + r.slot * C::STAGE;
           uint8_t* w = a + C::OFF_W;
           const uint32_t bar = mapa_u32(smem_u32(&full[r.slot]), 0);
-          const bool rot = t.upper && rank == 0;
+          const bool rot = t.upper;
           const int n = rot ? 3 : 2;
           if (any != ~0ull) {
             // rows behind the sequence become zeros: whatever they hold must not meet
@@ -569,7 +572,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
               mbar_expect_tx(land, n * CHUNK);
               tma_load_2d(w, &tm_kv, land, col, row);
               tma_load_2d(w + CHUNK, &tm_kv, land, col + 64, row);
-              if (rot) tma_load_2d(w + 2 * CHUNK, &tm_kv, land, kVlat, row);
+              if (rot) tma_load_2d(w + 2 * CHUNK, &tm_kv, land, kVlat + 32 * rank, row);
             }
             __syncwarp();
             ok = wait(land, lph, s_abort, p.status, SITE_LAND);
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
             if (any == ~0ull) {
               tma_load_2d_pair(w, &tm_kv, bar, col, row);
               tma_load_2d_pair(w + CHUNK, &tm_kv, bar, col + 64, row);
-              if (rot) tma_load_2d_pair(w + 2 * CHUNK, &tm_kv, bar, kVlat, row);
+              if (rot) tma_load_2d_pair(w + 2 * CHUNK, &tm_kv, bar, kVlat + 32 * rank, row);
             }
           }
           advance();
@@ -611,7 +614,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
     int n = 0;                                       // tasks so far
     bool ok = true;
     uint32_t more = 0;                               // accumulate
-    auto multiply = [&](bool rot) {
+    auto multiply = [&](uint32_t d, bool rot) {
       ok = wait(&full[r.slot], r.ph, s_abort, p.status, SITE_F);
       if (!ok) return;
       tc_fence_after();
@@ -620,9 +623,9 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           const uint64_t ak = desc_add(a, kk * (DKV ? 2048 : 32));
-          umma_bf16_pair(tmem, ak, desc_add(w, kk * 2048), IDESC, more | (kk > 0));
+          umma_bf16_pair(d, ak, desc_add(w, kk * 2048), IDESC, more | (kk > 0));
           if (rot)
-            umma_bf16_pair(tmem + 256, ak, desc_add(w, 2 * CHUNK + kk * 2048), IDESC_ROT, more | (kk > 0));
+            umma_bf16_pair(d + 256, ak, desc_add(w, 2 * CHUNK + kk * 2048), IDESC_ROT, more | (kk > 0));
         }
         umma_commit_pair(&empty[r.slot]);
       }
@@ -631,19 +634,20 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       r.next();
     };
     for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
-      const Task<DKV> t(p, task);
+      const Task<DKV> t(p, task, blockIdx.x >> 1, step);
       if (!t.there) continue;
       if (n > 0) ok = wait(dfree, (n - 1) & 1, s_abort, p.status, SITE_DF);
       tc_fence_after();
       ++n;
       more = 0;
+      const uint32_t d = tmem + (t.upper ? 192 : 0);
       if constexpr (DKV) {
         for (int x = t.x0; x < t.x1 && ok; ++x) {
           if (!t.sees(tile_pages(p, t.s, x))) continue;
-          for (int st = 0; st < 4 && ok; ++st) multiply(t.upper && !(st & 1));
+          for (int st = 0; st < 4 && ok; ++st) multiply(d, t.upper && !(st & 1));
         }
       } else {
-        for (int k = 0; k < t.list.count() && ok; ++k) multiply(t.upper);
+        for (int k = 0; k < t.list.count() && ok; ++k) multiply(d, t.upper);
       }
       if (elect_one_lane()) umma_commit_pair(done);
       __syncwarp();
@@ -654,12 +658,19 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
   } else if (warp >= 4) {
     // ---- out: a row (key) a thread; warps 4..7 the lower half of the columns ----
     const int sub = warp & 3, half = (warp >> 2) - 1, r = 128 * rank + 32 * sub + lane;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16);
     const uint32_t free_bar = mapa_u32(smem_u32(dfree), 0);
+    auto give = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(dfree);
+        else mbar_arrive_cluster_relaxed(free_bar);
+      }
+    };
     int n = 0;
     bool ok = true;
     for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
-      const Task<DKV> t(p, task);
+      const Task<DKV> t(p, task, blockIdx.x >> 1, step);
       if (!t.there) continue;
       const bool some = t.some(p);
       const int g = t.x0 * X + r;                    // dq: row of the sequence
@@ -667,8 +678,12 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       if (!ok) break;
       ++n;
       tc_fence_after();
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + (t.upper ? 192 : 0);
+      const bool shared = half != t.upper;           // this warp reads the columns that the next task uses
+      if (!shared) give();
 #pragma unroll 1
-      for (int q = 0; q < (t.upper ? 5 : 4); ++q) {
+      for (int i = 0; i < (t.upper ? 5 : 4); ++i) {
+        const int q = i < 4 && !t.upper ? (i + 2) & 3 : i;
         const int c = q < 4 ? 128 * half + 32 * q : 256 + 32 * half;
         uint32_t v[32];
         if (some) {
@@ -678,6 +693,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = 0;
         }
+        if (shared && i == 1) give();
         if constexpr (DKV) {
           float4* to = reinterpret_cast<float4*>(
               p.part + (part_row(p, t.s, t.b, t.g, t.kt) + r) * kRlat + 256 * t.upper + c);
@@ -697,12 +713,6 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
             to[e] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (rank == 0) mbar_arrive(dfree);
-        else mbar_arrive_cluster_relaxed(free_bar);
       }
     }
   }
