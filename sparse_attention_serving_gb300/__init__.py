@@ -184,12 +184,25 @@ class Rows:
             self.seq_stride = 0
             self.num_pages = base.shape[0]
             self.max_pages = block_table.shape[1]
+        self._key = self._pointer = None
+
+    def _p(self):
+        """A pointer to the C struct, made anew when a field has changed (the struct and its
+        pointer take 1.5 us)."""
+        table = self.block_table
+        key = (self.base.data_ptr(), table is not None and table.data_ptr(), self.seq_stride,
+               self.max_pages, self.num_pages)
+        if key != self._key:
+            self._pointer, self._key = ctypes.pointer(self.c()), key
+        return self._pointer
 
     def c(self) -> _Rows:
-        return _Rows(self.base.data_ptr(), int(self.seq_stride),
-                     0 if self.block_table is None else self.block_table.data_ptr(),
-                     int(self.max_pages), PAGE if self.block_table is not None else 0,
-                     int(self.num_pages))
+        table = self.block_table
+        if table is None:
+            return _Rows(self.base.data_ptr(), int(self.seq_stride), 0, int(self.max_pages), 0,
+                         int(self.num_pages))
+        return _Rows(self.base.data_ptr(), int(self.seq_stride), table.data_ptr(), int(self.max_pages),
+                     PAGE, int(self.num_pages))
 
 
 def workspace_bytes(op: int, B: int, Tq: int, max_kv_len: int, heads: int, topk: int) -> int:
@@ -635,11 +648,21 @@ def dsa_linear_fp8(codes, scale, w_codes, w_scale, out=None, out_dtype=torch.bfl
 # ---------------------------------------------------------------------------
 
 _I32, _I64 = torch.int32, torch.int64
+_INT = 1 << 31
 
 
-def _rows_on(rows, B: int, width: int, need_rows: int, dev: int, name: str):
-    """Refuse a row store that does not hold BF16 rows of `width`, at least `need_rows` of
-    each of B sequences, on the device."""
+def _rows_good(rows, B: int, width: int, need_rows: int, dev: int) -> bool:
+    """Whether a row store holds BF16 rows of `width`, at least `need_rows` of each of B
+    sequences, on the device."""
+    base, table = rows.base, rows.block_table
+    shape = base.shape
+    return (base.dtype is _BF16 and shape[2] == width and base.get_device() == dev
+            and ((B - 1) * rows.seq_stride + need_rows <= shape[0] * shape[1] if table is None else
+                 len(table.shape) == 2 and table.shape[0] >= B and table.get_device() == dev))
+
+
+def _refuse_rows(rows, B: int, width: int, need_rows: int, dev: int, name: str):
+    """Refuse a row store that _rows_good does not accept, by what is wrong with it."""
     if not isinstance(rows, Rows):
         raise TypeError(f"{name} must be Rows")
     base, table = rows.base, rows.block_table
@@ -657,45 +680,51 @@ def _rows_on(rows, B: int, width: int, need_rows: int, dev: int, name: str):
                          f"{rows.seq_stride}")
 
 
-def _operands(call: str, dev: int, operands):
-    """Refuse a call unless every operand (tensor, types, shape, name) has one of its types,
-    its shape, is contiguous and on the device."""
-    try:
-        for t, dtypes, shape, _ in operands:
-            if (t.dtype not in dtypes or t.shape != shape or not t.is_contiguous()
-                    or t.get_device() != dev):
-                _refuse(call, dev, *operands)
-    except AttributeError:
-        _refuse(call, dev, *operands)
+def _queries(call: str, q_lat):
+    """B, T, H of q_lat [B, T, H, 576]."""
+    shape = q_lat.shape
+    if len(shape) != 4 or shape[3] != RLAT:
+        raise ValueError(f"q_lat must be [B, T, H, {RLAT}], got {list(shape)}")
+    B, T, H, _ = shape
+    if B >= _SIZES or T >= _SIZES or H >= _SIZES:
+        _too_large(call, B=B, T=T, H=H)
+    return B, T, H
 
 
-def _shape4(t, name: str, last: int):
-    if t.dim() != 4 or t.shape[3] != last:
-        raise ValueError(f"{name} must be [B, T, H, {last}], got {list(t.shape)}")
-    if max(t.shape) >= _SIZES:
-        _too_large(name, B=t.shape[0], T=t.shape[1], H=t.shape[2])
-    return t.shape[:3]
-
-
-def _int32(call: str, **sizes):
+def _ints(call: str, **sizes):
     for name, v in sizes.items():
         if not isinstance(v, int):
             raise TypeError(f"{name} must be an int")
-        if v >= 1 << 31 or v < -(1 << 31):
+        if not -_INT <= v < _INT:
             raise DsaError(DSA_ERR_UNSUPPORTED, f"{call}: {name} = {v}")
 
 
-def _workspace_for(workspace, dev: int, stream, raw: int, *sizes):
-    if workspace is not None:
-        return workspace
+def _workspace_for(dev: int, stream, raw: int, *sizes):
     need = workspace_bytes(*sizes)
     workspace = _empty((need,), _U8, dev, stream)
     _check(lib.dsa_workspace_init(workspace.data_ptr(), need, raw), "dsa_workspace_init")
     return workspace
 
 
+def _zeros(shape, dtype, dev: int, stream):
+    if stream is None:
+        return torch.zeros(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.zeros(shape, dtype=dtype, device=dev)
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
+
+
+def _all_good(dev: int, *operands) -> bool:
+    """Whether every operand (tensor or None, type, shape) is of its type and shape,
+    contiguous and on the device."""
+    for t, dtype, shape in operands:
+        if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                                  and t.get_device() == dev):
+            return False
+    return True
 
 
 def dsa_cache_append_rope(k_pre, kv_new, k_cache: Rows, kv_cache: Rows, q_start, rope, pos=None,
@@ -715,50 +744,58 @@ def dsa_cache_append_rope(k_pre, kv_new, k_cache: Rows, kv_cache: Rows, q_start,
                                          q_pe, q_lat, q_idx, q_idx_out, kv_style, key_style, eps,
                                          workspace, stream)
     raw = _stream_on(dev, stream)
-    if k_pre.dim() != 3:
+    shape = k_pre.shape
+    if len(shape) != 3:
         raise ValueError("k_pre must be [B, Tq, D_I]")
-    B, Tq, D_I = k_pre.shape
-    if max(B, Tq, D_I) >= _SIZES:
+    B, Tq, D_I = shape
+    if B >= _SIZES or Tq >= _SIZES or D_I >= _SIZES:
         _too_large("dsa_cache_append_rope", B=B, Tq=Tq, D_I=D_I)
-    if not isinstance(rope, torch.Tensor):
-        raise TypeError("rope must be a torch.Tensor")
-    if rope.dim() != 2 or rope.shape[0] >= _SIZES:
-        raise ValueError("rope must be [n_pos, 64], n_pos below 2^30")
     if (q_pe is None) != (q_lat is None):
         raise ValueError("q_pe and q_lat go together")
     if q_idx is None and q_idx_out is not None:
         raise ValueError("q_idx_out needs q_idx")
-    H = H_I = 0
-    workspace = _workspace_for(workspace, dev, stream, raw, OP_CACHE_APPEND, B, Tq, 0, 0, 0)
-    operands = [(k_pre, (_F32,), k_pre.shape, "k_pre"), (kv_new, (_BF16,), (B, Tq, RLAT), "kv_new"),
-                (q_start, (_I32,), (B,), "q_start"),
-                (rope, (_F32,), (rope.shape[0], ROPE_DIMS), "rope")]
-    if pos is not None:
-        operands.append((pos, (_I32,), (B, Tq), "pos"))
-    if n_new is not None:
-        operands.append((n_new, (_I32,), (B,), "n_new"))
-    if q_pe is not None:
-        _device(q_pe, "q_pe")
-        _, _, H = _shape4(q_pe, "q_pe", ROPE_DIMS)
-        operands += [(q_pe, (_BF16,), (B, Tq, H, ROPE_DIMS), "q_pe"),
-                     (q_lat, (_BF16,), (B, Tq, H, RLAT), "q_lat")]
-    if q_idx is not None:
-        _device(q_idx, "q_idx")
-        _, _, H_I = _shape4(q_idx, "q_idx", D_I)
-        if q_idx_out is None:
-            q_idx_out = q_idx
-        operands += [(q_idx, (_BF16,), (B, Tq, H_I, D_I), "q_idx"),
-                     (q_idx_out, (_BF16,), (B, Tq, H_I, D_I), "q_idx_out")]
-    operands.append((workspace, (_U8,), getattr(workspace, "shape", None), "workspace"))
-    _operands("dsa_cache_append_rope", dev, operands)
-    _rows_on(k_cache, B, D_I, k_cache.seq_stride if isinstance(k_cache, Rows) else 0, dev, "k_cache")
-    _rows_on(kv_cache, B, RLAT, kv_cache.seq_stride if isinstance(kv_cache, Rows) else 0, dev,
-             "kv_cache")
-    kr, vr = k_cache.c(), kv_cache.c()
+    if q_idx_out is None:
+        q_idx_out = q_idx
+    for t, name in ((rope, "rope"), (q_pe, "q_pe"), (q_idx, "q_idx")):
+        if not isinstance(t, torch.Tensor) and (t is not None or name == "rope"):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    n_pos = rope.shape[0] if rope.shape else 0
+    H = 0 if q_pe is None else q_pe.shape[2] if len(q_pe.shape) == 4 else 0
+    H_I = 0 if q_idx is None else q_idx.shape[2] if len(q_idx.shape) == 4 else 0
+    if n_pos >= _SIZES or H >= _SIZES or H_I >= _SIZES:
+        _too_large("dsa_cache_append_rope", n_pos=n_pos, H=H, H_I=H_I)
+    if workspace is None:
+        workspace = _workspace_for(dev, stream, raw, OP_CACHE_APPEND, B, Tq, 0, 0, 0)
+    try:
+        good = (_all_good(dev, (k_pre, _F32, shape), (kv_new, _BF16, (B, Tq, RLAT)),
+                          (q_start, _I32, (B,)), (rope, _F32, (n_pos, ROPE_DIMS)),
+                          (pos, _I32, (B, Tq)), (n_new, _I32, (B,)),
+                          (q_pe, _BF16, (B, Tq, H, ROPE_DIMS)), (q_lat, _BF16, (B, Tq, H, RLAT)),
+                          (q_idx, _BF16, (B, Tq, H_I, D_I)))
+                and (q_idx_out is q_idx or _all_good(dev, (q_idx_out, _BF16, (B, Tq, H_I, D_I))))
+                and workspace.dtype is _U8 and workspace.is_contiguous()
+                and workspace.get_device() == dev and kv_new is not None and q_start is not None
+                and _rows_good(k_cache, B, D_I, k_cache.seq_stride, dev)
+                and _rows_good(kv_cache, B, RLAT, kv_cache.seq_stride, dev))
+    except AttributeError:
+        good = False
+    if not good:
+        for rows, width, name in ((k_cache, D_I, "k_cache"), (kv_cache, RLAT, "kv_cache")):
+            _refuse_rows(rows, B, width, rows.seq_stride if isinstance(rows, Rows) else 0, dev, name)
+        _refuse("dsa_cache_append_rope", dev, (k_pre, (_F32,), None, "k_pre"),
+                (kv_new, (_BF16,), (B, Tq, RLAT), "kv_new"), (q_start, (_I32,), (B,), "q_start"),
+                (rope, (_F32,), (n_pos, ROPE_DIMS), "rope"), (workspace, (_U8,), None, "workspace"),
+                *((t, (dt,), sh, name) for t, dt, sh, name in
+                  ((pos, _I32, (B, Tq), "pos"), (n_new, _I32, (B,), "n_new"),
+                   (q_pe, _BF16, (B, Tq, H, ROPE_DIMS), "q_pe"),
+                   (q_lat, _BF16, (B, Tq, H, RLAT), "q_lat"),
+                   (q_idx, _BF16, (B, Tq, H_I, D_I), "q_idx"),
+                   (q_idx_out, _BF16, (B, Tq, H_I, D_I), "q_idx_out")) if t is not None))
     code = lib.dsa_cache_append_rope(
-        k_pre.data_ptr(), kv_new.data_ptr(), kr, vr, q_start.data_ptr(), rope.data_ptr(),
-        rope.shape[0], _at(pos), _at(n_new), _at(q_pe), _at(q_lat), H, _at(q_idx), _at(q_idx_out),
-        H_I, B, Tq, D_I, kv_style, key_style, eps, workspace.data_ptr(), workspace.numel(), raw)
+        k_pre.data_ptr(), kv_new.data_ptr(), k_cache._p(), kv_cache._p(), q_start.data_ptr(),
+        rope.data_ptr(), n_pos, _at(pos), _at(n_new), _at(q_pe), _at(q_lat), H, _at(q_idx),
+        _at(q_idx_out), H_I, B, Tq, D_I, kv_style, key_style, eps, workspace.data_ptr(),
+        workspace.numel(), raw)
     if code:
         raise DsaError(code, "dsa_cache_append_rope")
     return workspace
@@ -779,40 +816,41 @@ def mla_tree_fwd(q_lat, kv: Rows, tree, kv_len, max_kv_len: int, n_draft=None,
             return mla_tree_fwd(q_lat, kv, tree, kv_len, max_kv_len, n_draft, scale, o_lat, lse,
                                 want_lse, workspace, stream)
     raw = _stream_on(dev, stream)
-    B, T, H = _shape4(q_lat, "q_lat", RLAT)
-    _int32("mla_tree_fwd", max_kv_len=max_kv_len)
+    B, T, H = _queries("mla_tree_fwd", q_lat)
+    _ints("mla_tree_fwd", max_kv_len=max_kv_len)
+    new = _empty if n_draft is None else _zeros
     if o_lat is None:
-        o_lat = _empty((B, T, H, VLAT), _BF16, dev, stream)
-        if n_draft is not None:
-            _zero(o_lat, stream)
+        o_lat = new((B, T, H, VLAT), _BF16, dev, stream)
     if lse is None and want_lse:
-        lse = _empty((B, T, H), _F32, dev, stream)
-        if n_draft is not None:
-            _zero(lse, stream)
-    workspace = _workspace_for(workspace, dev, stream, raw, OP_MLA_TREE, B, T, max_kv_len, H, 0)
-    operands = [(q_lat, (_BF16,), q_lat.shape, "q_lat"), (tree, (_I64,), (B, T), "tree"),
+        lse = new((B, T, H), _F32, dev, stream)
+    if workspace is None:
+        workspace = _workspace_for(dev, stream, raw, OP_MLA_TREE, B, T, max_kv_len, H, 0)
+    try:
+        good = (q_lat.dtype is _BF16 and q_lat.is_contiguous() and tree.dtype is _I64
+                and tree.shape == (B, T) and tree.is_contiguous() and kv_len.dtype is _I32
+                and kv_len.shape == (B,) and kv_len.is_contiguous() and o_lat.dtype is _BF16
+                and o_lat.shape == (B, T, H, VLAT) and o_lat.is_contiguous()
+                and workspace.dtype is _U8 and workspace.is_contiguous()
+                and dev == tree.get_device() == kv_len.get_device() == o_lat.get_device()
+                == workspace.get_device()
+                and (n_draft is None or _all_good(dev, (n_draft, _I32, (B,))))
+                and (lse is None or _all_good(dev, (lse, _F32, (B, T, H))))
+                and _rows_good(kv, B, RLAT, max_kv_len, dev))
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse_rows(kv, B, RLAT, max_kv_len, dev, "kv")
+        _refuse("mla_tree_fwd", dev, (q_lat, (_BF16,), None, "q_lat"), (tree, (_I64,), (B, T), "tree"),
                 (kv_len, (_I32,), (B,), "kv_len"), (o_lat, (_BF16,), (B, T, H, VLAT), "o_lat"),
-                (workspace, (_U8,), getattr(workspace, "shape", None), "workspace")]
-    if n_draft is not None:
-        operands.append((n_draft, (_I32,), (B,), "n_draft"))
-    if lse is not None:
-        operands.append((lse, (_F32,), (B, T, H), "lse"))
-    _operands("mla_tree_fwd", dev, operands)
-    _rows_on(kv, B, RLAT, max_kv_len, dev, "kv")
-    code = lib.mla_tree_fwd(q_lat.data_ptr(), kv.c(), tree.data_ptr(), kv_len.data_ptr(),
+                (workspace, (_U8,), None, "workspace"),
+                *((t, (dt,), sh, name) for t, dt, sh, name in
+                  ((n_draft, _I32, (B,), "n_draft"), (lse, _F32, (B, T, H), "lse")) if t is not None))
+    code = lib.mla_tree_fwd(q_lat.data_ptr(), kv._p(), tree.data_ptr(), kv_len.data_ptr(),
                             _at(n_draft), B, T, H, max_kv_len, scale, o_lat.data_ptr(), _at(lse),
                             workspace.data_ptr(), workspace.numel(), raw)
     if code:
         raise DsaError(code, "mla_tree_fwd")
     return o_lat, lse
-
-
-def _zero(t, stream):
-    if stream is None:
-        t.zero_()
-    else:
-        with torch.cuda.stream(stream):
-            t.zero_()
 
 
 def mla_window_fwd(q_lat, kv: Rows, q_start, kv_len, window: int, n_first: int, max_kv_len: int,
@@ -827,22 +865,34 @@ def mla_window_fwd(q_lat, kv: Rows, q_start, kv_len, window: int, n_first: int, 
             return mla_window_fwd(q_lat, kv, q_start, kv_len, window, n_first, max_kv_len, scale,
                                   o_lat, lse, want_lse, workspace, stream)
     raw = _stream_on(dev, stream)
-    B, Tq, H = _shape4(q_lat, "q_lat", RLAT)
-    _int32("mla_window_fwd", window=window, n_first=n_first, max_kv_len=max_kv_len)
+    B, Tq, H = _queries("mla_window_fwd", q_lat)
+    _ints("mla_window_fwd", window=window, n_first=n_first, max_kv_len=max_kv_len)
     if o_lat is None:
         o_lat = _empty((B, Tq, H, VLAT), _BF16, dev, stream)
     if lse is None and want_lse:
         lse = _empty((B, Tq, H), _F32, dev, stream)
-    workspace = _workspace_for(workspace, dev, stream, raw, OP_MLA_WINDOW, B, Tq, max_kv_len, H,
-                               min(window + n_first, max_kv_len))
-    operands = [(q_lat, (_BF16,), q_lat.shape, "q_lat"), (q_start, (_I32,), (B,), "q_start"),
-                (kv_len, (_I32,), (B,), "kv_len"), (o_lat, (_BF16,), (B, Tq, H, VLAT), "o_lat"),
-                (workspace, (_U8,), getattr(workspace, "shape", None), "workspace")]
-    if lse is not None:
-        operands.append((lse, (_F32,), (B, Tq, H), "lse"))
-    _operands("mla_window_fwd", dev, operands)
-    _rows_on(kv, B, RLAT, max_kv_len, dev, "kv")
-    code = lib.mla_window_fwd(q_lat.data_ptr(), kv.c(), q_start.data_ptr(), kv_len.data_ptr(), B, Tq,
+    if workspace is None:
+        workspace = _workspace_for(dev, stream, raw, OP_MLA_WINDOW, B, Tq, max_kv_len, H,
+                                   min(window + n_first, max_kv_len))
+    try:
+        good = (q_lat.dtype is _BF16 and q_lat.is_contiguous() and q_start.dtype is _I32
+                and q_start.shape == (B,) and q_start.is_contiguous() and kv_len.dtype is _I32
+                and kv_len.shape == (B,) and kv_len.is_contiguous() and o_lat.dtype is _BF16
+                and o_lat.shape == (B, Tq, H, VLAT) and o_lat.is_contiguous()
+                and workspace.dtype is _U8 and workspace.is_contiguous()
+                and dev == q_start.get_device() == kv_len.get_device() == o_lat.get_device()
+                == workspace.get_device()
+                and (lse is None or _all_good(dev, (lse, _F32, (B, Tq, H))))
+                and _rows_good(kv, B, RLAT, max_kv_len, dev))
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse_rows(kv, B, RLAT, max_kv_len, dev, "kv")
+        _refuse("mla_window_fwd", dev, (q_lat, (_BF16,), None, "q_lat"),
+                (q_start, (_I32,), (B,), "q_start"), (kv_len, (_I32,), (B,), "kv_len"),
+                (o_lat, (_BF16,), (B, Tq, H, VLAT), "o_lat"), (workspace, (_U8,), None, "workspace"),
+                *(() if lse is None else ((lse, (_F32,), (B, Tq, H), "lse"),)))
+    code = lib.mla_window_fwd(q_lat.data_ptr(), kv._p(), q_start.data_ptr(), kv_len.data_ptr(), B, Tq,
                               H, window, n_first, max_kv_len, scale, o_lat.data_ptr(), _at(lse),
                               workspace.data_ptr(), workspace.numel(), raw)
     if code:
@@ -863,23 +913,36 @@ def mla_window_bwd(q_lat, kv: Rows, q_start, kv_len, window: int, n_first: int, 
             return mla_window_bwd(q_lat, kv, q_start, kv_len, window, n_first, max_kv_len, o_lat, lse,
                                   d_o, scale, dq, dkv, workspace, stream)
     raw = _stream_on(dev, stream)
-    B, Tq, H = _shape4(q_lat, "q_lat", RLAT)
-    _int32("mla_window_bwd", window=window, n_first=n_first, max_kv_len=max_kv_len)
-    _rows_on(kv, B, RLAT, max_kv_len, dev, "kv")
+    B, Tq, H = _queries("mla_window_bwd", q_lat)
+    _ints("mla_window_bwd", window=window, n_first=n_first, max_kv_len=max_kv_len)
+    if not isinstance(kv, Rows) or not _rows_good(kv, B, RLAT, max_kv_len, dev):
+        _refuse_rows(kv, B, RLAT, max_kv_len, dev, "kv")
+    rows = kv.base.shape
     if dq is None:
         dq = _empty((B, Tq, H, RLAT), _BF16, dev, stream)
     if dkv is None:
-        dkv = _empty(kv.base.shape, _BF16, dev, stream)
-        _zero(dkv, stream)
-    workspace = _workspace_for(workspace, dev, stream, raw, OP_MLA_WINDOW_BWD, B, Tq, max_kv_len, H,
-                               min(window + n_first, max_kv_len))
-    _operands("mla_window_bwd", dev, [
-        (q_lat, (_BF16,), q_lat.shape, "q_lat"), (q_start, (_I32,), (B,), "q_start"),
-        (kv_len, (_I32,), (B,), "kv_len"), (o_lat, (_BF16,), (B, Tq, H, VLAT), "o_lat"),
-        (lse, (_F32,), (B, Tq, H), "lse"), (d_o, (_BF16,), (B, Tq, H, VLAT), "d_o"),
-        (dq, (_BF16,), (B, Tq, H, RLAT), "dq"), (dkv, (_BF16,), kv.base.shape, "dkv"),
-        (workspace, (_U8,), getattr(workspace, "shape", None), "workspace")])
-    code = lib.mla_window_bwd(q_lat.data_ptr(), kv.c(), q_start.data_ptr(), kv_len.data_ptr(), B, Tq,
+        dkv = _zeros(rows, _BF16, dev, stream)
+    if workspace is None:
+        workspace = _workspace_for(dev, stream, raw, OP_MLA_WINDOW_BWD, B, Tq, max_kv_len, H,
+                                   min(window + n_first, max_kv_len))
+    try:
+        good = (q_lat.dtype is _BF16 and q_lat.is_contiguous() and workspace.dtype is _U8
+                and workspace.is_contiguous() and workspace.get_device() == dev
+                and q_start is not None and kv_len is not None and o_lat is not None
+                and lse is not None and d_o is not None
+                and _all_good(dev, (q_start, _I32, (B,)), (kv_len, _I32, (B,)),
+                              (o_lat, _BF16, (B, Tq, H, VLAT)), (lse, _F32, (B, Tq, H)),
+                              (d_o, _BF16, (B, Tq, H, VLAT)), (dq, _BF16, (B, Tq, H, RLAT)),
+                              (dkv, _BF16, rows)))
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse("mla_window_bwd", dev, (q_lat, (_BF16,), None, "q_lat"),
+                (q_start, (_I32,), (B,), "q_start"), (kv_len, (_I32,), (B,), "kv_len"),
+                (o_lat, (_BF16,), (B, Tq, H, VLAT), "o_lat"), (lse, (_F32,), (B, Tq, H), "lse"),
+                (d_o, (_BF16,), (B, Tq, H, VLAT), "d_o"), (dq, (_BF16,), (B, Tq, H, RLAT), "dq"),
+                (dkv, (_BF16,), rows, "dkv"), (workspace, (_U8,), None, "workspace"))
+    code = lib.mla_window_bwd(q_lat.data_ptr(), kv._p(), q_start.data_ptr(), kv_len.data_ptr(), B, Tq,
                               H, window, n_first, max_kv_len, scale, o_lat.data_ptr(), lse.data_ptr(),
                               d_o.data_ptr(), dq.data_ptr(), dkv.data_ptr(), workspace.data_ptr(),
                               workspace.numel(), raw)

@@ -481,3 +481,70 @@ def test_streams_and_graphs(dsa):
     assert torch.equal(o, want[1][0]) and torch.equal(lse, want[1][1])
     for ws in work:
         _ok(dsa, ws)
+
+
+# ---------------------------------------------------------------------------
+# refusals of the binding
+# ---------------------------------------------------------------------------
+
+def _refusals(call, good, wrong):
+    call(**good)
+    for name, values in wrong.items():
+        for v in values:
+            with pytest.raises((TypeError, ValueError, RuntimeError)) as e:
+                call(**{**good, name: v})
+            assert "CUDA error" not in str(e.value), (name, v, e.value)
+
+
+def _other(t):
+    """Of another type, one short, strided, and on the CPU."""
+    wide = torch.empty((*t.shape[:-1], 2 * t.shape[-1]), dtype=t.dtype, device="cuda")
+    return [None, t.to(torch.float16), t[..., :-1].contiguous(), wide[..., ::2], t.cpu()]
+
+
+def test_binding_refusals(dsa):
+    gen = _gen(41)
+    B, T, H, S = 2, 3, 8, 70
+    base, q = _normal(gen, B, S, 576), _normal(gen, B, T, H, 576)
+    o, lse = _outputs(B, T, H)
+    kl, rows = _i32([67, 67]), dsa.Rows(base)
+    ws = dsa.new_workspace(1 << 26)
+    stores = [None, base, dsa.Rows(base[:1].contiguous()), dsa.Rows(base[..., :512].contiguous()),
+              dsa.Rows(torch.zeros((B, S, 576), dtype=torch.uint8, device="cuda")),
+              dsa.Rows(*ref.paged(base[:1].contiguous(), gen))]
+    sizes = [0, -1, 1 << 31, 2.5, S + 1]
+    masks = _masks(41, B, T, "tree")
+    common = dict(q_lat=_other(q)[1:], kv=stores, kv_len=_other(kl), max_kv_len=sizes, o_lat=_other(o)[1:],
+                  lse=_other(lse)[1:], scale=[0.0, -1.0, math.nan],
+                  workspace=[torch.zeros(64, dtype=torch.uint8, device="cuda"), ws.cpu(), ws.float()])
+    _refusals(dsa.mla_tree_fwd,
+              dict(q_lat=q, kv=rows, tree=masks, kv_len=kl, max_kv_len=S, o_lat=o, lse=lse, workspace=ws),
+              dict(common, tree=_other(masks), n_draft=_other(kl)[1:]))
+    window = dict(q_lat=q, kv=rows, q_start=kl - 3, kv_len=kl, window=9, n_first=1, max_kv_len=S, o_lat=o,
+                  lse=lse, workspace=ws)
+    spans = dict(q_start=_other(kl), window=[-1, 1 << 31, 1.5, None], n_first=[-1, 1 << 31, "1"])
+    _refusals(dsa.mla_window_fwd, window, dict(common, **spans))
+    d_o, dkv = _normal(gen, B, T, H, 512), torch.zeros_like(base)
+    _refusals(dsa.mla_window_bwd, dict(window, d_o=d_o, dkv=dkv, dq=torch.empty_like(q)),
+              dict(common, **spans, d_o=_other(d_o), dkv=_other(dkv)[1:], dq=_other(q)[1:],
+                   kv=stores + [dsa.Rows(*ref.paged(base, gen))]))
+    torch.cuda.synchronize()
+
+
+def test_append_binding_refusals(dsa):
+    gen = _gen(42)
+    B, T, S = 2, 3, 40
+    k_pre, kv_new = torch.randn((B, T, 128), device="cuda"), _normal(gen, B, T, 576)
+    k, v = torch.zeros((B, S, 128), dtype=torch.bfloat16, device="cuda"), _normal(gen, B, S, 576)
+    q_pe, q_lat, q_idx = _normal(gen, B, T, 8, 64), _normal(gen, B, T, 8, 576), _normal(gen, B, T, 4, 128)
+    table, qs, pos = torch.zeros((50, 64), device="cuda"), _i32([1, 2]), _i32([[0, 1, 2]] * 2)
+    good = dict(k_pre=k_pre, kv_new=kv_new, k_cache=dsa.Rows(k), kv_cache=dsa.Rows(v), q_start=qs,
+                rope=table, pos=pos, n_new=qs, q_pe=q_pe, q_lat=q_lat, q_idx=q_idx,
+                q_idx_out=torch.empty_like(q_idx))
+    _refusals(dsa.dsa_cache_append_rope, good,
+              dict(k_pre=_other(k_pre), kv_new=_other(kv_new), k_cache=[None, k, dsa.Rows(v)],
+                   kv_cache=[None, v, dsa.Rows(k), dsa.Rows(v[:1].contiguous())], q_start=_other(qs),
+                   rope=_other(table), pos=_other(pos)[1:], n_new=_other(qs)[1:], q_pe=_other(q_pe),
+                   q_lat=_other(q_lat), q_idx=_other(q_idx), q_idx_out=_other(q_idx)[1:],
+                   kv_style=[-1, 3], key_style=[7], eps=[-1.0, math.nan, math.inf]))
+    torch.cuda.synchronize()
