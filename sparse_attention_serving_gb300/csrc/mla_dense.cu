@@ -186,6 +186,21 @@ struct Line {
     n_blocks = p.nominal;
     if (p.nominal == 0) n_blocks = sq.ok ? max(((sq.L + 63) / 64 + 1) / 2, 1) : 1;
   }
+  // Blocks of the sequences at .. at + 31, a lane each, summed from `at` on.
+  __device__ __forceinline__ int64_t sums(int at, int& mine) const {
+    const int lane = threadIdx.x & 31;
+    Seq sq;
+    int n = 0, c = 0;
+    if (at + lane < p.B) measure(at + lane, sq, n, c);
+    mine = n * c;
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    return sum;
+  }
   // The sequence, tile and block at x (or behind the last sequence).
   __device__ __forceinline__ void seek(int64_t x) {
     if (p.nominal > 0) {
@@ -196,25 +211,17 @@ struct Line {
       if (b < p.B) measure(b, s, tiles, cost);
       return;
     }
-    const int lane = threadIdx.x & 31;
     for (b = 0; b < p.B; b += 32) {
-      Seq sq;
-      int n = 0, c = 0;
-      if (b + lane < p.B) measure(b + lane, sq, n, c);
-      int64_t sum = static_cast<int64_t>(n) * c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
-      }
+      int mine;
+      const int64_t sum = sums(b, mine);
       const unsigned over = __ballot_sync(0xffffffffu, sum > x);
       if (over != 0) {
         const int at = __ffs(over) - 1;
-        x -= __shfl_sync(0xffffffffu, sum - static_cast<int64_t>(n) * c, at);
+        const unsigned in = static_cast<unsigned>(x - __shfl_sync(0xffffffffu, sum - mine, at));
         b += at;
         measure(b, s, tiles, cost);
-        tile = static_cast<int>(x / cost);
-        j = static_cast<int>(x % cost);
+        tile = in / static_cast<unsigned>(cost);
+        j = in % static_cast<unsigned>(cost);
         return;
       }
       x -= __shfl_sync(0xffffffffu, sum, 31);
@@ -223,20 +230,23 @@ struct Line {
   __device__ __forceinline__ int64_t total() const {
     if (p.nominal > 0) return static_cast<int64_t>(p.B) * p.tiles * p.nominal;
     int64_t sum = 0;
-    for (int at = threadIdx.x & 31; at < p.B; at += 32) {
-      Seq sq;
-      int n, c;
-      measure(at, sq, n, c);
-      sum += static_cast<int64_t>(n) * c;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    int mine;
+    for (int at = 0; at < p.B; at += 32) sum += __shfl_sync(0xffffffffu, sums(at, mine), 31);
     return sum;
   }
   __device__ __forceinline__ Line(const Params& pp, int pair) : p(pp) {
-    const int64_t all = total(), n = min(all, static_cast<int64_t>(p.pairs));
+    const int64_t all = total();
+    const int n = static_cast<int>(min(all, static_cast<int64_t>(p.pairs)));
     if (pair >= n) return;        // a block each: the last pairs have nothing
-    int64_t x0 = all * pair / n, x1 = all * (pair + 1) / n;
+    // the first pairs have one block more
+    int64_t each, more;
+    if (all < (1ll << 31)) {
+      each = static_cast<unsigned>(all) / static_cast<unsigned>(n);
+      more = static_cast<unsigned>(all) % static_cast<unsigned>(n);
+    } else {
+      each = all / n, more = all % n;
+    }
+    int64_t x0 = each * pair + min(static_cast<int64_t>(pair), more), x1 = x0 + each + (pair < more);
     if (!p.cut) {                 // whole units: to the next unit's start
       seek(x1);
       if (x1 < all && j > 0) x1 += cost - j;
@@ -295,6 +305,13 @@ struct Feed {
   }
 };
 
+// Whether every query of the unit sees all of the 64 rows from kb on.
+__device__ __forceinline__ bool all_see(const Mask& m, const Unit& u, int kb) {
+  if (m.tree != nullptr) return kb + 63 < u.s.pos0;
+  const int t0 = u.s.pos0 + u.i0, t1 = u.s.pos0 + u.i1;
+  return kb + 63 <= t0 && t1 < u.s.L && (kb > t1 - m.window || kb + 63 < m.n_first);
+}
+
 template <int R>
 __global__ void __launch_bounds__(THREADS, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
@@ -310,22 +327,23 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* vempty = vfull + C::NV;
   uint64_t* sfull = vempty + C::NV;
   uint64_t* sfree = sfull + 1;                                       // even CTA
-  uint64_t* pready = sfull + 2;                                      // even CTA
+  uint64_t* pready = sfull + 2;                                      // odd CTA: for its warp 3
   uint64_t* odone = sfull + 3;                                       // a block's values added
   uint64_t* ofull = sfull + 4;                                       // a unit's
   uint64_t* ofree = sfull + 5;                                       // [2] even CTA: 2R columns read
-  uint64_t* lfull = sfull + 7;                                       // [2] a unit's sums, of both CTAs
-  uint64_t* lfree = sfull + 9;                                       // [2]
-  uint64_t* vland = sfull + 11;                                      // [2] this CTA's own copies
-  uint64_t* drain = sfull + 13;
-  uint64_t* ufull = sfull + 14;                                      // [UNITS]
+  uint64_t* lfull = sfull + 7;                                       // [2] a unit's sums, of this CTA's rows
+  uint64_t* lpeer = sfull + 9;                                       // [2] of the other's
+  uint64_t* lfree = sfull + 11;                                      // [2]
+  uint64_t* vland = sfull + 13;                                      // [2] this CTA's own copies
+  uint64_t* drain = sfull + 15;
+  uint64_t* ufull = sfull + 16;                                      // [UNITS]
   uint64_t* uempty = ufull + UNITS;                                  // [UNITS]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(uempty + UNITS);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
   int* s_slow = reinterpret_cast<int*>(tslot + 2);                   // [2]
   Unit* s_unit = reinterpret_cast<Unit*>(sm + C::OFF_MISC + 512);    // [UNITS]
   float* s_inv = reinterpret_cast<float*>(sm + C::OFF_MISC + 1024);  // [2][2R]
-  static_assert((2 * C::NK + 2 * C::NV + 14 + 2 * UNITS) * 8 + 16 <= 512, "misc");
+  static_assert((2 * C::NK + 2 * C::NV + 16 + 2 * UNITS) * 8 + 16 <= 512, "misc");
   static_assert(UNITS * sizeof(Unit) <= 512, "misc");
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -336,16 +354,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int k = 0; k < C::NV; ++k) mbar_init(&vfull[k], 2), mbar_init(&vempty[k], 1);
     mbar_init(sfull, 1);
     mbar_init(sfree, 8);
-    mbar_init(pready, 8);
+    mbar_init(pready, rank == 0 ? 5 : 4);
     mbar_init(odone, 1);
     mbar_init(ofull, 1);
     for (int k = 0; k < 2; ++k) {
       mbar_init(&ofree[k], 8);
-      mbar_init(&lfull[k], 8);
+      mbar_init(&lfull[k], 4);
+      mbar_init(&lpeer[k], 1);
       mbar_init(&lfree[k], 8);
       mbar_init(&vland[k], 1);
     }
-    for (int k = 0; k < UNITS; ++k) mbar_init(&ufull[k], 1), mbar_init(&uempty[k], rank == 0 ? 11 : 9);
+    for (int k = 0; k < UNITS; ++k) mbar_init(&ufull[k], 1), mbar_init(&uempty[k], rank == 0 ? 11 : 10);
     mbar_init(drain, 2);
     s_abort[0] = 0;
     s_slow[0] = s_slow[1] = 0;
@@ -563,12 +582,26 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       // every MMA of the pair is complete before anything is given up
       wait(drain, 0, s_abort, p.status, SITE_DRAIN);
+    } else {
+      // ---- tells the even CTA that this one's P is written: a release at cluster scope
+      // takes 0.5 us, in the softmax warps it set the pace of the pair ----
+      const uint32_t bar = mapa_u32(smem_u32(pready), 0);
+      int blk = 0;
+      bool ok = true;
+      while (const Unit* up = ok ? feed.next() : nullptr) {
+        const int nb = up->nb;
+        for (int j = 0; j < nb && ok; ++j, ++blk) {
+          ok = wait(pready, blk & 1, s_abort, p.status, SITE_P);
+          if (ok && lane == 0) mbar_arrive_cluster(bar);
+          __syncwarp();
+        }
+      }
     }
   } else if (warp < 8) {
     // ---- softmax: a row a thread ----
     const int sub = warp & 3, r = sub * 32 + lane;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + C::S_COL;
-    const uint32_t free_bar = mapa_u32(smem_u32(sfree), 0), p_bar = mapa_u32(smem_u32(pready), 0);
+    const uint32_t free_bar = mapa_u32(smem_u32(sfree), 0);
     uint8_t* prow = sm + C::OFF_P + (r >> 3) * 1024 + (r & 7) * 128;
     int blk = 0;
     bool ok = true;
@@ -581,17 +614,29 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint64_t bits =
           live && p.m.tree != nullptr ? p.m.tree[static_cast<int64_t>(u.b) * p.m.T + i] : 0;
       float l_sum = 0.f, m_ref = -INFINITY;
-      bool slow = false;
+      bool slow = false, good[2];                        // the block's pages are there: looked up a block ahead
+      auto look = [&](int j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = u.k0 + 2 * j + h;
+          good[h] = k < u.k1 && page_row(p.kv, u.b, u.pages.page(k)) >= 0;
+        }
+      };
+      look(0);
       for (int j = 0; j < u.nb && ok; ++j, ++blk) {
         // who sees what of the block's two pages (a row that is not there: all)
         uint64_t see[2], any[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int k = u.k0 + 2 * j + h;
           see[h] = any[h] = 0;
-          if (k < u.k1 && page_row(p.kv, u.b, u.pages.page(k)) >= 0) {
-            any[h] = range_bits(0, u.s.L, u.pages.page(k) * 64);
-            see[h] = live ? row_mask(p.m, u.s, i, bits, u.pages.page(k) * 64) : any[h];
+          if (good[h]) {
+            const int kb = u.pages.page(u.k0 + 2 * j + h) * 64;
+            if (all_see(p.m, u, kb)) {
+              see[h] = any[h] = ~0ull;
+            } else {
+              any[h] = range_bits(0, u.s.L, kb);
+              see[h] = live ? row_mask(p.m, u.s, i, bits, kb) : any[h];
+            }
           }
         }
         ok = wait(sfull, blk & 1, s_abort, p.status, SITE_SF);
@@ -608,6 +653,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (rank == 0) mbar_arrive(sfree);
           else mbar_arrive_cluster_relaxed(free_bar);
         }
+        look(j + 1);
         const bool full = __all_sync(0xffffffffu, (see[0] & see[1]) == ~0ull);
         if (!full) {
 #pragma unroll
@@ -659,10 +705,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive(pready);
-          else mbar_arrive_cluster(p_bar);
-        }
+        if (lane == 0) mbar_arrive(pready);
       }
       // what the epilogues of both CTAs need of this row, once they are done with the
       // unit before the last
@@ -686,11 +729,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         s_slow[bu] = 1;
         st_cluster_u32(smem_u32(&s_slow[bu]), rank ^ 1, 1);
       }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive_cluster(mapa_u32(smem_u32(&lfull[bu]), rank));
-        mbar_arrive_cluster(mapa_u32(smem_u32(&lfull[bu]), rank ^ 1));
-      }
+      mbar_arrive_warp(&lfull[bu]);
     }
   } else {
     // ---- out: lane = dim 256 rank + 128 m + 32 sub + lane, a row a column ----
@@ -706,7 +745,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int64_t part = static_cast<int64_t>(2 * pair + (at > 0)) * 2 * R;
       const bool parts = !u.whole();
       const float* inv = s_inv + bu * 2 * R;
-      ok = wait<true>(&lfull[bu], (at >> 1) & 1, s_abort, p.status, SITE_L);
+      // this CTA's sums have gone to both; its first warp says so to the other
+      ok = wait(&lfull[bu], (at >> 1) & 1, s_abort, p.status, SITE_L);
+      if (ok && sub == 0 && lane == 0) mbar_arrive_cluster(mapa_u32(smem_u32(&lpeer[bu]), rank ^ 1));
+      __syncwarp();
+      if (ok) ok = wait<true>(&lpeer[bu], (at >> 1) & 1, s_abort, p.status, SITE_L);
       if (ok && u.nb > 0) ok = wait(ofull, n & 1, s_abort, p.status, SITE_O);
       if (!ok) break;
       tc_fence_after();
@@ -736,10 +779,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int e = 0; e < 32; ++e)
               if (c0 + e < here) to[e * kVlat] = __uint_as_float(x[e]);
           } else {
-            uint16_t* to = p.o + (first + c0) * kVlat + dim;
+            // two rows of a dim become two dims of a row, between two lanes: 4-byte stores
+            const int odd = lane & 1;
+            uint16_t* to = p.o + (first + c0 + odd) * kVlat + dim - odd;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c0 + e < here) to[e * kVlat] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(x[e])));
+            for (int e = 0; e < 32; e += 2) {
+              const uint32_t w = pack_bf16x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              const uint32_t v = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), odd ? 0x3276 : 0x5410);
+              if (c0 + e + odd < here) *reinterpret_cast<uint32_t*>(to + e * kVlat) = v;
+            }
           }
         }
         tc_fence_before();
@@ -758,16 +806,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (sub == 0 && lane == 0) s_slow[bu] = 0;
         __syncwarp();
       }
-      if (lane == 0) {
-        mbar_arrive_cluster(mapa_u32(smem_u32(&lfree[bu]), rank));
-        mbar_arrive_cluster(mapa_u32(smem_u32(&lfree[bu]), rank ^ 1));
+      if (lane == 0) {                                   // the sums may be overwritten
+        const uint32_t there = mapa_u32(smem_u32(&lfree[bu]), rank ^ 1);
+        mbar_arrive(&lfree[bu]);
+        if (slow) mbar_arrive_cluster(there);            // after the flag's reset
+        else mbar_arrive_cluster_relaxed(there);
       }
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  cluster_arrive_relaxed();     // nothing of the pair's is read any more
+  cluster_wait();
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
