@@ -774,7 +774,7 @@ Plan plan(int B, int T, int H, int max_kv_len, int64_t span, int64_t window, int
   // segments: as many tasks as keep the pairs evenly busy, but the sums of each are
   // 590 KB to write and add
   int64_t seg = (2ll * B * q.RC * (span / 256 + 2) + TASKS - 1) / TASKS;
-  if (seg < 2) seg = 2;
+  if (seg < 4) seg = 4;
   q.seg = static_cast<int>(seg < q.RC ? seg : q.RC);
   q.G = (q.RC + q.seg - 1) / q.seg;
   const int64_t kf = (n_first + 255) / 256, nk = (window + seg_tokens(q.seg, H) + 254) / 256 + 1;
