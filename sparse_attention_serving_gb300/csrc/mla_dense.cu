@@ -13,7 +13,7 @@
 //   O^T [512 x 2R] += V^T . P^T                  cta_group::2, M = 256, N = 2R, twice:
 //        CTA c holds dims 256c .. 256c+255 of all 128 keys and P of its own rows,
 //        and accumulates its dims of all 2R rows
-// in TMEM columns 0 .. 4R-1 (O^T) and 128 more (S).  Transposing the value product
+// in TMEM columns 0 .. 4R-1 (O^T) and 128 more (S; R = 48: twice).  Transposing the value product
 // is what makes room: 512 dims of 96 rows would be all of a CTA's TMEM the other
 // way round.  Sharing the keys between two CTAs halves what the score product reads
 // of them through the shared-memory port: per block 216 KB (S) + 112 KB (O^T) are
@@ -60,9 +60,10 @@ struct Cfg {
   static constexpr int MISC = 1024 + 16 * R;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   static constexpr uint32_t S_COL = 4 * R;
+  static constexpr int NB = R == 96 ? 1 : 2;          // S buffers
   static_assert(SMEM <= 232448, "shared memory");
   static_assert(OFF_Q + 8 * QCH + 128 * 128 <= OFF_K, "the aliased rows stay inside Q and P");
-  static_assert(4 * R + 128 <= 512, "TMEM columns");
+  static_assert(4 * R + 128 * NB <= 512, "TMEM columns");
 };
 
 enum : uint32_t {
@@ -327,25 +328,25 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* kempty = kfull + C::NK;
   uint64_t* vfull = kempty + C::NK;                                  // even CTA
   uint64_t* vempty = vfull + C::NV;
-  uint64_t* sfull = vempty + C::NV;
-  uint64_t* sfree = sfull + 1;                                       // even CTA
-  uint64_t* pready = sfull + 2;                                      // odd CTA: for its warp 3
-  uint64_t* odone = sfull + 3;                                       // a block's values added
-  uint64_t* ofull = sfull + 4;                                       // a unit's
-  uint64_t* ofree = sfull + 5;                                       // [2] even CTA: 2R columns read
-  uint64_t* lfull = sfull + 7;                                       // [2] a unit's sums, of this CTA's rows
-  uint64_t* lpeer = sfull + 9;                                       // [2] of the other's
-  uint64_t* lfree = sfull + 11;                                      // [2]
-  uint64_t* vland = sfull + 13;                                      // [2] this CTA's own copies
-  uint64_t* drain = sfull + 15;
-  uint64_t* ufull = sfull + 16;                                      // [UNITS]
+  uint64_t* sfull = vempty + C::NV;                                  // [NB]
+  uint64_t* sfree = sfull + 2;                                       // [NB] even CTA
+  uint64_t* pready = sfull + 4;                                      // odd CTA: for its warp 3
+  uint64_t* odone = sfull + 5;                                       // a block's values added
+  uint64_t* ofull = sfull + 6;                                       // a unit's
+  uint64_t* ofree = sfull + 7;                                       // [2] even CTA: 2R columns read
+  uint64_t* lfull = sfull + 9;                                       // [2] a unit's sums, of this CTA's rows
+  uint64_t* lpeer = sfull + 11;                                      // [2] of the other's
+  uint64_t* lfree = sfull + 13;                                      // [2]
+  uint64_t* vland = sfull + 15;                                      // [2] this CTA's own copies
+  uint64_t* drain = sfull + 17;
+  uint64_t* ufull = sfull + 18;                                      // [UNITS]
   uint64_t* uempty = ufull + UNITS;                                  // [UNITS]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(uempty + UNITS);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
   int* s_slow = reinterpret_cast<int*>(tslot + 2);                   // [2]
   Unit* s_unit = reinterpret_cast<Unit*>(sm + C::OFF_MISC + 512);    // [UNITS]
   float* s_inv = reinterpret_cast<float*>(sm + C::OFF_MISC + 1024);  // [2][2R]
-  static_assert((2 * C::NK + 2 * C::NV + 16 + 2 * UNITS) * 8 + 16 <= 512, "misc");
+  static_assert((2 * C::NK + 2 * C::NV + 18 + 2 * UNITS) * 8 + 16 <= 512, "misc");
   static_assert(UNITS * sizeof(Unit) <= 512, "misc");
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -354,8 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (tid == 0) {
     for (int k = 0; k < C::NK; ++k) mbar_init(&kfull[k], 1), mbar_init(&kempty[k], 1);
     for (int k = 0; k < C::NV; ++k) mbar_init(&vfull[k], 2), mbar_init(&vempty[k], 1);
-    mbar_init(sfull, 1);
-    mbar_init(sfree, 8);
+    for (int k = 0; k < C::NB; ++k) mbar_init(&sfull[k], 1), mbar_init(&sfree[k], 8);
     mbar_init(pready, rank == 0 ? 5 : 4);
     mbar_init(odone, 1);
     mbar_init(ofull, 1);
@@ -522,7 +522,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         while (const Unit* up = ok ? feed.next() : nullptr) {
         const Unit& u = *up;
           for (int j = 0; j < u.nb && ok; ++j, ++blk) {
-            if (blk > 0) ok = wait(sfree, (blk - 1) & 1, s_abort, p.status, SITE_SE);
+            const int bu = blk % C::NB;
+            if (blk >= C::NB) ok = wait(&sfree[bu], (blk / C::NB - 1) & 1, s_abort, p.status, SITE_SE);
             tc_fence_after();
             for (int c = 0; c < 9 && ok; ++c) {
               ok = wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
@@ -532,10 +533,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint64_t a = desc_add(qd, c * C::QCH), w = desc_add(kd, r.slot * CHUNK);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  umma_bf16_pair(tmem + C::S_COL, desc_add(a, kk * 32), desc_add(w, kk * 32), IDESC_S,
+                  umma_bf16_pair(tmem + C::S_COL + 128 * bu, desc_add(a, kk * 32), desc_add(w, kk * 32), IDESC_S,
                                  c > 0 || kk > 0);
                 umma_commit_pair(&kempty[r.slot]);
-                if (c == 8) umma_commit_pair(sfull);
+                if (c == 8) umma_commit_pair(&sfull[bu]);
               }
               __syncwarp();
               r.next();
@@ -641,19 +642,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
         }
-        ok = wait(sfull, blk & 1, s_abort, p.status, SITE_SF);
+        const int sb = blk % C::NB;
+        ok = wait(&sfull[sb], (blk / C::NB) & 1, s_abort, p.status, SITE_SF);
         if (!ok) break;
         tc_fence_after();
         uint32_t z[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(taddr + 32 * c, z[c]);
+        for (int c = 0; c < 4; ++c) tmem_ld32(taddr + 128 * sb + 32 * c, z[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_wait_regs(z[c]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (rank == 0) mbar_arrive(sfree);
-          else mbar_arrive_cluster_relaxed(free_bar);
+          if (rank == 0) mbar_arrive(&sfree[sb]);
+          else mbar_arrive_cluster_relaxed(free_bar + 8 * sb);
         }
         look(j + 1);
         const bool full = __all_sync(0xffffffffu, (see[0] & see[1]) == ~0ull);
