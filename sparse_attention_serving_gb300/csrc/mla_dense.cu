@@ -5,24 +5,25 @@
 //   o = sum_s softmax(z)_s KV[s, 0:512],   lse = log sum_s exp(z_s)
 //
 // The (query, head) rows of a sequence are packed: a unit is 2R consecutive ones
-// (R = 96, or 48 where a sequence has no more than 96), done by a pair of CTAs.
+// (R = 96, 64 or 48: plan()), done by a pair of CTAs.
 // Rows of the cache come 64 at a time (a page), a block is two such pages.
-//   S [R rows per CTA x 128 keys] = Q . K^T      cta_group::2, M = 256, N = 128:
-//        each CTA holds its own R queries (the MMA's other 128 - R rows alias what
+//   S [R rows per CTA x 128 keys] = Q . K^T      cta_group::2, N = 128, M = 256 (R = 96)
+//        or 128 (64, 48): each CTA holds its own R queries (the MMA's other rows alias what
 //        lies behind them and are not read) and the keys of one of the two pages
 //   O^T [512 x 2R] += V^T . P^T                  cta_group::2, M = 256, N = 2R, twice:
 //        CTA c holds dims 256c .. 256c+255 of all 128 keys and P of its own rows,
 //        and accumulates its dims of all 2R rows
-// in TMEM columns 0 .. 4R-1 (O^T) and 128 more (S; R = 48: twice).  Transposing the value product
+// in TMEM columns 0 .. 4R-1 (O^T) and 128 more (S; R <= 64: 64, twice).  Transposing the value product
 // is what makes room: 512 dims of 96 rows would be all of a CTA's TMEM the other
 // way round.  Sharing the keys between two CTAs halves what the score product reads
 // of them through the shared-memory port: per block 216 KB (S) + 112 KB (O^T) are
 // read, 136 KB copied in and 24 KB of P written, about 3,800 cycles at 128 bytes,
 // beside 3,840 cycles of MMAs (R = 96).
 //
-// Roles (12 warps): 0 copies Q (chunk by chunk beside a unit's first K) and K, 1 copies V, 2 and 3 of the even CTA issue the
-// two products, 4..7 hold a row a thread: its 128 scores, P = 2^(z - m) to BF16 in
-// shared memory; 8..11 write O^T / l out while the next unit's first products run.
+// Roles (12 warps): 0 copies Q (chunk by chunk beside a unit's first K) and K, 1 copies
+// V, 2 and 3 of the even CTA issue the two products, 4..7 hold a row (R <= 64: and one
+// of the two pages) a thread: its scores, P = 2^(z - m) to BF16 in shared memory; 8..11
+// write O^T / l out while the next unit's first products run.
 // m is the maximum of the first block in which the row sees anything, so O^T is
 // never rescaled; a row whose later scores exceed it by 2^100 sends its unit to
 // attend_row.  So does a row of the sequence that holds an infinity or a NaN and that
@@ -49,21 +50,23 @@ constexpr float FAR = 100.f;              // exponents that P may reach
 template <int R_>
 struct Cfg {
   static constexpr int R = R_;
+  static constexpr int HALVES = R <= 64 ? 2 : 1;      // threads that share a row's scores
   static constexpr int NK = R == 96 ? 5 : 8;          // K slots: a chunk of own keys
-  static constexpr int NV = R == 96 ? 3 : 5;          // V slots: 64 keys x 128 dims
+  static constexpr int NV = R == 96 ? 3 : R == 64 ? 4 : 5;   // V slots: 64 keys x 128 dims
   static constexpr int QCH = R * 128;                 // 64 dims of the queries
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_P = OFF_Q + 9 * QCH;
   static constexpr int OFF_K = OFF_P + 2 * QCH;
   static constexpr int OFF_V = OFF_K + NK * CHUNK;
   static constexpr int OFF_MISC = OFF_V + NV * 2 * CHUNK;
-  static constexpr int MISC = 1024 + 16 * R;
+  static constexpr int MISC = 1024 + 16 * R + (HALVES == 2 ? 2048 : 0);
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   static constexpr uint32_t S_COL = 4 * R;
-  static constexpr int NB = R == 96 ? 1 : 2;          // S buffers
+  static constexpr int SW = 128 / HALVES;             // columns of a score buffer
+  static constexpr int NB = R == 96 ? 1 : 2;          // score buffers
   static_assert(SMEM <= 232448, "shared memory");
-  static_assert(OFF_Q + 8 * QCH + 128 * 128 <= OFF_K, "the aliased rows stay inside Q and P");
-  static_assert(4 * R + 128 * NB <= 512, "TMEM columns");
+  static_assert(OFF_Q + 8 * QCH + 128 * 128 / HALVES <= OFF_K, "the aliased rows stay inside Q and P");
+  static_assert(4 * R + SW * NB <= 512, "TMEM columns");
 };
 
 enum : uint32_t {
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                 const Params p) {
   using C = Cfg<R>;
-  constexpr uint32_t IDESC_S = idesc_bf16(256, 128, false, false);
+  constexpr uint32_t IDESC_S = idesc_bf16(256 / C::HALVES, 128, false, false);
   constexpr uint32_t IDESC_O = idesc_bf16(256, 2 * R, true, false);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_align1024(smem_raw);
@@ -347,6 +350,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   Unit* s_unit = reinterpret_cast<Unit*>(sm + C::OFF_MISC + 512);    // [UNITS]
   float* s_inv = reinterpret_cast<float*>(sm + C::OFF_MISC + 1024);  // [2][2R]
   static_assert((2 * C::NK + 2 * C::NV + 18 + 2 * UNITS) * 8 + 16 <= 512, "misc");
+  float* s_top = s_inv + 4 * R;                                      // HALVES = 2: [2][2][64] maxima
+  float* s_sum = s_top + 256;                                        // [2][2][64] sums
   static_assert(UNITS * sizeof(Unit) <= 512, "misc");
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -533,7 +538,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint64_t a = desc_add(qd, c * C::QCH), w = desc_add(kd, r.slot * CHUNK);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  umma_bf16_pair(tmem + C::S_COL + 128 * bu, desc_add(a, kk * 32), desc_add(w, kk * 32), IDESC_S,
+                  umma_bf16_pair(tmem + C::S_COL + C::SW * bu, desc_add(a, kk * 32), desc_add(w, kk * 32), IDESC_S,
                                  c > 0 || kk > 0);
                 umma_commit_pair(&kempty[r.slot]);
                 if (c == 8) umma_commit_pair(&sfull[bu]);
@@ -601,13 +606,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   } else if (warp < 8) {
-    // ---- softmax: a row a thread ----
-    const int sub = warp & 3, r = sub * 32 + lane;
+    // ---- softmax: a row a thread, or (HALVES = 2) a row and one of the block's pages:
+    // the MMA of 128 rows leaves a CTA's 64 in lanes 0..63 (first page) and 64..127 ----
+    constexpr int PG = 2 / C::HALVES, CH = 2 * PG;       // pages and 32-column chunks of a thread
+    const int sub = warp & 3, half = C::HALVES == 2 ? sub >> 1 : 0;
+    const int r = (C::HALVES == 2 ? sub & 1 : sub) * 32 + lane;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(sub * 32) << 16) + C::S_COL;
     const uint32_t free_bar = mapa_u32(smem_u32(sfree), 0);
-    uint8_t* prow = sm + C::OFF_P + (r >> 3) * 1024 + (r & 7) * 128;
-    int blk = 0;
+    uint8_t* prow = sm + C::OFF_P + half * C::QCH + (r >> 3) * 1024 + (r & 7) * 128;
+    int blk = 0, met = 0;                                // met: exchanges of the two halves so far
     bool ok = true;
+    // the other half's value of what this thread gives (HALVES = 2)
+    auto exchange = [&](float* s_buf, int turn, float v) {
+      float* buf = s_buf + (turn & 1) * 128;
+      buf[half * 64 + r] = v;
+      named_bar_sync(2 + (sub & 1), 64);
+      return buf[(half ^ 1) * 64 + r];
+    };
     while (const Unit* up = ok ? feed.next() : nullptr) {
       const Unit& u = *up;
       const int at = feed.at;
@@ -617,23 +632,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint64_t bits =
           live && p.m.tree != nullptr ? p.m.tree[static_cast<int64_t>(u.b) * p.m.T + i] : 0;
       float l_sum = 0.f, m_ref = -INFINITY;
-      bool slow = false, good[2];                        // the block's pages are there: looked up a block ahead
+      bool slow = false, good[PG];                       // the block's pages are there: looked up a block ahead
       auto look = [&](int j) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = u.k0 + 2 * j + h;
+        for (int h = 0; h < PG; ++h) {
+          const int k = u.k0 + 2 * j + half + h;
           good[h] = k < u.k1 && page_row(p.kv, u.b, u.pages.page(k)) >= 0;
         }
       };
       look(0);
-      for (int j = 0; j < u.nb && ok; ++j, ++blk) {
-        // who sees what of the block's two pages (a row that is not there: all)
-        uint64_t see[2], any[2];
+      for (int j = 0; j < u.nb && (C::HALVES == 2 || ok); ++j, ++blk) {
+        // who sees what of the pages (a row that is not there: all)
+        uint64_t see[PG], any[PG], all = ~0ull, some = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < PG; ++h) {
           see[h] = any[h] = 0;
           if (good[h]) {
-            const int kb = u.pages.page(u.k0 + 2 * j + h) * 64;
+            const int kb = u.pages.page(u.k0 + 2 * j + half + h) * 64;
             if (all_see(p.m, u, kb)) {
               see[h] = any[h] = ~0ull;
             } else {
@@ -641,16 +656,20 @@ __global__ void __launch_bounds__(THREADS, 1)
               see[h] = live ? row_mask(p.m, u.s, i, bits, kb) : any[h];
             }
           }
+          all &= see[h];
+          some |= see[h];
         }
         const int sb = blk % C::NB;
-        ok = wait(&sfull[sb], (blk / C::NB) & 1, s_abort, p.status, SITE_SF);
+        ok = ok && wait(&sfull[sb], (blk / C::NB) & 1, s_abort, p.status, SITE_SF);
+        // (HALVES = 2: the two warps that share rows leave together, by a vote)
+        if (C::HALVES == 2) ok = !named_bar_or(2 + (sub & 1), 64, !ok);
         if (!ok) break;
         tc_fence_after();
-        uint32_t z[4][32];
+        uint32_t z[CH][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(taddr + 128 * sb + 32 * c, z[c]);
+        for (int c = 0; c < CH; ++c) tmem_ld32(taddr + C::SW * sb + 32 * c, z[c]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait_regs(z[c]);
+        for (int c = 0; c < CH; ++c) tmem_ld_wait_regs(z[c]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -658,10 +677,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           else mbar_arrive_cluster_relaxed(free_bar + 8 * sb);
         }
         look(j + 1);
-        const bool full = __all_sync(0xffffffffu, (see[0] & see[1]) == ~0ull);
-        if (!full) {
+        if (!__all_sync(0xffffffffu, all == ~0ull)) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < CH; ++c) {
             const uint32_t sees = static_cast<uint32_t>(see[c >> 1] >> (32 * (c & 1)));
             const uint32_t others = static_cast<uint32_t>(any[c >> 1] >> (32 * (c & 1))) & ~sees;
             float hidden = 0.f;
@@ -673,18 +691,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (hidden != 0.f) slow = true;              // a NaN: somebody else's row holds one
           }
         }
-        if (__any_sync(0xffffffffu, m_ref == -INFINITY && (see[0] | see[1]) != 0)) {
+        // the row's reference, once it sees something (both of its threads know m_ref and
+        // live, so both warps come here or neither)
+        if (__any_sync(0xffffffffu, m_ref == -INFINITY && (C::HALVES == 2 ? live : some != 0))) {
           float top = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(z[c][e]));
+          if (C::HALVES == 2) top = fmaxf(top, exchange(s_top, met++, top));
           if (m_ref == -INFINITY) m_ref = top * p.scale_log2;
         }
         const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
         float sums[4] = {0.f, 0.f, 0.f, 0.f}, most = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < CH; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float a0 = fmaf(__uint_as_float(z[c][e]), p.scale_log2, neg);
@@ -698,10 +719,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         l_sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
         // P is free once the block before has been multiplied
         if (blk > 0) ok = wait(odone, (blk - 1) & 1, s_abort, p.status, SITE_O);
-        if (!ok) break;
-        if (r < R) {
+        if (ok && r < R) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               *reinterpret_cast<uint4*>(prow + (c >> 1) * C::QCH + (((4 * (c & 1) + q) ^ (r & 7)) << 4)) =
@@ -709,21 +729,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pready);
+        if (ok && lane == 0) mbar_arrive(pready);
       }
       // what the epilogues of both CTAs need of this row, once they are done with the
       // unit before the last
       const int bu = at & 1;
       if (ok && at > 1) ok = wait(&lfree[bu], ((at >> 1) - 1) & 1, s_abort, p.status, SITE_L);
+      if (C::HALVES == 2) ok = !named_bar_or(2 + (sub & 1), 64, !ok);
       if (!ok) break;
-      if (live) {
+      if (C::HALVES == 2) {
+        const float other = exchange(s_sum, at, l_sum);
+        l_sum = half == 0 ? l_sum + other : other + l_sum;
+      }
+      if (live && half == 0) {
         const float lse2 = l_sum == 0.f ? -INFINITY : m_ref + log2f(l_sum);
         if (!u.whole())
           p.part_lse[(2 * pair + (at > 0)) * 2 * R + rank * R + r] = lse2;
         else if (p.lse != nullptr)
           p.lse[static_cast<int64_t>(u.b) * p.m.T * p.H + g] = lse2 * 0.6931471805599453f;
       }
-      if (r < R) {
+      if (r < R && half == 0) {
         const float inv = l_sum != 0.f ? 1.f / l_sum : 0.f;
         float* to = &s_inv[bu * 2 * R + rank * R + r];
         *to = inv;
@@ -901,12 +926,19 @@ struct Plan {
 // outputs and their joining take about as long (9 us).
 Plan plan(int B, int T, int H, int64_t span) {
   Plan q{};
-  const int64_t rows = static_cast<int64_t>(T) * H;
-  q.R = rows <= 96 ? 48 : 96;
-  q.tiles = static_cast<int>((rows + 2 * q.R - 1) / (2 * q.R));
-  const int64_t tokens = (2 * q.R + H - 2) / H + 1;      // of a unit
-  q.blocks = static_cast<int>((span + tokens + 64) / 128 + 2);
-  const int64_t units = static_cast<int64_t>(B) * q.tiles, most = num_sms() / 2;
+  const int64_t rows = static_cast<int64_t>(T) * H, most = num_sms() / 2;
+  auto set = [&](int R) {
+    q.R = R;
+    q.tiles = static_cast<int>((rows + 2 * R - 1) / (2 * R));
+    const int64_t tokens = (2 * R + H - 2) / H + 1;      // of a unit
+    q.blocks = static_cast<int>((span + tokens + 64) / 128 + 2);
+  };
+  // 96 rows a CTA copy the least per row; 64 have the shorter chain from a block to the
+  // next, which counts where a pair has few blocks (5 trees of 33 tokens, 8 heads: 25.5
+  // us against 28.8; 2048 queries, window 1024: 438 against 409)
+  set(rows <= 96 ? 48 : rows <= 128 ? 64 : 96);
+  if (q.R == 96 && static_cast<int64_t>(B) * q.tiles * q.blocks < 4 * most) set(64);
+  const int64_t units = static_cast<int64_t>(B) * q.tiles;
   q.cut = (units + most - 1) / most * q.blocks * most > units * q.blocks + 3 * most;
   const int64_t pieces = units * (q.cut ? q.blocks : 1);
   q.pairs = static_cast<int>(pieces < most ? pieces : most);
@@ -969,7 +1001,9 @@ dsa_status_t dense_fwd_launch(const DenseArgs& a, cudaStream_t stream) {
   p.part_lse = p.part_o + rows * kVlat;
   p.stretch = reinterpret_cast<Stretch*>(p.part_lse + rows);
   p.status = a.status;
-  return q.R == 96 ? launch<96>(a, q, p, stream) : launch<48>(a, q, p, stream);
+  return q.R == 96   ? launch<96>(a, q, p, stream)
+         : q.R == 64 ? launch<64>(a, q, p, stream)
+                     : launch<48>(a, q, p, stream);
 }
 
 }  // namespace dsa

@@ -76,6 +76,10 @@ WINDOW_CASES = [
     (1, 300, 3, [77], 64, 64, False),
     (1, 4, 96, [4000], 2 ** 31 - 1, 2 ** 31 - 1, True),   # everything
     (70, 3, 5, [i * 7 for i in range(70)], 90, 2, True),
+    # enough work for the largest tiles: some whole units, some cut ones
+    (1, 260, 96, [100], 300, 5, True),
+    (2, 401, 33, [0, 1000], 500, 65, False),
+    (40, 3, 128, [20 * i for i in range(40)], 200, 1, True),
 ]
 
 
@@ -228,6 +232,9 @@ TREE_CASES = [
     (2, 16, 40, [0, 10], None, "none", False),        # prefix or nothing
     (2, 5, 96, [0, 0], [5, 2], "any", True),
     (1, 3, 1, [300], None, "tree", False),
+    (8, 16, 96, [1000, 0, 63, 700, 1500, 129, 64, 900], [16, 3, 16, 0, 1, 16, 9, 12], "tree", True),
+    (3, 40, 96, [640, 2000, 1], None, "tree", False),
+    (100, 2, 96, [5 * i for i in range(100)], None, "tree", True),
 ]
 
 
