@@ -599,7 +599,7 @@ static dsa_status_t dense_args(const uint16_t* q_lat, const dsa_rows_t* kv, cons
       !aligned(lim, 4))
     return DSA_ERR_INVALID_ARGUMENT;
   if (B <= 0 || T <= 0 || H <= 0 || max_kv_len <= 0) return DSA_ERR_INVALID_ARGUMENT;
-  if (!(scale > 0.f) || !(scale < 3.0e38f)) return DSA_ERR_INVALID_ARGUMENT;
+  if (!(scale > 0.f) || !(scale < 2.0e38f)) return DSA_ERR_INVALID_ARGUMENT;
   if (H > 128) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(B) * T * H >= (int64_t(1) << 31) - 4096) return DSA_ERR_UNSUPPORTED;
   dsa_status_t st = resolve_rows(kv, B, max_kv_len, kRlat, &a->kv);

@@ -25,7 +25,7 @@
 // of the two pages) a thread: its scores, P = 2^(z - m) to BF16 in shared memory; 8..11
 // write O^T / l out while the next unit's first products run.
 // m is the maximum of the first block in which the row sees anything, so O^T is
-// never rescaled; a row whose later scores exceed it by 2^100 sends its unit to
+// never rescaled; a row whose later scores exceed it by 2^80 sends its unit to
 // attend_row.  So does a row of the sequence that holds an infinity or a NaN and that
 // some query of the unit does not see (0 * NaN would reach it).  Rows behind the
 // sequence, in its last page, are zeroed in V before use.
@@ -45,7 +45,7 @@ namespace dsa {
 namespace dense {
 
 constexpr int THREADS = 384;
-constexpr float FAR = 100.f;              // exponents that P may reach
+constexpr float FAR = 80.f;               // exponents that P may reach: 2^80 times 2^47 is FP32's range
 
 template <int R_>
 struct Cfg {
@@ -415,7 +415,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!more) break;
         if (at == 0) mine.first = u.id, mine.j0 = u.j0;
         if (u.j0 == 0 && u.j1 < u.of) mine.head = u.id, mine.slot = 2 * pair + (at > 0);
-        if (rank == 0 && lane == 0 && u.g0 == 0 && u.j0 == 0) report_seq(p.m, u.s, u.b, p.status);
         const int qrow = static_cast<int>(static_cast<int64_t>(u.b) * p.m.T * p.H) + u.g0 + rank * R;
         for (int j = 0; j < u.nb && ok; ++j) {
           const int k = u.k0 + 2 * j + rank;
@@ -550,6 +549,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (elect_one_lane()) umma_commit_pair(drain);
         __syncwarp();
+      } else {
+        // every sequence, whether it has a unit or not
+        for (int b = pair * 32 + lane; b < p.B; b += p.pairs * 32) report_seq(p.m, seq_of(p.m, b), b, p.status);
       }
     } else if (rank == 0) {
       // ---- values ----

@@ -233,3 +233,63 @@ def test_append_then_tree_then_window(dsa):
         r_o, r_lse, o_off, lse_off = ref.forward(last[b], cache[:n], see)
         ref.within(w[b], r_o, o_off, "window o_lat")
         ref.within(w_lse[b], r_lse, lse_off, "window lse")
+
+
+def test_append_rope_in_a_graph(dsa):
+    """Captured and replayed with other tokens and places."""
+    gen = _gen(8)
+    B, T, S = 2, 3, 100
+    k, v = (torch.zeros((B, S, w), dtype=torch.bfloat16, device="cuda") for w in (128, 576))
+    table, qs = _table(S), _i32([0, 0])
+    k_pre = torch.zeros((B, T, 128), device="cuda")
+    kv_new, q_pe = (torch.zeros((B, T, w), dtype=torch.bfloat16, device="cuda") for w in (576, 8 * 64))
+    q_pe = q_pe.view(B, T, 8, 64)
+    q_lat = torch.zeros((B, T, 8, 576), dtype=torch.bfloat16, device="cuda")
+    ws = dsa.new_workspace(256)
+
+    def call(k, v, q_lat):
+        dsa.dsa_cache_append_rope(k_pre, kv_new, dsa.Rows(k), dsa.Rows(v), qs, table, q_pe=q_pe,
+                                  q_lat=q_lat, workspace=ws)
+
+    call(k, v, q_lat)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(k, v, q_lat)
+    for start in ([5, 90], [97, 0]):
+        qs.copy_(_i32(start))
+        k_pre.normal_(generator=gen)
+        kv_new.normal_(generator=gen)
+        q_pe.normal_(generator=gen)
+        other = [x.clone() for x in (k, v, q_lat)]
+        graph.replay()
+        call(*other)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((k, v, q_lat), other))
+    assert dsa.read_device_status(ws)[0] == dsa.DSA_OK
+
+
+def test_append_rope_beyond_32_bit_offsets(dsa):
+    """Caches and queries of more than 2^31 elements: the last rows."""
+    gen = _gen(9)
+    pages, T, H = 60000, 21000, 96
+    v = torch.zeros((pages, 64, 576), dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros((pages, 64, 128), dtype=torch.bfloat16, device="cuda")
+    n = -(-T // 64)
+    table = torch.arange(pages - 2 * n, pages, device="cuda", dtype=torch.int32).view(2, n).contiguous()
+    q_lat = torch.zeros((2, T, H, 576), dtype=torch.bfloat16, device="cuda")
+    assert v.numel() > 2 ** 31 and q_lat.numel() > 2 ** 31
+    k_pre = torch.randn((2, T, 128), generator=gen, device="cuda")
+    kv_new = torch.randn((2, T, 576), generator=gen, device="cuda").to(torch.bfloat16)
+    q_pe = torch.randn((2, T, H, 64), generator=gen, device="cuda").to(torch.bfloat16)
+    rope = _table(T)
+    ws = dsa.dsa_cache_append_rope(k_pre, kv_new, dsa.Rows(k, table), dsa.Rows(v, table), _i32([0, 0]),
+                                   rope, q_pe=q_pe, q_lat=q_lat)
+    assert dsa.read_device_status(ws)[0] == dsa.DSA_OK
+    got = ref.logical(v, table, 1, T)
+    assert torch.equal(got[:, :512], kv_new[1, :, :512].double())
+    ang = rope.double()
+    x = q_pe[1, -3:].double()
+    c, s = ang[-3:, None, :32], ang[-3:, None, 32:]
+    want = torch.cat([x[..., :32] * c - x[..., 32:] * s, x[..., 32:] * c + x[..., :32] * s], -1)
+    size = (x[..., :32].abs() + x[..., 32:].abs()).repeat(1, 1, 2)
+    assert ((q_lat[1, -3:, :, 512:].double() - want).abs() <= want.abs() * ref.HALF + size * 2.0 ** -22).all()

@@ -80,6 +80,7 @@ WINDOW_CASES = [
     (1, 260, 96, [100], 300, 5, True),
     (2, 401, 33, [0, 1000], 500, 65, False),
     (40, 3, 128, [20 * i for i in range(40)], 200, 1, True),
+    (1, 3000, 1, [0], 200, 3, False),              # one head: a unit of 128 or more queries
 ]
 
 
@@ -301,6 +302,45 @@ def test_tree_bad_lengths_are_flagged(dsa):
     assert (lse[1] == -math.inf).all() and (lse[2, 0] == -math.inf).all() and (o[1] == 0).all()
 
 
+def test_tree_counts_out_of_range(dsa):
+    """n_draft below 0 and above T: taken as the nearer bound and flagged, also where a sequence
+    then has no token at all."""
+    gen = _gen(15)
+    q, base = _normal(gen, 2, 3, 8, 576), _normal(gen, 2, 40, 576)
+    masks = _masks(15, 2, 3, "tree")
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_TREE, 2, 3, 40, 8, 0))
+    want, _ = dsa.mla_tree_fwd(q, dsa.Rows(base), masks, _i32([10, 20]), 40, workspace=ws)
+    _ok(dsa, ws)
+    for counts, rows in (([3, -1], [3, 0]), ([9, 3], [3, 3]), ([-7, -7], [0, 0])):
+        o, lse = _outputs(2, 3, 8)
+        dsa.mla_tree_fwd(q, dsa.Rows(base), masks, _i32([10, 20]), 40, n_draft=_i32(counts), o_lat=o,
+                         lse=lse, workspace=ws)
+        assert dsa.read_device_status(ws)[0] == dsa.DSA_ERR_BAD_INDEX, counts
+        for b in range(2):
+            assert torch.equal(o[b, :rows[b]], want[b, :rows[b]])
+            assert (o[b, rows[b]:] == SENTINEL).all() and (lse[b, rows[b]:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("rise", [0.0, 300.0])
+def test_tree_pieces_by_the_slow_path(dsa, rise):
+    """A long prefix, cut into pieces: with scores that rise beyond an exponent's range, and with
+    a sibling's NaN in the last piece."""
+    gen = _gen(16)
+    T, H, L = 3, 40, 5000
+    q, base = _normal(gen, 1, T, H, 576), _normal(gen, 1, L + T, 576)
+    q[..., 0] = 16.0
+    if rise:
+        base[0, :L, 0] = (torch.arange(L, device="cuda") / L * rise / (16 * ref.SCALE)).to(torch.bfloat16)
+    base[0, L + 1] = math.nan
+    masks = torch.tensor([[1, 3, 5]], dtype=torch.int64, device="cuda")
+    o, lse = dsa.mla_tree_fwd(q, dsa.Rows(base), masks, _i32([L]), L + T)
+    see = _tree_sees(masks[0], L, T, T)[[0, 2]]
+    r_o, r_lse, o_off, lse_off = ref.forward(q[0, [0, 2]], base[0], see)
+    ref.within(o[0, [0, 2]], r_o, o_off, "o_lat")
+    ref.within(lse[0, [0, 2]], r_lse, lse_off, "lse")
+    assert torch.isnan(o[0, 1]).all()
+
+
 def test_tree_of_one_chain_is_the_window_without_end(dsa):
     """A chain of drafted tokens sees what causal queries see."""
     gen = _gen(14)
@@ -333,6 +373,9 @@ BWD_CASES = [
     (2, 5, 96, [70, 0], 0, 3),
     (2, 5, 3, [70, 0], 0, 0),
     (1, 300, 2, [0], 2 ** 31 - 1, 0),
+    (1, 900, 3, [0], 10, 300),                     # first tokens in two key tiles
+    (2, 700, 1, [500, 0], 260, 1),                 # one head: a tile of 128 queries
+    (1, 200, 96, [0], 150, 4),                     # several tasks for each pair
 ]
 
 
@@ -438,6 +481,32 @@ def test_window_backward_bad_sequence(dsa):
     assert (dkv[0, 13:] == SENTINEL).all() and (dkv[0, 3:13] != SENTINEL).any()
 
 
+def test_window_backward_in_chunks(dsa):
+    """More P and dZ than the workspace takes at a time: dkv's sums go on from chunk to chunk."""
+    B, Tq, H, window, first = 8, 4224, 8, 4000, 70      # 4.6 GB of blocks, 4.3 at a time
+    gen = _gen(27)
+    base, q, d_o = _normal(gen, B, Tq, 576), _normal(gen, B, Tq, H, 576), _normal(gen, B, Tq, H, 512)
+    rows, qs, kl = dsa.Rows(base), _i32([0] * B), _i32([Tq] * B)
+    need = dsa.workspace_bytes(dsa.OP_MLA_WINDOW_BWD, B, Tq, Tq, H, window + first)
+    ws = dsa.new_workspace(need)
+    o, lse = dsa.mla_window_fwd(q, rows, qs, kl, window, first, Tq)
+    dq, dkv = dsa.mla_window_bwd(q, rows, qs, kl, window, first, Tq, o, lse, d_o, workspace=ws)
+    _ok(dsa, ws)
+    t = torch.arange(Tq, device="cuda")
+    see = ref.window_sees(t[:, None], t, window, first)
+    for b in (0, B - 1):
+        r_dkv = off = 0
+        for h in range(H):                           # a head at a time: 64-bit scores of 4224 x 4224
+            g, k, g_off, k_off = ref.backward(q[b, :, h:h + 1], base[b], see, o[b, :, h:h + 1],
+                                              lse[b, :, h:h + 1], d_o[b, :, h:h + 1])
+            ref.within(dq[b, :, h:h + 1], g, g_off, f"dq of {b}, head {h}")
+            r_dkv, off = r_dkv + k, off + k_off
+        # a head's bound counts Tq additions, a sum over all heads H times as many: their share
+        # 2 Tq ADD of a bound that is at least (HALF + 2 Tq ADD) of the same magnitudes
+        share = 2 * Tq * ref.ADD / (ref.HALF + 2 * Tq * ref.ADD)
+        ref.within(dkv[b], r_dkv, off * (1 + (H - 1) * share), f"dkv of {b}")
+
+
 # ---------------------------------------------------------------------------
 # both: equal bits, graphs, streams
 # ---------------------------------------------------------------------------
@@ -488,6 +557,142 @@ def test_streams_and_graphs(dsa):
     assert torch.equal(o, want[1][0]) and torch.equal(lse, want[1][1])
     for ws in work:
         _ok(dsa, ws)
+
+
+def test_window_step_in_a_graph(dsa):
+    """Forward and backward captured together and replayed on other inputs, beside an eager call
+    of the same operators with a workspace of its own."""
+    gen = _gen(34)
+    B, Tq, H, S, window, first = 2, 60, 96, 60, 30, 2
+    qs, kl = _i32([0, 0]), _i32([S, S])
+    need = max(dsa.workspace_bytes(op, B, Tq, S, H, window + first)
+               for op in (dsa.OP_MLA_WINDOW, dsa.OP_MLA_WINDOW_BWD))
+    sets = [[_normal(gen, B, S, 576), _normal(gen, B, Tq, H, 576), _normal(gen, B, Tq, H, 512)]
+            for _ in range(2)]
+
+    def step(base, q, d_o, ws, o=None, lse=None, dq=None, dkv=None):
+        rows = dsa.Rows(base)
+        o, lse = dsa.mla_window_fwd(q, rows, qs, kl, window, first, S, o_lat=o, lse=lse, workspace=ws)
+        return (o, lse, *dsa.mla_window_bwd(q, rows, qs, kl, window, first, S, o, lse, d_o, dq=dq,
+                                            dkv=dkv, workspace=ws))
+
+    work = [dsa.new_workspace(need) for _ in range(2)]
+    want = [step(*x, work[0]) for x in sets]
+    held = [x.clone() for x in sets[0]]
+    out = [torch.empty_like(x) for x in want[0]]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*held, work[0], *out)
+    for k in (1, 0, 1):
+        for x, y in zip(held, sets[k]):
+            x.copy_(y)
+        graph.replay()
+        eager = step(*sets[1 - k], work[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want[k]))
+        assert all(torch.equal(x, y) for x, y in zip(eager, want[1 - k]))
+    for ws in work:
+        _ok(dsa, ws)
+
+
+def test_calls_in_a_row_share_a_workspace(dsa):
+    """Different operators and sizes one after another on one stream, nothing between them: the
+    launches overlap, their results and the bytes behind the workspace do not change."""
+    gen = _gen(35)
+    S, H = 1500, 96
+    base = _normal(gen, 3, S, 576)
+    rows = dsa.Rows(base)
+    calls = []
+    for B, T, kind in ((3, 1, "tree"), (1, 40, "window"), (2, 8, "tree"), (3, 300, "window"),
+                       (1, 130, "bwd"), (2, 1, "window")):
+        q = _normal(gen, B, T, H, 576)
+        if kind == "tree":
+            masks, kl = _masks(35, B, T, "tree"), _i32([S - T] * B)
+            need = dsa.workspace_bytes(dsa.OP_MLA_TREE, B, T, S, H, 0)
+            calls.append((need, lambda ws, q=q, m=masks, kl=kl: dsa.mla_tree_fwd(q, rows, m, kl, S, workspace=ws)))
+        else:
+            qs, kl = _i32([S - T] * B), _i32([S] * B)
+            if kind == "window":
+                need = dsa.workspace_bytes(dsa.OP_MLA_WINDOW, B, T, S, H, 204)
+                calls.append((need, lambda ws, q=q, qs=qs, kl=kl: dsa.mla_window_fwd(
+                    q, rows, qs, kl, 200, 4, S, workspace=ws)))
+            else:
+                o, lse = dsa.mla_window_fwd(q, rows, qs, kl, 200, 4, S)
+                d_o = _normal(gen, B, T, H, 512)
+                need = dsa.workspace_bytes(dsa.OP_MLA_WINDOW_BWD, B, T, S, H, 204)
+                calls.append((need, lambda ws, q=q, qs=qs, kl=kl, o=o, lse=lse, d_o=d_o: dsa.mla_window_bwd(
+                    q, rows, qs, kl, 200, 4, S, o, lse, d_o, workspace=ws)))
+    want = []
+    for need, call in calls:
+        guard = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+        ws = guard[:need]
+        ws[:256] = 0
+        want.append(call(ws))
+        _ok(dsa, ws)
+        assert (guard[need:] == 171).all()
+    ws = dsa.new_workspace(max(need for need, _ in calls))
+    for _ in range(3):
+        got = [call(ws) for _, call in calls]
+    torch.cuda.synchronize()
+    _ok(dsa, ws)
+    for x, y in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(x, y))
+
+
+def test_rows_with_a_stride_of_their_own(dsa):
+    """Sequences packed more tightly than their store's rows: kv as one run of rows."""
+    gen = _gen(36)
+    flat = _normal(gen, 1, 250, 576)
+    q = _normal(gen, 2, 20, 8, 576)
+    rows = dsa.Rows(flat, seq_stride=130)                 # sequences at rows 0 and 130, of 120
+    qs, kl = _i32([100, 100]), _i32([120, 120])
+    o, lse = dsa.mla_window_fwd(q, rows, qs, kl, 50, 2, 120)
+    t = torch.arange(100, 120, device="cuda")
+    see = ref.window_sees(t[:, None], torch.arange(120, device="cuda"), 50, 2)
+    for b in range(2):
+        r_o, r_lse, o_off, lse_off = ref.forward(q[b], flat[0, 130 * b:130 * b + 120], see)
+        ref.within(o[b], r_o, o_off, "o_lat")
+        ref.within(lse[b], r_lse, lse_off, "lse")
+
+
+def test_beyond_32_bit_offsets(dsa):
+    """Queries, outputs and a paged cache of more than 2^31 elements each."""
+    gen = _gen(37)
+    B, T, H, pages = 2, 21000, 96, 60000
+    pool = torch.zeros((pages, 64, 576), dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(pages - 2 * 329, pages, device="cuda", dtype=torch.int32).view(2, 329).contiguous()
+    pool[table.flatten().long()] = _normal(gen, 2 * 329, 64, 576)
+    q = torch.empty((B, T, H, 576), dtype=torch.bfloat16, device="cuda")
+    for b in range(B):
+        q[b] = _normal(gen, T, H, 576)
+    assert q.numel() > 2 ** 31 and pool.numel() > 2 ** 31
+    rows = dsa.Rows(pool, table)
+    o, lse = dsa.mla_window_fwd(q, rows, _i32([0, 0]), _i32([T, T]), 70, 2, T)
+    cache = ref.logical(pool, table, 1, T)
+    at = torch.arange(T - 40, T, device="cuda")
+    near = torch.cat([torch.arange(2, device="cuda"), torch.arange(T - 200, T, device="cuda")])
+    see = ref.window_sees(at[:, None], near, 70, 2)
+    r_o, r_lse, o_off, lse_off = ref.forward(q[1, -40:], cache[near], see)
+    ref.within(o[1, -40:], r_o, o_off, "o_lat")
+    ref.within(lse[1, -40:], r_lse, lse_off, "lse")
+    masks = torch.ones((B, 1), dtype=torch.int64, device="cuda")
+    o, lse = dsa.mla_tree_fwd(q[:, -1:].contiguous(), rows, masks, _i32([T - 1, 2000]), T)
+    see = torch.ones((1, T), dtype=torch.bool, device="cuda")
+    r_o, r_lse, o_off, lse_off = ref.forward(q[0, -1:], ref.logical(pool, table, 0, T), see)
+    ref.within(o[0], r_o, o_off, "o_lat")
+    del o, lse
+    d_o = torch.zeros((B, T, H, 512), dtype=torch.bfloat16, device="cuda")
+    d_o[1, -40:] = _normal(gen, 40, H, 512)
+    base = torch.stack([ref.logical(pool, table, b, T).to(torch.bfloat16) for b in range(B)])
+    qs, kl = _i32([0, 0]), _i32([T, T])
+    o, lse = dsa.mla_window_fwd(q, dsa.Rows(base), qs, kl, 70, 2, T)
+    dq, dkv = dsa.mla_window_bwd(q, dsa.Rows(base), qs, kl, 70, 2, T, o, lse, d_o)
+    see = ref.window_sees(at[:, None], near, 70, 2)
+    r_dq, r_dkv, dq_off, dkv_off = ref.backward(q[1, -40:], cache[near], see, o[1, -40:], lse[1, -40:],
+                                                d_o[1, -40:])
+    ref.within(dq[1, -40:], r_dq, dq_off, "dq")
+    ref.within(dkv[1][near], r_dkv, dkv_off, "dkv")
 
 
 # ---------------------------------------------------------------------------
