@@ -86,8 +86,9 @@ struct Params {
 
   // first row (128 bytes each) of a block in the workspace's tensor map; which: P and
   // dZ, then their second parts
+  template <int PARTS>
   __device__ __forceinline__ int64_t block_row(int b, int rt, int k, int which) const {
-    return X + (((static_cast<int64_t>(b) * q.RC + rt - rt0) * q.np + k) * 2 * q.parts + which) * X;
+    return X + (((static_cast<int64_t>(b) * q.RC + rt - rt0) * q.np + k) * 2 * PARTS + which) * X;
   }
 };
 
@@ -349,15 +350,15 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         // the lane pair's two keys in the two blocks: row r at 128 r, 16-byte units xor r
-        uint8_t* dst = p.pz + 128 * p.block_row(t.b, t.rt, k, 0) + (key & 6) * 2;
+        uint8_t* dst = p.pz + 128 * p.block_row<TWO ? 2 : 1>(t.b, t.rt, k, 0) + (key & 6) * 2;
 #pragma unroll 1
-        for (int q = 0; q < 64; q += 32) {
-          uint32_t z[32], dp[32];
-          tmem_ld32(taddr + bu * 256 + q, z);
-          tmem_ld32(taddr + bu * 256 + 128 + q, dp);
+        for (int q = 0; q < 64; q += 16) {
+          uint32_t z[16], dp[16];
+          tmem_ld16(taddr + bu * 256 + q, z);
+          tmem_ld16(taddr + bu * 256 + 128 + q, dp);
           tmem_ld_wait_regs(z);
           tmem_ld_wait_regs(dp);
-          if (q == 32) {
+          if (q == 48) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -367,13 +368,13 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
           }
           if (k < t.np) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 16; ++e) {
               const int r = r0 + q + e;
-              const float4 w = rows[r];
+              const float2 w = *reinterpret_cast<const float2*>(&rows[r]);
               float pr = ex2(fmaf(__uint_as_float(z[e]), p.scale_log2, -w.x));
               float dz = p.scale * pr * (__uint_as_float(dp[e]) - w.y);
               if (!all) {
-                const int tt = __float_as_int(w.z);
+                const int tt = __float_as_int(rows[r].z);
                 const bool sees = kp <= tt && (tt - kp < p.m.window || kp < p.m.n_first);
                 pr = sees ? pr : 0.f;
                 dz = sees ? dz : 0.f;
@@ -478,7 +479,8 @@ struct Task {
   }
 };
 
-template <bool DKV>
+// PARTS: of P and dZ.
+template <bool DKV, int PARTS>
 __global__ void __launch_bounds__(Prod::THREADS, 1)
     product_kernel(const __grid_constant__ CUtensorMap tm_pz, const __grid_constant__ CUtensorMap tm_kv,
                    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
           if (!t.sees(l)) continue;
           const int c0 = place(l, 4 * t.kt + 2 * rank), c1 = place(l, 4 * t.kt + 2 * rank + 1);
 #pragma unroll 1
-          for (int st = 0; st < 4 * p.q.parts && ok; ++st) {   // dZ and q or P and d_o, 64 rows, a part
+          for (int st = 0; st < 4 * PARTS && ok; ++st) {   // dZ and q or P and d_o, 64 rows, a part
             const int dz = 1 - (st & 1), which = dz + 2 * (st >> 2), y = 64 * (st >> 1 & 1);
             if (!acquire()) break;
             if (elect_one_lane()) {
@@ -556,9 +558,9 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
               const bool rot = t.upper && dz;
               mbar_expect_tx_cluster(bar, (rot ? 5 : 4) * CHUNK);
               tma_load_2d_pair(a, &tm_pz, bar, 0,
-                               c0 < 0 ? 0 : static_cast<int>(p.block_row(t.b, x, c0, which)) + y);
+                               c0 < 0 ? 0 : static_cast<int>(p.block_row<PARTS>(t.b, x, c0, which)) + y);
               tma_load_2d_pair(a + CHUNK, &tm_pz, bar, 0,
-                               c1 < 0 ? 0 : static_cast<int>(p.block_row(t.b, x, c1, which)) + y);
+                               c1 < 0 ? 0 : static_cast<int>(p.block_row<PARTS>(t.b, x, c1, which)) + y);
               const CUtensorMap* tm = dz ? &tm_q : &tm_do;
               tma_load_3d_pair(w, tm, bar, col, x * X + y, t.b);
               tma_load_3d_pair(w + CHUNK, tm, bar, col + 64, x * X + y, t.b);
@@ -569,8 +571,8 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
         }
       } else {
         const Pages l = tile_pages(p, t.s, t.x0 + rank);
-        for (int k = 0; k < t.list.count() * p.q.parts && ok; ++k) {
-          const int pg = t.list.page(k / p.q.parts), part = k % p.q.parts, c = place(l, pg), row = static_cast<int>(page_row(p.kv, t.b, pg));
+        for (int k = 0; k < t.list.count() * PARTS && ok; ++k) {
+          const int pg = t.list.page(k / PARTS), part = k % PARTS, c = place(l, pg), row = static_cast<int>(page_row(p.kv, t.b, pg));
           const uint64_t any = range_bits(0, t.s.L, pg * 64);
           if (!acquire()) break;
           uint8_t* a = sm + r.slot * C::STAGE;
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
             } else {
               mbar_expect_tx_cluster_release(bar, 2 * CHUNK);
             }
-            const int br = c < 0 ? 0 : static_cast<int>(p.block_row(t.b, t.x0 + rank, c, 1 + 2 * part));
+            const int br = c < 0 ? 0 : static_cast<int>(p.block_row<PARTS>(t.b, t.x0 + rank, c, 1 + 2 * part));
             tma_load_2d_pair(a, &tm_pz, bar, 0, br);
             tma_load_2d_pair(a + CHUNK, &tm_pz, bar, 0, br + 64);
             if (any == ~0ull) {
@@ -657,10 +659,10 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       if constexpr (DKV) {
         for (int x = t.x0; x < t.x1 && ok; ++x) {
           if (!t.sees(tile_pages(p, t.s, x))) continue;
-          for (int st = 0; st < 4 * p.q.parts && ok; ++st) multiply(d, t.upper && !(st & 1));
+          for (int st = 0; st < 4 * PARTS && ok; ++st) multiply(d, t.upper && !(st & 1));
         }
       } else {
-        for (int k = 0; k < t.list.count() * p.q.parts && ok; ++k) multiply(d, t.upper);
+        for (int k = 0; k < t.list.count() * PARTS && ok; ++k) multiply(d, t.upper);
       }
       if (elect_one_lane()) umma_commit_pair(done);
       __syncwarp();
@@ -887,10 +889,10 @@ dsa_status_t window_bwd_launch(const WindowBwdArgs& a, cudaStream_t stream) {
     dsa_status_t st = launch_pairs("pz_kernel", q.parts == 2 ? pz_kernel<true> : pz_kernel<false>, some, Pz::THREADS, Pz::SMEM, stream, tq_tile,
                                    td_tile, tk, p);
     if (st == DSA_OK)
-      st = launch_pairs("product_kernel", product_kernel<false>, some, Prod::THREADS, Prod::SMEM, stream,
+      st = launch_pairs("product_kernel", q.parts == 2 ? product_kernel<false, 2> : product_kernel<false, 1>, some, Prod::THREADS, Prod::SMEM, stream,
                         tp, tk, tq, td, p, static_cast<int>(tiles));
     if (st == DSA_OK)
-      st = launch_pairs("product_kernel", product_kernel<true>, sums, Prod::THREADS,
+      st = launch_pairs("product_kernel", q.parts == 2 ? product_kernel<true, 2> : product_kernel<true, 1>, sums, Prod::THREADS,
                         Prod::SMEM, stream, tp, tk, tq, td, p, static_cast<int>(sums));
     if (st != DSA_OK) return st;
     launch_overlapped(reduce_kernel, static_cast<unsigned>(static_cast<int64_t>(f.B) * f.max_kv_len), 144, 0,
