@@ -25,10 +25,14 @@
 // of the two pages) a thread: its scores, P = 2^(z - m) to BF16 in shared memory; 8..11
 // write O^T / l out while the next unit's first products run.
 // m is the maximum of the first block in which the row sees anything, so O^T is
-// never rescaled; a row whose later scores exceed it by 2^80 sends its unit to
-// attend_row.  So does a row of the sequence that holds an infinity or a NaN and that
-// some query of the unit does not see (0 * NaN would reach it).  Rows behind the
-// sequence, in its last page, are zeroed in V before use.
+// never rescaled.  A row whose later scores exceed it by 2^80 leaves the maximum that it
+// met where its output goes, and its unit is done a second time with that, after all
+// others of the pair (512 queries, 96 heads, window 1024: 0.14 ms, every unit twice 0.24;
+// row by row it was 34).  The second time stands behind the kernel's end, in a function of
+// its own: units put back into the line cost every call 1.1 us at that end.  A unit some of
+// whose queries do not see a row of the sequence that holds an infinity or a NaN (0 * NaN
+// would reach them) goes to attend_row (33 ms there); the waits of the others last as long
+// as it moves on.  Rows behind the sequence, in its last page, are zeroed in V before use.
 //
 // Persistent: the blocks of all units stand in one line, and every pair of SMs takes
 // an equal stretch of it (whole units where there are many).  A unit that is cut has
@@ -45,6 +49,7 @@ namespace dsa {
 namespace dense {
 
 constexpr int THREADS = 384;
+constexpr int REDO = 1024;                // units of a pair that may be done twice; more: attend_row
 constexpr float FAR = 80.f;               // exponents that P may reach: 2^80 times 2^47 is FP32's range
 
 template <int R_>
@@ -59,7 +64,7 @@ struct Cfg {
   static constexpr int OFF_K = OFF_P + 2 * QCH;
   static constexpr int OFF_V = OFF_K + NK * CHUNK;
   static constexpr int OFF_MISC = OFF_V + NV * 2 * CHUNK;
-  static constexpr int MISC = 1024 + 16 * R + (HALVES == 2 ? 2048 : 0);
+  static constexpr int MISC = 1024 + 16 * R + (HALVES == 2 ? 2048 : 0) + 5 * REDO / 8;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   static constexpr uint32_t S_COL = 4 * R;
   static constexpr int SW = 128 / HALVES;             // columns of a score buffer
@@ -72,7 +77,7 @@ struct Cfg {
 enum : uint32_t {
   SITE_Q = 0x710, SITE_KF = 0x711, SITE_KE = 0x712, SITE_VF = 0x713, SITE_VE = 0x714,
   SITE_SF = 0x715, SITE_SE = 0x716, SITE_P = 0x717, SITE_O = 0x718, SITE_VT = 0x719,
-  SITE_DRAIN = 0x71a, SITE_OE = 0x71b, SITE_L = 0x71c, SITE_U = 0x71d
+  SITE_OE = 0x71b, SITE_L = 0x71c, SITE_U = 0x71d
 };
 
 // A pair's stretch of the line, as combine_kernel needs it: the unit and the block
@@ -172,6 +177,7 @@ struct Unit {
   Pages pages;
   int k0, k1, nb;
   int j0, j1, of;                 // blocks j0 .. j1-1 of `of`
+  int no;                         // which of its pair's
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == of; }
 };
 
@@ -318,78 +324,105 @@ __device__ __forceinline__ bool all_see(const Mask& m, const Unit& u, int kb) {
   return kb + 63 <= t0 && t1 < u.s.L && (kb > t1 - m.window || kb + 63 < m.n_first);
 }
 
+// What a CTA keeps in shared memory beside its operands.
 template <int R>
-__global__ void __launch_bounds__(THREADS, 1)
-    pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
-                const Params p) {
+struct Shared {
   using C = Cfg<R>;
-  constexpr uint32_t IDESC_S = idesc_bf16(256 / C::HALVES, 128, false, false);
-  constexpr uint32_t IDESC_O = idesc_bf16(256, 2 * R, true, false);
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = smem_align1024(smem_raw);
-  uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);   // even CTA
-  uint64_t* kempty = kfull + C::NK;
-  uint64_t* vfull = kempty + C::NK;                                  // even CTA
-  uint64_t* vempty = vfull + C::NV;
-  uint64_t* sfull = vempty + C::NV;                                  // [NB]
-  uint64_t* sfree = sfull + 2;                                       // [NB] even CTA
-  uint64_t* pready = sfull + 4;                                      // odd CTA: for its warp 3
-  uint64_t* odone = sfull + 5;                                       // a block's values added
-  uint64_t* ofull = sfull + 6;                                       // a unit's
-  uint64_t* ofree = sfull + 7;                                       // [2] even CTA: 2R columns read
-  uint64_t* lfull = sfull + 9;                                       // [2] a unit's sums, of this CTA's rows
-  uint64_t* lpeer = sfull + 11;                                      // [2] of the other's
-  uint64_t* lfree = sfull + 13;                                      // [2]
-  uint64_t* vland = sfull + 15;                                      // [2] this CTA's own copies
-  uint64_t* drain = sfull + 17;
-  uint64_t* ufull = sfull + 18;                                      // [UNITS]
-  uint64_t* uempty = ufull + UNITS;                                  // [UNITS]
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(uempty + UNITS);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
-  int* s_slow = reinterpret_cast<int*>(tslot + 2);                   // [2]
-  Unit* s_unit = reinterpret_cast<Unit*>(sm + C::OFF_MISC + 512);    // [UNITS]
-  float* s_inv = reinterpret_cast<float*>(sm + C::OFF_MISC + 1024);  // [2][2R]
-  static_assert((2 * C::NK + 2 * C::NV + 18 + 2 * UNITS) * 8 + 16 <= 512, "misc");
-  float* s_top = s_inv + 4 * R;                                      // HALVES = 2: [2][2][64] maxima
-  float* s_sum = s_top + 256;                                        // [2][2][64] sums
+  static constexpr int BARS = 2 * C::NK + 2 * C::NV + 19 + 2 * UNITS;
+  uint64_t *kfull, *kempty;      // kfull, vfull, sfree, ofree: the even CTA's
+  uint64_t *vfull, *vempty;
+  uint64_t *sfull, *sfree;       // [NB]
+  uint64_t *pready;              // odd CTA: for its warp 3
+  uint64_t *odone, *ofull;       // a block's values added; a unit's
+  uint64_t *ofree;               // [2] 2R columns read
+  uint64_t *lfull, *lpeer;       // [2] a unit's sums, of this CTA's rows, of the other's
+  uint64_t *lfree;               // [2]
+  uint64_t *vland;               // [2] this CTA's own copies
+  uint64_t *drain;               // [2]
+  uint64_t *ufull, *uempty;      // [UNITS]
+  uint32_t* tslot;
+  volatile int* s_abort;         // [2] the second moves while attend_row goes on
+  int* s_slow;                   // [2] x a row is far, an attend_row is needed
+  volatile int *s_any, *s_go;    // units are to be done again; the other CTA says so too
+  Unit* s_unit;                  // [UNITS]
+  float* s_inv;                  // [2][2R]
+  float *s_top, *s_sum;          // HALVES = 2: [2][2][64] maxima, sums
+  uint32_t* s_redo;              // a bit a unit
+  uint32_t* s_noted;             // [4 warps] the warp's rows have left their maxima
+  static_assert(BARS * 8 + 36 <= 512, "misc");
   static_assert(UNITS * sizeof(Unit) <= 512, "misc");
 
-  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
-
-  if (tid == 0) {
+  __device__ __forceinline__ explicit Shared(uint8_t* sm) {
+    kfull = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);
+    kempty = kfull + C::NK;
+    vfull = kempty + C::NK;
+    vempty = vfull + C::NV;
+    sfull = vempty + C::NV;
+    sfree = sfull + 2;
+    pready = sfull + 4;
+    odone = sfull + 5;
+    ofull = sfull + 6;
+    ofree = sfull + 7;
+    lfull = sfull + 9;
+    lpeer = sfull + 11;
+    lfree = sfull + 13;
+    vland = sfull + 15;
+    drain = sfull + 17;
+    ufull = sfull + 19;
+    uempty = ufull + UNITS;
+    tslot = reinterpret_cast<uint32_t*>(uempty + UNITS);
+    s_abort = reinterpret_cast<volatile int*>(tslot + 1);
+    s_slow = reinterpret_cast<int*>(tslot + 3);
+    s_any = reinterpret_cast<volatile int*>(tslot + 7);
+    s_go = s_any + 1;
+    s_unit = reinterpret_cast<Unit*>(sm + C::OFF_MISC + 512);
+    s_inv = reinterpret_cast<float*>(sm + C::OFF_MISC + 1024);
+    s_top = s_inv + 4 * R;
+    s_sum = s_top + 256;
+    s_redo = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC + C::MISC - 5 * REDO / 8);
+    s_noted = s_redo + REDO / 32;
+  }
+  __device__ __forceinline__ void barriers(int rank) const {
     for (int k = 0; k < C::NK; ++k) mbar_init(&kfull[k], 1), mbar_init(&kempty[k], 1);
     for (int k = 0; k < C::NV; ++k) mbar_init(&vfull[k], 2), mbar_init(&vempty[k], 1);
-    for (int k = 0; k < C::NB; ++k) mbar_init(&sfull[k], 1), mbar_init(&sfree[k], 8);
     mbar_init(pready, rank == 0 ? 5 : 4);
     mbar_init(odone, 1);
     mbar_init(ofull, 1);
     for (int k = 0; k < 2; ++k) {
+      mbar_init(&sfull[k], 1);
+      mbar_init(&sfree[k], 8);
       mbar_init(&ofree[k], 8);
       mbar_init(&lfull[k], 4);
       mbar_init(&lpeer[k], 1);
       mbar_init(&lfree[k], 8);
       mbar_init(&vland[k], 1);
+      mbar_init(&drain[k], 1);
     }
     for (int k = 0; k < UNITS; ++k) mbar_init(&ufull[k], 1), mbar_init(&uempty[k], rank == 0 ? 11 : 10);
-    mbar_init(drain, 2);
-    s_abort[0] = 0;
-    s_slow[0] = s_slow[1] = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_kv);
   }
-  if (warp == 2) {
-    tmem_alloc_pair(tslot, 512);
-    tmem_relinquish_pair();
-  }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
-  pdl_wait();
-  pdl_start_next();
+};
+
+// What the warps do from the first unit to the last.  AGAIN: only the units that have to
+// be done a second time.
+template <int R, bool AGAIN>
+__device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const Params& p,
+                                      uint8_t* sm, uint32_t tmem) {
+  using C = Cfg<R>;
+  constexpr uint32_t IDESC_S = idesc_bf16(256 / C::HALVES, 128, false, false);
+  constexpr uint32_t IDESC_O = idesc_bf16(256, 2 * R, true, false);
+  const auto [kfull, kempty, vfull, vempty, sfull, sfree, pready, odone, ofull, ofree, lfull, lpeer, lfree,
+              vland, drain, ufull, uempty, tslot, s_abort, s_slow, s_any, s_go, s_unit, s_inv, s_top, s_sum,
+              s_redo, s_noted] = Shared<R>(sm);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
+  // An issuer that gives up: its MMAs are complete before the pair leaves.  (Otherwise those
+  // who waited for what they gave have seen that.)
+  auto give_up = [&](uint64_t* bar) {
+    if (elect_one_lane()) umma_commit_pair(bar);
+    __syncwarp();
+    settle(bar, 0);
+  };
   Feed feed{s_unit, ufull, uempty, s_abort, p.status};
 
   if (warp < 4) {
@@ -402,8 +435,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       Stretch mine{-1, 0, -1, 0};
       int used = 0;
       bool ok = true;
-      for (int at = 0;; ++at) {
-        const bool more = line.next(u);
+      for (int at = 0, no = 0;; ++at) {
+        bool more = line.next(u);
+        if (AGAIN)
+          for (; more && !(no < REDO && s_redo[no >> 5] >> (no & 31) & 1); ++no) more = line.next(u);
+        u.no = no++;
         if (!more) u.b = -1;
         if (at >= UNITS) ok = wait(&uempty[at % UNITS], (at / UNITS - 1) & 1, s_abort, p.status, SITE_U);
         if (!ok) break;
@@ -445,13 +481,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (!ok) break;
       }
-      if (rank == 0 && lane == 0 && p.cut) p.stretch[pair] = mine;
+      if (!AGAIN && rank == 0 && lane == 0 && p.cut) p.stretch[pair] = mine;
       // the pair's copies have landed and the last arrivals of the MMAs have come
       // before either CTA leaves
       for (; used > 0; --used) {
         if (--r.slot < 0) r.slot = C::NK - 1, r.ph ^= 1;
-        if (rank == 0) wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
-        if (ok) wait(&kempty[r.slot], r.ph, s_abort, p.status, SITE_KE);
+        if (rank == 0) settle(&kfull[r.slot], r.ph);
+        if (ok) settle(&kempty[r.slot], r.ph);
       }
     } else if (warp == 1) {
       // ---- V: the own 256 dims of both pages, 128 at a time ----
@@ -512,8 +548,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       for (; used > 0; --used) {
         if (--r.slot < 0) r.slot = C::NV - 1, r.ph ^= 1;
-        if (rank == 0) wait(&vfull[r.slot], r.ph, s_abort, p.status, SITE_VF);
-        if (ok) wait(&vempty[r.slot], r.ph, s_abort, p.status, SITE_VE);
+        if (rank == 0) settle(&vfull[r.slot], r.ph);
+        if (ok) settle(&vempty[r.slot], r.ph);
       }
     } else if (warp == 2) {
       if (rank == 0) {
@@ -547,9 +583,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
         }
-        if (elect_one_lane()) umma_commit_pair(drain);
-        __syncwarp();
-      } else {
+        if (!ok) give_up(&drain[0]);
+      } else if (!AGAIN) {
         // every sequence, whether it has a unit or not
         for (int b = pair * 32 + lane; b < p.B; b += p.pairs * 32) report_seq(p.m, seq_of(p.m, b), b, p.status);
       }
@@ -588,10 +623,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         ++n;
       }
-      if (elect_one_lane()) umma_commit_pair(drain);
-      __syncwarp();
-      // every MMA of the pair is complete before anything is given up
-      wait(drain, 0, s_abort, p.status, SITE_DRAIN);
+      if (!ok) give_up(&drain[1]);
     } else {
       // ---- tells the even CTA that this one's P is written: a release at cluster scope
       // takes 0.5 us, in the softmax warps it set the pace of the pair ----
@@ -633,8 +665,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int i = live ? g / p.H : 0;
       const uint64_t bits =
           live && p.m.tree != nullptr ? p.m.tree[static_cast<int64_t>(u.b) * p.m.T + i] : 0;
-      float l_sum = 0.f, m_ref = -INFINITY;
-      bool slow = false, good[PG];                       // the block's pages are there: looked up a block ahead
+      // where the row leaves its maximum (HALVES = 2: its two threads theirs)
+      auto note = [&] {
+        return u.whole() ? reinterpret_cast<float*>(p.o + (static_cast<int64_t>(u.b) * p.m.T * p.H + g) * kVlat)
+                         : p.part_o + (static_cast<int64_t>(2 * pair + (u.no > 0)) * 2 * R + rank * R + r) * kVlat;
+      };
+      float l_sum = 0.f, m_ref = -INFINITY, peak = 0.f;  // peak: of z - m; infinite: for attend_row
+      if (AGAIN && live)
+#pragma unroll
+        for (int h = 0; h < C::HALVES; ++h)
+          if (s_noted[((C::HALVES == 2 ? sub & 1 : sub) + 2 * h) * (REDO / 32) + (u.no >> 5)] >> (u.no & 31) & 1)
+            m_ref = fmaxf(m_ref, note()[h]);
+      bool good[PG];                       // the block's pages are there: looked up a block ahead
       auto look = [&](int j) {
 #pragma unroll
         for (int h = 0; h < PG; ++h) {
@@ -690,7 +732,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (others >> e & 1) hidden = fmaf(__uint_as_float(z[c][e]), 0.f, hidden);
               if (!(sees >> e & 1)) z[c][e] = 0xff800000u;
             }
-            if (hidden != 0.f) slow = true;              // a NaN: somebody else's row holds one
+            if (hidden != 0.f) peak = INFINITY;          // a NaN: somebody else's row holds one
           }
         }
         // the row's reference, once it sees something (both of its threads know m_ref and
@@ -705,19 +747,18 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (m_ref == -INFINITY) m_ref = top * p.scale_log2;
         }
         const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-        float sums[4] = {0.f, 0.f, 0.f, 0.f}, most = -INFINITY;
+        float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float a0 = fmaf(__uint_as_float(z[c][e]), p.scale_log2, neg);
             const float a1 = fmaf(__uint_as_float(z[c][e + 1]), p.scale_log2, neg);
-            most = fmaxf(most, fmaxf(a0, a1));
+            peak = fmaxf(peak, fmaxf(a0, a1));
             const float p0 = ex2(a0), p1 = ex2(a1);
             sums[(e >> 1) & 3] += p0 + p1;
             z[c][e >> 1] = pack_bf16x2(p0, p1);
           }
-        if (most > FAR) slow = true;
         l_sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
         // P is free once the block before has been multiplied
         if (blk > 0) ok = wait(odone, (blk - 1) & 1, s_abort, p.status, SITE_O);
@@ -746,7 +787,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (live && half == 0) {
         const float lse2 = l_sum == 0.f ? -INFINITY : m_ref + log2f(l_sum);
         if (!u.whole())
-          p.part_lse[(2 * pair + (at > 0)) * 2 * R + rank * R + r] = lse2;
+          p.part_lse[(2 * pair + (u.no > 0)) * 2 * R + rank * R + r] = lse2;
         else if (p.lse != nullptr)
           p.lse[static_cast<int64_t>(u.b) * p.m.T * p.H + g] = lse2 * 0.6931471805599453f;
       }
@@ -756,12 +797,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         *to = inv;
         st_cluster_u32(smem_u32(to), rank ^ 1, __float_as_uint(inv));
       }
-      if (__any_sync(0xffffffffu, slow && live) && lane == 0) {
-        s_slow[bu] = 1;
-        st_cluster_u32(smem_u32(&s_slow[bu]), rank ^ 1, 1);
+      if (__any_sync(0xffffffffu, live && peak > FAR)) {
+        if (live) note()[half] = m_ref + peak;
+        const bool bad = __any_sync(0xffffffffu, live && peak == INFINITY);
+        if (lane == 0) {
+          if (u.no < REDO) s_noted[sub * (REDO / 32) + (u.no >> 5)] |= 1u << (u.no & 31);
+          for (int k = 0; k <= bad; ++k) {
+            s_slow[2 * bu + k] = 1;
+            st_cluster_u32(smem_u32(&s_slow[2 * bu + k]), rank ^ 1, 1);
+          }
+        }
       }
       mbar_arrive_warp(&lfull[bu]);
     }
+    if (blk > 0) settle(odone, (blk - 1) & 1);           // (not waited for above)
   } else {
     // ---- out: lane = dim 256 rank + 128 m + 32 sub + lane, a row a column ----
     const int sub = warp & 3;
@@ -773,7 +822,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int at = feed.at;
       const int bu = at & 1, here = min(2 * R, u.rows - u.g0);   // rows that are there
       const int64_t first = static_cast<int64_t>(u.b) * p.m.T * p.H + u.g0;
-      const int64_t part = static_cast<int64_t>(2 * pair + (at > 0)) * 2 * R;
+      const int64_t part = static_cast<int64_t>(2 * pair + (u.no > 0)) * 2 * R;
       const bool parts = !u.whole();
       const float* inv = s_inv + bu * 2 * R;
       // this CTA's sums have gone to both; its first warp says so to the other
@@ -784,7 +833,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (ok && u.nb > 0) ok = wait(ofull, n & 1, s_abort, p.status, SITE_O);
       if (!ok) break;
       tc_fence_after();
-      const bool slow = reinterpret_cast<volatile int*>(s_slow)[bu] != 0;
+      const bool slow = reinterpret_cast<volatile int*>(s_slow)[2 * bu] != 0;
 #pragma unroll 1
       for (int m = 0; m < 2; ++m) {
         const int dim = 256 * rank + 128 * m + 32 * sub + lane;
@@ -830,11 +879,22 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (u.nb > 0) ++n;
       if (slow) {
-        for (int r = rank * R + sub; r < min(here, rank * R + R); r += 4)
+        // (both CTAs come to the same)
+        const bool again = !AGAIN && u.no < REDO && reinterpret_cast<volatile int*>(s_slow)[2 * bu + 1] == 0;
+        for (int r = rank * R + sub; !again && r < min(here, rank * R + R); r += 4) {
           attend_row(p, u.s, u.pages, u.k0, u.k1, u.b, u.g0 + r, parts ? p.part_o + (part + r) * kVlat : nullptr,
                      parts ? p.part_lse + part + r : nullptr);
-        named_bar_sync(1, 128);                          // all of them have read the flag
-        if (sub == 0 && lane == 0) s_slow[bu] = 0;
+          if (lane == 0) {                               // whoever waits, here or there, waits on
+            const uint32_t beat = static_cast<uint32_t>(globaltimer_ns());
+            s_abort[1] = static_cast<int>(beat);
+            st_cluster_u32(smem_u32(const_cast<int*>(s_abort + 1)), rank ^ 1, beat);
+          }
+        }
+        named_bar_sync(1, 128);                          // all of them have read the flags
+        if (sub == 0 && lane == 0) {
+          s_slow[2 * bu] = s_slow[2 * bu + 1] = 0;
+          if (again) s_redo[u.no >> 5] |= 1u << (u.no & 31), s_any[0] = 1;
+        }
         __syncwarp();
       }
       if (lane == 0) {                                   // the sums may be overwritten
@@ -845,11 +905,72 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   }
+}
+
+template <int R>
+__device__ __noinline__ void roles_again(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const Params& p,
+                                         uint8_t* sm, uint32_t tmem) {
+  roles<R, true>(tm_q, tm_kv, p, sm, tmem);
+}
+
+template <int R>
+__global__ void __launch_bounds__(THREADS, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_align1024(smem_raw);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), rank = blockIdx.x & 1;
+  uint32_t tmem;
+  {
+    const Shared<R> x(sm);
+    if (tid == 0) {
+      x.barriers(rank);
+      x.s_abort[0] = x.s_abort[1] = 0;
+      x.s_any[0] = x.s_go[0] = 0;
+      for (int k = 0; k < 4; ++k) x.s_slow[k] = 0;
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_kv);
+    }
+    if (tid < 5 * REDO / 32) x.s_redo[tid] = 0;
+    if (warp == 2) {
+      tmem_alloc_pair(x.tslot, 512);
+      tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    tmem = *x.tslot;
+  }
+  pdl_wait();
+  pdl_start_next();
+  roles<R, false>(tm_q, tm_kv, p, sm, tmem);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  const Shared<R> x(sm);
+  const bool again = x.s_any[0] != 0 && x.s_abort[0] == 0;
+  if (again) {
+    if (tid == 0) st_cluster_u32(smem_u32(const_cast<int*>(x.s_go)), rank ^ 1, 1);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  }
   cluster_arrive_relaxed();     // nothing of the pair's is read any more
   cluster_wait();
+  if (again && x.s_go[0] != 0) {
+    // all copies, products and arrivals of both CTAs are in: the barriers start over
+    if (tid == 0) {
+      for (int k = 0; k < Shared<R>::BARS; ++k) mbar_inval(&x.kfull[k]);
+      x.barriers(rank);
+    }
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    roles_again<R>(tm_q, tm_kv, p, sm, tmem);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+  }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);

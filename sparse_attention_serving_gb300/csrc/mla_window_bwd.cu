@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
     for (int k = 0; k < C::NS; ++k) mbar_init(&kfull[k], 1), mbar_init(&kempty[k], 1);
     for (int k = 0; k < 2; ++k) mbar_init(&afull[k], 1), mbar_init(&afree[k], 16);
     mbar_init(drain, 1);
-    s_abort[0] = 0;
+    s_abort[0] = s_abort[1] = 0;
     fence_mbar_init();
     tma_prefetch_desc(rank == 0 ? &tm_q : &tm_do);
     tma_prefetch_desc(&tm_kv);
@@ -274,8 +274,8 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
     }
     for (; used > 0; --used) {
       if (--r.slot < 0) r.slot = C::NS - 1, r.ph ^= 1;
-      if (rank == 0) wait(&kfull[r.slot], r.ph, s_abort, p.status, SITE_KF);
-      if (ok) wait(&kempty[r.slot], r.ph, s_abort, p.status, SITE_KE);
+      if (rank == 0) settle(&kfull[r.slot], r.ph);
+      if (ok) settle(&kempty[r.slot], r.ph);
     }
   } else if (warp == 1 && rank == 0) {
     const uint64_t kd = smem_desc(smem_u32(sm + C::OFF_K), 16, 1024);
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
     }
     if (elect_one_lane()) umma_commit_pair(drain);
     __syncwarp();
-    wait(drain, 0, s_abort, p.status, SITE_DRAIN);
+    settle(drain, 0);
   } else if (warp >= 4) {
     // ---- a key a thread, 64 of the tile's rows a warp ----
     const int sub = warp & 3, r0 = (warp - 4) / 4 * 64, key = sub * 32 + lane;
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
     mbar_init(done, 1);
     mbar_init(dfree, 16);
     mbar_init(drain, 1);
-    s_abort[0] = 0;
+    s_abort[0] = s_abort[1] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_pz);
     tma_prefetch_desc(DKV ? &tm_q : &tm_kv);
@@ -619,8 +619,8 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
     }
     for (; used > 0; --used) {
       if (--r.slot < 0) r.slot = C::NS - 1, r.ph ^= 1;
-      if (rank == 0) wait(&full[r.slot], r.ph, s_abort, p.status, SITE_F);
-      if (ok) wait(&empty[r.slot], r.ph, s_abort, p.status, SITE_E);
+      if (rank == 0) settle(&full[r.slot], r.ph);
+      if (ok) settle(&empty[r.slot], r.ph);
     }
   } else if (warp == 1 && rank == 0) {
     const uint64_t ad = DKV ? smem_desc(smem_u32(sm), CHUNK, 1024) : smem_desc(smem_u32(sm), 16, 1024);
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
     }
     if (elect_one_lane()) umma_commit_pair(drain);
     __syncwarp();
-    wait(drain, 0, s_abort, p.status, SITE_DRAIN);
+    settle(drain, 0);
   } else if (warp >= 4) {
     // ---- out: a row (key) a thread; warps 4..7 the lower half of the columns ----
     const int sub = warp & 3, half = (warp >> 2) - 1, r = 128 * rank + 32 * sub + lane;

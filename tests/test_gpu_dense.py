@@ -142,6 +142,60 @@ def test_window_forward_rising_scores(dsa, rise):
     ref.within(lse[0], r_lse, lse_off, "lse")
 
 
+@pytest.mark.parametrize("case", [(2, 600, 96, 500, 4), (1, 20, 8, 300, 0), (3, 12, 8, 400, 2), (1, 1, 96, 900, 0)],
+                         ids=str)
+def test_window_units_done_twice(dsa, case):
+    """Scores of some heads and of some queries that rise far beyond an exponent's range, for every
+    number of rows that a CTA may hold."""
+    B, Tq, H, window, first = case
+    gen = _gen(40)
+    S = 1000
+    q, base = _normal(gen, B, Tq, H, 576), _normal(gen, B, S, 576)
+    q[..., 0] = 0
+    q[:, Tq // 3:, ::3, 0] = 16.0
+    q[:, Tq // 2:, 1::5, 0] = -16.0
+    base[..., 0] = (torch.arange(S, device="cuda") / S * 700 / (16 * ref.SCALE)).to(torch.bfloat16)
+    start = S - Tq
+    rows, qs, kl = dsa.Rows(base), _i32([start] * B), _i32([S] * B)
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_WINDOW, B, Tq, S, H, window + first))
+    o, lse = dsa.mla_window_fwd(q, rows, qs, kl, window, first, S, workspace=ws)
+    again, _ = dsa.mla_window_fwd(q, rows, qs, kl, window, first, S, workspace=ws)
+    _ok(dsa, ws)
+    assert torch.equal(o, again)
+    see = ref.window_sees(torch.arange(start, S, device="cuda")[:, None],
+                          torch.arange(S, device="cuda"), window, first)
+    for b in range(B):
+        for at in range(0, Tq, 100):
+            part = slice(at, min(at + 100, Tq))
+            r_o, r_lse, o_off, lse_off = ref.forward(q[b, part], base[b], see[part])
+            ref.within(o[b, part], r_o, o_off, "o_lat")
+            ref.within(lse[b, part], r_lse, lse_off, "lse")
+
+
+def test_window_more_units_than_are_done_twice(dsa):
+    """Each pair of SMs holds more units than it can mark."""
+    gen = _gen(41)
+    H, window = 8, 200
+    T = 76 * 1024 * 192 // H + 30000
+    q = torch.zeros((1, T, H, 576), dtype=torch.bfloat16, device="cuda")
+    base = torch.zeros((1, T, 576), dtype=torch.bfloat16, device="cuda")
+    base[0] = _normal(gen, T, 576)
+    q[0, :, :, :16] = _normal(gen, T, H, 16)
+    # a page's last row may be far above the pages before: scores of 0, 111, 222 or 333
+    q[..., 20] = 16.0
+    page = torch.arange(T // 64, device="cuda")
+    base[..., 20] = 0
+    base[0, 63::64, 20] = (page % 4 * 96).to(torch.bfloat16)[:len(base[0, 63::64])]
+    o, lse = dsa.mla_window_fwd(q, dsa.Rows(base), _i32([0]), _i32([T]), window, 0, T)
+    for at in (0, 100000, T // 2, T - 40000, T - 64):
+        t = torch.arange(at, at + 64, device="cuda")
+        near = torch.arange(max(at - window, 0), at + 64, device="cuda")
+        see = ref.window_sees(t[:, None], near, window, 0)
+        r_o, r_lse, o_off, lse_off = ref.forward(q[0, t], base[0, near], see)
+        ref.within(o[0, t], r_o, o_off, f"o_lat at {at}")
+        ref.within(lse[0, t], r_lse, lse_off, f"lse at {at}")
+
+
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 def test_window_row_reaches_only_who_sees_it(dsa, value):
     """A row that holds an infinity or a NaN: queries whose window has left it keep to the bounds
@@ -339,6 +393,52 @@ def test_tree_pieces_by_the_slow_path(dsa, rise):
     ref.within(o[0, [0, 2]], r_o, o_off, "o_lat")
     ref.within(lse[0, [0, 2]], r_lse, lse_off, "lse")
     assert torch.isnan(o[0, 1]).all()
+
+
+@pytest.mark.parametrize("case", [(1, 3, 40, 5000), (4, 8, 96, 6000), (1, 1, 96, 9000)], ids=str)
+def test_tree_pieces_done_twice(dsa, case):
+    """Pieces of a long prefix whose scores rise beyond an exponent's range within the piece."""
+    B, T, H, L = case
+    gen = _gen(42)
+    q, base = _normal(gen, B, T, H, 576), _normal(gen, B, L + T, 576)
+    q[:, :, ::2, 0] = 16.0
+    wave = (torch.arange(L, device="cuda") % 500) / 500 * 600
+    base[:, :L, 0] = (wave / (16 * ref.SCALE)).to(torch.bfloat16)
+    masks = _masks(42, B, T, "tree")
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_TREE, B, T, L + T, H, 0))
+    o, lse = dsa.mla_tree_fwd(q, dsa.Rows(base), masks, _i32([L] * B), L + T, workspace=ws)
+    _ok(dsa, ws)
+    for b in range(B):
+        r_o, r_lse, o_off, lse_off = ref.forward(q[b], base[b], _tree_sees(masks[b], L, T, T))
+        ref.within(o[b], r_o, o_off, "o_lat")
+        ref.within(lse[b], r_lse, lse_off, "lse")
+
+
+def test_tree_long_row_by_row(dsa):
+    """A sibling's NaN behind a prefix that takes seconds row by row: the waits last."""
+    gen = _gen(43)
+    B, T, H, pages = 152, 2, 96, 8192
+    L = pages * 64 - 64
+    pool = torch.empty((pages + B, 64, 576), dtype=torch.bfloat16, device="cuda")
+    for at in range(0, pages + B, 1024):
+        pool[at:at + 1024] = _normal(gen, min(1024, pages + B - at), 64, 576)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(B, 1)
+    table[:, -1] = pages + torch.arange(B, device="cuda")
+    pool[pages + 7, 1] = math.nan                     # drafted token 1 of sequence 7
+    q = _normal(gen, B, T, H, 576)
+    masks = torch.tensor([[1, 3]] * B, dtype=torch.int64, device="cuda")
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_TREE, B, T, L + T, H, 0))
+    rows = dsa.Rows(pool, table.contiguous())
+    o, lse = dsa.mla_tree_fwd(q, rows, masks, _i32([L] * B), L + T, workspace=ws)
+    _ok(dsa, ws)
+    assert torch.isnan(o[7, 1]).all() and not torch.isnan(o[8:]).any()
+    see = torch.ones((1, L + 1), dtype=torch.bool, device="cuda")
+    for b, i in ((7, 0), (6, 0)):
+        for h in range(0, H, 32):
+            cache = ref.logical(pool, table, b, L + 1)
+            r_o, r_lse, o_off, lse_off = ref.forward(q[b, i:i + 1, h:h + 32], cache, see)
+            ref.within(o[b, i:i + 1, h:h + 32], r_o, o_off, "o_lat")
+            ref.within(lse[b, i:i + 1, h:h + 32], r_lse, lse_off, "lse")
 
 
 def test_tree_of_one_chain_is_the_window_without_end(dsa):
