@@ -56,12 +56,13 @@ template <int R_>
 struct Cfg {
   static constexpr int R = R_;
   static constexpr int HALVES = R <= 64 ? 2 : 1;      // threads that share a row's scores
-  static constexpr int NK = R == 96 ? 5 : 8;          // K slots: a chunk of own keys
+  static constexpr int NK = R == 96 ? 5 : R == 64 ? 6 : 7;   // K slots: a chunk of own keys
   static constexpr int NV = R == 96 ? 3 : R == 64 ? 4 : 5;   // V slots: 64 keys x 128 dims
   static constexpr int QCH = R * 128;                 // 64 dims of the queries
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_P = OFF_Q + 9 * QCH;
-  static constexpr int OFF_K = OFF_P + 2 * QCH;
+  static constexpr int NP = R == 96 ? 1 : 2;          // P of as many blocks (4 x 1 over 131072: 131.6 -> 129.3 us)
+  static constexpr int OFF_K = OFF_P + 2 * NP * QCH;
   static constexpr int OFF_V = OFF_K + NK * CHUNK;
   static constexpr int OFF_MISC = OFF_V + NV * 2 * CHUNK;
   static constexpr int MISC = 1024 + 16 * R + (HALVES == 2 ? 2048 : 0) + 5 * REDO / 8;
@@ -328,12 +329,12 @@ __device__ __forceinline__ bool all_see(const Mask& m, const Unit& u, int kb) {
 template <int R>
 struct Shared {
   using C = Cfg<R>;
-  static constexpr int BARS = 2 * C::NK + 2 * C::NV + 19 + 2 * UNITS;
+  static constexpr int BARS = 2 * C::NK + 2 * C::NV + 21 + 2 * UNITS;
   uint64_t *kfull, *kempty;      // kfull, vfull, sfree, ofree: the even CTA's
   uint64_t *vfull, *vempty;
   uint64_t *sfull, *sfree;       // [NB]
-  uint64_t *pready;              // odd CTA: for its warp 3
-  uint64_t *odone, *ofull;       // a block's values added; a unit's
+  uint64_t* pready;              // [NP] odd CTA: for its warp 3
+  uint64_t *odone, *ofull;       // [NP] a block's values added; a unit's
   uint64_t *ofree;               // [2] 2R columns read
   uint64_t *lfull, *lpeer;       // [2] a unit's sums, of this CTA's rows, of the other's
   uint64_t *lfree;               // [2]
@@ -360,15 +361,15 @@ struct Shared {
     sfull = vempty + C::NV;
     sfree = sfull + 2;
     pready = sfull + 4;
-    odone = sfull + 5;
-    ofull = sfull + 6;
-    ofree = sfull + 7;
-    lfull = sfull + 9;
-    lpeer = sfull + 11;
-    lfree = sfull + 13;
-    vland = sfull + 15;
-    drain = sfull + 17;
-    ufull = sfull + 19;
+    odone = sfull + 6;
+    ofull = sfull + 8;
+    ofree = sfull + 9;
+    lfull = sfull + 11;
+    lpeer = sfull + 13;
+    lfree = sfull + 15;
+    vland = sfull + 17;
+    drain = sfull + 19;
+    ufull = sfull + 21;
     uempty = ufull + UNITS;
     tslot = reinterpret_cast<uint32_t*>(uempty + UNITS);
     s_abort = reinterpret_cast<volatile int*>(tslot + 1);
@@ -385,12 +386,12 @@ struct Shared {
   __device__ __forceinline__ void barriers(int rank) const {
     for (int k = 0; k < C::NK; ++k) mbar_init(&kfull[k], 1), mbar_init(&kempty[k], 1);
     for (int k = 0; k < C::NV; ++k) mbar_init(&vfull[k], 2), mbar_init(&vempty[k], 1);
-    mbar_init(pready, rank == 0 ? 5 : 4);
-    mbar_init(odone, 1);
     mbar_init(ofull, 1);
     for (int k = 0; k < 2; ++k) {
       mbar_init(&sfull[k], 1);
       mbar_init(&sfree[k], 8);
+      mbar_init(&pready[k], rank == 0 ? 5 : 4);
+      mbar_init(&odone[k], 1);
       mbar_init(&ofree[k], 8);
       mbar_init(&lfull[k], 4);
       mbar_init(&lpeer[k], 1);
@@ -454,7 +455,6 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
         const int qrow = static_cast<int>(static_cast<int64_t>(u.b) * p.m.T * p.H) + u.g0 + rank * R;
         for (int j = 0; j < u.nb && ok; ++j) {
           const int k = u.k0 + 2 * j + rank;
-          const bool both = u.k0 + 2 * j + 1 < u.k1;       // else the odd CTA's slots keep what they hold
           int64_t row = 0;
           if (k < u.k1) {
             row = page_row(p.kv, u.b, u.pages.page(k));
@@ -469,10 +469,13 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
             if (!ok) break;
             if (elect_one_lane()) {
               const uint32_t bar = mapa_u32(smem_u32(&kfull[r.slot]), 0);
-              if (rank == 0) mbar_expect_tx(&kfull[r.slot], (both ? 2 : 1) * CHUNK + (j == 0 ? 2 * C::QCH : 0));
+              if (rank == 0) mbar_expect_tx(&kfull[r.slot], 2 * CHUNK + (j == 0 ? 2 * C::QCH : 0));
               if (j == 0) tma_load_2d_pair(sm + C::OFF_Q + c * C::QCH, &tm_q, bar, 64 * c, qrow);
               if (k < u.k1)
                 tma_load_2d_pair(sm + C::OFF_K + r.slot * CHUNK, &tm_kv, bar, 64 * c, static_cast<int>(row));
+              else    // no second page: the slot keeps what it holds.  Counted all the same: products
+                      // that did not need this CTA could free the slot twice between two of its looks
+                mbar_complete_tx_cluster(bar, CHUNK);
             }
             __syncwarp();
             if (used < C::NK) ++used;
@@ -599,7 +602,8 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
         const Unit& u = *up;
         if (u.nb == 0) continue;
         for (int j = 0; j < u.nb && ok; ++j, ++blk) {
-          ok = wait(pready, blk & 1, s_abort, p.status, SITE_P);
+          const int pb = blk % C::NP;
+          ok = wait(&pready[pb], blk / C::NP & 1, s_abort, p.status, SITE_P);
           const int nt = u.k0 + 2 * j + 1 < u.k1 ? 4 : 2;
           for (int t = 0; t < nt && ok; ++t) {           // page t >> 1, dims 128 (t & 1)
             // the unit before has been read out
@@ -608,13 +612,13 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
             if (!ok) break;
             tc_fence_after();
             if (elect_one_lane()) {
-              const uint64_t a = desc_add(vd, r.slot * 2 * CHUNK), w = desc_add(pd, (t >> 1) * C::QCH);
+              const uint64_t a = desc_add(vd, r.slot * 2 * CHUNK), w = desc_add(pd, (2 * pb + (t >> 1)) * C::QCH);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 umma_bf16_pair(tmem + (t & 1) * 2 * R, desc_add(a, kk * 2048), desc_add(w, kk * 32),
                                IDESC_O, j > 0 || t > 1 || kk > 0);
               umma_commit_pair(&vempty[r.slot]);
-              if (t == nt - 1) umma_commit_pair(odone);
+              if (t == nt - 1) umma_commit_pair(&odone[pb]);
               if (t == nt - 1 && j == u.nb - 1) umma_commit_pair(ofull);
             }
             __syncwarp();
@@ -633,8 +637,9 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
       while (const Unit* up = ok ? feed.next() : nullptr) {
         const int nb = up->nb;
         for (int j = 0; j < nb && ok; ++j, ++blk) {
-          ok = wait(pready, blk & 1, s_abort, p.status, SITE_P);
-          if (ok && lane == 0) mbar_arrive_cluster(bar);
+          const int pb = blk % C::NP;
+          ok = wait(&pready[pb], blk / C::NP & 1, s_abort, p.status, SITE_P);
+          if (ok && lane == 0) mbar_arrive_cluster(bar + 8 * pb);
           __syncwarp();
         }
       }
@@ -760,19 +765,20 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
             z[c][e >> 1] = pack_bf16x2(p0, p1);
           }
         l_sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
-        // P is free once the block before has been multiplied
-        if (blk > 0) ok = wait(odone, (blk - 1) & 1, s_abort, p.status, SITE_O);
+        // P is free once the block that had its place has been multiplied
+        const int pb = blk % C::NP;
+        if (blk >= C::NP) ok = wait(&odone[pb], (blk / C::NP - 1) & 1, s_abort, p.status, SITE_O);
         if (ok && r < R) {
 #pragma unroll
           for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(prow + (c >> 1) * C::QCH + (((4 * (c & 1) + q) ^ (r & 7)) << 4)) =
+              *reinterpret_cast<uint4*>(prow + (2 * pb + (c >> 1)) * C::QCH + (((4 * (c & 1) + q) ^ (r & 7)) << 4)) =
                   make_uint4(z[c][4 * q], z[c][4 * q + 1], z[c][4 * q + 2], z[c][4 * q + 3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(pready);
+        if (ok && lane == 0) mbar_arrive(&pready[pb]);
       }
       // what the epilogues of both CTAs need of this row, once they are done with the
       // unit before the last
@@ -810,7 +816,8 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
       }
       mbar_arrive_warp(&lfull[bu]);
     }
-    if (blk > 0) settle(odone, (blk - 1) & 1);           // (not waited for above)
+    for (int k = max(blk - C::NP, 0); k < blk; ++k)      // (not waited for above)
+      settle(&odone[k % C::NP], k / C::NP & 1);
   } else {
     // ---- out: lane = dim 256 rank + 128 m + 32 sub + lane, a row a column ----
     const int sub = warp & 3;

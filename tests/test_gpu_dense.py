@@ -414,6 +414,32 @@ def test_tree_pieces_done_twice(dsa, case):
         ref.within(lse[b], r_lse, lse_off, "lse")
 
 
+@pytest.mark.parametrize("case", [(76, 1, 96, 16384), (76, 1, 96, 8192), (76, 1, 96, 64), (76, 1, 96, 0),
+                                  (40, 8, 96, 4096), (90, 13, 8, 4096), (3, 1, 96, 65536)], ids=str)
+def test_tree_odd_pages_that_all_share(dsa, case):
+    """Odd numbers of pages and a cache that stays in L2: a block without a second page must not
+    run ahead of the CTA that has none to copy."""
+    gen = _gen(44)
+    B, T, H, L = case
+    pages = 400
+    pool = _normal(gen, pages, 64, 576)
+    P = L // 64 + 1
+    table = (torch.arange(B * P, device="cuda") % pages).view(B, P).to(torch.int32).contiguous()
+    rows, q, kl = dsa.Rows(pool, table), _normal(gen, B, T, H, 576), _i32([L] * B)
+    masks = torch.full((B, T), (1 << T) - 1, dtype=torch.int64, device="cuda")
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_TREE, B, T, L + T, H, 0))
+    first, _ = dsa.mla_tree_fwd(q, rows, masks, kl, L + T, workspace=ws)
+    for _ in range(40):
+        o, lse = dsa.mla_tree_fwd(q, rows, masks, kl, L + T, workspace=ws)
+        assert torch.equal(o, first)
+    _ok(dsa, ws)
+    see = torch.ones((T, L + T), dtype=torch.bool, device="cuda")
+    for b in (0, B - 1):
+        r_o, r_lse, o_off, lse_off = ref.forward(q[b], ref.logical(pool, table, b, L + T), see)
+        ref.within(o[b], r_o, o_off, "o_lat")
+        ref.within(lse[b], r_lse, lse_off, "lse")
+
+
 def test_tree_long_row_by_row(dsa):
     """A sibling's NaN behind a prefix that takes seconds row by row: the waits last."""
     gen = _gen(43)
