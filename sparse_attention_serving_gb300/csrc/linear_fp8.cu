@@ -595,6 +595,7 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
   using C = Wide;
   constexpr uint32_t IDESC = idesc_e4m3(256, 256);
   extern __shared__ uint8_t smem_raw[];
+  cluster_arrive_relaxed();
   uint8_t* sm = smem_align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);   // used in the even CTA
   uint64_t* done = full + C::NST;      // a stage's MMAs are complete: it is empty and its block summed
@@ -621,6 +622,8 @@ __global__ void __launch_bounds__(Wide::NTHREADS, 1)
     s_abort[0] = 0;
     fence_mbar_init();
   }
+  __syncwarp();
+  cluster_wait();                      // the other CTA runs
   if (warp == C::EW + 1) {
     tmem_alloc_pair(tslot, 512);
     tmem_relinquish_pair();
