@@ -171,6 +171,9 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* tmap, ui
       : "memory");
 }
 // Allocation and release of TMEM columns in both CTAs: one warp of each executes them.
+// Not before the other CTA runs: behind a cluster barrier of its own, which all threads
+// arrive at when they start.  (An allocation that began before waits for ever; seen where
+// other streams' CTAs come and go and the two do not start together.)
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem_word, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                    smem_u32(dst_smem_word)),
@@ -211,6 +214,12 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(smem_u32(bar)),
       "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// The same on this CTA's barrier alone.
+__device__ __forceinline__ void umma_commit_pair_own(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
       : "memory");
 }
 // Register budget of this warpgroup from here on (all its warps execute it).

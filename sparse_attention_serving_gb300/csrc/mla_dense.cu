@@ -343,7 +343,7 @@ struct Shared {
   uint64_t *ufull, *uempty;      // [UNITS]
   uint32_t* tslot;
   volatile int* s_abort;         // [2] the second moves while attend_row goes on
-  int* s_slow;                   // [2] x a row is far, an attend_row is needed
+  volatile int* s_slow;          // [2] x unit + 1 of which a row is far, of which a row needs attend_row
   volatile int *s_any, *s_go;    // units are to be done again; the other CTA says so too
   Unit* s_unit;                  // [UNITS]
   float* s_inv;                  // [2][2R]
@@ -373,7 +373,7 @@ struct Shared {
     uempty = ufull + UNITS;
     tslot = reinterpret_cast<uint32_t*>(uempty + UNITS);
     s_abort = reinterpret_cast<volatile int*>(tslot + 1);
-    s_slow = reinterpret_cast<int*>(tslot + 3);
+    s_slow = reinterpret_cast<volatile int*>(tslot + 3);
     s_any = reinterpret_cast<volatile int*>(tslot + 7);
     s_go = s_any + 1;
     s_unit = reinterpret_cast<Unit*>(sm + C::OFF_MISC + 512);
@@ -420,7 +420,7 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
   // An issuer that gives up: its MMAs are complete before the pair leaves.  (Otherwise those
   // who waited for what they gave have seen that.)
   auto give_up = [&](uint64_t* bar) {
-    if (elect_one_lane()) umma_commit_pair(bar);
+    if (elect_one_lane()) umma_commit_pair_own(bar);
     __syncwarp();
     settle(bar, 0);
   };
@@ -662,7 +662,10 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
       named_bar_sync(2 + (sub & 1), 64);
       return buf[(half ^ 1) * 64 + r];
     };
-    while (const Unit* up = ok ? feed.next() : nullptr) {
+    while (true) {
+      const Unit* up = ok ? feed.next() : nullptr;
+      // (HALVES = 2: the two warps that share rows come and leave together, by votes)
+      if (C::HALVES == 2 ? named_bar_or(2 + (sub & 1), 64, up == nullptr) : up == nullptr) break;
       const Unit& u = *up;
       const int at = feed.at;
       const int g = u.g0 + rank * R + r;
@@ -710,7 +713,6 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
         }
         const int sb = blk % C::NB;
         ok = ok && wait(&sfull[sb], (blk / C::NB) & 1, s_abort, p.status, SITE_SF);
-        // (HALVES = 2: the two warps that share rows leave together, by a vote)
         if (C::HALVES == 2) ok = !named_bar_or(2 + (sub & 1), 64, !ok);
         if (!ok) break;
         tc_fence_after();
@@ -809,8 +811,8 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
         if (lane == 0) {
           if (u.no < REDO) s_noted[sub * (REDO / 32) + (u.no >> 5)] |= 1u << (u.no & 31);
           for (int k = 0; k <= bad; ++k) {
-            s_slow[2 * bu + k] = 1;
-            st_cluster_u32(smem_u32(&s_slow[2 * bu + k]), rank ^ 1, 1);
+            s_slow[2 * bu + k] = at + 1;
+            st_cluster_u32(smem_u32(const_cast<int*>(s_slow + 2 * bu + k)), rank ^ 1, at + 1);
           }
         }
       }
@@ -840,7 +842,7 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
       if (ok && u.nb > 0) ok = wait(ofull, n & 1, s_abort, p.status, SITE_O);
       if (!ok) break;
       tc_fence_after();
-      const bool slow = reinterpret_cast<volatile int*>(s_slow)[2 * bu] != 0;
+      const bool slow = s_slow[2 * bu] == at + 1;
 #pragma unroll 1
       for (int m = 0; m < 2; ++m) {
         const int dim = 256 * rank + 128 * m + 32 * sub + lane;
@@ -887,7 +889,7 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
       if (u.nb > 0) ++n;
       if (slow) {
         // (both CTAs come to the same)
-        const bool again = !AGAIN && u.no < REDO && reinterpret_cast<volatile int*>(s_slow)[2 * bu + 1] == 0;
+        const bool again = !AGAIN && u.no < REDO && s_slow[2 * bu + 1] != at + 1;
         for (int r = rank * R + sub; !again && r < min(here, rank * R + R); r += 4) {
           attend_row(p, u.s, u.pages, u.k0, u.k1, u.b, u.g0 + r, parts ? p.part_o + (part + r) * kVlat : nullptr,
                      parts ? p.part_lse + part + r : nullptr);
@@ -897,18 +899,13 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
             st_cluster_u32(smem_u32(const_cast<int*>(s_abort + 1)), rank ^ 1, beat);
           }
         }
-        named_bar_sync(1, 128);                          // all of them have read the flags
-        if (sub == 0 && lane == 0) {
-          s_slow[2 * bu] = s_slow[2 * bu + 1] = 0;
-          if (again) s_redo[u.no >> 5] |= 1u << (u.no & 31), s_any[0] = 1;
-        }
+        if (again && sub == 0 && lane == 0) s_redo[u.no >> 5] |= 1u << (u.no & 31), s_any[0] = 1;
         __syncwarp();
       }
       if (lane == 0) {                                   // the sums may be overwritten
         const uint32_t there = mapa_u32(smem_u32(&lfree[bu]), rank ^ 1);
         mbar_arrive(&lfree[bu]);
-        if (slow) mbar_arrive_cluster(there);            // after the flag's reset
-        else mbar_arrive_cluster_relaxed(there);
+        mbar_arrive_cluster_relaxed(there);
       }
     }
   }
@@ -928,6 +925,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* sm = smem_align1024(smem_raw);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), rank = blockIdx.x & 1;
   uint32_t tmem;
+  cluster_arrive_relaxed();
   {
     const Shared<R> x(sm);
     if (tid == 0) {
@@ -939,6 +937,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       tma_prefetch_desc(&tm_kv);
     }
     if (tid < 5 * REDO / 32) x.s_redo[tid] = 0;
+    __syncwarp();
+    cluster_wait();             // the other CTA runs
     if (warp == 2) {
       tmem_alloc_pair(x.tslot, 512);
       tmem_relinquish_pair();
@@ -957,17 +957,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   const Shared<R> x(sm);
   const bool again = x.s_any[0] != 0 && x.s_abort[0] == 0;
-  if (again) {
-    if (tid == 0) st_cluster_u32(smem_u32(const_cast<int*>(x.s_go)), rank ^ 1, 1);
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  }
-  cluster_arrive_relaxed();     // nothing of the pair's is read any more
-  cluster_wait();
+  if (again && tid == 0) st_cluster_u32(smem_u32(const_cast<int*>(x.s_go)), rank ^ 1, 1);
+  cluster_sync();               // nothing of the pair's is read or arrived at any more
   if (again && x.s_go[0] != 0) {
     // all copies, products and arrivals of both CTAs are in: the barriers start over
     if (tid == 0) {
       for (int k = 0; k < Shared<R>::BARS; ++k) mbar_inval(&x.kfull[k]);
       x.barriers(rank);
+      for (int k = 0; k < 4; ++k) x.s_slow[k] = 0;
     }
     __syncthreads();
     cluster_sync();

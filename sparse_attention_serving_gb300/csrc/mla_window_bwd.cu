@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
   const int rank = blockIdx.x & 1, tasks = p.B * p.q.RC, step = gridDim.x >> 1;
 
   extern __shared__ uint8_t smem_raw[];
+  cluster_arrive_relaxed();
   uint8_t* sm = smem_align1024(smem_raw);
   uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);   // even CTA
   uint64_t* kempty = kfull + C::NS;
@@ -221,6 +222,8 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
     tma_prefetch_desc(rank == 0 ? &tm_q : &tm_do);
     tma_prefetch_desc(&tm_kv);
   }
+  __syncwarp();
+  cluster_wait();                                    // the other CTA runs
   if (warp == 1) {
     tmem_alloc_pair(tslot, 512);
     tmem_relinquish_pair();
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
         }
       }
     }
-    if (elect_one_lane()) umma_commit_pair(drain);
+    if (elect_one_lane()) umma_commit_pair_own(drain);
     __syncwarp();
     settle(drain, 0);
   } else if (warp >= 4) {
@@ -434,9 +437,10 @@ struct Task {
   Pages list;                    // dq: pages of the two tiles
   bool there;
 
-  // The pair's tasks are `first` + k * step; their dims alternate whatever the step.
-  __device__ __forceinline__ Task(const Params& p, int task, int first, int step) {
-    upper = (task ^ (step & 1 ? 0 : (task - first) / step)) & 1;
+  // n: tasks that the pair has had so far.  Its dims alternate; of two neighbouring pairs,
+  // which have the same rows throughout, one has the upper ones.
+  __device__ __forceinline__ Task(const Params& p, int task, int n) {
+    upper = (task ^ n) & 1;
     int u = task >> 1;
     kt = g = 0;
     list = Pages{0, 0, 0};
@@ -489,6 +493,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
   constexpr uint32_t IDESC = idesc_bf16(256, 256, DKV, true), IDESC_ROT = idesc_bf16(256, 64, DKV, true);
   const int rank = blockIdx.x & 1, step = gridDim.x >> 1;
   extern __shared__ uint8_t smem_raw[];
+  cluster_arrive_relaxed();
   uint8_t* sm = smem_align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);    // even CTA
   uint64_t* empty = full + C::NS;
@@ -512,6 +517,8 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
     tma_prefetch_desc(DKV ? &tm_q : &tm_kv);
     if (DKV) tma_prefetch_desc(&tm_do);
   }
+  __syncwarp();
+  cluster_wait();                                    // the other CTA runs
   if (warp == 1) {
     tmem_alloc_pair(tslot, 512);
     tmem_relinquish_pair();
@@ -526,7 +533,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
 
   if (warp == 0) {
     Ring<C::NS> r;
-    int used = 0;
+    int used = 0, n = 0;
     uint32_t lph = 0;
     bool ok = true;
     auto acquire = [&] {
@@ -539,8 +546,9 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       r.next();
     };
     for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
-      const Task<DKV> t(p, task, blockIdx.x >> 1, step);
+      const Task<DKV> t(p, task, n);
       if (!t.there) continue;
+      ++n;
       const int col = 256 * t.upper + 128 * rank;
       if constexpr (DKV) {
         for (int x = t.x0; x < t.x1 && ok; ++x) {
@@ -579,12 +587,12 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
           uint8_t* w = a + C::OFF_W;
           const uint32_t bar = mapa_u32(smem_u32(&full[r.slot]), 0);
           const bool rot = t.upper;
-          const int n = rot ? 3 : 2;
+          const int boxes = rot ? 3 : 2;
           if (any != ~0ull) {
             // rows behind the sequence become zeros: whatever they hold must not meet
             // the zeros of dZ
             if (elect_one_lane()) {
-              mbar_expect_tx(land, n * CHUNK);
+              mbar_expect_tx(land, boxes * CHUNK);
               tma_load_2d(w, &tm_kv, land, col, row);
               tma_load_2d(w + CHUNK, &tm_kv, land, col + 64, row);
               if (rot) tma_load_2d(w + 2 * CHUNK, &tm_kv, land, kVlat + 32 * rank, row);
@@ -593,14 +601,14 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
             ok = wait(land, lph, s_abort, p.status, SITE_LAND);
             lph ^= 1;
             if (!ok) break;
-            for (int e = lane; e < n * CHUNK / 16; e += 32)
+            for (int e = lane; e < boxes * CHUNK / 16; e += 32)
               if (!(any >> ((e >> 3) & 63) & 1)) reinterpret_cast<uint4*>(w)[e] = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
           }
           if (elect_one_lane()) {
             if (any == ~0ull) {
-              mbar_expect_tx_cluster(bar, (2 + n) * CHUNK);
+              mbar_expect_tx_cluster(bar, (2 + boxes) * CHUNK);
             } else {
               mbar_expect_tx_cluster_release(bar, 2 * CHUNK);
             }
@@ -649,7 +657,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       r.next();
     };
     for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
-      const Task<DKV> t(p, task, blockIdx.x >> 1, step);
+      const Task<DKV> t(p, task, n);
       if (!t.there) continue;
       if (n > 0) ok = wait(dfree, (n - 1) & 1, s_abort, p.status, SITE_DF);
       tc_fence_after();
@@ -667,7 +675,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       if (elect_one_lane()) umma_commit_pair(done);
       __syncwarp();
     }
-    if (elect_one_lane()) umma_commit_pair(drain);
+    if (elect_one_lane()) umma_commit_pair_own(drain);
     __syncwarp();
     settle(drain, 0);
   } else if (warp >= 4) {
@@ -685,7 +693,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
     int n = 0;
     bool ok = true;
     for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
-      const Task<DKV> t(p, task, blockIdx.x >> 1, step);
+      const Task<DKV> t(p, task, n);
       if (!t.there) continue;
       const bool some = t.some(p);
       const int g = t.x0 * X + r;                    // dq: row of the sequence
@@ -885,7 +893,7 @@ dsa_status_t window_bwd_launch(const WindowBwdArgs& a, cudaStream_t stream) {
     const int64_t pairs = num_sms() / 2, tiles = static_cast<int64_t>(f.B) * q.RC;
     const int64_t sums = 2ll * f.B * q.G * q.per_seg();
     if (sums > (1 << 30) || tiles > (1 << 30)) return DSA_ERR_UNSUPPORTED;
-    const int64_t some = tiles < pairs ? tiles : pairs;
+    const int64_t some = tiles < pairs ? tiles : pairs / 2 * 2;   // (even, as the tiles are)
     dsa_status_t st = launch_pairs("pz_kernel", q.parts == 2 ? pz_kernel<true> : pz_kernel<false>, some, Pz::THREADS, Pz::SMEM, stream, tq_tile,
                                    td_tile, tk, p);
     if (st == DSA_OK)

@@ -633,9 +633,91 @@ def test_window_backward_in_chunks(dsa):
         ref.within(dkv[b], r_dkv, off * (1 + (H - 1) * share), f"dkv of {b}")
 
 
+def test_window_backward_last_chunk_in_part(dsa):
+    """The last chunk holds some tiles of each sequence only: a pair of SMs passes over tasks."""
+    B, Tq, H, window, first = 2, 5000, 96, 1000, 4       # 3750 tiles each, 3448 at a time
+    gen = _gen(28)
+    base, q, d_o = _normal(gen, B, Tq, 576), _normal(gen, B, Tq, H, 576), _normal(gen, B, Tq, H, 512)
+    rows, qs, kl = dsa.Rows(base), _i32([0] * B), _i32([Tq] * B)
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_WINDOW_BWD, B, Tq, Tq, H, window + first))
+    o, lse = dsa.mla_window_fwd(q, rows, qs, kl, window, first, Tq)
+    dq, dkv = dsa.mla_window_bwd(q, rows, qs, kl, window, first, Tq, o, lse, d_o, workspace=ws)
+    for _ in range(3):
+        dq2, dkv2 = dsa.mla_window_bwd(q, rows, qs, kl, window, first, Tq, o, lse, d_o, workspace=ws)
+        assert torch.equal(dq, dq2) and torch.equal(dkv, dkv2)
+    _ok(dsa, ws)
+    near = torch.cat([torch.arange(first, device="cuda"), torch.arange(Tq - 1700, Tq, device="cuda")])
+    for b in range(B):
+        for at in range(Tq - 600, Tq, 100):
+            t = torch.arange(at, at + 100, device="cuda")
+            see = ref.window_sees(t[:, None], near, window, first)
+            r_dq, _, dq_off, _ = ref.backward(q[b, t], base[b, near], see, o[b, t], lse[b, t], d_o[b, t])
+            ref.within(dq[b, t], r_dq, dq_off, f"dq of {b} from {at}")
+
+
 # ---------------------------------------------------------------------------
 # both: equal bits, graphs, streams
 # ---------------------------------------------------------------------------
+
+def test_beside_other_streams(dsa):
+    """Pairs of CTAs whose two do not start together, as SMs fall free one by one: training steps
+    and decode steps on three streams, an FP8 product and large copies on two more."""
+    gen = _gen(29)
+    streams = [torch.cuda.Stream() for _ in range(5)]
+
+    def step(B, Tq, H, start, window, first):
+        S = start + Tq
+        base, q, d_o = _normal(gen, B, S, 576), _normal(gen, B, Tq, H, 576), _normal(gen, B, Tq, H, 512)
+        rows, qs, kl = dsa.Rows(base), _i32([start] * B), _i32([S] * B)
+        ws = dsa.new_workspace(max(dsa.workspace_bytes(op, B, Tq, S, H, window + first)
+                                   for op in (dsa.OP_MLA_WINDOW, dsa.OP_MLA_WINDOW_BWD)))
+        o, lse = _outputs(B, Tq, H)
+        dq, dkv = torch.zeros_like(q), torch.zeros_like(base)
+
+        def run(s):
+            dsa.mla_window_fwd(q, rows, qs, kl, window, first, S, o_lat=o, lse=lse, workspace=ws, stream=s)
+            dsa.mla_window_bwd(q, rows, qs, kl, window, first, S, o, lse, d_o, dq=dq, dkv=dkv,
+                               workspace=ws, stream=s)
+        return run, (o, lse, dq, dkv), ws
+
+    def decode(B, L, H):
+        base, q = _normal(gen, B, L + 1, 576), _normal(gen, B, 1, H, 576)
+        rows, kl, masks = dsa.Rows(base), _i32([L] * B), torch.ones((B, 1), dtype=torch.int64, device="cuda")
+        ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_TREE, B, 1, L + 1, H, 0))
+        o, lse = _outputs(B, 1, H)
+        return (lambda s: dsa.mla_tree_fwd(q, rows, masks, kl, L + 1, o_lat=o, lse=lse, workspace=ws, stream=s),
+                (o, lse), ws)
+
+    def product(M, N, K):
+        codes, scale = dsa.dsa_quant_fp8(_normal(gen, M * K // 128, 128))
+        w, w_scale = dsa.dsa_quant_fp8_weight(_normal(gen, N, K))
+        codes, scale = codes.view(M, K), scale.view(M, K // 128)
+        ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_LINEAR_FP8, M, 1, K, N, 0))
+        out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+        return (lambda s: dsa.dsa_linear_fp8(codes, scale, w, w_scale, out=out, workspace=ws, stream=s),
+                (out,), ws)
+
+    jobs = [step(76, 5, 96, 700, 300, 70), step(76, 5, 8, 900, 64, 0), decode(16, 2000, 96),
+            product(1024, 7168, 512)]
+    want = []
+    for run, outs, ws in jobs:
+        run(None)
+        _ok(dsa, ws)
+        want.append([t.clone() for t in outs])
+    big = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    copy = torch.empty_like(big)
+    torch.cuda.synchronize()
+    for i in range(600):
+        for s, (run, _, _) in zip(streams, jobs):
+            run(s)
+        if i % 3 == 0:
+            with torch.cuda.stream(streams[4]):
+                copy.copy_(big)
+    torch.cuda.synchronize()
+    for (_, outs, ws), expected in zip(jobs, want):
+        _ok(dsa, ws)
+        assert all(torch.equal(a, b) for a, b in zip(outs, expected))
+
 
 def test_equal_calls_give_equal_bits(dsa):
     case = (2, 100, 96, [0, 37], 50, 4, False)
