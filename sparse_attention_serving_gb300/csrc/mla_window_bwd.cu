@@ -483,18 +483,14 @@ struct Task {
   }
 };
 
-// PARTS: of P and dZ.
+// The tasks first, first + step, ... of one kind.  PARTS: of P and dZ.
 template <bool DKV, int PARTS>
-__global__ void __launch_bounds__(Prod::THREADS, 1)
-    product_kernel(const __grid_constant__ CUtensorMap tm_pz, const __grid_constant__ CUtensorMap tm_kv,
-                   const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                   const Params p, int tasks) {
+__device__ __forceinline__ void product(const CUtensorMap& tm_pz, const CUtensorMap& tm_kv, const CUtensorMap& tm_q,
+                                        const CUtensorMap& tm_do, const Params& p, uint8_t* sm, int first,
+                                        int step, int tasks) {
   using C = Prod;
   constexpr uint32_t IDESC = idesc_bf16(256, 256, DKV, true), IDESC_ROT = idesc_bf16(256, 64, DKV, true);
-  const int rank = blockIdx.x & 1, step = gridDim.x >> 1;
-  extern __shared__ uint8_t smem_raw[];
-  cluster_arrive_relaxed();
-  uint8_t* sm = smem_align1024(smem_raw);
+  const int rank = blockIdx.x & 1;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_MISC);    // even CTA
   uint64_t* empty = full + C::NS;
   uint64_t* land = empty + C::NS;
@@ -545,7 +541,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       if (used < C::NS) ++used;
       r.next();
     };
-    for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
+    for (int task = first; task < tasks && ok; task += step) {
       const Task<DKV> t(p, task, n);
       if (!t.there) continue;
       ++n;
@@ -656,7 +652,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
       more = 1;
       r.next();
     };
-    for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
+    for (int task = first; task < tasks && ok; task += step) {
       const Task<DKV> t(p, task, n);
       if (!t.there) continue;
       if (n > 0) ok = wait(dfree, (n - 1) & 1, s_abort, p.status, SITE_DF);
@@ -692,7 +688,7 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
     };
     int n = 0;
     bool ok = true;
-    for (int task = blockIdx.x >> 1; task < tasks && ok; task += step) {
+    for (int task = first; task < tasks && ok; task += step) {
       const Task<DKV> t(p, task, n);
       if (!t.there) continue;
       const bool some = t.some(p);
@@ -747,6 +743,25 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
+}
+
+// Both products in one launch: neither needs the other's results.  The first dq_pairs pairs
+// share dq's tasks, the others have a task of dkv each and follow as SMs fall free (a launch
+// for each: 3 x 301 tokens, 8 heads 49.0 us instead of 45.3, 4096 tokens 1.99 ms instead of
+// 1.97).
+template <int PARTS>
+__global__ void __launch_bounds__(Prod::THREADS, 1)
+    product_kernel(const __grid_constant__ CUtensorMap tm_pz, const __grid_constant__ CUtensorMap tm_kv,
+                   const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                   const __grid_constant__ Params p, int dq_pairs, int dq_tasks, int dkv_tasks) {
+  extern __shared__ uint8_t smem_raw[];
+  cluster_arrive_relaxed();
+  uint8_t* sm = smem_align1024(smem_raw);
+  const int pair = blockIdx.x >> 1;
+  if (pair < dq_pairs)
+    product<false, PARTS>(tm_pz, tm_kv, tm_q, tm_do, p, sm, pair, dq_pairs, dq_tasks);
+  else
+    product<true, PARTS>(tm_pz, tm_kv, tm_q, tm_do, p, sm, pair - dq_pairs, dkv_tasks, dkv_tasks);
 }
 
 // dkv of a row: its segments in order (and what earlier chunks left), four dims a thread.
@@ -897,11 +912,9 @@ dsa_status_t window_bwd_launch(const WindowBwdArgs& a, cudaStream_t stream) {
     dsa_status_t st = launch_pairs("pz_kernel", q.parts == 2 ? pz_kernel<true> : pz_kernel<false>, some, Pz::THREADS, Pz::SMEM, stream, tq_tile,
                                    td_tile, tk, p);
     if (st == DSA_OK)
-      st = launch_pairs("product_kernel", q.parts == 2 ? product_kernel<false, 2> : product_kernel<false, 1>, some, Prod::THREADS, Prod::SMEM, stream,
-                        tp, tk, tq, td, p, static_cast<int>(tiles));
-    if (st == DSA_OK)
-      st = launch_pairs("product_kernel", q.parts == 2 ? product_kernel<true, 2> : product_kernel<true, 1>, sums, Prod::THREADS,
-                        Prod::SMEM, stream, tp, tk, tq, td, p, static_cast<int>(sums));
+      st = launch_pairs("product_kernel", q.parts == 2 ? product_kernel<2> : product_kernel<1>, some + sums,
+                        Prod::THREADS, Prod::SMEM, stream, tp, tk, tq, td, p, static_cast<int>(some),
+                        static_cast<int>(tiles), static_cast<int>(sums));
     if (st != DSA_OK) return st;
     launch_overlapped(reduce_kernel, static_cast<unsigned>(static_cast<int64_t>(f.B) * f.max_kv_len), 144, 0,
                       0, stream, p);
