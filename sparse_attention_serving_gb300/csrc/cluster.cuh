@@ -83,7 +83,10 @@ __device__ __forceinline__ void cluster_sync() {
       "barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
           : "memory");
 }
-// The same in two halves and without ordering memory: only keeps CTAs alive.
+// The same in two halves; relaxed: without ordering memory, only keeps CTAs alive.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_arrive_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }

@@ -246,6 +246,13 @@ struct Line {
     return sum;
   }
   __device__ __forceinline__ Line(const Params& pp, int pair) : p(pp) {
+    if (!p.cut && p.pairs == p.B * p.tiles) {          // a unit each
+      b = pair / p.tiles;
+      tile = pair % p.tiles;
+      measure(b, s, tiles, cost);
+      left = tile < tiles ? cost : 0;
+      return;
+    }
     // at least two blocks each (5 trees of 33 tokens, 120 blocks: 34 us with all 76 pairs
     // at work, 28 with 60): the last pairs may have nothing
     const int64_t all = total();
@@ -430,7 +437,13 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
     if (warp == 0) {
       // ---- the own page's K, chunk by chunk; beside the first block's, Q's: the
       // products that read a chunk of the unit before are those that free K's slot ----
+      // (the lengths are looked up while the other warps and the other CTA get ready)
+      if (!AGAIN) {
+        pdl_wait();
+        pdl_start_next();
+      }
       Line<R> line(p, pair);
+      if (!AGAIN) cluster_wait();
       Unit u;
       Ring<C::NK> r;
       Stretch mine{-1, 0, -1, 0};
@@ -944,13 +957,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       tmem_relinquish_pair();
     }
     tc_fence_before();
-    __syncthreads();
-    cluster_sync();
+    cluster_arrive();
+    if (warp != 0) {            // warp 0: in roles
+      cluster_wait();
+      pdl_wait();
+      pdl_start_next();
+    }
     tc_fence_after();
-    tmem = *x.tslot;
+    tmem = warp != 0 ? *x.tslot : 0;
   }
-  pdl_wait();
-  pdl_start_next();
   roles<R, false>(tm_q, tm_kv, p, sm, tmem);
   __syncwarp();
   tc_fence_before();
