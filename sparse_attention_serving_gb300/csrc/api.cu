@@ -188,8 +188,8 @@ size_t dsa_workspace_bytes(dsa_op_t op, int B, int Tq, int max_kv_len, int heads
     }
     if (heads > 0) {
       const int64_t span = topk <= 0 ? 1 : topk < max_kv_len ? topk : max_kv_len;
-      if (op == DSA_OP_MLA_TREE) extra = dense_scratch_bytes(B, Tq, heads, max_kv_len);
-      if (op == DSA_OP_MLA_WINDOW) extra = dense_scratch_bytes(B, Tq, heads, span);
+      if (op == DSA_OP_MLA_TREE) extra = dense_scratch_bytes(B, Tq, heads, max_kv_len, true);
+      if (op == DSA_OP_MLA_WINDOW) extra = dense_scratch_bytes(B, Tq, heads, span, false);
       if (op == DSA_OP_MLA_WINDOW_BWD)
         extra = window_bwd_scratch_bytes(B, Tq, heads, max_kv_len, span);
     }

@@ -51,7 +51,7 @@ struct DenseArgs {
   size_t scratch_bytes;
 };
 // span: the keys that one query may see at most
-size_t dense_scratch_bytes(int B, int T, int H, int64_t span);
+size_t dense_scratch_bytes(int B, int T, int H, int64_t span, bool tree);
 dsa_status_t dense_fwd_launch(const DenseArgs& a, cudaStream_t stream);
 
 struct WindowBwdArgs {

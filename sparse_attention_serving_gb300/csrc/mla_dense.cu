@@ -1063,17 +1063,19 @@ struct Plan {
   int R, tiles, blocks, pairs;      // blocks: of a unit, at most
   bool cut;
 };
-// span: the keys that one query may see at most.  Units are cut where the pair with
-// the most whole ones would have three blocks more to do than the mean: the pieces'
-// outputs and their joining take about as long (9 us).
-Plan plan(int B, int T, int H, int64_t span) {
+// span: the keys that one query may see at most; tree: they are all of the sequence's, from
+// row 0.  Units are cut where the pair with the most whole ones would have three blocks more
+// to do than the mean, and more than four: the pieces' outputs and their joining take about
+// as long (1 x 1 over 400 rows, four blocks: 15.3 us whole, 15.6 cut; over 600, five: 17.8
+// whole, 15.8 cut; 4 x 1 over 300: 13.6 whole, 17.8 cut).
+Plan plan(int B, int T, int H, int64_t span, bool tree) {
   Plan q{};
   const int64_t rows = static_cast<int64_t>(T) * H, most = num_sms() / 2;
   auto set = [&](int R) {
     q.R = R;
     q.tiles = static_cast<int>((rows + 2 * R - 1) / (2 * R));
     const int64_t tokens = (2 * R + H - 2) / H + 1;      // of a unit
-    q.blocks = static_cast<int>((span + tokens + 64) / 128 + 2);
+    q.blocks = static_cast<int>(tree ? (span + 127) / 128 : (span + tokens + 64) / 128 + 2);
   };
   // 96 rows a CTA copy the least per row; 64 have the shorter chain from a block to the
   // next, which counts where a pair has few blocks (5 trees of 33 tokens, 8 heads: 25.5
@@ -1081,7 +1083,8 @@ Plan plan(int B, int T, int H, int64_t span) {
   set(rows <= 96 ? 48 : rows <= 128 ? 64 : 96);
   if (q.R == 96 && static_cast<int64_t>(B) * q.tiles * q.blocks < 4 * most) set(64);
   const int64_t units = static_cast<int64_t>(B) * q.tiles;
-  q.cut = (units + most - 1) / most * q.blocks * most > units * q.blocks + 3 * most;
+  const int64_t whole = (units + most - 1) / most * q.blocks * most;
+  q.cut = whole > units * q.blocks + 3 * most && whole > 4 * most;
   const int64_t pieces = units * (q.cut ? q.blocks : 1);
   q.pairs = static_cast<int>(pieces < most ? pieces : most);
   return q;
@@ -1114,8 +1117,8 @@ dsa_status_t launch(const DenseArgs& a, const Plan& q, const Params& p, cudaStre
 
 }  // namespace dense
 
-size_t dense_scratch_bytes(int B, int T, int H, int64_t span) {
-  return dense::part_bytes(dense::plan(B, T, H, span));
+size_t dense_scratch_bytes(int B, int T, int H, int64_t span, bool tree) {
+  return dense::part_bytes(dense::plan(B, T, H, span, tree));
 }
 
 dsa_status_t dense_fwd_launch(const DenseArgs& a, cudaStream_t stream) {
@@ -1123,7 +1126,7 @@ dsa_status_t dense_fwd_launch(const DenseArgs& a, cudaStream_t stream) {
   int64_t span = a.max_kv_len;
   if (a.tree == nullptr && static_cast<int64_t>(a.window) + a.n_first < span)
     span = a.window + a.n_first > 0 ? a.window + a.n_first : 1;
-  const Plan q = plan(a.B, a.T, a.H, span);
+  const Plan q = plan(a.B, a.T, a.H, span, a.tree != nullptr);
   if (a.scratch_bytes < part_bytes(q)) return DSA_ERR_WORKSPACE_TOO_SMALL;
   Params p{};
   p.q = a.q_lat;
