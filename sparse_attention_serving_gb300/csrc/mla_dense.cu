@@ -1004,30 +1004,40 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
   const int pair = blockIdx.x / (R / 2), r = blockIdx.x % (R / 2) * 4 + (threadIdx.x >> 5);
   pdl_wait();
   pdl_start_next();
-  const Stretch mine = p.stretch[pair];
-  if (mine.head < 0) return;
-  const int b = mine.head / p.tiles, g = mine.head % p.tiles * 2 * R + r;
-  if (g >= seq_of(p.m, b).n * p.H) return;
-  // the pieces: mine.slot, then 2k of the next pairs for as long as they go on with it
-  const int lane = threadIdx.x & 31;
-  int n = 1;
-  for (int k = pair + 1 + lane;; k += 32) {
-    const bool on = k < p.pairs && p.stretch[k].first == mine.head && p.stretch[k].j0 > 0;
-    const unsigned off = ~__ballot_sync(0xffffffffu, on);
-    n += off != 0 ? __ffs(off) - 1 : 32;
-    if (off != 0) break;
+  // the pieces: the pair's last one, then the first ones of the next pairs for as long as they
+  // go on with the unit.  What may be wanted is read at once (pairs that have had no unit
+  // hold anything: not used)
+  const int lane = threadIdx.x & 31, next = pair + lane;
+  Stretch mine{-1, 0, -1, 0};
+  float l = -INFINITY;
+  if (next < p.pairs) {
+    mine = p.stretch[next];
+    if (lane > 0) l = p.part_lse[static_cast<int64_t>(next) * 4 * R + r];
   }
-  auto at = [&](int k) { return static_cast<int64_t>(k == 0 ? mine.slot : 2 * (pair + k)) * 2 * R + r; };
+  const int head = __shfl_sync(0xffffffffu, mine.head, 0), slot = __shfl_sync(0xffffffffu, mine.slot, 0);
+  if (head < 0) return;
+  const int b = head / p.tiles, g = head % p.tiles * 2 * R + r;
+  if (lane == 0) l = p.part_lse[static_cast<int64_t>(slot) * 2 * R + r];
+  if (g >= seq_of(p.m, b).n * p.H) return;
+  unsigned off = ~__ballot_sync(0xffffffffu, lane == 0 || (mine.first == head && mine.j0 > 0));
+  int n = off != 0 ? __ffs(off) - 1 : 32;
+  for (int k = next + 32; off == 0; k += 32) {
+    const bool on = k < p.pairs && p.stretch[k].first == head && p.stretch[k].j0 > 0;
+    off = ~__ballot_sync(0xffffffffu, on);
+    n += off != 0 ? __ffs(off) - 1 : 32;
+  }
+  auto at = [&](int k) { return static_cast<int64_t>(k == 0 ? slot : 2 * (pair + k)) * 2 * R + r; };
   // their weights, a lane each
-  float top = -INFINITY;
-  for (int k = lane; k < n; k += 32) top = fmaxf(top, p.part_lse[at(k)]);
+  if (lane >= n) l = -INFINITY;
+  float top = l;
+  for (int k = lane + 32; k < n; k += 32) top = fmaxf(top, p.part_lse[at(k)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float sum = 0.f, acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
   for (int k0 = 0; k0 < n; k0 += 32) {
-    const float l = k0 + lane < n ? p.part_lse[at(k0 + lane)] : -INFINITY;
+    if (k0 > 0) l = k0 + lane < n ? p.part_lse[at(k0 + lane)] : -INFINITY;
     const float w = l == -INFINITY ? 0.f : exp2f(l - top);
     const int m = min(32, n - k0);
 #pragma unroll 2
