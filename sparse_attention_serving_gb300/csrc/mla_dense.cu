@@ -32,7 +32,9 @@
 // its own: units put back into the line cost every call 1.1 us at that end.  A unit some of
 // whose queries do not see a row of the sequence that holds an infinity or a NaN (0 * NaN
 // would reach them) goes to attend_row (33 ms there); the waits of the others last as long
-// as it moves on.  Rows behind the sequence, in its last page, are zeroed in V before use.
+// as it moves on.  So does one with a reference that FP32 rounds too coarsely: beyond 2^28 it
+// is off the maximum by 8 and more, beyond 2^31 by more than an exponent holds (LOST).
+// Rows behind the sequence, in its last page, are zeroed in V before use.
 //
 // Persistent: the blocks of all units stand in one line, and every pair of SMs takes
 // an equal stretch of it (whole units where there are many).  A unit that is cut has
@@ -55,6 +57,7 @@ namespace dense {
 constexpr int THREADS = 384;
 constexpr int REDO = 1024;                // units of a pair that may be done twice; more: attend_row
 constexpr float FAR = 80.f;               // exponents that P may reach: 2^80 times 2^47 is FP32's range
+constexpr float LOST = 0x1p-16f;          // a sum of P that only a reference above the maximum leaves
 
 template <int R_>
 struct Cfg {
@@ -811,6 +814,9 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
         const float other = exchange(s_sum, at, l_sum);
         l_sum = half == 0 ? l_sum + other : other + l_sum;
       }
+      // P of the maximum is 2^0 but for the reference's rounding: one that is far too high shows in
+      // the sum, one far too low in the peak
+      if (m_ref > -INFINITY && l_sum < LOST) peak = INFINITY;
       if (live && half == 0) {
         const float lse2 = l_sum == 0.f ? -INFINITY : m_ref + log2f(l_sum);
         if (!u.whole())
