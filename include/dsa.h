@@ -469,6 +469,8 @@ dsa_status_t dsa_cache_append_rope(const float* k_pre, const uint16_t* kv_new,
  * A token that sees nothing gets o_lat = 0 and lse = -inf.  What a row holds (an
  * infinity or a NaN too) reaches only the tokens that see it; such a row is fast
  * behind the sequence's last, and slow where some tokens do not see it.
+ * Finite values whose magnitudes add up to less than 2^107 over a token's rows give
+ * finite outputs, whatever the scores.
  * kv_len[b] < 0, kv_len[b] + n_draft[b] > max_kv_len (the sequence's tokens then see
  * nothing), n_draft outside [0, T] (taken as the nearer bound) and pages outside the
  * pool (not seen) are recorded as DSA_ERR_BAD_INDEX.
@@ -490,7 +492,8 @@ dsa_status_t mla_tree_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const uin
  *   window >= 0, n_first >= 0      both 0: every query gets o_lat = 0, lse = -inf
  * Only rows that some query sees are needed (a cache may have dropped the rest:
  * pages in between are not looked up).  What a row holds reaches only the queries
- * that see it.  A query at or beyond kv_len[b], kv_len[b] > max_kv_len, q_start < 0
+ * that see it.  Finite values whose magnitudes add up to less than 2^107 over a
+ * query's rows give finite outputs, whatever the scores.  A query at or beyond kv_len[b], kv_len[b] > max_kv_len, q_start < 0
  * (nothing seen) and pages outside the pool (not seen): DSA_ERR_BAD_INDEX.
  * Supported: 1 <= H <= 128.  Equal calls give equal bits.
  * Workspace: dsa_workspace_bytes(DSA_OP_MLA_WINDOW, B, Tq, max_kv_len, H, window + n_first).

@@ -150,6 +150,11 @@ __device__ __forceinline__ void mbar_expect_tx_cluster_release(uint32_t bar_clus
 __device__ __forceinline__ void st_cluster_u32(uint32_t saddr, uint32_t rank, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_u32(saddr, rank)), "r"(v) : "memory");
 }
+// Bits set in a word of CTA `rank`.
+__device__ __forceinline__ void or_cluster_u32(uint32_t saddr, uint32_t rank, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(mapa_u32(saddr, rank)), "r"(v)
+               : "memory");
+}
 
 // ---------------------------------------------------------------------------
 // CTA pairs (cta_group::2): two CTAs of a cluster whose ranks differ in the

@@ -34,6 +34,10 @@
 // would reach them) goes to attend_row (33 ms there); the waits of the others last as long
 // as it moves on.  So does one with a reference that FP32 rounds too coarsely: beyond 2^28 it
 // is off the maximum by 8 and more, beyond 2^31 by more than an exponent holds (LOST).
+// P up to 2^80 leaves the FP32 sums 2^47 for the values: where a row's P passed 2^20 and its
+// O^T is not finite although its sum of P is, its unit is marked, and all warps do the marked
+// units' rows by attend_row at the end (looking for it in every unit's outputs took 1 % of
+// a call; in those alone 2,048 queries 408 -> 409 us, 417 -> 421 where all have such a row).
 // Rows behind the sequence, in its last page, are zeroed in V before use.
 //
 // Persistent: the blocks of all units stand in one line, and every pair of SMs takes
@@ -57,6 +61,7 @@ namespace dense {
 constexpr int THREADS = 384;
 constexpr int REDO = 1024;                // units of a pair that may be done twice; more: attend_row
 constexpr float FAR = 80.f;               // exponents that P may reach: 2^80 times 2^47 is FP32's range
+constexpr float RISE = 20.f;              // above it, P may be what takes P V out of FP32's range
 constexpr float LOST = 0x1p-16f;          // a sum of P that only a reference above the maximum leaves
 
 template <int R_>
@@ -74,7 +79,7 @@ struct Cfg {
   static constexpr int OFF_K = OFF_P + 2 * NP * QCH;
   static constexpr int OFF_V = OFF_K + NK * CHUNK;
   static constexpr int OFF_MISC = OFF_V + NV * 2 * CHUNK;
-  static constexpr int MISC = 1024 + 16 * R + (HALVES == 2 ? 2048 : 0) + 5 * REDO / 8;
+  static constexpr int MISC = 1024 + 16 * R + (HALVES == 2 ? 2048 : 0) + 6 * REDO / 8;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   static constexpr uint32_t S_COL = 4 * R;
   static constexpr int SW = 128 / HALVES;             // columns of a score buffer
@@ -359,14 +364,16 @@ struct Shared {
   uint64_t *ufull, *uempty;      // [UNITS]
   uint32_t* tslot;
   volatile int* s_abort;         // [2] the second moves while attend_row goes on
-  volatile int* s_slow;          // [2] x unit + 1 of which a row is far, of which a row needs attend_row
+  volatile int* s_slow;          // [2] x unit + 1 of which a row is far, needs attend_row, is above RISE
   volatile int *s_any, *s_go;    // units are to be done again; the other CTA says so too
+  volatile uint32_t* s_past;     // units stand in s_beyond (of either CTA: both are told)
   Unit* s_unit;                  // [UNITS]
   float* s_inv;                  // [2][2R]
   float *s_top, *s_sum;          // HALVES = 2: [2][2][64] maxima, sums
   uint32_t* s_redo;              // a bit a unit
   uint32_t* s_noted;             // [4 warps] the warp's rows have left their maxima
-  static_assert(BARS * 8 + 36 <= 512, "misc");
+  uint32_t* s_beyond;            // a bit a unit, the last for all from there on: P times V left FP32's range
+  static_assert(BARS * 8 + 48 <= 512, "misc");
   static_assert(UNITS * sizeof(Unit) <= 512, "misc");
 
   __device__ __forceinline__ explicit Shared(uint8_t* sm) {
@@ -390,14 +397,16 @@ struct Shared {
     tslot = reinterpret_cast<uint32_t*>(uempty + UNITS);
     s_abort = reinterpret_cast<volatile int*>(tslot + 1);
     s_slow = reinterpret_cast<volatile int*>(tslot + 3);
-    s_any = reinterpret_cast<volatile int*>(tslot + 7);
+    s_any = reinterpret_cast<volatile int*>(tslot + 9);
     s_go = s_any + 1;
+    s_past = reinterpret_cast<volatile uint32_t*>(s_any + 2);
     s_unit = reinterpret_cast<Unit*>(sm + C::OFF_MISC + 512);
     s_inv = reinterpret_cast<float*>(sm + C::OFF_MISC + 1024);
     s_top = s_inv + 4 * R;
     s_sum = s_top + 256;
-    s_redo = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC + C::MISC - 5 * REDO / 8);
+    s_redo = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC + C::MISC - 6 * REDO / 8);
     s_noted = s_redo + REDO / 32;
+    s_beyond = s_noted + 4 * (REDO / 32);
   }
   __device__ __forceinline__ void barriers(int rank) const {
     for (int k = 0; k < C::NK; ++k) mbar_init(&kfull[k], 1), mbar_init(&kempty[k], 1);
@@ -420,6 +429,34 @@ struct Shared {
   }
 };
 
+// Whether P V, of 32 dims and `here` rows, is an infinity or a NaN in a row whose sum of P is
+// neither: marks the unit in both CTAs.  By a warp.
+__device__ __noinline__ void mark_beyond(uint32_t taddr, int here, const float* inv, int no, uint32_t* beyond,
+                                         volatile uint32_t* past) {
+  bool some = false;
+#pragma unroll 1
+  for (int c = 0; c < here; c += 32) {
+    uint32_t x[32];
+    tmem_ld32(taddr + c, x);
+    tmem_ld_wait_regs(x);
+    float sum = 0.f;                                     // NaN with an infinity or a NaN
+#pragma unroll
+    for (int e = 0; e < 32; ++e) sum = fmaf(__uint_as_float(x[e]), 0.f, sum);
+    if (!__any_sync(0xffffffffu, sum != 0.f)) continue;
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      some |= c + e < here && inv[c + e] < INFINITY && !(fabsf(__uint_as_float(x[e])) < INFINITY);
+  }
+  if (__any_sync(0xffffffffu, some)) {
+    const int k = min(no, REDO - 1), lane = threadIdx.x & 31;
+    if (lane < 2) {
+      or_cluster_u32(smem_u32(beyond + (k >> 5)), lane, 1u << (k & 31));
+      or_cluster_u32(smem_u32(const_cast<uint32_t*>(past)), lane, 1u);
+    }
+    __syncwarp();
+  }
+}
+
 // What the warps do from the first unit to the last.  AGAIN: only the units that have to
 // be done a second time.
 template <int R, bool AGAIN>
@@ -429,8 +466,8 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
   constexpr uint32_t IDESC_S = idesc_bf16(256 / C::HALVES, 128, false, false);
   constexpr uint32_t IDESC_O = idesc_bf16(256, 2 * R, true, false);
   const auto [kfull, kempty, vfull, vempty, sfull, sfree, pready, odone, ofull, ofree, lfull, lpeer, lfree,
-              vland, drain, ufull, uempty, tslot, s_abort, s_slow, s_any, s_go, s_unit, s_inv, s_top, s_sum,
-              s_redo, s_noted] = Shared<R>(sm);
+              vland, drain, ufull, uempty, tslot, s_abort, s_slow, s_any, s_go, s_past, s_unit, s_inv, s_top,
+              s_sum, s_redo, s_noted, s_beyond] = Shared<R>(sm);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
   // An issuer that gives up: its MMAs are complete before the pair leaves.  (Otherwise those
@@ -830,14 +867,16 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
         *to = inv;
         st_cluster_u32(smem_u32(to), rank ^ 1, __float_as_uint(inv));
       }
-      if (__any_sync(0xffffffffu, live && peak > FAR)) {
-        if (live) note()[half] = m_ref + peak;
+      if (__any_sync(0xffffffffu, live && peak > RISE)) {
+        const bool far = __any_sync(0xffffffffu, live && peak > FAR);
         const bool bad = __any_sync(0xffffffffu, live && peak == INFINITY);
+        if (far && live) note()[half] = m_ref + peak;
         if (lane == 0) {
-          if (u.no < REDO) s_noted[sub * (REDO / 32) + (u.no >> 5)] |= 1u << (u.no & 31);
-          for (int k = 0; k <= bad; ++k) {
-            s_slow[2 * bu + k] = at + 1;
-            st_cluster_u32(smem_u32(const_cast<int*>(s_slow + 2 * bu + k)), rank ^ 1, at + 1);
+          if (far && u.no < REDO) s_noted[sub * (REDO / 32) + (u.no >> 5)] |= 1u << (u.no & 31);
+          for (int k = 0; k < 3; ++k) {
+            if (k == 0 ? !far : k == 1 && !bad) continue;
+            s_slow[3 * bu + k] = at + 1;
+            st_cluster_u32(smem_u32(const_cast<int*>(s_slow + 3 * bu + k)), rank ^ 1, at + 1);
           }
         }
       }
@@ -867,7 +906,7 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
       if (ok && u.nb > 0) ok = wait(ofull, n & 1, s_abort, p.status, SITE_O);
       if (!ok) break;
       tc_fence_after();
-      const bool slow = s_slow[2 * bu] == at + 1;
+      const bool slow = s_slow[3 * bu] == at + 1, rise = s_slow[3 * bu + 2] == at + 1;
 #pragma unroll 1
       for (int m = 0; m < 2; ++m) {
         const int dim = 256 * rank + 128 * m + 32 * sub + lane;
@@ -904,6 +943,7 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
             }
           }
         }
+        if (rise && u.nb > 0 && !slow) mark_beyond(taddr, here, inv, u.no, s_beyond, s_past);
         tc_fence_before();
         __syncwarp();
         if (u.nb > 0 && lane == 0) {                     // these columns may be overwritten
@@ -914,7 +954,7 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm_q, const CUtensorMap
       if (u.nb > 0) ++n;
       if (slow) {
         // (both CTAs come to the same)
-        const bool again = !AGAIN && u.no < REDO && s_slow[2 * bu + 1] != at + 1;
+        const bool again = !AGAIN && u.no < REDO && s_slow[3 * bu + 1] != at + 1;
         for (int r = rank * R + sub; !again && r < min(here, rank * R + R); r += 4) {
           attend_row(p, u.s, u.pages, u.k0, u.k1, u.b, u.g0 + r, parts ? p.part_o + (part + r) * kVlat : nullptr,
                      parts ? p.part_lse + part + r : nullptr);
@@ -942,6 +982,28 @@ __device__ __noinline__ void roles_again(const CUtensorMap& tm_q, const CUtensor
   roles<R, true>(tm_q, tm_kv, p, sm, tmem);
 }
 
+// The pair's units marked in s_beyond, row by row: means of finite values, of which P V (P up
+// to 2^FAR) was not finite.  By all warps of both CTAs.
+template <int R>
+__device__ __noinline__ void by_rows(const Params& p, uint8_t* sm) {
+  const Shared<R> x(sm);
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, warp = threadIdx.x >> 5;
+  Line<R> line(p, pair);
+  Unit next;
+  for (int no = 0; line.next(next); ++no) {
+    const int k = min(no, REDO - 1);
+    if (!(x.s_beyond[k >> 5] >> (k & 31) & 1)) continue;
+    __syncthreads();
+    if (threadIdx.x == 0) x.s_unit[0] = next;
+    __syncthreads();
+    const Unit& u = x.s_unit[0];
+    const int64_t part = static_cast<int64_t>(2 * pair + (no > 0)) * 2 * R;
+    for (int r = 2 * warp + rank; r < min(2 * R, u.rows - u.g0); r += 2 * (THREADS / 32))
+      attend_row(p, u.s, u.pages, u.k0, u.k1, u.b, u.g0 + r, u.whole() ? nullptr : p.part_o + (part + r) * kVlat,
+                 u.whole() ? nullptr : p.part_lse + part + r);
+  }
+}
+
 template <int R>
 __global__ void __launch_bounds__(THREADS, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
@@ -957,11 +1019,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       x.barriers(rank);
       x.s_abort[0] = x.s_abort[1] = 0;
       x.s_any[0] = x.s_go[0] = 0;
-      for (int k = 0; k < 4; ++k) x.s_slow[k] = 0;
+      x.s_past[0] = 0;
+      for (int k = 0; k < 6; ++k) x.s_slow[k] = 0;
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_kv);
     }
-    if (tid < 5 * REDO / 32) x.s_redo[tid] = 0;
+    if (tid < 6 * REDO / 32) x.s_redo[tid] = 0;
     __syncwarp();
     cluster_wait();             // the other CTA runs
     if (warp == 2) {
@@ -991,7 +1054,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (tid == 0) {
       for (int k = 0; k < Shared<R>::BARS; ++k) mbar_inval(&x.kfull[k]);
       x.barriers(rank);
-      for (int k = 0; k < 4; ++k) x.s_slow[k] = 0;
+      for (int k = 0; k < 6; ++k) x.s_slow[k] = 0;
     }
     __syncthreads();
     cluster_sync();
@@ -1006,6 +1069,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
+  if (x.s_past[0] != 0 && x.s_abort[0] == 0) by_rows<R>(p, sm);
 }
 
 // Joins the pieces of the unit that pair blockIdx.x / 2R begins and does not end:

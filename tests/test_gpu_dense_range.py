@@ -101,3 +101,58 @@ def test_scores_far_from_zero(dsa, case, scores):
     off = (2 * ref.HALF + ref.HALF ** 2 + 2.0 ** -20) * v.abs()
     ref.within(o, v.expand(o.shape), off.expand(o.shape), "o_lat")
     ref.within(lse, z, z.abs() * 2.0 ** -22, "lse")
+
+
+@pytest.mark.parametrize("rise", [30.0, 55.0, -55.0])
+@pytest.mark.parametrize("case", CASES + [(80, 1, 96, 500, 300, True), (77, 1, 128, 500, 300, False)], ids=str)
+def test_large_values_behind_a_rise(dsa, case, rise):
+    """Values of 2^100 behind scores that rise (from the first keys on, or above them) by less than what
+    has a unit done again: P times V leaves FP32's range, the weighted mean does not."""
+    B, T, H, L, at, tree = case
+    gen = _gen(51)
+    q = torch.zeros((B, T, H, 576), dtype=torch.bfloat16, device="cuda")
+    q[..., DIM] = 1.0
+    q[..., DIM + 1:] = _normal(gen, B, T, H, 576 - DIM - 1)
+    base = _normal(gen, B, L + T, 576)
+    base[..., :512] *= 2.0 ** 100
+    base[..., DIM] = 0
+    base[:, at:at + 3, DIM] = rise / ref.SCALE
+    rows, kl = dsa.Rows(base), _i32([L] * B)
+    masks = torch.ones((B, T), dtype=torch.int64, device="cuda") << torch.arange(T, device="cuda")
+    t = torch.arange(L, L + T, device="cuda")[:, None]
+    s = torch.arange(L + T, device="cuda")
+    if tree:
+        o, lse = dsa.mla_tree_fwd(q, rows, masks, kl, L + T)
+        see = (s < L) | (s == t)
+    else:
+        o, lse = dsa.mla_window_fwd(q, rows, kl, _i32([L + T] * B), L + T, 0, L + T)
+        see = s <= t
+    for b in range(B):
+        for i in range(0, T, 100):
+            part = slice(i, min(i + 100, T))
+            r_o, r_lse, o_off, lse_off = ref.forward(q[b, part], base[b], see[part])
+            ref.within(o[b, part], r_o, o_off, "o_lat")
+            ref.within(lse[b, part], r_lse, lse_off, "lse")
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_a_row_that_all_see_makes_no_zeros(dsa, value):
+    """A row of the prefix that holds an infinity or a NaN, and a rise: every token's outputs say so, as
+    the formula's do; the next sequence's do not."""
+    gen = _gen(52)
+    B, T, H, L = 2, 4, 96, 700
+    q, base = _normal(gen, B, T, H, 576), _normal(gen, B, L + T, 576)
+    base[0, 300, 5] = value
+    q[..., DIM] = 1.0
+    base[:, 400, DIM] = 40.0 / ref.SCALE
+    masks = torch.ones((B, T), dtype=torch.int64, device="cuda") << torch.arange(T, device="cuda")
+    o, lse = dsa.mla_tree_fwd(q, dsa.Rows(base), masks, _i32([L] * B), L + T)
+    z = torch.einsum("thr,nr->thn", q[0].double(), base[0].double())[..., 300]
+    hit = z != -math.inf                                # there the weight is 0, and 0 * inf at dim 5
+    assert not torch.isfinite(lse[0][hit] + o[0][hit].float().sum(-1)).any()
+    if value == math.inf:
+        assert torch.isfinite(lse[0][~hit]).all() and not torch.isfinite(o[0][~hit][:, 5]).any()
+    see = torch.cat([torch.ones((T, L), dtype=torch.bool), torch.eye(T, dtype=torch.bool)], 1).cuda()
+    r_o, r_lse, o_off, lse_off = ref.forward(q[1], base[1], see)
+    ref.within(o[1], r_o, o_off, "o_lat")
+    ref.within(lse[1], r_lse, lse_off, "lse")
