@@ -518,7 +518,8 @@ dsa_status_t mla_window_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const i
  *   dkv                 BF16   rows numbered like kv's ([B, seq_stride, 576]):
  *                       rows 0 .. kv_len[b]-1 are written (0 where no query of the
  *                       call sees them), the rows behind them left as they were
- * Sums are FP32 and rounded once; p and dz are rounded to BF16 for the products.
+ * Sums are FP32 and rounded once; p and dz are rounded to BF16 for the products (each
+ * of the products that add up to a gradient is off by up to 2^-8 of itself).
  * They are added in a fixed order: equal calls give equal bits.
  * A sequence with kv_len[b] > max_kv_len or q_start[b] < 0 gets dq = 0 and no dkv;
  * errors as for mla_window_fwd.  A paged kv: DSA_ERR_UNSUPPORTED.

@@ -27,11 +27,12 @@
 // in length and are dealt out as SMs fall free): the next task's
 // copies (pz: of its q and d_o too, chunk by chunk beside the first keys) and first
 // products run while the last one's results are written out.
-// Tiles go in chunks where P and dZ of all would take more than kChunkBytes.  For few
-// rows, where single roundings of dZ show in the result (dq off by up to 1.6 times its
-// own rounding; over many rows they average to 1.4), P and dZ are each two BF16 numbers,
-// the second what the first's rounding left: their products are added too, for a
-// microsecond or two.
+// Tiles go in chunks where P and dZ of all would take more than kChunkBytes.
+// P and dZ are rounded to BF16 once, whatever the call's sizes: each of the products that
+// add up to a gradient is off by up to 2^-8, independently, so that dq and dkv are off by
+// sqrt(2) times their own final rounding (root mean square; 1.0 to 1.7 times for a few rows
+// of a few keys).  A second BF16 number for what that leaves would double what the products
+// multiply, 1,664 of a pair's 2,816 dims, and P and dZ in the workspace.
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -47,7 +48,6 @@ using namespace dense;
 constexpr int X = 128;                              // rows of a tile
 constexpr int BLOCK = X * 128;                      // bytes of a block: 128 rows x 64 keys
 constexpr int64_t kChunkBytes = int64_t(4) << 30;   // P and dZ at a time
-constexpr int64_t FEW = 2048;                       // rows up to which P and dZ are in two parts
 constexpr int TASKS = 600;                          // dkv tasks aimed at: about eight a pair of SMs
 
 enum : uint32_t {
@@ -58,7 +58,6 @@ enum : uint32_t {
 
 struct Plan {
   int RT, RC, np;        // tiles of a sequence, of a chunk; pages a tile may see at most
-  int parts;             // of P and dZ: 1 or 2
   int KT, KF;            // tiles of 256 keys; those that hold first tokens
   int seg, G, nk;        // tiles of a segment; segments of a chunk; key tiles that a segment's
                          // windows reach
@@ -76,7 +75,7 @@ struct Params {
   const uint16_t* d_o;
   const float* lse;
   float2* rows;          // [B, T * H] lse (base 2), D
-  uint8_t* pz;           // a block of zeros, then [B, RC, np, parts, P | dZ] blocks
+  uint8_t* pz;           // a block of zeros, then [B, RC, np, P | dZ] blocks
   float* part;           // [B, G, nk + KF, 256, 576]
   float* acc;            // [B, max_kv_len, 576] between chunks
   uint16_t* dq;
@@ -84,11 +83,9 @@ struct Params {
   int first_chunk, last_chunk;
   uint32_t* status;
 
-  // first row (128 bytes each) of a block in the workspace's tensor map; which: P and
-  // dZ, then their second parts
-  template <int PARTS>
+  // first row (128 bytes each) of a block in the workspace's tensor map; which: P, dZ
   __device__ __forceinline__ int64_t block_row(int b, int rt, int k, int which) const {
-    return X + (((static_cast<int64_t>(b) * q.RC + rt - rt0) * q.np + k) * 2 * PARTS + which) * X;
+    return X + (((static_cast<int64_t>(b) * q.RC + rt - rt0) * q.np + k) * 2 + which) * X;
   }
 };
 
@@ -192,7 +189,6 @@ __device__ __forceinline__ Tile tile_at(const Params& p, int task) {
   return t;
 }
 
-template <bool TWO>
 __global__ void __launch_bounds__(Pz::THREADS, 1)
     pz_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
               const __grid_constant__ CUtensorMap tm_kv, const Params p) {
@@ -353,7 +349,7 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         // the lane pair's two keys in the two blocks: row r at 128 r, 16-byte units xor r
-        uint8_t* dst = p.pz + 128 * p.block_row<TWO ? 2 : 1>(t.b, t.rt, k, 0) + (key & 6) * 2;
+        uint8_t* dst = p.pz + 128 * p.block_row(t.b, t.rt, k, 0) + (key & 6) * 2;
 #pragma unroll 1
         for (int q = 0; q < 64; q += 16) {
           uint32_t z[16], dp[16];
@@ -385,18 +381,13 @@ __global__ void __launch_bounds__(Pz::THREADS, 1)
               // two rows of a key become two keys of a row, between two lanes: 4-byte
               // stores (2-byte ones: pz 0.10 ms more at 4096 tokens)
               z[e] = pack_bf16x2(pr, dz);
-              auto put = [&](uint32_t v0, uint32_t v1, uint8_t* base) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
-                const uint32_t k0 = lane & 1 ? got : v0, k1 = lane & 1 ? v1 : got;
+              if (e & 1) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 1 ? z[e - 1] : z[e], 1);
+                const uint32_t k0 = lane & 1 ? got : z[e - 1], k1 = lane & 1 ? z[e] : got;
                 const int rr = r - 1 + (lane & 1);
-                uint8_t* to = base + rr * 128 + ((unit ^ (rr & 7)) << 4);
+                uint8_t* to = dst + rr * 128 + ((unit ^ (rr & 7)) << 4);
                 *reinterpret_cast<uint32_t*>(to) = __byte_perm(k0, k1, 0x5410);
                 *reinterpret_cast<uint32_t*>(to + BLOCK) = __byte_perm(k0, k1, 0x7632);
-              };
-              if (e & 1) put(z[e - 1], z[e], dst);
-              if (TWO) {
-                dp[e] = pack_bf16x2(pr - lo_f(z[e]), dz - hi_f(z[e]));
-                if (e & 1) put(dp[e - 1], dp[e], dst + 2 * BLOCK);
               }
             }
           }
@@ -483,8 +474,8 @@ struct Task {
   }
 };
 
-// The tasks first, first + step, ... of one kind.  PARTS: of P and dZ.
-template <bool DKV, int PARTS>
+// The tasks first, first + step, ... of one kind.
+template <bool DKV>
 __device__ __forceinline__ void product(const CUtensorMap& tm_pz, const CUtensorMap& tm_kv, const CUtensorMap& tm_q,
                                         const CUtensorMap& tm_do, const Params& p, uint8_t* sm, int first,
                                         int step, int tasks) {
@@ -552,8 +543,8 @@ __device__ __forceinline__ void product(const CUtensorMap& tm_pz, const CUtensor
           if (!t.sees(l)) continue;
           const int c0 = place(l, 4 * t.kt + 2 * rank), c1 = place(l, 4 * t.kt + 2 * rank + 1);
 #pragma unroll 1
-          for (int st = 0; st < 4 * PARTS && ok; ++st) {   // dZ and q or P and d_o, 64 rows, a part
-            const int dz = 1 - (st & 1), which = dz + 2 * (st >> 2), y = 64 * (st >> 1 & 1);
+          for (int st = 0; st < 4 && ok; ++st) {     // dZ and q or P and d_o, 64 rows
+            const int dz = 1 - (st & 1), y = 64 * (st >> 1);
             if (!acquire()) break;
             if (elect_one_lane()) {
               uint8_t* a = sm + r.slot * C::STAGE;
@@ -562,9 +553,9 @@ __device__ __forceinline__ void product(const CUtensorMap& tm_pz, const CUtensor
               const bool rot = t.upper && dz;
               mbar_expect_tx_cluster(bar, (rot ? 5 : 4) * CHUNK);
               tma_load_2d_pair(a, &tm_pz, bar, 0,
-                               c0 < 0 ? 0 : static_cast<int>(p.block_row<PARTS>(t.b, x, c0, which)) + y);
+                               c0 < 0 ? 0 : static_cast<int>(p.block_row(t.b, x, c0, dz)) + y);
               tma_load_2d_pair(a + CHUNK, &tm_pz, bar, 0,
-                               c1 < 0 ? 0 : static_cast<int>(p.block_row<PARTS>(t.b, x, c1, which)) + y);
+                               c1 < 0 ? 0 : static_cast<int>(p.block_row(t.b, x, c1, dz)) + y);
               const CUtensorMap* tm = dz ? &tm_q : &tm_do;
               tma_load_3d_pair(w, tm, bar, col, x * X + y, t.b);
               tma_load_3d_pair(w + CHUNK, tm, bar, col + 64, x * X + y, t.b);
@@ -575,8 +566,8 @@ __device__ __forceinline__ void product(const CUtensorMap& tm_pz, const CUtensor
         }
       } else {
         const Pages l = tile_pages(p, t.s, t.x0 + rank);
-        for (int k = 0; k < t.list.count() * PARTS && ok; ++k) {
-          const int pg = t.list.page(k / PARTS), part = k % PARTS, c = place(l, pg), row = static_cast<int>(page_row(p.kv, t.b, pg));
+        for (int k = 0; k < t.list.count() && ok; ++k) {
+          const int pg = t.list.page(k), c = place(l, pg), row = static_cast<int>(page_row(p.kv, t.b, pg));
           const uint64_t any = range_bits(0, t.s.L, pg * 64);
           if (!acquire()) break;
           uint8_t* a = sm + r.slot * C::STAGE;
@@ -608,7 +599,7 @@ __device__ __forceinline__ void product(const CUtensorMap& tm_pz, const CUtensor
             } else {
               mbar_expect_tx_cluster_release(bar, 2 * CHUNK);
             }
-            const int br = c < 0 ? 0 : static_cast<int>(p.block_row<PARTS>(t.b, t.x0 + rank, c, 1 + 2 * part));
+            const int br = c < 0 ? 0 : static_cast<int>(p.block_row(t.b, t.x0 + rank, c, 1));
             tma_load_2d_pair(a, &tm_pz, bar, 0, br);
             tma_load_2d_pair(a + CHUNK, &tm_pz, bar, 0, br + 64);
             if (any == ~0ull) {
@@ -663,10 +654,10 @@ __device__ __forceinline__ void product(const CUtensorMap& tm_pz, const CUtensor
       if constexpr (DKV) {
         for (int x = t.x0; x < t.x1 && ok; ++x) {
           if (!t.sees(tile_pages(p, t.s, x))) continue;
-          for (int st = 0; st < 4 * PARTS && ok; ++st) multiply(d, t.upper && !(st & 1));
+          for (int st = 0; st < 4 && ok; ++st) multiply(d, t.upper && !(st & 1));
         }
       } else {
-        for (int k = 0; k < t.list.count() * PARTS && ok; ++k) multiply(d, t.upper);
+        for (int k = 0; k < t.list.count() && ok; ++k) multiply(d, t.upper);
       }
       if (elect_one_lane()) umma_commit_pair(done);
       __syncwarp();
@@ -749,7 +740,6 @@ __device__ __forceinline__ void product(const CUtensorMap& tm_pz, const CUtensor
 // share dq's tasks, the others have a task of dkv each and follow as SMs fall free (a launch
 // for each: 3 x 301 tokens, 8 heads 49.0 us instead of 45.3, 4096 tokens 1.99 ms instead of
 // 1.97).
-template <int PARTS>
 __global__ void __launch_bounds__(Prod::THREADS, 1)
     product_kernel(const __grid_constant__ CUtensorMap tm_pz, const __grid_constant__ CUtensorMap tm_kv,
                    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -759,9 +749,9 @@ __global__ void __launch_bounds__(Prod::THREADS, 1)
   uint8_t* sm = smem_align1024(smem_raw);
   const int pair = blockIdx.x >> 1;
   if (pair < dq_pairs)
-    product<false, PARTS>(tm_pz, tm_kv, tm_q, tm_do, p, sm, pair, dq_pairs, dq_tasks);
+    product<false>(tm_pz, tm_kv, tm_q, tm_do, p, sm, pair, dq_pairs, dq_tasks);
   else
-    product<true, PARTS>(tm_pz, tm_kv, tm_q, tm_do, p, sm, pair - dq_pairs, dkv_tasks, dkv_tasks);
+    product<true>(tm_pz, tm_kv, tm_q, tm_do, p, sm, pair - dq_pairs, dkv_tasks, dkv_tasks);
 }
 
 // dkv of a row: its segments in order (and what earlier chunks left), four dims a thread.
@@ -805,8 +795,7 @@ Plan plan(int B, int T, int H, int max_kv_len, int64_t span, int64_t window, int
   const int64_t tokens = (X + H - 2) / H + 1;
   const int64_t np = (span + tokens) / 64 + 4, most = (S + 63) / 64;
   q.np = static_cast<int>(np < most ? np : most);
-  q.parts = B * rows <= FEW ? 2 : 1;
-  int64_t rc = kChunkBytes / (static_cast<int64_t>(B) * q.np * 2 * q.parts * BLOCK) / 2 * 2;
+  int64_t rc = kChunkBytes / (static_cast<int64_t>(B) * q.np * 2 * BLOCK) / 2 * 2;
   if (rc < 2) rc = 2;
   q.RC = static_cast<int>(rc < q.RT ? rc : q.RT);
   q.KT = static_cast<int>((S + 255) / 256);
@@ -831,7 +820,7 @@ Sizes sizes(const Plan& q, int B, int T, int H, int max_kv_len, int64_t span) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   Sizes z{};
   z.rows = up(static_cast<size_t>(B) * T * H * sizeof(float2));
-  z.pz = BLOCK + static_cast<size_t>(B) * q.RC * q.np * 2 * q.parts * BLOCK;
+  z.pz = BLOCK + static_cast<size_t>(B) * q.RC * q.np * 2 * BLOCK;
   const int64_t all = most_key_tiles(q.seg, H, span), twice = 2ll * q.KT;
   z.part = static_cast<size_t>(B) * q.G * (all < twice ? all : twice) * 256 * kRlat * sizeof(float);
   z.acc = q.RC < q.RT ? up(static_cast<size_t>(B) * max_kv_len * kRlat * sizeof(float)) : 0;
@@ -909,12 +898,11 @@ dsa_status_t window_bwd_launch(const WindowBwdArgs& a, cudaStream_t stream) {
     const int64_t sums = 2ll * f.B * q.G * q.per_seg();
     if (sums > (1 << 30) || tiles > (1 << 30)) return DSA_ERR_UNSUPPORTED;
     const int64_t some = tiles < pairs ? tiles : pairs / 2 * 2;   // (even, as the tiles are)
-    dsa_status_t st = launch_pairs("pz_kernel", q.parts == 2 ? pz_kernel<true> : pz_kernel<false>, some, Pz::THREADS, Pz::SMEM, stream, tq_tile,
-                                   td_tile, tk, p);
+    dsa_status_t st = launch_pairs("pz_kernel", pz_kernel, some, Pz::THREADS, Pz::SMEM, stream, tq_tile, td_tile,
+                                   tk, p);
     if (st == DSA_OK)
-      st = launch_pairs("product_kernel", q.parts == 2 ? product_kernel<2> : product_kernel<1>, some + sums,
-                        Prod::THREADS, Prod::SMEM, stream, tp, tk, tq, td, p, static_cast<int>(some),
-                        static_cast<int>(tiles), static_cast<int>(sums));
+      st = launch_pairs("product_kernel", product_kernel, some + sums, Prod::THREADS, Prod::SMEM, stream, tp, tk,
+                        tq, td, p, static_cast<int>(some), static_cast<int>(tiles), static_cast<int>(sums));
     if (st != DSA_OK) return st;
     launch_overlapped(reduce_kernel, static_cast<unsigned>(static_cast<int64_t>(f.B) * f.max_kv_len), 144, 0,
                       0, stream, p);
