@@ -760,7 +760,8 @@ __global__ void __launch_bounds__(144) reduce_kernel(const Params p) {
   pdl_wait();
   pdl_start_next();
   const Seq s = seq_of(p.m, b);
-  if (!s.ok || key >= s.L) return;
+  // (rows of a sequence whose queries are all behind its end get their zeros)
+  if (s.pos0 < 0 || s.L > p.m.max_kv_len || key >= s.L) return;
   const int2 tiles = tiles_of(p, s, kt);
   float4* acc = reinterpret_cast<float4*>(p.acc + (static_cast<int64_t>(b) * p.m.max_kv_len + key) * kRlat) +
                 threadIdx.x;

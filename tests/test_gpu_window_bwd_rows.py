@@ -53,3 +53,24 @@ def test_gradients_alone_and_in_a_batch(dsa, case):
         alone, _ = _gradients(dsa, q[one].contiguous(), base[one].contiguous(), d_o[one].contiguous(),
                               starts[one], window, first)
         assert torch.equal(dq[b], alone[0]), b
+
+
+def test_rows_of_a_sequence_without_queries(dsa):
+    """Queries at or beyond kv_len see nothing and are flagged; the rows below kv_len get their zeros."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(61)
+    B, T, H, S = 4, 3, 8, 600
+    q, base, d_o = _normal(gen, B, T, H, 576), _normal(gen, B, S, 576), _normal(gen, B, T, H, 512)
+    starts, lens = [597, 300, 520, 0], [600, 300, 257, 0]
+    qs, kl = _i32(starts), _i32(lens)
+    ws = dsa.new_workspace(dsa.workspace_bytes(dsa.OP_MLA_WINDOW_BWD, B, T, S, H, 90))
+    dkv = torch.full((B, S, 576), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    o, lse = dsa.mla_window_fwd(q, dsa.Rows(base), qs, kl, 88, 2, S)
+    dq, _ = dsa.mla_window_bwd(q, dsa.Rows(base), qs, kl, 88, 2, S, o, lse, d_o, dkv=dkv, workspace=ws)
+    assert dsa.read_device_status(ws)[0] == dsa.DSA_ERR_BAD_INDEX
+    assert (dq[1:] == 0).all()
+    for b in range(B):
+        assert (dkv[b, lens[b]:] == SENTINEL).all() and not (dkv[b, :lens[b]] == SENTINEL).any(), b
+    for b in (1, 2):
+        assert (dkv[b, :lens[b]] == 0).all(), b
+    assert (dkv[0, 512:] != 0).any() and (dkv[0, 2:500] == 0).all()
