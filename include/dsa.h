@@ -119,7 +119,8 @@ typedef enum { DSA_ROPE_NONE = 0, DSA_ROPE_HALVES = 1, DSA_ROPE_PAIRS = 2 } dsa_
  * indexer, H for sparse MLA, ignored for the gate; for the FP8 projection
  * B = M, Tq = 1, max_kv_len = K, heads = N; for the tree Tq = T and topk is
  * ignored; for the window and its backward pass topk = window + n_first).
- * Always >= 256. */
+ * Always >= 256.  For these three a size never falls as B, Tq, max_kv_len or topk
+ * grows: one taken for a loop's largest call serves its smaller ones. */
 size_t dsa_workspace_bytes(dsa_op_t op, int B, int Tq, int max_kv_len, int heads, int topk);
 
 /* Zero the status header of a workspace (asynchronous on `stream`). */

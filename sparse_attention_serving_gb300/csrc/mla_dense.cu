@@ -1203,8 +1203,17 @@ dsa_status_t launch(const DenseArgs& a, const Plan& q, const Params& p, cudaStre
 
 }  // namespace dense
 
+// What these and all smaller calls need at most: whether units are cut, and for how many pairs,
+// goes up and down with the sizes (76 sequences may stay whole where 75 are cut).
 size_t dense_scratch_bytes(int B, int T, int H, int64_t span, bool tree) {
-  return dense::part_bytes(dense::plan(B, T, H, span, tree));
+  const int64_t rows = static_cast<int64_t>(T) * H, most = num_sms() / 2;
+  dense::Plan q{};
+  q.R = rows <= 96 ? 48 : rows <= 128 ? 64 : 96;
+  const int64_t units = B * ((rows + 127) / 128);
+  const int64_t blocks = tree ? (span + 127) / 128 : (span + 2 * q.R + 64) / 128 + 2;
+  q.cut = units > most || blocks > 4;
+  q.pairs = static_cast<int>(units < most && units * blocks < most ? units * blocks : most);
+  return dense::part_bytes(q);
 }
 
 dsa_status_t dense_fwd_launch(const DenseArgs& a, cudaStream_t stream) {

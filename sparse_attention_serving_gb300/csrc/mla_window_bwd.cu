@@ -840,8 +840,27 @@ dsa_status_t launch_pairs(const char* what, Kernel kernel, int64_t pairs, int th
 
 }  // namespace wbw
 
+// What these and all smaller calls with as many heads need at most; sizes() itself goes up and down
+// with the segments.  With N = B RC tiles and s = span / 256 + 2, a segment has seg =
+// max(4, N s / 300) tiles (or all of its sequence's) and reaches at most r = s + 3 + seg / 2H key
+// tiles, 2 KT where that is less, so that there are B G <= min(N / 4, 300 / s) + B segments and
+// B G r <= min(N / 4, 300 / s) (s + 3) + N / H + B (s + 3), where s >= 2.
 size_t window_bwd_scratch_bytes(int B, int T, int H, int max_kv_len, int64_t span) {
-  return wbw::sizes(wbw::plan(B, T, H, max_kv_len, span, span, 0), B, T, H, max_kv_len, span).total();
+  using namespace wbw;
+  const Plan q = plan(B, T, H, max_kv_len, span, span, 0);
+  Sizes z = sizes(q, B, T, H, max_kv_len, span);
+  const int64_t tiles = static_cast<int64_t>(B) * q.RT, tile = static_cast<int64_t>(q.np) * 2 * BLOCK;
+  const int64_t least = 2 * B * tile, some = kChunkBytes > least ? kChunkBytes : least;
+  z.pz = BLOCK + static_cast<size_t>(tiles < some / tile ? tiles * tile : some);
+  const int64_t twice = 2ll * q.KT, far = span / 256 + 5, reach = far < twice ? far : twice;
+  const int64_t few = (tiles * reach + 3) / 4;
+  const int64_t sums = (few < 750 ? few : 750) + tiles / H + 1 + B * reach;
+  const int64_t segs = static_cast<int64_t>(B) * ((q.RT + 3) / 4);
+  const int64_t all = (segs < 150 + B ? segs : 150 + B) * twice;
+  z.part = static_cast<size_t>(sums < all ? sums : all) * 256 * kRlat * sizeof(float);
+  const size_t acc = static_cast<size_t>(B) * max_kv_len * kRlat * sizeof(float);
+  z.acc = q.RT > 2 && tiles > kChunkBytes / tile ? (acc + 255) / 256 * 256 : 0;
+  return z.total();
 }
 
 dsa_status_t window_bwd_launch(const WindowBwdArgs& a, cudaStream_t stream) {
