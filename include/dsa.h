@@ -439,7 +439,8 @@ dsa_status_t dsa_linear_fp8(const uint8_t* a_codes, const float* a_scale, const 
  * outside the table leaves out all of its token; n_new outside [0, Tq] is taken as
  * the nearer bound.  Each is recorded as DSA_ERR_BAD_INDEX.  No output may overlap
  * an input (q_idx_out = q_idx apart) or another output.
- * Supported: D_I in {64, 128}; B, Tq >= 1; 1 <= H, H_I <= 1024 where given; n_pos >= 1.
+ * Supported: D_I in {64, 128}; B, Tq >= 1; 1 <= H, H_I <= 1024 where given; n_pos >= 1;
+ * B * Tq < 2^25, and B * Tq * ceil((96 + 4 H + 8 H_I) / 128) < 2^31.
  * All arrays but the int32 ones (4) 16-byte aligned.  Workspace: the 256-byte
  * status header.
  */

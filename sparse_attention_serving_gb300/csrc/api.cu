@@ -557,7 +557,6 @@ dsa_status_t dsa_cache_append_rope(const float* k_pre, const uint16_t* kv_new,
     return DSA_ERR_INVALID_ARGUMENT;
   if (D_I != 64 && D_I != 128) return DSA_ERR_UNSUPPORTED;
   if ((q_pe != nullptr && H > 1024) || (q_idx != nullptr && H_I > 1024)) return DSA_ERR_UNSUPPORTED;
-  // at most 49 CTAs a token
   if (static_cast<int64_t>(B) * Tq >= (int64_t(1) << 25)) return DSA_ERR_UNSUPPORTED;
   AppendRopeArgs a{};
   dsa_status_t st = resolve_rows(k_cache, B, 0, D_I, &a.k_cache);

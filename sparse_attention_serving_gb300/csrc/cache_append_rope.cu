@@ -293,7 +293,9 @@ dsa_status_t cache_append_rope_launch(const AppendRopeArgs& a, cudaStream_t stre
   p.chunks = (p.items + THREADS - 1) / THREADS;
   p.eps = a.eps;
   p.status = a.status;
-  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Tq * p.chunks);
+  const int64_t ctas = static_cast<int64_t>(a.B) * a.Tq * p.chunks;
+  if (ctas > 0x7fffffff) return DSA_ERR_UNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>(ctas);
   if (a.D_I == 128)
     append_rope_kernel<128><<<grid, THREADS, 0, stream>>>(p);
   else
