@@ -472,11 +472,12 @@ dsa_status_t dsa_cache_append_rope(const float* k_pre, const uint16_t* kv_new,
  * infinity or a NaN too) reaches only the tokens that see it; such a row is fast
  * behind the sequence's last, and slow where some tokens do not see it.
  * Finite values whose magnitudes add up to less than 2^107 over a token's rows give
- * finite outputs, whatever the scores.
+ * finite outputs, whatever its (finite) scores.
  * kv_len[b] < 0, kv_len[b] + n_draft[b] > max_kv_len (the sequence's tokens then see
  * nothing), n_draft outside [0, T] (taken as the nearer bound) and pages outside the
  * pool (not seen) are recorded as DSA_ERR_BAD_INDEX.
- * Supported: 1 <= H <= 128, 1 <= T <= 64.  Equal calls give equal bits.
+ * Supported: 1 <= H <= 128, 1 <= T <= 64, max_kv_len + T <= 2^31 - 256.  Equal calls
+ * give equal bits.
  * Workspace: dsa_workspace_bytes(DSA_OP_MLA_TREE, B, T, max_kv_len, H, 0).
  */
 dsa_status_t mla_tree_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const uint64_t* tree,
@@ -495,9 +496,11 @@ dsa_status_t mla_tree_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const uin
  * Only rows that some query sees are needed (a cache may have dropped the rest:
  * pages in between are not looked up).  What a row holds reaches only the queries
  * that see it.  Finite values whose magnitudes add up to less than 2^107 over a
- * query's rows give finite outputs, whatever the scores.  A query at or beyond kv_len[b], kv_len[b] > max_kv_len, q_start < 0
- * (nothing seen) and pages outside the pool (not seen): DSA_ERR_BAD_INDEX.
- * Supported: 1 <= H <= 128.  Equal calls give equal bits.
+ * query's rows give finite outputs, whatever its (finite) scores.  A query at or beyond
+ * kv_len[b], kv_len[b] > max_kv_len, q_start < 0 (nothing seen) and pages outside the
+ * pool (not seen): DSA_ERR_BAD_INDEX.
+ * Supported: 1 <= H <= 128, max_kv_len + Tq <= 2^31 - 256.  Equal calls give equal
+ * bits.
  * Workspace: dsa_workspace_bytes(DSA_OP_MLA_WINDOW, B, Tq, max_kv_len, H, window + n_first).
  */
 dsa_status_t mla_window_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const int32_t* q_start,
@@ -525,7 +528,7 @@ dsa_status_t mla_window_fwd(const uint16_t* q_lat, const dsa_rows_t* kv, const i
  * They are added in a fixed order: equal calls give equal bits.
  * A sequence with kv_len[b] > max_kv_len or q_start[b] < 0 gets dq = 0 and no dkv;
  * errors as for mla_window_fwd.  A paged kv: DSA_ERR_UNSUPPORTED.
- * Supported: 1 <= H <= 128.
+ * Supported: 1 <= H <= 128, max_kv_len + Tq <= 2^31 - 256.
  * Workspace: dsa_workspace_bytes(DSA_OP_MLA_WINDOW_BWD, B, Tq, max_kv_len, H, window + n_first).
  */
 dsa_status_t mla_window_bwd(const uint16_t* q_lat, const dsa_rows_t* kv, const int32_t* q_start,

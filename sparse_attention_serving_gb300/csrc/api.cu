@@ -601,6 +601,8 @@ static dsa_status_t dense_args(const uint16_t* q_lat, const dsa_rows_t* kv, cons
   if (!(scale > 0.f) || !(scale < 2.0e38f)) return DSA_ERR_INVALID_ARGUMENT;
   if (H > 128) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(B) * T * H >= (int64_t(1) << 31) - 4096) return DSA_ERR_UNSUPPORTED;
+  // positions of all queries, and the last page's end, in 32 bits
+  if (static_cast<int64_t>(max_kv_len) + T > (int64_t(1) << 31) - 256) return DSA_ERR_UNSUPPORTED;
   dsa_status_t st = resolve_rows(kv, B, max_kv_len, kRlat, &a->kv);
   if (st != DSA_OK) return st;
   st = check_ws(workspace, ws_bytes,

@@ -1,5 +1,6 @@
 """Workspace sizes of mla_tree_fwd, mla_window_fwd and mla_window_bwd that a caller takes for several
 calls.  CPU only."""
+import ctypes
 import random
 
 import pytest
@@ -49,3 +50,17 @@ def test_workspace_stays_small_where_nothing_is_cut(dsa):
     """A few short sequences need no more than the status header."""
     for B, S in ((1, 512), (64, 512), (4, 100)):
         assert dsa.workspace_bytes(dsa.OP_MLA_TREE, B, 1, S, 96, 0) == 256
+
+
+def test_positions_beyond_32_bits_are_refused(dsa):
+    """A query's position, and the end of the last page, have to fit 32 bits (a pool of few pages may
+    stand for any number of rows).  Refused calls do not get as far as a launch."""
+    fake, ws = ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 24)
+    rows = dsa._Rows(1 << 20, 0, 1 << 20, 1 << 25, 64, 4)
+    for S, T in ((2 ** 31 - 1, 1), (2 ** 31 - 65, 64), (2 ** 31 - 256, 1)):
+        code = dsa.lib.mla_tree_fwd(fake, rows, fake, fake, None, 1, T, 96, S, 0.1, fake, fake, ws, 1 << 40, None)
+        assert code == dsa.DSA_ERR_UNSUPPORTED, (S, T)
+    for S, T in ((2 ** 31 - 1, 1), (2 ** 31 - 1, 4096), (2 ** 31 - 4096, 4096)):
+        code = dsa.lib.mla_window_fwd(fake, rows, fake, fake, 1, T, 96, 64, 4, S, 0.1, fake, fake, ws, 1 << 40,
+                                      None)
+        assert code == dsa.DSA_ERR_UNSUPPORTED, (S, T)
