@@ -10,7 +10,7 @@
 
 namespace dsa {
 
-constexpr int kRlat = 576;  // latent row: 512 c_kv + 64 unrotated k_pe
+constexpr int kRlat = 576;  // latent row: 512 c_kv + 64 k_pe (rotated or not)
 constexpr int kVlat = 512;  // value width
 constexpr int kPage = 64;   // tokens per cache page
 

@@ -51,8 +51,8 @@ constexpr int64_t kChunkBytes = int64_t(4) << 30;   // P and dZ at a time
 constexpr int TASKS = 600;                          // dkv tasks aimed at: about eight a pair of SMs
 
 enum : uint32_t {
-  SITE_B = 0x720, SITE_KF = 0x721, SITE_KE = 0x722, SITE_AF = 0x723, SITE_AE = 0x724,
-  SITE_F = 0x725, SITE_E = 0x726, SITE_LAND = 0x727, SITE_DONE = 0x728, SITE_DRAIN = 0x729,
+  SITE_KF = 0x721, SITE_KE = 0x722, SITE_AF = 0x723, SITE_AE = 0x724,
+  SITE_F = 0x725, SITE_E = 0x726, SITE_LAND = 0x727, SITE_DONE = 0x728,
   SITE_DF = 0x72a
 };
 
