@@ -32,8 +32,8 @@
 // its own: units put back into the line cost every call 1.1 us at that end.  A unit some of
 // whose queries do not see a row of the sequence that holds an infinity or a NaN (0 * NaN
 // would reach them) goes to attend_row (33 ms there); the waits of the others last as long
-// as it moves on.  So does one with a reference that FP32 rounds too coarsely: beyond 2^28 it
-// is off the maximum by 8 and more, beyond 2^31 by more than an exponent holds (LOST).
+// as it moves on.  So does one with a reference that FP32 rounds too coarsely: from 2^28 on it
+// is off the maximum by up to 16 and more, from 2^31 on by more than an exponent holds (LOST).
 // P up to 2^80 leaves the FP32 sums 2^47 for the values: where a row's P passed 2^20 and its
 // O^T is not finite although its sum of P is, its unit is marked, and all warps do the marked
 // units' rows by attend_row at the end (looking for it in every unit's outputs took 1 % of
